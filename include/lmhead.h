@@ -376,6 +376,141 @@ int32_t lmhead_wgrad(const void *dlogits, int64_t ldd, const void *x, int64_t ld
                      int64_t M, int64_t K, int64_t V, void *stream);
 
 /*
+ * lmhead_logits_lora -- logits of a batch whose tokens use different low-rank
+ * adapters beside the shared vocabulary weight
+ *
+ *  z[m][v] = sum_k x[m][k] W[v][k] + s_a sum_j (sum_k x[m][k] A_a[j][k]) B_a[v][j],
+ *  a = adapter[m].  An extension the pages do not describe: lmhead_logits for
+ *  a batch that mixes requests of several fine-tuned variants.
+ *
+ *  x, W, out, out_dtype as lmhead_logits (FP32 keeps the FP32 sum, BF16 rounds
+ *  it once).
+ *  A        BF16 [n_adapters][rank][K], row pitch lda >= K, pitch stride_a
+ *           between adapters (both multiples of 8; stride_a at least one
+ *           adapter's span).
+ *  B        BF16 [n_adapters][V][rank], row pitch ldb >= rank, pitch stride_b
+ *           (the same).
+ *  adapter  int32 [M], the token's adapter in any order; a negative value:
+ *           none (the row equals lmhead_logits' up to rounding).  A value >=
+ *           n_adapters cannot be reported from the kernel: that row is NaN.
+ *  scale    FP32 [n_adapters] or NULL (1).
+ *  rank     1 .. 128, n_adapters >= 0.
+ *  One token's result depends on its own x and adapter only: a NaN or infinity
+ *  in another token or another adapter of the batch does not reach it.
+ *  A x is an FP32 sum and enters the second product unrounded (in three BF16
+ *  pieces of 8 bits).
+ *  workspace: device memory of at least lmhead_logits_lora_workspace_bytes(M,
+ *  V, rank, out_dtype) bytes (negative LMH_ERR_* for bad sizes), 16-byte
+ *  aligned; its contents do not matter on entry.  Two calls that share one
+ *  must be ordered on one stream.  out and workspace must not overlap each
+ *  other or an input.
+ */
+int64_t lmhead_logits_lora_workspace_bytes(int64_t M, int64_t V, int64_t rank, int32_t out_dtype);
+int32_t lmhead_logits_lora(const void *x, int64_t ldx, const void *W, int64_t ldw, const void *A,
+                           int64_t lda, int64_t stride_a, const void *B, int64_t ldb,
+                           int64_t stride_b, const int32_t *adapter, const float *scale,
+                           int64_t n_adapters, int64_t rank, void *out, int64_t ldo,
+                           int32_t out_dtype, int64_t M, int64_t K, int64_t V, void *workspace,
+                           int64_t workspace_bytes, void *stream);
+
+/*
+ * lmhead_lora_bwd -- gradients of the adapters' part of lmhead_logits_lora
+ *
+ *  With u[m] = s_a A_a x[m] and t[m] = s_a B_a^T g[m] (g = dlogits, a =
+ *  adapter[m]):
+ *    dX[m]  = A_a^T t[m]          (the adapters' part only: lmhead_dgrad with
+ *                                  FP32 dX gives the shared part, and
+ *                                  accumulate adds this one to it)
+ *    dA_a   = sum over a's tokens of t[m] x[m]^T
+ *    dB_a   = sum over a's tokens of g[m] u[m]^T
+ *  dlogits BF16 [M x V], ldd >= V; x BF16 [M x K]; A, B, adapter, scale, rank
+ *  and n_adapters as lmhead_logits_lora.
+ *  dX FP32 [M x K], dA FP32 [n_adapters][rank][K], dB FP32
+ *  [n_adapters][V][rank], pitches multiples of 4; each may be NULL (not
+ *  computed).  accumulate == 0 overwrites them (an adapter without tokens and
+ *  a token without an adapter get zeros), accumulate != 0 adds to them.  A
+ *  token whose id is >= n_adapters gets a NaN row in dX and enters no other
+ *  gradient.  u and t are FP32 sums, not rounded before the second product.
+ *  Results are deterministic.
+ *  workspace as lmhead_logits_lora, of lmhead_lora_bwd_workspace_bytes(M, K,
+ *  V, rank, n_adapters) bytes.  Limits (LMH_ERR_SHAPE): M <= 2^22,
+ *  ceil(V / 256) n_adapters and ceil(K / 256) (n_adapters + 2) <= 2^23, M + 64
+ *  (n_adapters + 1) < 2^31.
+ */
+int64_t lmhead_lora_bwd_workspace_bytes(int64_t M, int64_t K, int64_t V, int64_t rank,
+                                        int64_t n_adapters);
+int32_t lmhead_lora_bwd(const void *dlogits, int64_t ldd, const void *x, int64_t ldx, const void *A,
+                        int64_t lda, int64_t stride_a, const void *B, int64_t ldb, int64_t stride_b,
+                        const int32_t *adapter, const float *scale, int64_t n_adapters, int64_t rank,
+                        float *dX, int64_t lddx, float *dA, int64_t ldda, int64_t stride_da,
+                        float *dB, int64_t lddb, int64_t stride_db, int32_t accumulate, int64_t M,
+                        int64_t K, int64_t V, void *workspace, int64_t workspace_bytes,
+                        void *stream);
+
+/*
+ * lmhead_beam_select -- the next beams of a beam search from its logits
+ *
+ *  Request b holds beams w < n_beams; row b n_beams + w of the logits and
+ *  scores[b][w] (the beam's summed log-probability) belong to beam w.  Every
+ *  (w, v) is a candidate with
+ *    c = scores[b][w] + log softmax(logits row)[v],
+ *  except that a finished beam has c = scores[b][w] at v = eos and -inf
+ *  elsewhere.  A NaN c counts as -inf, as does every candidate of a beam whose
+ *  score is NaN or +inf.  The n_out largest are returned in descending order,
+ *  equal ones by ascending w n_cols + v:
+ *    out_scores[b][i] = c (computed in FP64, rounded once to FP32),
+ *    out_parent[b][i] = w, out_token[b][i] = v,
+ *    out_finished[b][i] = 1 if beam w was finished or v == eos, else 0.
+ *  The logits are read once; rows of finished beams and of beams whose score
+ *  is -inf, NaN or +inf are not read (but for at most 2 n_out values where
+ *  fewer than n_out candidates lie above -inf).
+ *
+ *  logits   [n_requests n_beams x n_cols], leading dimension ld, FP32 or BF16
+ *           (logits_dtype), as lmhead_logits writes them.
+ *  scores   FP32 [n_requests x n_beams]; finished uint8 of that shape or NULL
+ *           (none).  eos: any value; outside [0, n_cols) no token ends a beam.
+ *  Limits: 1 <= n_beams, n_out <= 64; n_out <= n_beams n_cols < 2^31;
+ *  n_requests <= 2^23 and n_requests n_beams ceil(n_cols / 2048) <= 2^25.
+ *  out_scores may be `scores` and out_finished may be `finished` when n_out ==
+ *  n_beams; no other overlap.
+ *  workspace as lmhead_logits_lora, of lmhead_beam_select_workspace_bytes(
+ *  n_requests, n_beams, n_cols, n_out) bytes.
+ */
+int64_t lmhead_beam_select_workspace_bytes(int64_t n_requests, int64_t n_beams, int64_t n_cols,
+                                           int64_t n_out);
+int32_t lmhead_beam_select(const void *logits, int64_t ld, int32_t logits_dtype, int64_t n_requests,
+                           int64_t n_beams, int64_t n_cols, const float *scores,
+                           const uint8_t *finished, int32_t eos, int64_t n_out, float *out_scores,
+                           int32_t *out_parent, int32_t *out_token, uint8_t *out_finished,
+                           void *workspace, int64_t workspace_bytes, void *stream);
+
+/*
+ * lmhead_beam_reorder -- per-beam states after a selection
+ *
+ *  A state is n_outer x (n_requests beams) x n_heads runs of n_positions
+ *  positions of position_bytes contiguous bytes (a key or value cache of
+ *  [layer][beam][head][position][dim], token histories [beam][position], ...),
+ *  of any element type; src_outer / src_row / src_head are its strides in
+ *  BYTES, and any alignment will do.
+ *    dst run (o, b beams_out + i, h) = src run (o, b beams_in + parent[b][i], h)
+ *  for the first lengths[b] positions (int32 [n_requests], clamped to [0,
+ *  n_positions]; NULL: all).  Positions from there on, and rows whose parent
+ *  lies outside [0, beams_in), are left as they were.
+ *  parent int32 [n_requests x beams_out], as lmhead_beam_select writes it.
+ *  In place: dst == src with equal strides and beams_out == beams_in; any
+ *  parent map, rows that stay are not touched.  Any other overlap of dst with
+ *  src, parent or lengths is LMH_ERR_ALIAS.  The runs of dst must be disjoint
+ *  (LMH_ERR_SHAPE).  Limits: beams <= 64; n_requests n_heads ceil(n_positions
+ *  position_bytes / 1024) <= 2^23; spans up to 2^44 bytes.
+ */
+int32_t lmhead_beam_reorder(const void *src, int64_t src_outer, int64_t src_row, int64_t src_head,
+                            void *dst, int64_t dst_outer, int64_t dst_row, int64_t dst_head,
+                            const int32_t *parent, const int32_t *lengths, int64_t n_outer,
+                            int64_t n_requests, int64_t beams_in, int64_t beams_out,
+                            int64_t n_heads, int64_t n_positions, int64_t position_bytes,
+                            void *stream);
+
+/*
  * lmhead_diag_mfma_loop -- diagnostic: the sustained BF16 matrix-core rate.
  *
  *  Not a step of the method: a register-only loop that the benchmark runs

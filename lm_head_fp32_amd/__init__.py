@@ -14,6 +14,8 @@ Shapes (row-major, last dimension contiguous, rows may be padded):
   stats {m, d, X_y, loss} per row; dlogits [n, V] fp32 or bf16
   dgrad: dlogits [M, V] bf16, W [V, K] bf16 -> dX [M, K]
   wgrad: dlogits [M, V] bf16, x [M, K] bf16 -> dW [V, K] fp32
+  adapters: A [n, r, K] bf16, B [n, V, r] bf16, adapter [M] int32, scale [n] fp32
+  beams: logits [B * W, V] fp32 or bf16, scores [B, W] fp32, parent [B, n_out] int32
 """
 import ctypes
 import os
@@ -26,6 +28,9 @@ __all__ = [
     "lmhead_xent_partial", "lmhead_xent_merge", "lmhead_xent_mean", "lmhead_xent_bwd",
     "lmhead_xent_fused", "lmhead_dgrad", "lmhead_dgrad_noalloc", "lmhead_wgrad",
     "lmhead_status_str", "lmhead_version", "lmhead_diag_mfma_loop", "lmhead_dgrad_workspace_bytes",
+    "lmhead_logits_lora", "lmhead_logits_lora_workspace_bytes", "lmhead_lora_bwd",
+    "lmhead_lora_bwd_workspace_bytes", "lmhead_beam_select", "lmhead_beam_select_workspace_bytes",
+    "lmhead_beam_reorder",
 ]
 
 LMH_BF16, LMH_FP32, LMH_FP16 = 0, 1, 2
@@ -60,6 +65,18 @@ _SIGNATURES = {
                          _vp], _i32),
     "lmhead_dgrad_noalloc": ([_vp, _i64, _vp, _i64, _vp, _i64, _i32, _i64, _i64, _i64, _i32,
                               _vp], _i32),
+    "lmhead_logits_lora_workspace_bytes": ([_i64, _i64, _i64, _i32], _i64),
+    "lmhead_logits_lora": ([_vp, _i64, _vp, _i64, _vp, _i64, _i64, _vp, _i64, _i64, _vp, _vp, _i64,
+                            _i64, _vp, _i64, _i32, _i64, _i64, _i64, _vp, _i64, _vp], _i32),
+    "lmhead_lora_bwd_workspace_bytes": ([_i64, _i64, _i64, _i64, _i64], _i64),
+    "lmhead_lora_bwd": ([_vp, _i64, _vp, _i64, _vp, _i64, _i64, _vp, _i64, _i64, _vp, _vp, _i64, _i64,
+                         _vp, _i64, _vp, _i64, _i64, _vp, _i64, _i64, _i32, _i64, _i64, _i64, _vp,
+                         _i64, _vp], _i32),
+    "lmhead_beam_select_workspace_bytes": ([_i64, _i64, _i64, _i64], _i64),
+    "lmhead_beam_select": ([_vp, _i64, _i32, _i64, _i64, _i64, _vp, _vp, _i32, _i64, _vp, _vp, _vp,
+                            _vp, _vp, _i64, _vp], _i32),
+    "lmhead_beam_reorder": ([_vp, _i64, _i64, _i64, _vp, _i64, _i64, _i64, _vp, _vp, _i64, _i64,
+                             _i64, _i64, _i64, _i64, _i64, _vp], _i32),
 }
 
 DGRAD_NOALLOC_MAX_BYTES = 64 << 20  # LMH_DGRAD_NOALLOC_MAX_BYTES in lmhead.h
@@ -508,6 +525,320 @@ def lmhead_wgrad(dlogits, x, dW=None, accumulate=False, stream=None):
     _check("lmhead_wgrad", lib().lmhead_wgrad(pd, ldd, px, ldx, pw, ldw, int(bool(accumulate)),
                                               M, K, V, _stream(stream)))
     return dW
+
+
+# ------------------------------------------------- adapters of many requests
+
+def _stack(t, name, dtype):
+    """(pointer, row pitch, pitch between matrices) of a 3-D GPU tensor with a
+    contiguous last dimension; a pitch that is never used (one row, one
+    matrix) is given as the library's alignment asks."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name}: expected a GPU tensor")
+    _on_current_device(t, name)
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    if t.dim() != 3:
+        raise ValueError(f"{name}: expected a 3-D tensor, got shape {tuple(t.shape)}")
+    n, rows, cols = t.shape
+    if cols > 1 and t.stride(2) != 1:
+        raise ValueError(f"{name}: last dimension must be contiguous")
+    ld = t.stride(1) if rows > 1 else (cols + 7) // 8 * 8
+    return _vp(t.data_ptr()), int(ld), int(t.stride(0)) if n > 1 else int(rows * ld)
+
+
+def _empty_stack(n, rows, cols, like):
+    """FP32 [n, rows, cols] whose rows start at multiples of four elements."""
+    ld = max((cols + 3) // 4 * 4, 4)
+    t = torch.empty((n, rows, ld), dtype=torch.float32, device=like.device)
+    return t if ld == cols else t[:, :, :cols]
+
+
+def _workspace(fn, need, workspace, like, stream):
+    """(tensor, bytes) of a workspace of at least `need` bytes: the caller's, or
+    one from torch's caching allocator, marked as in use on the launch stream
+    (a raw stream handle needs an explicit workspace)."""
+    if workspace is None:
+        if stream is not None and not isinstance(stream, torch.cuda.Stream):
+            raise ValueError(f"{fn} on a raw stream handle needs an explicit workspace")
+        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=like.device)
+        if stream is not None:
+            workspace.record_stream(stream)
+        return workspace, max(need, 16)
+    if not isinstance(workspace, torch.Tensor) or not workspace.is_cuda or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous GPU tensor")
+    _on_current_device(workspace, "workspace")
+    return workspace, workspace.numel() * workspace.element_size()
+
+
+def _adapter_args(x, A, B, adapter, scale, V):
+    """Checked adapter arguments: A [n, r, K], B [n, V, r], adapter [M],
+    scale [n] or None."""
+    pa, lda, sa = _stack(A, "A", torch.bfloat16)
+    pb, ldb, sb = _stack(B, "B", torch.bfloat16)
+    n, r, K = A.shape
+    if K != x.shape[1] or tuple(B.shape) != (n, V, r):
+        raise ValueError("A must be [n, r, K] and B [n, V, r]")
+    pi = _vec(adapter, "adapter", torch.int32, x.shape[0])
+    ps = None if scale is None else _vec(scale, "scale", torch.float32, n)
+    return (pa, lda, sa, pb, ldb, sb, pi, ps, n, r)
+
+
+def lmhead_logits_lora_workspace_bytes(M, V, rank, out_dtype="fp32"):
+    """Workspace bytes lmhead_logits_lora needs."""
+    need = int(lib().lmhead_logits_lora_workspace_bytes(int(M), int(V), int(rank), _dtype_code(out_dtype)))
+    if need < 0:
+        _check("lmhead_logits_lora_workspace_bytes", -need)
+    return need
+
+
+def lmhead_logits_lora(x, W, A, B, adapter, scale=None, out=None, out_dtype=None, workspace=None,
+                       stream=None):
+    """Logits of a batch whose tokens use different low-rank adapters:
+    logits[m] = x[m] . W^T + scale[a] (x[m] . A[a]^T) . B[a]^T, a = adapter[m].
+
+    A [n, r, K] and B [n, V, r] bf16 (r <= 128); adapter int32 [M] in any
+    order, negative: none, >= n: a NaN row; scale fp32 [n] or None (1).  out
+    and out_dtype as in lmhead_logits ('bf16' unless stated).  The adapters'
+    part is as exact as the FP32 logits."""
+    code = _out_code("lmhead_logits_lora", out, out_dtype, "bf16")
+    px, ldx = _mat(x, "x", torch.bfloat16)
+    pw, ldw = _mat(W, "W", torch.bfloat16)
+    M, K = x.shape
+    V = W.shape[0]
+    if W.shape[1] != K:
+        raise ValueError("x and W disagree on K")
+    ad = _adapter_args(x, A, B, adapter, scale, V)
+    if out is None:
+        if code not in (LMH_BF16, LMH_FP32):
+            _check("lmhead_logits_lora", 1)
+        out = _empty_rows(M, V, _TORCH_DT[code], x)
+    po, ldo = _mat(out, "out", out.dtype)
+    if out.shape != (M, V):
+        raise ValueError("out must be [M, V]")
+    ws, nbytes = _workspace("lmhead_logits_lora", lmhead_logits_lora_workspace_bytes(M, V, ad[9], code),
+                            workspace, x, stream)
+    _check("lmhead_logits_lora",
+           lib().lmhead_logits_lora(px, ldx, pw, ldw, *ad, po, ldo, code, M, K, V, ws.data_ptr(), nbytes,
+                                    _stream(stream)))
+    return out
+
+
+def lmhead_lora_bwd_workspace_bytes(M, K, V, rank, n_adapters):
+    """Workspace bytes lmhead_lora_bwd needs."""
+    need = int(lib().lmhead_lora_bwd_workspace_bytes(int(M), int(K), int(V), int(rank), int(n_adapters)))
+    if need < 0:
+        _check("lmhead_lora_bwd_workspace_bytes", -need)
+    return need
+
+
+def lmhead_lora_bwd(dlogits, x, A, B, adapter, scale=None, dX=None, dA=None, dB=None,
+                    accumulate=False, workspace=None, stream=None):
+    """Gradients of the adapters' part of lmhead_logits_lora: (dX [M, K],
+    dA [n, r, K], dB [n, V, r]), all fp32.
+
+    dlogits [M, V] bf16; x, A, B, adapter and scale as in the forward.  False
+    in the place of an output skips it.  accumulate=True adds to the given
+    ones (dX: to the shared part that lmhead_dgrad wrote), all of which must
+    then be passed or False."""
+    pg, ldg = _mat(dlogits, "dlogits", torch.bfloat16)
+    px, ldx = _mat(x, "x", torch.bfloat16)
+    M, V = dlogits.shape
+    K = x.shape[1]
+    if x.shape[0] != M:
+        raise ValueError("dlogits and x disagree on M")
+    ad = _adapter_args(x, A, B, adapter, scale, V)
+    n, r = ad[8], ad[9]
+    if accumulate and (dX is None or dA is None or dB is None):
+        raise ValueError("accumulate=True needs existing dX, dA and dB (or False)")
+    if dX is None:
+        dX = _empty_rows(M, K, torch.float32, x)
+    if dA is None:
+        dA = _empty_stack(n, r, K, x)
+    if dB is None:
+        dB = _empty_stack(n, V, r, x)
+    outs = []
+    if dX is False:
+        outs += [None, 0]
+    else:
+        outs += _mat(dX, "dX", torch.float32)
+        if dX.shape != (M, K):
+            raise ValueError("dX must be [M, K]")
+    for t, name, shape in ((dA, "dA", (n, r, K)), (dB, "dB", (n, V, r))):
+        if t is False:
+            outs += [None, 0, 0]
+            continue
+        outs += _stack(t, name, torch.float32)
+        if tuple(t.shape) != shape:
+            raise ValueError(f"{name} must be {list(shape)}")
+    ws, nbytes = _workspace("lmhead_lora_bwd", lmhead_lora_bwd_workspace_bytes(M, K, V, r, n), workspace,
+                            x, stream)
+    _check("lmhead_lora_bwd",
+           lib().lmhead_lora_bwd(pg, ldg, px, ldx, *ad, *outs, int(bool(accumulate)), M, K, V,
+                                 ws.data_ptr(), nbytes, _stream(stream)))
+    return tuple(None if t is False else t for t in (dX, dA, dB))
+
+
+# ------------------------------------------------------------- beam search
+
+def lmhead_beam_select_workspace_bytes(n_requests, n_beams, n_cols, n_out):
+    """Workspace bytes lmhead_beam_select needs."""
+    need = int(lib().lmhead_beam_select_workspace_bytes(int(n_requests), int(n_beams), int(n_cols),
+                                                        int(n_out)))
+    if need < 0:
+        _check("lmhead_beam_select_workspace_bytes", -need)
+    return need
+
+
+def _flags(t, name, n):
+    if isinstance(t, torch.Tensor) and t.dtype == torch.bool:
+        return _vec(t, name, torch.bool, n)
+    return _vec(t, name, torch.uint8, n)
+
+
+def lmhead_beam_select(logits, scores, n_out=None, finished=None, eos=-1, out_scores=None,
+                       out_parent=None, out_token=None, out_finished=None, workspace=None, stream=None):
+    """The next beams: per request the n_out best of scores[b, w] +
+    log_softmax(logits[b W + w])[v] over all beams and tokens, equal ones by
+    ascending w V + v (computed in 64 bits).
+
+    logits [B * W, V] fp32 or bf16; scores [B, W] fp32; finished [B, W] bool or
+    uint8 or None: a finished beam keeps its score and offers `eos` only.
+    n_out: W unless stated, at most 64.  Returns (scores [B, n_out] fp32,
+    parent [B, n_out] int32, token [B, n_out] int32, finished [B, n_out]
+    bool); out_scores and out_finished may be `scores` and `finished`."""
+    if not isinstance(scores, torch.Tensor) or scores.dim() != 2:
+        raise ValueError("scores: expected a [B, W] tensor")
+    if not isinstance(logits, torch.Tensor) or logits.dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError("logits: expected a GPU float32 or bfloat16 tensor")
+    pz, ld = _mat(logits, "logits", logits.dtype)
+    B, W = scores.shape
+    V = logits.shape[1]
+    if logits.shape[0] != B * W:
+        raise ValueError("logits must have a row for every beam: [B * W, V]")
+    k = W if n_out is None else int(n_out)
+    ps = _vec(scores, "scores", torch.float32, B * W)
+    pf = None if finished is None else _flags(finished, "finished", B * W)
+    dev = logits.device
+    if out_scores is None:
+        out_scores = torch.empty((B, k), dtype=torch.float32, device=dev)
+    if out_parent is None:
+        out_parent = torch.empty((B, k), dtype=torch.int32, device=dev)
+    if out_token is None:
+        out_token = torch.empty((B, k), dtype=torch.int32, device=dev)
+    if out_finished is None:
+        out_finished = torch.empty((B, k), dtype=torch.bool, device=dev)
+    for t, name in ((out_scores, "out_scores"), (out_parent, "out_parent"), (out_token, "out_token"),
+                    (out_finished, "out_finished")):
+        if not isinstance(t, torch.Tensor) or tuple(t.shape) != (B, k):
+            raise ValueError(f"{name} must be [B, n_out]")
+    po = _vec(out_scores, "out_scores", torch.float32, B * k)
+    pp = _vec(out_parent, "out_parent", torch.int32, B * k)
+    pt = _vec(out_token, "out_token", torch.int32, B * k)
+    pe = _flags(out_finished, "out_finished", B * k)
+    code = _DT[logits.dtype]
+    need = lmhead_beam_select_workspace_bytes(B, W, V, k)
+    ws, nbytes = _workspace("lmhead_beam_select", need, workspace, logits, stream)
+    _check("lmhead_beam_select",
+           lib().lmhead_beam_select(pz, ld, code, B, W, V, ps, pf, int(eos), k, po, pp, pt, pe,
+                                    ws.data_ptr(), nbytes, _stream(stream)))
+    return out_scores, out_parent, out_token, out_finished
+
+
+def _merged(shape, strides, name):
+    """(size, stride) of several dimensions walked as one."""
+    if 0 in shape:
+        return 0, 0
+    size, stride = 1, 0
+    for n, st in zip(reversed(shape), reversed(strides)):
+        if n == 1:
+            continue
+        if size == 1:
+            size, stride = n, st
+        elif st == stride * size:
+            size *= n
+        else:
+            raise ValueError(f"{name}: dimensions of strides {tuple(strides)} cannot be walked as one")
+    return size, stride
+
+
+def _runs(t, name, beam_dim, len_dim):
+    """(pointer, [outer, row, head strides in bytes], n_outer, rows, n_heads,
+    positions, bytes per position) of a per-beam state."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name}: expected a GPU tensor")
+    _on_current_device(t, name)
+    shape, strides, esz = list(t.shape), list(t.stride()), t.element_size()
+    tail = len(shape) if len_dim is None else len_dim + 1
+    # The contiguous run from the end: with lengths exactly the dimensions
+    # after len_dim, else as far as it goes.
+    run, d = 1, len(shape)
+    while d > (beam_dim + 1 if len_dim is None else tail):
+        if shape[d - 1] != 1 and strides[d - 1] != run:
+            if len_dim is None:
+                break
+            raise ValueError(f"{name}: the dimensions after len_dim must be contiguous")
+        run *= shape[d - 1]
+        d -= 1
+    positions = 1
+    if len_dim is not None:
+        positions = shape[len_dim]
+        if positions > 1 and strides[len_dim] != run:
+            raise ValueError(f"{name}: the positions along len_dim must be contiguous")
+        d = len_dim
+    n_outer, so = _merged(shape[:beam_dim], strides[:beam_dim], name)
+    n_heads, sh = _merged(shape[beam_dim + 1:d], strides[beam_dim + 1:d], name)
+    return (_vp(t.data_ptr()), [so * esz, strides[beam_dim] * esz, sh * esz], n_outer, shape[beam_dim],
+            n_heads, positions, run * esz)
+
+
+def lmhead_beam_reorder(state, parent, out=None, beam_dim=0, len_dim=None, lengths=None, stream=None):
+    """Per-beam states after a selection: along beam_dim, row b W_out + i of the
+    result is row b W_in + parent[b, i] of `state`.  Returns the result.
+
+    state: any dtype, e.g. a cache [layers, B * W, heads, T, D] (beam_dim=1,
+    len_dim=3) or histories [B * W, T] (beam_dim=0).  parent [B, W_out] int32;
+    a row whose parent lies outside [0, W_in) is left as it was.
+    out=None reorders in place (W_out == W_in).  lengths int32 [B]: only the
+    first lengths[b] positions along len_dim move, the rest stays as it was;
+    the positions and the dimensions after them must be contiguous."""
+    if not isinstance(parent, torch.Tensor) or parent.dim() != 2:
+        raise ValueError("parent: expected a [B, W_out] tensor")
+    if not isinstance(state, torch.Tensor):
+        raise TypeError("state: expected a GPU tensor")
+    nd = state.dim()
+    beam_dim = beam_dim + nd if beam_dim < 0 else beam_dim
+    if not 0 <= beam_dim < nd:
+        raise ValueError("beam_dim is not a dimension of state")
+    if len_dim is not None:
+        len_dim = len_dim + nd if len_dim < 0 else len_dim
+        if not beam_dim < len_dim < nd:
+            raise ValueError("len_dim must be a dimension after beam_dim")
+    elif lengths is not None:
+        raise ValueError("lengths needs len_dim")
+    B, W_out = parent.shape
+    ps, ss, n_outer, rows, n_heads, positions, pos_bytes = _runs(state, "state", beam_dim, len_dim)
+    if B and rows % B:
+        raise ValueError("state does not hold the same number of beams for every request")
+    W_in = rows // B if B else 0
+    dst = state if out is None else out
+    want = list(state.shape)
+    want[beam_dim] = B * W_out
+    if not isinstance(dst, torch.Tensor) or dst.dtype != state.dtype or list(dst.shape) != want:
+        raise ValueError(f"the result is {want} {state.dtype}" +
+                         (": in place needs as many beams as before" if out is None else ""))
+    if out is None:
+        pd, ds = ps, ss
+    else:
+        pd, ds, *same = _runs(dst, "out", beam_dim, len_dim)
+        if [same[0]] + same[2:] != [n_outer, n_heads, positions, pos_bytes]:
+            raise ValueError("state and out are laid out too differently: their contiguous parts differ")
+    pp = _vec(parent, "parent", torch.int32, B * W_out)
+    pl = None if lengths is None else _vec(lengths, "lengths", torch.int32, B)
+    _check("lmhead_beam_reorder",
+           lib().lmhead_beam_reorder(ps, *ss, pd, *ds, pp, pl, n_outer, B, W_in, W_out, n_heads, positions,
+                                     pos_bytes, _stream(stream)))
+    return dst
 
 
 MFMA_LOOP_FLOP_PER_WORKGROUP_ITER = 2 * 32 * 32 * 16 * 8 * 4  # 8 chains x 4 waves

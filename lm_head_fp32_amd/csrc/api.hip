@@ -10,8 +10,10 @@
 #include <limits.h>
 #include <stdint.h>
 
+#include <algorithm>
 #include <atomic>
 #include <mutex>
+#include <utility>
 
 // The fixed scratch array of lmhead_dgrad_noalloc: the V-split dgrad's FP32
 // partial sums live here instead of in a caller workspace.  Each GPU the
@@ -204,6 +206,81 @@ int32_t launch_dgrad_split(const void *dlogits, int64_t ldd, const void *W, int6
     p.P = V;
     return launch_status(lmh::launch_gemm_dgrad_split(p, dx_dtype != LMH_FP32, splits, ws,
                                                       static_cast<hipStream_t>(stream)));
+}
+
+// --------------------------------------------------------------------------
+// Low-rank adapters.
+constexpr int64_t kMaxRank = 128;
+
+// A three-dimensional operand [n][rows][cols] with row pitch ld and pitch
+// `stride` between the n matrices (both multiples of `mult` elements).
+int32_t check_stack(const void *p, int64_t n, int64_t rows, int64_t cols, int64_t ld,
+                    int64_t stride, int mult)
+{
+    if (n == 0 || rows == 0 || cols == 0)
+        return LMH_OK;
+    LMH_TRY(check_matrix(p, rows, cols, ld, mult));
+    const int64_t one = (rows - 1) * ld + cols;  // <= kMaxSpanElems
+    if (n > 1 && (stride < one || !span_fits(n, one, stride)))
+        return LMH_ERR_SHAPE;
+    if (n > 1 && stride % mult != 0)
+        return LMH_ERR_ALIGN;
+    return LMH_OK;
+}
+
+Span span_of_stack(const void *p, int64_t n, int64_t rows, int64_t cols, int64_t ld, int64_t stride,
+                   int64_t esz)
+{
+    if (n <= 0 || rows <= 0 || cols <= 0)
+        return span_of(p, 0, 0, 0, 1);
+    return span_of(p, n, (rows - 1) * ld + cols, n > 1 ? stride : 0, esz);
+}
+
+// True when any output span overlaps an input span or another output.
+bool outputs_clash(const Span *outs, int n_out, const Span *ins, int n_in)
+{
+    for (int i = 0; i < n_out; ++i) {
+        for (int j = 0; j < n_in; ++j)
+            if (overlaps(outs[i], ins[j]))
+                return true;
+        for (int j = 0; j < i; ++j)
+            if (overlaps(outs[i], outs[j]))
+                return true;
+    }
+    return false;
+}
+
+Span bytes_span(const void *p, int64_t bytes)
+{
+    return span_of(p, 1, bytes, bytes, 1);
+}
+
+// Sizes shared by the adapter calls.
+bool adapter_sizes_ok(int64_t M, int64_t K, int64_t V, int64_t rank, int64_t n)
+{
+    return M >= 0 && K >= 0 && V >= 0 && M <= kMaxDim && K <= kMaxDim && V <= kMaxDim && rank >= 1 &&
+           rank <= kMaxRank && n >= 0 && n <= (kMaxLaunchItems / 256) - 2;
+}
+
+// The gradients' launches: one workgroup of 256 per (256 columns, group), and
+// 4 work-items per rank of every token; positions are kept in 32 bits.
+bool lora_bwd_fits(int64_t M, int64_t K, int64_t V, int64_t rank, int64_t n)
+{
+    const int64_t most = kMaxLaunchItems / 256;
+    return ceil_div(V, 256) <= most / std::max<int64_t>(n, 1) && ceil_div(K, 256) <= most / (n + 2) &&
+           M <= kMaxLaunchItems / (4 * kMaxRank) && M + 64 * (n + 1) <= kMaxDim;
+}
+
+constexpr int64_t kMaxBeams = 64;
+
+// The selection's sizes: every position w V + v in 32 bits, one wave per 2048
+// columns of a row, one workgroup per request.
+bool beam_sizes_ok(int64_t B, int64_t W, int64_t V, int64_t n_out)
+{
+    if (B < 0 || B > kMaxLaunchItems / 256 || W < 1 || W > kMaxBeams || V < 1 || V > kMaxDim / W ||
+        n_out < 1 || n_out > kMaxBeams || n_out > W * V)
+        return false;
+    return B == 0 || lmh::beam_segments(V) <= kMaxLaunchItems / 64 / (B * W);
 }
 
 }  // namespace
@@ -638,6 +715,273 @@ int32_t lmhead_wgrad(const void *dlogits, int64_t ldd, const void *x, int64_t ld
     return launch_status(lmh::launch_gemm_wgrad(
         p, accumulate ? lmh::Epi::kAccumF32 : lmh::Epi::kStoreF32,
         static_cast<hipStream_t>(stream)));
+}
+
+int64_t lmhead_logits_lora_workspace_bytes(int64_t M, int64_t V, int64_t rank, int32_t out_dtype)
+{
+    if (check_dtype_out(out_dtype) != LMH_OK)
+        return -static_cast<int64_t>(LMH_ERR_DTYPE);
+    if (!adapter_sizes_ok(M, 0, V, rank, 0) || !span_fits(M, V + 3, V + 3))
+        return -static_cast<int64_t>(LMH_ERR_SHAPE);
+    return lmh::lora_logits_workspace_bytes(M, V, rank, out_dtype == LMH_BF16);
+}
+
+int32_t lmhead_logits_lora(const void *x, int64_t ldx, const void *W, int64_t ldw, const void *A,
+                           int64_t lda, int64_t stride_a, const void *B, int64_t ldb,
+                           int64_t stride_b, const int32_t *adapter, const float *scale,
+                           int64_t n_adapters, int64_t rank, void *out, int64_t ldo,
+                           int32_t out_dtype, int64_t M, int64_t K, int64_t V, void *workspace,
+                           int64_t workspace_bytes, void *stream)
+{
+    LMH_TRY(check_dtype_out(out_dtype));
+    if (!adapter_sizes_ok(M, K, V, rank, n_adapters) || workspace_bytes < 0 || !span_fits(M, V + 3, V + 3))
+        return LMH_ERR_SHAPE;
+    const bool bf16 = out_dtype == LMH_BF16;
+    const int64_t osz = bf16 ? 2 : 4;
+    LMH_TRY(check_matrix(out, M, V, ldo, bf16 ? 8 : 4));
+    if (M == 0 || V == 0)
+        return LMH_OK;
+    LMH_TRY(check_matrix(x, M, K, ldx, 8));
+    LMH_TRY(check_matrix(W, V, K, ldw, 8));
+    LMH_TRY(check_stack(A, n_adapters, rank, K, lda, stride_a, 8));
+    LMH_TRY(check_stack(B, n_adapters, V, rank, ldb, stride_b, 8));
+    if (!adapter || !workspace)
+        return LMH_ERR_NULL;
+    if (!aligned4(adapter) || (scale && !aligned4(scale)) || !aligned16(workspace))
+        return LMH_ERR_ALIGN;
+    const int64_t need = lmh::lora_logits_workspace_bytes(M, V, rank, bf16);
+    if (workspace_bytes < need || !gemm_grid_fits(V, M, false))
+        return LMH_ERR_SHAPE;
+    const Span outs[] = {span_of(out, M, V, ldo, osz), bytes_span(workspace, need)};
+    const Span ins[] = {span_of(x, M, K, ldx, 2), span_of(W, V, K, ldw, 2),
+                        span_of_stack(A, n_adapters, rank, K, lda, stride_a, 2),
+                        span_of_stack(B, n_adapters, V, rank, ldb, stride_b, 2),
+                        span_of(adapter, 1, M, M, 4),
+                        span_of(scale, scale ? 1 : 0, n_adapters, n_adapters, 4)};
+    if (outputs_clash(outs, 2, ins, 6))
+        return LMH_ERR_ALIAS;
+    lmh::GemmProblem p;
+    p.A = static_cast<const uint16_t *>(W);
+    p.lda = ldw;
+    p.B = static_cast<const uint16_t *>(x);
+    p.ldb = ldx;
+    p.D = out;
+    p.ldd = ldo;
+    p.R = V;
+    p.C = M;
+    p.P = K;
+    lmh::LoraAdapters ad;
+    ad.A = static_cast<const uint16_t *>(A);
+    ad.lda = lda, ad.stride_a = stride_a;
+    ad.B = static_cast<const uint16_t *>(B);
+    ad.ldb = ldb, ad.stride_b = stride_b;
+    ad.adapter = adapter;
+    ad.scale = scale;
+    ad.n = n_adapters;
+    ad.r = static_cast<int>(rank);
+    return launch_status(lmh::launch_logits_lora(p, bf16, ad, workspace, static_cast<hipStream_t>(stream)));
+}
+
+int64_t lmhead_lora_bwd_workspace_bytes(int64_t M, int64_t K, int64_t V, int64_t rank,
+                                        int64_t n_adapters)
+{
+    if (!adapter_sizes_ok(M, K, V, rank, n_adapters) || !lora_bwd_fits(M, K, V, rank, n_adapters) ||
+        !span_fits(M, V + 3, V + 3))
+        return -static_cast<int64_t>(LMH_ERR_SHAPE);
+    return lmh::lora_bwd_workspace_bytes(M, V, rank, n_adapters);
+}
+
+int32_t lmhead_lora_bwd(const void *dlogits, int64_t ldd, const void *x, int64_t ldx, const void *A,
+                        int64_t lda, int64_t stride_a, const void *B, int64_t ldb, int64_t stride_b,
+                        const int32_t *adapter, const float *scale, int64_t n_adapters, int64_t rank,
+                        float *dX, int64_t lddx, float *dA, int64_t ldda, int64_t stride_da,
+                        float *dB, int64_t lddb, int64_t stride_db, int32_t accumulate, int64_t M,
+                        int64_t K, int64_t V, void *workspace, int64_t workspace_bytes, void *stream)
+{
+    if (!adapter_sizes_ok(M, K, V, rank, n_adapters) || !lora_bwd_fits(M, K, V, rank, n_adapters) ||
+        workspace_bytes < 0 || !span_fits(M, V + 3, V + 3))
+        return LMH_ERR_SHAPE;
+    if (!dX && !dA && !dB)
+        return LMH_OK;
+    LMH_TRY(check_matrix(dlogits, M, V, ldd, 8));
+    LMH_TRY(check_matrix(x, M, K, ldx, 8));
+    LMH_TRY(check_stack(A, n_adapters, rank, K, lda, stride_a, 8));
+    LMH_TRY(check_stack(B, n_adapters, V, rank, ldb, stride_b, 8));
+    if (dX)
+        LMH_TRY(check_matrix(dX, M, K, lddx, 4));
+    if (dA)
+        LMH_TRY(check_stack(dA, n_adapters, rank, K, ldda, stride_da, 4));
+    if (dB)
+        LMH_TRY(check_stack(dB, n_adapters, V, rank, lddb, stride_db, 4));
+    if ((M > 0 && !adapter) || !workspace)
+        return LMH_ERR_NULL;
+    if (!aligned4(adapter) || (scale && !aligned4(scale)) || !aligned16(workspace))
+        return LMH_ERR_ALIGN;
+    const int64_t need = lmh::lora_bwd_workspace_bytes(M, V, rank, n_adapters);
+    if (workspace_bytes < need)
+        return LMH_ERR_SHAPE;
+    const Span outs[] = {bytes_span(workspace, need), span_of(dX, dX ? M : 0, K, lddx, 4),
+                         span_of_stack(dA, dA ? n_adapters : 0, rank, K, ldda, stride_da, 4),
+                         span_of_stack(dB, dB ? n_adapters : 0, V, rank, lddb, stride_db, 4)};
+    const Span ins[] = {span_of(dlogits, M, V, ldd, 2), span_of(x, M, K, ldx, 2),
+                        span_of_stack(A, n_adapters, rank, K, lda, stride_a, 2),
+                        span_of_stack(B, n_adapters, V, rank, ldb, stride_b, 2),
+                        span_of(adapter, 1, M, M, 4),
+                        span_of(scale, scale ? 1 : 0, n_adapters, n_adapters, 4)};
+    if (outputs_clash(outs, 4, ins, 6))
+        return LMH_ERR_ALIAS;
+    lmh::LoraBwd p;
+    p.g = static_cast<const uint16_t *>(dlogits);
+    p.ldg = ldd;
+    p.x = static_cast<const uint16_t *>(x);
+    p.ldx = ldx;
+    p.ad.A = static_cast<const uint16_t *>(A);
+    p.ad.lda = lda, p.ad.stride_a = stride_a;
+    p.ad.B = static_cast<const uint16_t *>(B);
+    p.ad.ldb = ldb, p.ad.stride_b = stride_b;
+    p.ad.adapter = adapter;
+    p.ad.scale = scale;
+    p.ad.n = n_adapters;
+    p.ad.r = static_cast<int>(rank);
+    p.dX = dX, p.lddx = lddx;
+    p.dA = dA, p.ldda = ldda, p.stride_da = stride_da;
+    p.dB = dB, p.lddb = lddb, p.stride_db = stride_db;
+    p.accumulate = accumulate != 0;
+    p.M = M, p.K = K, p.V = V;
+    return launch_status(lmh::launch_lora_bwd(p, workspace, static_cast<hipStream_t>(stream)));
+}
+
+int64_t lmhead_beam_select_workspace_bytes(int64_t n_requests, int64_t n_beams, int64_t n_cols,
+                                           int64_t n_out)
+{
+    if (!beam_sizes_ok(n_requests, n_beams, n_cols, n_out))
+        return -static_cast<int64_t>(LMH_ERR_SHAPE);
+    return lmh::beam_workspace_bytes(n_requests * n_beams, n_cols, n_out);
+}
+
+int32_t lmhead_beam_select(const void *logits, int64_t ld, int32_t logits_dtype, int64_t n_requests,
+                           int64_t n_beams, int64_t n_cols, const float *scores,
+                           const uint8_t *finished, int32_t eos, int64_t n_out, float *out_scores,
+                           int32_t *out_parent, int32_t *out_token, uint8_t *out_finished,
+                           void *workspace, int64_t workspace_bytes, void *stream)
+{
+    LMH_TRY(check_dtype_out(logits_dtype));
+    if (!beam_sizes_ok(n_requests, n_beams, n_cols, n_out) || workspace_bytes < 0)
+        return LMH_ERR_SHAPE;
+    if (n_requests == 0)
+        return LMH_OK;
+    const bool bf16 = logits_dtype == LMH_BF16;
+    const int64_t rows = n_requests * n_beams, outs_n = n_requests * n_out;
+    LMH_TRY(check_matrix(logits, rows, n_cols, ld, bf16 ? 8 : 4));
+    if (!scores || !out_scores || !out_parent || !out_token || !out_finished || !workspace)
+        return LMH_ERR_NULL;
+    if (!aligned4(scores) || !aligned4(out_scores) || !aligned4(out_parent) || !aligned4(out_token) ||
+        !aligned16(workspace))
+        return LMH_ERR_ALIGN;
+    const int64_t need = lmh::beam_workspace_bytes(rows, n_cols, n_out);
+    if (workspace_bytes < need)
+        return LMH_ERR_SHAPE;
+    const Span z = span_of(logits, rows, n_cols, ld, bf16 ? 2 : 4);
+    const Span ss = bytes_span(scores, 4 * rows);
+    const Span sf = span_of(finished, finished ? 1 : 0, rows, rows, 1);
+    const Span outs[] = {bytes_span(workspace, need), bytes_span(out_parent, 4 * outs_n),
+                         bytes_span(out_token, 4 * outs_n), bytes_span(out_scores, 4 * outs_n),
+                         bytes_span(out_finished, outs_n)};
+    // The scores and flags may be replaced in place: a request's old ones are
+    // read before its new ones are written, in the same places.
+    const bool same = n_out == n_beams;
+    const Span ins[] = {z, same && out_scores == scores ? bytes_span(scores, 0) : ss,
+                        same && out_finished == finished ? bytes_span(finished, 0) : sf};
+    if (outputs_clash(outs, 5, ins, 3) || overlaps(outs[0], ss) || overlaps(outs[0], sf))
+        return LMH_ERR_ALIAS;
+    for (int i = 1; i < 5; ++i)
+        if ((i != 3 && overlaps(outs[i], ss)) || (i != 4 && overlaps(outs[i], sf)))
+            return LMH_ERR_ALIAS;
+    return launch_status(lmh::launch_beam_select(logits, ld, bf16, n_requests, n_beams, n_cols, scores,
+                                                 finished, eos, n_out, out_scores, out_parent, out_token,
+                                                 out_finished, workspace,
+                                                 static_cast<hipStream_t>(stream)));
+}
+
+int32_t lmhead_beam_reorder(const void *src, int64_t src_outer, int64_t src_row, int64_t src_head,
+                            void *dst, int64_t dst_outer, int64_t dst_row, int64_t dst_head,
+                            const int32_t *parent, const int32_t *lengths, int64_t n_outer,
+                            int64_t n_requests, int64_t beams_in, int64_t beams_out, int64_t n_heads,
+                            int64_t n_positions, int64_t position_bytes, void *stream)
+{
+    if (n_outer < 0 || n_requests < 0 || beams_in < 0 || beams_out < 0 || n_heads < 0 ||
+        n_positions < 0 || position_bytes < 0 || n_outer > kMaxDim || n_requests > kMaxDim ||
+        beams_in > kMaxBeams || beams_out > kMaxBeams || n_heads > kMaxDim || n_positions > kMaxDim ||
+        position_bytes > kMaxDim)
+        return LMH_ERR_SHAPE;
+    if (n_outer == 0 || n_requests == 0 || beams_out == 0 || n_heads == 0 || n_positions == 0 ||
+        position_bytes == 0)
+        return LMH_OK;
+    if (beams_in == 0)
+        return LMH_ERR_SHAPE;
+    const int64_t run = n_positions * position_bytes;  // < 2^62
+    const int64_t rows_in = n_requests * beams_in, rows_out = n_requests * beams_out;
+    // Bytes a tensor of [outer][rows][heads] runs spans; -1 when a stride is
+    // negative or the span passes 2^44 bytes.
+    auto extent = [&](int64_t so, int64_t sr, int64_t sh, int64_t rows) -> int64_t {
+        int64_t total = run;
+        const int64_t n[3] = {n_outer, rows, n_heads}, st[3] = {so, sr, sh};
+        for (int i = 0; i < 3; ++i) {
+            if (n[i] == 1)
+                continue;
+            if (st[i] < 0 || total > kMaxSpanElems || st[i] > (kMaxSpanElems - total) / (n[i] - 1))
+                return -1;
+            total += st[i] * (n[i] - 1);
+        }
+        return total > kMaxSpanElems ? -1 : total;
+    };
+    const int64_t src_bytes = extent(src_outer, src_row, src_head, rows_in);
+    const int64_t dst_bytes = extent(dst_outer, dst_row, dst_head, rows_out);
+    if (src_bytes < 0 || dst_bytes < 0)
+        return LMH_ERR_SHAPE;
+    // Destination runs must be disjoint: strides in ascending order, each at
+    // least what lies inside it.
+    int64_t dims[3][2] = {{dst_outer, n_outer}, {dst_row, rows_out}, {dst_head, n_heads}};
+    for (int i = 0; i < 3; ++i)
+        if (dims[i][1] == 1)
+            dims[i][0] = 0;
+    for (int i = 0; i < 3; ++i)
+        for (int j = 0; j < 2; ++j)
+            if (dims[j][0] > dims[j + 1][0])
+                std::swap(dims[j], dims[j + 1]);
+    int64_t inside = run;
+    for (int i = 0; i < 3; ++i) {
+        if (dims[i][1] == 1)
+            continue;
+        if (dims[i][0] < inside)
+            return LMH_ERR_SHAPE;
+        inside += dims[i][0] * (dims[i][1] - 1);
+    }
+    if (!src || !dst || !parent)
+        return LMH_ERR_NULL;
+    if (!aligned4(parent) || (lengths && !aligned4(lengths)))
+        return LMH_ERR_ALIGN;
+    // One launch covers at least one outer block.
+    const int64_t per_row = ceil_div(run, 256 * 4);
+    if (per_row > kMaxLaunchItems / 256 || n_requests > kMaxLaunchItems / 256 / per_row ||
+        n_heads > kMaxLaunchItems / 256 / per_row / n_requests)
+        return LMH_ERR_SHAPE;
+    const Span sp = bytes_span(parent, 4 * rows_out);
+    const Span sl = span_of(lengths, lengths ? 1 : 0, n_requests, n_requests, 4);
+    const Span sd = bytes_span(dst, dst_bytes);
+    if (overlaps(sd, sp) || overlaps(sd, sl))
+        return LMH_ERR_ALIAS;
+    if (src == dst) {
+        if (beams_in != beams_out || (n_outer > 1 && src_outer != dst_outer) ||
+            (rows_in > 1 && src_row != dst_row) || (n_heads > 1 && src_head != dst_head))
+            return LMH_ERR_ALIAS;
+    } else if (overlaps(sd, bytes_span(src, src_bytes))) {
+        return LMH_ERR_ALIAS;
+    }
+    const int64_t ss[3] = {src_outer, src_row, src_head}, ds[3] = {dst_outer, dst_row, dst_head};
+    return launch_status(lmh::launch_beam_reorder(src, dst, ss, ds, parent, lengths, n_outer, n_requests,
+                                                  beams_in, beams_out, n_heads, n_positions,
+                                                  position_bytes, static_cast<hipStream_t>(stream)));
 }
 
 int32_t lmhead_diag_mfma_loop(int64_t iters, int64_t n_workgroups, int32_t operands, float *sink,

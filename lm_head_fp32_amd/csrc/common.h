@@ -119,6 +119,56 @@ int mfma_loop_chains();
 hipError_t launch_mfma_loop(int64_t iters, int64_t n_workgroups, bool random_operands,
                             float *sink, hipStream_t s);
 
+// Low-rank adapters: A [n][r][K] and B [n][V][r] BF16, contiguous in K and r;
+// token m uses adapter[m] (negative: none); scale [n] or null (1).
+struct LoraAdapters {
+    const uint16_t *A;
+    int64_t lda, stride_a;
+    const uint16_t *B;
+    int64_t ldb, stride_b;
+    const int32_t *adapter;
+    const float *scale;
+    int64_t n;
+    int r;
+};
+
+// Gradients of the adapters' part of the logits; dX, dA, dB may be null.
+struct LoraBwd {
+    const uint16_t *g;
+    int64_t ldg;
+    const uint16_t *x;
+    int64_t ldx;
+    LoraAdapters ad;
+    float *dX;
+    int64_t lddx;
+    float *dA;
+    int64_t ldda, stride_da;
+    float *dB;
+    int64_t lddb, stride_db;
+    bool accumulate;
+    int64_t M, K, V;
+};
+
+int64_t lora_logits_workspace_bytes(int64_t M, int64_t V, int64_t r, bool bf16);
+int64_t lora_bwd_workspace_bytes(int64_t M, int64_t V, int64_t r, int64_t n);
+// p as for launch_gemm_logits (R = V, C = M, P = K), with D the final logits.
+hipError_t launch_logits_lora(const GemmProblem &p, bool bf16, const LoraAdapters &ad, void *workspace,
+                              hipStream_t s);
+hipError_t launch_lora_bwd(const LoraBwd &p, void *workspace, hipStream_t s);
+
+int64_t beam_segments(int64_t V);
+int64_t beam_workspace_bytes(int64_t n_rows, int64_t V, int64_t n_out);
+hipError_t launch_beam_select(const void *logits, int64_t ld, bool bf16, int64_t B, int64_t W,
+                              int64_t V, const float *scores, const uint8_t *finished, int32_t eos,
+                              int64_t n_out, float *out_scores, int32_t *out_parent,
+                              int32_t *out_token, uint8_t *out_finished, void *workspace,
+                              hipStream_t s);
+// Strides in bytes: outer, row (beam), head.
+hipError_t launch_beam_reorder(const void *src, void *dst, const int64_t (&src_strides)[3],
+                               const int64_t (&dst_strides)[3], const int32_t *parent,
+                               const int32_t *lengths, int64_t n_outer, int64_t B, int64_t W_in,
+                               int64_t W_out, int64_t H, int64_t T, int64_t pos_bytes, hipStream_t s);
+
 // exp(z - m) as one hardware base-2 exponential; the same form everywhere the
 // cross-entropy statistics are computed (CE kernels, logits GEMM epilogue).
 constexpr float kLog2e = 1.4426950408889634f;

@@ -1,0 +1,929 @@
+// lora.hip -- low-rank adapters of many requests beside the shared vocabulary
+// weight, on gfx950: the adapters' part of the logits and their gradients.
+//
+// Token m uses adapter a = adapter[m] (a < 0: none), A_a [r][K], B_a [V][r]:
+//   z[m][v]    = sum_k x[m][k] W[v][k] + sum_j u[m][j] B_a[v][j],
+//   u[m][j]    = s_a sum_k x[m][k] A_a[j][k]
+//   t[m][j]    = s_a sum_v g[m][v] B_a[v][j]          (g = dlogits)
+//   dX[m][k]   = sum_j t[m][j] A_a[j][k]
+//   dA_a[j][k] = sum over a's tokens of t[m][j] x[m][k]
+//   dB_a[v][j] = sum over a's tokens of g[m][v] u[m][j]
+//
+// Every product runs on the BF16 matrix cores with FP32 accumulation.  u and t
+// are FP32 sums that enter a second product; rounding them to BF16 would leave
+// the FP32 logits and gradients with 2^-9 relative errors in the adapter's
+// part, so each is cut into three BF16 pieces of 8 significant bits (hi + mid
+// + lo = the FP32 value exactly, truncating) and the product runs over the
+// three pieces: 3 r extra contraction steps against K or V of the main
+// products.
+//
+// A batch mixes requests.  A tile's tokens may use different adapters, and one
+// request's adapter must never touch another's result (0 x NaN included), so
+// an adapter's product is formed for the whole tile into registers of its own
+// and added only in the columns (tokens) that use it.
+#include "common.h"
+
+#include <algorithm>
+
+namespace lmh {
+
+namespace {
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+
+constexpr int64_t kMaxItems = int64_t{1} << 31;  // work-items per launch
+
+// 8 BF16 words at p, of which the first n (any value) are valid, the rest 0.
+__device__ __forceinline__ uint4 load8(const uint16_t *p, int64_t n)
+{
+    if (n >= 8)
+        return *reinterpret_cast<const uint4 *>(p);
+    uint32_t w[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        if (e < n)
+            w[e >> 1] |= static_cast<uint32_t>(p[e]) << ((e & 1) * 16);
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+__device__ __forceinline__ bf16x8 as_frag(const uint4 &v)
+{
+    return __builtin_bit_cast(bf16x8, v);
+}
+
+// The first n of 8 BF16 words, the rest 0.
+__device__ __forceinline__ uint4 keep8(uint4 v, int64_t n)
+{
+    const uint32_t in[4] = {v.x, v.y, v.z, v.w};
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        w[i] = n >= 2 * i + 2 ? in[i] : n == 2 * i + 1 ? (in[i] & 0xffffu) : 0u;
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+__device__ __forceinline__ f32x4 mfma16(bf16x8 a, bf16x8 b, f32x4 c)
+{
+    // Lane l: a row l % 16, b column l % 16, both at contraction 8 (l / 16) ..;
+    // c rows 4 (l / 16) .. + 3, column l % 16.
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+}
+
+// FP32 -> three BF16 pieces whose sum is the value: each the upper 16 bits of
+// what is left.  A non-finite value keeps it all in the first.
+__device__ __forceinline__ void split3(float v, uint32_t (&p)[3])
+{
+    const uint32_t hi = __float_as_uint(v) & 0xffff0000u;
+    const bool finite = (hi & 0x7f800000u) != 0x7f800000u;
+    const float r1 = v - __uint_as_float(hi);
+    const uint32_t mid = __float_as_uint(r1) & 0xffff0000u;
+    const float r2 = r1 - __uint_as_float(mid);
+    p[0] = (v != v) ? 0x7fc0u : hi >> 16;
+    p[1] = finite ? mid >> 16 : 0u;
+    p[2] = finite ? __float_as_uint(r2) >> 16 : 0u;
+}
+
+// Adapters a tile's 16 tokens use: lane l holds token l % 16's id; bit t of the
+// mask is token t.
+__device__ __forceinline__ int32_t first_id(int32_t id, uint32_t todo)
+{
+    return __builtin_amdgcn_readlane(id, __builtin_ctz(todo));
+}
+__device__ __forceinline__ uint32_t tokens_of(int32_t id, int32_t a)
+{
+    return static_cast<uint32_t>(__ballot(id == a)) & 0xffffu;
+}
+
+// Row length of the pieces of one token's u or t: [hi | mid | lo] of RP words
+// each, RP the rank rounded up to 16, 32, 64 or 128; for RP = 16 one more
+// group of 16 zeros makes whole 32-deep contraction steps.
+__host__ __device__ constexpr int piece_row(int RP)
+{
+    return RP == 16 ? 64 : 3 * RP;
+}
+
+// ---------------------------------------------------------------------------
+// u = s_a A_a x for 16 tokens, one of the adapters they use (blockIdx.y: the
+// slot-th distinct one, in token order) and 16 of its ranks (blockIdx.z).  The
+// 16 waves split K and are summed in order through LDS.  Latency-bound: a few
+// hundred KiB per workgroup, so all of K runs in one workgroup (a second
+// launch to join parts would cost more) and slots spread over the chip.
+// Written as pieces: rows [token][piece_row] (u3), or ranks by grouped
+// position [3][RP][Mp] (uT, for the gradients).
+constexpr int kShrinkThreads = 1024;
+
+__global__ __launch_bounds__(kShrinkThreads) void lora_shrink_kernel(
+    const uint16_t *__restrict__ x, int64_t ldx, int64_t M, int64_t K, LoraAdapters ad, int64_t blk0,
+    int RP, uint16_t *__restrict__ u3, uint16_t *__restrict__ uT, int64_t Mp,
+    const int32_t *__restrict__ ppos)
+{
+    constexpr int NW = kShrinkThreads / 64;
+    __shared__ f32x4 red[NW][64];
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int t16 = lane & 15, q = lane >> 4;
+    const int64_t tok = (blk0 + blockIdx.x) * 16 + t16;
+    const int32_t id = tok < M ? ad.adapter[tok] : -1;
+    const bool valid = id >= 0 && id < ad.n;
+    uint32_t todo = static_cast<uint32_t>(__ballot(valid)) & 0xffffu;
+    for (unsigned s = 0; s < blockIdx.y && todo; ++s)
+        todo &= ~tokens_of(id, first_id(id, todo));
+    if (!todo)
+        return;  // uniform over the workgroup: every wave holds the same tokens
+    const int32_t a = first_id(id, todo);
+
+    const int j0 = blockIdx.z * 16;
+    const uint16_t *pa = ad.A + a * ad.stride_a + static_cast<int64_t>(min(j0 + t16, ad.r - 1)) * ad.lda;
+    const uint16_t *px = x + min(tok, M - 1) * ldx;
+    const int64_t per_wave = (K + 32 * NW - 1) / (32 * NW) * 32;
+    int64_t k = wave * per_wave;
+    const int64_t kend = min(K, k + per_wave);
+    f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (; k + 256 <= kend; k += 256) {
+        uint4 va[8], vx[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            va[i] = *reinterpret_cast<const uint4 *>(pa + k + 32 * i + 8 * q);
+            vx[i] = *reinterpret_cast<const uint4 *>(px + k + 32 * i + 8 * q);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            acc = mfma16(as_frag(va[i]), as_frag(vx[i]), acc);
+    }
+    for (; k < kend; k += 32) {
+        const int64_t kk = k + 8 * q;
+        acc = mfma16(as_frag(load8(pa + kk, K - kk)), as_frag(load8(px + kk, K - kk)), acc);
+    }
+    red[wave][lane] = acc;
+    __syncthreads();
+    if (tid >= 256)
+        return;
+    // Thread: token tid % 16 (= t16), rank j0 + tid / 16.
+    const int jj = tid >> 4, j = j0 + jj;
+    float sum = 0.0f;
+#pragma unroll
+    for (int w = 0; w < NW; ++w)
+        sum += red[w][(jj >> 2) * 16 + t16][jj & 3];
+    if (id != a || tok >= M)
+        return;
+    sum = j < ad.r ? sum * (ad.scale ? ad.scale[a] : 1.0f) : 0.0f;
+    uint32_t p[3];
+    split3(sum, p);
+    if (u3) {
+        uint16_t *row = u3 + tok * piece_row(RP) + j;
+        row[0] = static_cast<uint16_t>(p[0]);
+        row[RP] = static_cast<uint16_t>(p[1]);
+        row[2 * RP] = static_cast<uint16_t>(p[2]);
+        if (RP == 16)
+            row[48] = 0;
+    }
+    if (uT) {
+        uint16_t *col = uT + j * Mp + ppos[tok];
+        col[0] = static_cast<uint16_t>(p[0]);
+        col[RP * Mp] = static_cast<uint16_t>(p[1]);
+        col[2 * RP * Mp] = static_cast<uint16_t>(p[2]);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// logits += u B^T for 16 tokens x 256 vocabulary rows: reads the FP32 product
+// z, adds each token's adapter, stores FP32 (in place) or BF16 (rounded once).
+// Wave w holds rows 64 w .. + 63 as four 16 x 16 results; B rows go straight
+// from memory into matrix operands (the fragment is 16 contiguous bytes of a
+// row).  Bound by B of the adapters in use and by z, read and written once.
+template <int RP, bool BF16>
+__global__ __launch_bounds__(256) void lora_expand_kernel(const float *z, int64_t ldz, void *out,
+                                                          int64_t ldo, int64_t M, int64_t V,
+                                                          LoraAdapters ad,
+                                                          const uint16_t *__restrict__ u3,
+                                                          int64_t tok_blocks, int64_t blk0)
+{
+    constexpr int U = RP < 32 ? 1 : RP / 32;     // distinct 32-deep steps over a rank
+    constexpr int S = piece_row(RP) / 32;        // steps over the three pieces
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int t16 = lane & 15, q = lane >> 4;
+    const int64_t id_blk = blk0 + blockIdx.x;
+    const int64_t vt = id_blk / tok_blocks;
+    const int64_t tok = (id_blk - vt * tok_blocks) * 16 + t16;
+    const int32_t id = tok < M ? ad.adapter[tok] : -1;
+    const bool valid = id >= 0 && id < ad.n;
+    uint32_t todo = static_cast<uint32_t>(__ballot(valid)) & 0xffffu;
+    const bool bad = id >= ad.n;
+    if (!BF16 && !todo && !__ballot(bad))
+        return;
+    const int64_t v0 = vt * 256 + wave * 64;
+    if (v0 >= V)
+        return;
+    bf16x8 fu[S];
+    const uint16_t *pu = u3 + min(tok, M - 1) * piece_row(RP) + 8 * q;
+    if (todo) {
+#pragma unroll
+        for (int s = 0; s < S; ++s)
+            fu[s] = as_frag(*reinterpret_cast<const uint4 *>(pu + 32 * s));
+    }
+    f32x4 acc[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int64_t v = v0 + 16 * i + 4 * q;
+        acc[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        if (tok < M) {
+            const float *p = z + tok * ldz + v;
+            if (v + 4 <= V)
+                acc[i] = *reinterpret_cast<const f32x4 *>(p);
+            else
+                for (int e = 0; e < 4 && v + e < V; ++e)
+                    acc[i][e] = p[e];
+        }
+    }
+    while (todo) {
+        const int32_t a = first_id(id, todo);
+        todo &= ~tokens_of(id, a);
+        const uint16_t *pb = ad.B + a * ad.stride_b;
+        f32x4 tmp[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            tmp[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int uu = 0; uu < U; ++uu) {
+            const int j = RP == 16 ? 8 * (q & 1) : 32 * uu + 8 * q;
+            bf16x8 fb[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int64_t v = min(v0 + 16 * i + t16, V - 1);
+                fb[i] = as_frag(load8(pb + v * ad.ldb + j, ad.r - j));
+            }
+#pragma unroll
+            for (int s = uu; s < S; s += U)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    tmp[i] = mfma16(fb[i], fu[s], tmp[i]);
+        }
+        if (id == a) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                acc[i] += tmp[i];
+        }
+    }
+    if (tok >= M)
+        return;
+    if (bad) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            acc[i] = f32x4{NAN, NAN, NAN, NAN};
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int64_t v = v0 + 16 * i + 4 * q;
+        if constexpr (BF16) {
+            uint16_t *p = static_cast<uint16_t *>(out) + tok * ldo + v;
+            uint32_t h[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                h[e] = f32_to_bf16_bits(acc[i][e]);
+            if (v + 4 <= V)
+                store8(p, make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16)), false);
+            else
+                for (int e = 0; e < 4 && v + e < V; ++e)
+                    p[e] = static_cast<uint16_t>(h[e]);
+        } else {
+            float *p = static_cast<float *>(out) + tok * ldo + v;
+            if (v + 4 <= V)
+                *reinterpret_cast<f32x4 *>(p) = acc[i];
+            else
+                for (int e = 0; e < 4 && v + e < V; ++e)
+                    p[e] = acc[i][e];
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Gradients.  The tokens are grouped by adapter first (stable): group g < n
+// holds adapter g's tokens, group n the tokens on none, group n + 1 those
+// whose id is not an adapter.  offset[g] is the group's first place in
+// order[]; a second numbering starts every group at a multiple of 64
+// (group_base), so that a chunk of 64 tokens of one group is 128 contiguous,
+// aligned bytes of a rank's row in uT and tT.
+__host__ __device__ __forceinline__ int64_t group_base(int64_t offset, int64_t g)
+{
+    // Room enough: floor64(o + c) - floor64(o) + 64 >= ceil64(c).
+    return offset / 64 * 64 + 64 * g;
+}
+
+// One workgroup per group: counts the ids below and in its group, then writes
+// its tokens in order.  Reads the ids n + 2 times in all (they stay in L2);
+// no workgroup waits for another.
+__global__ __launch_bounds__(256) void lora_group_kernel(const int32_t *__restrict__ adapter, int64_t M,
+                                                         int64_t n, int32_t *__restrict__ offset,
+                                                         int32_t *__restrict__ order,
+                                                         int32_t *__restrict__ ppos)
+{
+    __shared__ int32_t part[4];
+    __shared__ int32_t total;
+    const int64_t g = blockIdx.x;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    auto cls = [&](int32_t id) { return id < 0 ? n : id >= n ? n + 1 : static_cast<int64_t>(id); };
+    int32_t less = 0;
+    for (int64_t m = tid; m < M; m += 256)
+        less += cls(adapter[m]) < g;
+#pragma unroll
+    for (int off = 32; off >= 1; off >>= 1)
+        less += __shfl_xor(less, off, 64);
+    if (lane == 0)
+        part[wave] = less;
+    __syncthreads();
+    const int32_t first = part[0] + part[1] + part[2] + part[3];
+    if (tid == 0) {
+        offset[g] = first;
+        if (g == n + 1)
+            offset[n + 2] = static_cast<int32_t>(M);
+        total = 0;
+    }
+    const int32_t base = static_cast<int32_t>(group_base(first, g));
+    for (int64_t m0 = 0; m0 < M; m0 += 256) {
+        const int64_t m = m0 + tid;
+        const bool mine = m < M && cls(adapter[m]) == g;
+        const uint64_t mask = __ballot(mine);
+        __syncthreads();  // part[] and total of the round before are read
+        if (lane == 0)
+            part[wave] = __popcll(mask);
+        __syncthreads();
+        int32_t at = total + __popcll(mask & ((1ull << lane) - 1ull));
+        for (int w = 0; w < wave; ++w)
+            at += part[w];
+        if (mine) {
+            order[first + at] = static_cast<int32_t>(m);
+            if (g < n)
+                ppos[m] = base + at;
+        }
+        __syncthreads();
+        if (tid == 0)
+            total += part[0] + part[1] + part[2] + part[3];
+    }
+}
+
+// A staged tile: 64 rows (tokens, or ranks) of 256 BF16 words, 16-byte chunk c
+// of row p at chunk c ^ tile_key(p).  The key separates the eight rows that a
+// quarter of a row-wise fragment read touches, and the two groups of four rows
+// that half of a transposing read touches.
+__device__ __forceinline__ int tile_key(int p)
+{
+    return ((p & 3) << 2) ^ ((p >> 2) & 1) ^ (((p >> 3) & 1) << 1);
+}
+
+typedef short v4i16 __attribute__((ext_vector_type(4)));
+typedef short v8i16 __attribute__((ext_vector_type(8)));
+
+// Transposed fragment: lane l receives column n0 + l % 16 at rows p .. p + 7,
+// p = the lane group's first row (a multiple of 8).  Within a group of 16
+// lanes, lane 4 b + a addresses row b, columns 4 a .. 4 a + 3, and the
+// transposing read hands lane i column i of the four rows.
+__device__ __forceinline__ bf16x8 tile_column_frag(const uint16_t *tile, int p, int n0, int lane)
+{
+    typedef __attribute__((address_space(3))) v4i16 lds_v4;
+    const int b = (lane >> 2) & 3, col = n0 + 4 * (lane & 3);
+    auto at = [&](int row) {
+        return tile + row * 256 + (((col >> 3) ^ tile_key(row)) << 3) + (col & 7);
+    };
+    const v4i16 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4 *)(at(p + b)));
+    const v4i16 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4 *)(at(p + 4 + b)));
+    const v8i16 c = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+    return __builtin_bit_cast(bf16x8, c);
+}
+
+// Row fragment: 8 columns from n (a multiple of 8) of row p.
+__device__ __forceinline__ bf16x8 tile_row_frag(const uint16_t *tile, int p, int n)
+{
+    return *reinterpret_cast<const bf16x8 *>(tile + p * 256 + (((n >> 3) ^ tile_key(p)) << 3));
+}
+
+// The registers of one tile on its way from memory: 64 tokens x 256 columns by
+// 256 threads, thread = (row 8 i + tid / 32, chunk tid % 32).
+struct TokenTile {
+    uint4 v[8];
+    __device__ __forceinline__ void load(const uint16_t *base, int64_t ld, const int32_t *order,
+                                         int64_t first, int64_t count, int64_t col0, int64_t ncols,
+                                         int tid)
+    {
+        const int64_t col = col0 + 8 * (tid & 31);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int64_t row = 8 * i + (tid >> 5);
+            v[i] = make_uint4(0u, 0u, 0u, 0u);
+            if (row < count && col < ncols)
+                v[i] = load8(base + static_cast<int64_t>(order[first + row]) * ld + col, ncols - col);
+        }
+    }
+    __device__ __forceinline__ void store(uint16_t *tile, int tid) const
+    {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int row = 8 * i + (tid >> 5);
+            *reinterpret_cast<uint4 *>(tile + row * 256 + (((tid & 31) ^ tile_key(row)) << 3)) = v[i];
+        }
+    }
+};
+
+__device__ __forceinline__ void store_f32x4(float *p, f32x4 v, int64_t n, bool add)
+{
+    if (n >= 4) {
+        if (add)
+            v += *reinterpret_cast<const f32x4 *>(p);
+        *reinterpret_cast<f32x4 *>(p) = v;
+    } else {
+        for (int e = 0; e < n; ++e)
+            p[e] = add ? p[e] + v[e] : v[e];
+    }
+}
+
+// One workgroup per (256 vocabulary columns, adapter): walks the adapter's
+// tokens 64 at a time and takes both products from one read of g: its part of
+// t (over these 256 columns; joined by lora_t_kernel) and dB (accumulated over
+// the tokens in registers).  B^T sits in LDS.  Bound by the one read of g;
+// the parts of t cost 8 RP bytes per token and block against 512 of g.
+template <int RP>
+__global__ __launch_bounds__(256) void lora_bwd_v_kernel(
+    const uint16_t *__restrict__ g, int64_t ldg, int64_t M, int64_t V, LoraAdapters ad,
+    const int32_t *__restrict__ offset, const int32_t *__restrict__ order,
+    const uint16_t *__restrict__ uT, int64_t Mp, float *__restrict__ tpart, float *__restrict__ dB,
+    int64_t lddb, int64_t stride_db, int accumulate, int64_t nvb)
+{
+    constexpr int JF = RP / 16, LDB = 256 + 8;
+    __shared__ __attribute__((aligned(16))) uint16_t sG[64 * 256];
+    __shared__ __attribute__((aligned(16))) uint16_t sBT[RP * LDB];
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int t16 = lane & 15, q = lane >> 4;
+    const int64_t a = blockIdx.x / nvb, vb = blockIdx.x - a * nvb;
+    const int64_t v0 = vb * 256;
+    const int64_t o0 = offset[a], cnt = offset[a + 1] - o0;
+    const int64_t pp0 = group_base(o0, a);
+    if (cnt == 0 && (accumulate || !dB))
+        return;
+
+    TokenTile nxt;
+    if (cnt > 0)
+        nxt.load(g, ldg, order, o0, cnt, v0, V, tid);
+    if (tpart && cnt > 0) {
+        const int64_t v = v0 + tid;
+        const uint16_t *pb = ad.B + a * ad.stride_b + v * ad.ldb;
+#pragma unroll
+        for (int j = 0; j < RP; j += 8) {
+            const uint4 w = (v < V && j < ad.r) ? load8(pb + j, ad.r - j) : make_uint4(0u, 0u, 0u, 0u);
+            const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                sBT[(j + e) * LDB + tid] = static_cast<uint16_t>(ws[e >> 1] >> (16 * (e & 1)));
+        }
+    }
+    f32x4 accB[JF][4];
+#pragma unroll
+    for (int jf = 0; jf < JF; ++jf)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            accB[jf][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+
+    for (int64_t c = 0; c < cnt; c += 64) {
+        __syncthreads();  // the tile of the chunk before is read
+        nxt.store(sG, tid);
+        __syncthreads();
+        if (c + 64 < cnt)
+            nxt.load(g, ldg, order, o0 + c + 64, cnt - c - 64, v0, V, tid);
+        if (tpart) {
+            // Ranks (rows) x this wave's 16 tokens, over the 256 columns.
+            f32x4 acc[JF];
+#pragma unroll
+            for (int jf = 0; jf < JF; ++jf)
+                acc[jf] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int s = 0; s < 8; ++s) {
+                const bf16x8 ft = tile_row_frag(sG, 16 * wave + t16, 32 * s + 8 * q);
+#pragma unroll
+                for (int jf = 0; jf < JF; ++jf)
+                    acc[jf] = mfma16(*reinterpret_cast<const bf16x8 *>(
+                                         sBT + (16 * jf + t16) * LDB + 32 * s + 8 * q),
+                                     ft, acc[jf]);
+            }
+            const int64_t at = c + 16 * wave + t16;
+            if (at < cnt) {
+                float *p = tpart + (vb * M + order[o0 + at]) * RP + 4 * q;
+#pragma unroll
+                for (int jf = 0; jf < JF; ++jf)
+                    *reinterpret_cast<f32x4 *>(p + 16 * jf) = acc[jf];
+            }
+        }
+        if (dB) {
+            // Ranks (rows) x this wave's 64 columns, over the 64 tokens.
+#pragma unroll
+            for (int ks = 0; ks < 2; ++ks) {
+                bf16x8 fg[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    fg[i] = tile_column_frag(sG, 32 * ks + 8 * q, 64 * wave + 16 * i, lane);
+                const int64_t at = c + 32 * ks + 8 * q;
+#pragma unroll
+                for (int jf = 0; jf < JF; ++jf)
+#pragma unroll
+                    for (int p = 0; p < 3; ++p) {
+                        uint4 w = *reinterpret_cast<const uint4 *>(
+                            uT + (p * RP + 16 * jf + t16) * Mp + pp0 + at);
+                        if (c + 64 > cnt)
+                            w = keep8(w, cnt - at);
+                        const bf16x8 fu = as_frag(w);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            accB[jf][i] = mfma16(fu, fg[i], accB[jf][i]);
+                    }
+            }
+        }
+    }
+    if (!dB)
+        return;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int64_t v = v0 + 64 * wave + 16 * i + t16;
+        if (v >= V)
+            continue;
+        float *p = dB + a * stride_db + v * lddb;
+#pragma unroll
+        for (int jf = 0; jf < JF; ++jf) {
+            const int j = 16 * jf + 4 * q;
+            store_f32x4(p + j, accB[jf][i], ad.r - j, accumulate != 0);
+        }
+    }
+}
+
+// t = s_a x the sum of its parts, in block order per lane and then by lane:
+// 16 lanes share one group of four ranks of one token.  Written as pieces in
+// rows (t3) and by rank and grouped position (tT).
+__global__ __launch_bounds__(256) void lora_t_kernel(const float *__restrict__ tpart, int64_t nvb,
+                                                     int64_t M, int RP, LoraAdapters ad,
+                                                     const int32_t *__restrict__ ppos,
+                                                     uint16_t *__restrict__ t3,
+                                                     uint16_t *__restrict__ tT, int64_t Mp)
+{
+    __shared__ f32x4 red[16][16];
+    const int tid = threadIdx.x, col = tid & 15, part = tid >> 4;
+    const int64_t n4 = M * RP / 4;
+    const int64_t i4 = static_cast<int64_t>(blockIdx.x) * 16 + col;
+    f32x4 sum = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (i4 < n4) {
+        const f32x4 *p = reinterpret_cast<const f32x4 *>(tpart) + i4;
+#pragma unroll 8
+        for (int64_t b = part; b < nvb; b += 16)
+            sum += p[b * n4];
+    }
+    red[part][col] = sum;
+    __syncthreads();
+    if (part != 0 || i4 >= n4)
+        return;
+#pragma unroll
+    for (int w = 1; w < 16; ++w)
+        sum += red[w][col];
+    const int64_t m = i4 * 4 / RP;
+    const int j = static_cast<int>(i4 * 4 - m * RP);
+    const int32_t a = ad.adapter[m];
+    if (a < 0 || a >= ad.n)
+        return;  // its parts were never written, and t is not read
+    const float s = ad.scale ? ad.scale[a] : 1.0f;
+    uint16_t *row = t3 + m * piece_row(RP) + j;
+    uint16_t *colp = tT + j * Mp + ppos[m];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        uint32_t p[3];
+        split3(j + e < ad.r ? sum[e] * s : 0.0f, p);
+#pragma unroll
+        for (int k = 0; k < 3; ++k) {
+            row[k * RP + e] = static_cast<uint16_t>(p[k]);
+            colp[(k * RP + e) * Mp] = static_cast<uint16_t>(p[k]);
+        }
+        if (RP == 16)
+            row[48 + e] = 0;
+    }
+}
+
+// One workgroup per (256 columns of K, group): walks the group's tokens 64 at
+// a time; dX = t A from A_a's block in LDS, dA accumulated over the tokens from
+// one read of x.  The group of tokens on no adapter gets zeros in dX, that of
+// ids that are no adapter NaN.  Bound by writing dX.
+template <int RP>
+__global__ __launch_bounds__(256) void lora_bwd_k_kernel(
+    const uint16_t *__restrict__ x, int64_t ldx, int64_t K, LoraAdapters ad,
+    const int32_t *__restrict__ offset, const int32_t *__restrict__ order,
+    const uint16_t *__restrict__ t3, const uint16_t *__restrict__ tT, int64_t Mp,
+    float *__restrict__ dX, int64_t lddx, float *__restrict__ dA, int64_t ldda, int64_t stride_da,
+    int accumulate, int64_t nkb)
+{
+    constexpr int JF = RP / 16;
+    constexpr int U = RP < 32 ? 1 : RP / 32, S = piece_row(RP) / 32;
+    __shared__ __attribute__((aligned(16))) uint16_t sX[64 * 256];
+    __shared__ __attribute__((aligned(16))) uint16_t sA[RP * 256];
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int t16 = lane & 15, q = lane >> 4;
+    const int64_t a = blockIdx.x / nkb, kb = blockIdx.x - a * nkb;
+    const int64_t k0 = kb * 256;
+    const int64_t o0 = offset[a], cnt = offset[a + 1] - o0;
+    if (a >= ad.n) {
+        if (!dX || (a == ad.n && accumulate))
+            return;
+        const float fill = a == ad.n ? 0.0f : NAN;
+        const int64_t k = k0 + 4 * lane;
+        for (int64_t i = wave; i < cnt; i += 4)
+            store_f32x4(dX + static_cast<int64_t>(order[o0 + i]) * lddx + k,
+                        f32x4{fill, fill, fill, fill}, K - k, false);
+        return;
+    }
+    const int64_t pp0 = group_base(o0, a);
+    if (cnt == 0 && (accumulate || !dA))
+        return;
+
+    TokenTile nxt;
+    if (dA && cnt > 0)
+        nxt.load(x, ldx, order, o0, cnt, k0, K, tid);
+    if (dX && cnt > 0) {
+        const int64_t col = k0 + 8 * (tid & 31);
+        for (int j = tid >> 5; j < RP; j += 8) {
+            const uint4 w = (j < ad.r && col < K)
+                                ? load8(ad.A + a * ad.stride_a + j * ad.lda + col, K - col)
+                                : make_uint4(0u, 0u, 0u, 0u);
+            *reinterpret_cast<uint4 *>(sA + j * 256 + (((tid & 31) ^ tile_key(j)) << 3)) = w;
+        }
+    }
+    f32x4 accA[4][JF];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int jf = 0; jf < JF; ++jf)
+            accA[i][jf] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+
+    for (int64_t c = 0; c < cnt; c += 64) {
+        __syncthreads();
+        if (dA)
+            nxt.store(sX, tid);
+        __syncthreads();
+        if (dA && c + 64 < cnt)
+            nxt.load(x, ldx, order, o0 + c + 64, cnt - c - 64, k0, K, tid);
+        if (dX) {
+            // This wave's 64 columns (rows) x 16 tokens at a time.
+#pragma unroll
+            for (int tf = 0; tf < 4; ++tf) {
+                const int64_t at = c + 16 * tf + t16;
+                if (c + 16 * tf >= cnt)
+                    break;
+                const int64_t m = order[o0 + min(at, cnt - 1)];
+                const uint16_t *pt = t3 + m * piece_row(RP) + 8 * q;
+                f32x4 acc[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    acc[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                for (int uu = 0; uu < U; ++uu) {
+                    const int p = RP == 16 ? 8 * (q & 1) : 32 * uu + 8 * q;
+                    bf16x8 fa[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        fa[i] = tile_column_frag(sA, p, 64 * wave + 16 * i, lane);
+#pragma unroll
+                    for (int s = uu; s < S; s += U) {
+                        const bf16x8 ft = as_frag(*reinterpret_cast<const uint4 *>(pt + 32 * s));
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            acc[i] = mfma16(fa[i], ft, acc[i]);
+                    }
+                }
+                if (at < cnt) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int64_t k = k0 + 64 * wave + 16 * i + 4 * q;
+                        store_f32x4(dX + m * lddx + k, acc[i], K - k, accumulate != 0);
+                    }
+                }
+            }
+        }
+        if (dA) {
+#pragma unroll
+            for (int ks = 0; ks < 2; ++ks) {
+                bf16x8 fx[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    fx[i] = tile_column_frag(sX, 32 * ks + 8 * q, 64 * wave + 16 * i, lane);
+                const int64_t at = c + 32 * ks + 8 * q;
+#pragma unroll
+                for (int jf = 0; jf < JF; ++jf)
+#pragma unroll
+                    for (int p = 0; p < 3; ++p) {
+                        uint4 w = *reinterpret_cast<const uint4 *>(
+                            tT + (p * RP + 16 * jf + t16) * Mp + pp0 + at);
+                        if (c + 64 > cnt)
+                            w = keep8(w, cnt - at);
+                        const bf16x8 ft = as_frag(w);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            accA[i][jf] = mfma16(fx[i], ft, accA[i][jf]);
+                    }
+            }
+        }
+    }
+    if (!dA)
+        return;
+#pragma unroll
+    for (int jf = 0; jf < JF; ++jf) {
+        const int j = 16 * jf + t16;
+        if (j >= ad.r)
+            continue;
+        float *p = dA + a * stride_da + j * ldda;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int64_t k = k0 + 64 * wave + 16 * i + 4 * q;
+            store_f32x4(p + k, accA[i][jf], K - k, accumulate != 0);
+        }
+    }
+}
+
+int rank_bucket(int64_t r)
+{
+    return r <= 16 ? 16 : r <= 32 ? 32 : r <= 64 ? 64 : 128;
+}
+
+int64_t round256(int64_t b)
+{
+    return (b + 255) / 256 * 256;
+}
+
+// Grouped positions: every group starts at a multiple of 64 (group_base).
+int64_t grouped_length(int64_t M, int64_t n)
+{
+    return M / 64 * 64 + 64 * (n + 1);
+}
+
+hipError_t launch_shrink(const uint16_t *x, int64_t ldx, int64_t M, int64_t K, const LoraAdapters &ad,
+                         uint16_t *u3, uint16_t *uT, int64_t Mp, const int32_t *ppos, hipStream_t s)
+{
+    const int RP = rank_bucket(ad.r);
+    const int64_t blocks = (M + 15) / 16;
+    const int64_t slots = std::min<int64_t>(std::min<int64_t>(ad.n, 16), M), zr = RP / 16;
+    const int64_t most = kMaxItems / kShrinkThreads / (slots * zr);
+    for (int64_t b0 = 0; b0 < blocks; b0 += most) {
+        const dim3 grid(static_cast<unsigned>(std::min(most, blocks - b0)), static_cast<unsigned>(slots),
+                        static_cast<unsigned>(zr));
+        hipLaunchKernelGGL(lora_shrink_kernel, grid, dim3(kShrinkThreads), 0, s, x, ldx, M, K, ad, b0, RP,
+                           u3, uT, Mp, ppos);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess)
+            return e;
+    }
+    return hipSuccess;
+}
+
+template <int RP>
+hipError_t launch_expand(const float *z, int64_t ldz, void *out, int64_t ldo, bool bf16, int64_t M,
+                         int64_t V, const LoraAdapters &ad, const uint16_t *u3, hipStream_t s)
+{
+    const int64_t tb = (M + 15) / 16, blocks = (V + 255) / 256 * tb, most = kMaxItems / 256;
+    for (int64_t b0 = 0; b0 < blocks; b0 += most) {
+        const dim3 grid(static_cast<unsigned>(std::min(most, blocks - b0)));
+        if (bf16)
+            hipLaunchKernelGGL((lora_expand_kernel<RP, true>), grid, dim3(256), 0, s, z, ldz, out, ldo, M, V,
+                               ad, u3, tb, b0);
+        else
+            hipLaunchKernelGGL((lora_expand_kernel<RP, false>), grid, dim3(256), 0, s, z, ldz, out, ldo, M,
+                               V, ad, u3, tb, b0);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess)
+            return e;
+    }
+    return hipSuccess;
+}
+
+// The gradients' workspace, in order.
+struct BwdLayout {
+    int64_t offset, order, ppos, uT, t3, tT, tpart, end;
+};
+
+BwdLayout bwd_layout(int64_t M, int64_t V, int64_t r, int64_t n)
+{
+    const int64_t RP = rank_bucket(r), Mp = grouped_length(M, n), nvb = (V + 255) / 256;
+    BwdLayout l;
+    l.offset = 0;
+    l.order = l.offset + round256(4 * (n + 3));
+    l.ppos = l.order + round256(4 * M);
+    l.uT = l.ppos + round256(4 * M);
+    l.t3 = l.uT + round256(2 * 3 * RP * Mp);
+    l.tT = l.t3 + round256(2 * piece_row(static_cast<int>(RP)) * M);
+    l.tpart = l.tT + round256(2 * 3 * RP * Mp);
+    l.end = l.tpart + round256(4 * nvb * M * RP);
+    return l;
+}
+
+template <int RP>
+hipError_t launch_bwd_v(const LoraBwd &p, const BwdLayout &l, char *ws, hipStream_t s)
+{
+    const int64_t nvb = (p.V + 255) / 256;
+    hipLaunchKernelGGL((lora_bwd_v_kernel<RP>), dim3(static_cast<unsigned>(nvb * p.ad.n)), dim3(256), 0, s,
+                       p.g, p.ldg, p.M, p.V, p.ad, reinterpret_cast<const int32_t *>(ws + l.offset),
+                       reinterpret_cast<const int32_t *>(ws + l.order),
+                       reinterpret_cast<const uint16_t *>(ws + l.uT), grouped_length(p.M, p.ad.n),
+                       (p.dX || p.dA) ? reinterpret_cast<float *>(ws + l.tpart) : nullptr, p.dB, p.lddb,
+                       p.stride_db, p.accumulate ? 1 : 0, nvb);
+    return hipGetLastError();
+}
+
+template <int RP>
+hipError_t launch_bwd_k(const LoraBwd &p, const BwdLayout &l, char *ws, hipStream_t s)
+{
+    const int64_t nkb = (p.K + 255) / 256;
+    hipLaunchKernelGGL((lora_bwd_k_kernel<RP>), dim3(static_cast<unsigned>(nkb * (p.ad.n + 2))), dim3(256),
+                       0, s, p.x, p.ldx, p.K, p.ad, reinterpret_cast<const int32_t *>(ws + l.offset),
+                       reinterpret_cast<const int32_t *>(ws + l.order),
+                       reinterpret_cast<const uint16_t *>(ws + l.t3),
+                       reinterpret_cast<const uint16_t *>(ws + l.tT), grouped_length(p.M, p.ad.n), p.dX,
+                       p.lddx, p.dA, p.ldda, p.stride_da, p.accumulate ? 1 : 0, nkb);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+int64_t lora_logits_workspace_bytes(int64_t M, int64_t V, int64_t r, bool bf16)
+{
+    const int64_t u = round256(2 * piece_row(rank_bucket(r)) * M);
+    return u + (bf16 ? round256(4 * M * ((V + 3) / 4 * 4)) : 0);
+}
+
+int64_t lora_bwd_workspace_bytes(int64_t M, int64_t V, int64_t r, int64_t n)
+{
+    return bwd_layout(M, V, r, n).end;
+}
+
+hipError_t launch_logits_lora(const GemmProblem &p, bool bf16, const LoraAdapters &ad, void *workspace,
+                              hipStream_t s)
+{
+    const int64_t M = p.C, K = p.P, V = p.R;
+    uint16_t *u3 = static_cast<uint16_t *>(workspace);
+    GemmProblem f = p;  // the shared product, FP32: in place, or in the workspace for BF16 logits
+    if (bf16) {
+        f.D = static_cast<char *>(workspace) + round256(2 * piece_row(rank_bucket(ad.r)) * M);
+        f.ldd = (V + 3) / 4 * 4;
+    }
+    f.stream_out = false;  // read back at once
+    hipError_t e = hipSuccess;
+    if (ad.n > 0)
+        e = launch_shrink(p.B, p.ldb, M, K, ad, u3, nullptr, 0, nullptr, s);
+    if (e == hipSuccess)
+        e = launch_gemm_logits(f, Epi::kStoreF32, s);
+    if (e != hipSuccess)
+        return e;
+    const float *z = static_cast<const float *>(f.D);
+    switch (rank_bucket(ad.r)) {
+    case 16: return launch_expand<16>(z, f.ldd, p.D, p.ldd, bf16, M, V, ad, u3, s);
+    case 32: return launch_expand<32>(z, f.ldd, p.D, p.ldd, bf16, M, V, ad, u3, s);
+    case 64: return launch_expand<64>(z, f.ldd, p.D, p.ldd, bf16, M, V, ad, u3, s);
+    default: return launch_expand<128>(z, f.ldd, p.D, p.ldd, bf16, M, V, ad, u3, s);
+    }
+}
+
+hipError_t launch_lora_bwd(const LoraBwd &p, void *workspace, hipStream_t s)
+{
+    const BwdLayout l = bwd_layout(p.M, p.V, p.ad.r, p.ad.n);
+    char *ws = static_cast<char *>(workspace);
+    const int RP = rank_bucket(p.ad.r);
+    int32_t *offset = reinterpret_cast<int32_t *>(ws + l.offset);
+    int32_t *order = reinterpret_cast<int32_t *>(ws + l.order);
+    int32_t *ppos = reinterpret_cast<int32_t *>(ws + l.ppos);
+    const int64_t Mp = grouped_length(p.M, p.ad.n), nvb = (p.V + 255) / 256;
+    hipLaunchKernelGGL(lora_group_kernel, dim3(static_cast<unsigned>(p.ad.n + 2)), dim3(256), 0, s,
+                       p.ad.adapter, p.M, p.ad.n, offset, order, ppos);
+    hipError_t e = hipGetLastError();
+    if (e == hipSuccess && p.dB && p.ad.n > 0 && p.M > 0)
+        e = launch_shrink(p.x, p.ldx, p.M, p.K, p.ad, nullptr, reinterpret_cast<uint16_t *>(ws + l.uT), Mp,
+                          ppos, s);
+    if (e == hipSuccess && p.ad.n > 0 && p.V > 0) {
+        switch (RP) {
+        case 16: e = launch_bwd_v<16>(p, l, ws, s); break;
+        case 32: e = launch_bwd_v<32>(p, l, ws, s); break;
+        case 64: e = launch_bwd_v<64>(p, l, ws, s); break;
+        default: e = launch_bwd_v<128>(p, l, ws, s); break;
+        }
+    }
+    if (e != hipSuccess || (!p.dX && !p.dA) || p.K == 0)
+        return e;
+    if (p.ad.n > 0 && p.M > 0) {
+        const int64_t n4 = p.M * RP / 4;
+        hipLaunchKernelGGL(lora_t_kernel, dim3(static_cast<unsigned>((n4 + 15) / 16)), dim3(256), 0, s,
+                           reinterpret_cast<const float *>(ws + l.tpart), nvb, p.M, RP, p.ad, ppos,
+                           reinterpret_cast<uint16_t *>(ws + l.t3),
+                           reinterpret_cast<uint16_t *>(ws + l.tT), Mp);
+        e = hipGetLastError();
+        if (e != hipSuccess)
+            return e;
+    }
+    switch (RP) {
+    case 16: return launch_bwd_k<16>(p, l, ws, s);
+    case 32: return launch_bwd_k<32>(p, l, ws, s);
+    case 64: return launch_bwd_k<64>(p, l, ws, s);
+    default: return launch_bwd_k<128>(p, l, ws, s);
+    }
+}
+
+}  // namespace lmh
