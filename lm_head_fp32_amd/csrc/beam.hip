@@ -32,12 +32,13 @@ namespace {
 
 constexpr int kBeamMax = 64;       // beams per request, and beams selected
 constexpr int kScanWaves = 4;      // waves per scan workgroup
-constexpr int kCandCap = 512;      // candidates a wave can rank at once
+constexpr int kSegCols = 2048;     // columns a wave holds at a time, 32 a lane
+constexpr int kCandCap = 512;      // candidates a wave can hold
 
+// What a wave leaves of its segment of a row, besides its list.
 struct SegRecord {
-    double d;  // sum over the segment of exp(z - m); NaN: the row holds NaN or +inf
-    float m;   // max of the segment
-    float pad;
+    double d;     // sum over the segment of exp(z - base); NaN: it holds NaN or +inf
+    double base;  // about the segment's maximum; -inf: nothing above -inf
 };
 static_assert(sizeof(SegRecord) == 16, "one 16-byte record per segment");
 
@@ -45,7 +46,7 @@ static_assert(sizeof(SegRecord) == 16, "one 16-byte record per segment");
 __device__ __forceinline__ uint32_t order_key(float f)
 {
     const uint32_t u = __float_as_uint(f + 0.0f);
-    return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+    return u ^ (static_cast<uint32_t>(static_cast<int32_t>(u) >> 31) | 0x80000000u);
 }
 __device__ __forceinline__ float key_value(uint32_t k)
 {
@@ -72,6 +73,37 @@ __device__ __forceinline__ double exp_nonpos(double x)
     return ldexp(p, static_cast<int>(n));
 }
 
+// Sum of exp(v[i] - N ln 2) for an integer N, as 2^(z log2 e - N): one FP64
+// product per value, split into integer n and fraction f by adding 1.5 x 2^52
+// (n is then in the low word), 2^f from a polynomial whose relative error
+// alternates below 1.9e-9 on [-1/2, 1/2] (fitted by exchange), 2^n by an integer
+// add to the exponent: 12 full-rate instructions a value and one conversion.
+// Values below `low` count as that; z log2 e - N must lie within +-1000 and |N|
+// below 2^30.
+template <int PER>
+__device__ __forceinline__ double sum_exp(const float (&v)[PER], float low, double n0)
+{
+    constexpr double kLog2E = 1.4426950408889634, kMagic = 6755399441055744.0;
+    const double c = kMagic - n0;
+    double d = 0.0;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        const double z = static_cast<double>(__builtin_amdgcn_fmed3f(v[i], low, INFINITY));
+        const double t = fma(z, kLog2E, c);
+        const double f = fma(z, kLog2E, c - t);
+        double p = 0.0001534581202420037;
+        p = fma(p, f, 0.0013399931219698897);
+        p = fma(p, f, 0.009618488957041028);
+        p = fma(p, f, 0.055503287769636304);
+        p = fma(p, f, 0.24022646890634677);
+        p = fma(p, f, 0.6931472057372686);
+        p = fma(p, f, 1.0000000005541663);
+        const int n = static_cast<int>(__double_as_longlong(t));  // the low word
+        d += __hiloint2double(__double2hiint(p) + (n << 20), __double2loint(p));
+    }
+    return d;
+}
+
 __device__ __forceinline__ double shfl_xor_f64(double v, int off)
 {
     const uint64_t u = __double_as_longlong(v);
@@ -87,123 +119,170 @@ __device__ __forceinline__ uint64_t shfl_xor_u64(uint64_t u, int off)
     return (static_cast<uint64_t>(hi) << 32) | lo;
 }
 
+// Reductions over the wave, every lane getting the result: lanes of a row of
+// 16 through DPP (quad permutations, then rotations by 4 and 8), the four rows
+// through LDS permutes.
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp(uint32_t v)
+{
+    return static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(v), CTRL, 0xf, 0xf, true));
+}
+template <int CTRL>
+__device__ __forceinline__ double dpp_f64(double v)
+{
+    const uint64_t u = __double_as_longlong(v);
+    return __longlong_as_double((static_cast<uint64_t>(dpp<CTRL>(static_cast<uint32_t>(u >> 32))) << 32) |
+                                dpp<CTRL>(static_cast<uint32_t>(u)));
+}
+constexpr int kQuadXor1 = 0xb1, kQuadXor2 = 0x4e, kRowRor4 = 0x124, kRowRor8 = 0x128;
+
+__device__ __forceinline__ float wave_maximum(float m)  // NaN if any lane's is
+{
+    m = __builtin_elementwise_maximum(m, __uint_as_float(dpp<kQuadXor1>(__float_as_uint(m))));
+    m = __builtin_elementwise_maximum(m, __uint_as_float(dpp<kQuadXor2>(__float_as_uint(m))));
+    m = __builtin_elementwise_maximum(m, __uint_as_float(dpp<kRowRor4>(__float_as_uint(m))));
+    m = __builtin_elementwise_maximum(m, __uint_as_float(dpp<kRowRor8>(__float_as_uint(m))));
+    m = __builtin_elementwise_maximum(m, __shfl_xor(m, 16, 64));
+    return __builtin_elementwise_maximum(m, __shfl_xor(m, 32, 64));
+}
+
+__device__ __forceinline__ double wave_sum(double d)
+{
+    d += dpp_f64<kQuadXor1>(d);
+    d += dpp_f64<kQuadXor2>(d);
+    d += dpp_f64<kRowRor4>(d);
+    d += dpp_f64<kRowRor8>(d);
+    d += shfl_xor_f64(d, 16);
+    return d + shfl_xor_f64(d, 32);
+}
+
 // True when the beam can offer a candidate above -inf by its score alone.
 __device__ __forceinline__ bool score_alive(float s)
 {
     return s > -INFINITY && s < INFINITY;  // false for NaN
 }
 
-// Reads PER values of the segment [j0, j0 + 64 PER) of a row: lane l holds, in
-// v[4 u + e] (FP32) or v[8 u + e] (BF16), column j0 + (64 u + l) * G + e with G
-// values per 16-byte load; columns at or past V read as -inf.
-template <bool BF16, int PER>
-__device__ __forceinline__ void load_segment(const void *row, int64_t V, int64_t j0, int lane,
-                                             float (&v)[PER])
-{
-    constexpr int G = BF16 ? 8 : 4;
-    if (j0 + 64 * PER <= V) {
+// A segment of a row on its way from memory: lane l holds columns
+// j0 + (64 u + l) G + e, G per 16-byte load; columns at or past V read as -inf.
+template <bool BF16>
+struct Segment {
+    static constexpr int G = BF16 ? 8 : 4, NQ = 32 / G;
+    uint4 q[NQ];
+    __device__ __forceinline__ void load(const void *row, int64_t V, int64_t j0, int lane)
+    {
+        if (j0 + kSegCols <= V) {
 #pragma unroll
-        for (int u = 0; u < PER / G; ++u) {
-            const int64_t j = j0 + static_cast<int64_t>(64 * u + lane) * G;
-            if constexpr (BF16) {
-                const uint4 q = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(row) + j);
-                const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+            for (int u = 0; u < NQ; ++u)
+                q[u] = *reinterpret_cast<const uint4 *>(static_cast<const char *>(row) +
+                                                        (j0 + (64 * u + lane) * G) * (16 / G));
+            return;
+        }
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
+        for (int u = 0; u < NQ; ++u) {
+            uint32_t w[4];
+            const int64_t j = j0 + (64 * u + lane) * G;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                if constexpr (BF16) {
+                    const uint16_t *p = static_cast<const uint16_t *>(row) + j + 2 * e;
+                    const uint32_t lo = j + 2 * e < V ? p[0] : 0xff80u;
+                    const uint32_t hi = j + 2 * e + 1 < V ? p[1] : 0xff80u;
+                    w[e] = lo | (hi << 16);
+                } else {
+                    w[e] = j + e < V ? static_cast<const uint32_t *>(row)[j + e] : 0xff800000u;
+                }
+            }
+            q[u] = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+    }
+    __device__ __forceinline__ void values(float (&v)[32]) const
+    {
+#pragma unroll
+        for (int u = 0; u < NQ; ++u) {
+            const uint32_t w[4] = {q[u].x, q[u].y, q[u].z, q[u].w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                if constexpr (BF16) {
                     v[8 * u + 2 * e] = __uint_as_float(w[e] << 16);
                     v[8 * u + 2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
+                } else {
+                    v[4 * u + e] = __uint_as_float(w[e]);
                 }
-            } else {
-                const float4 q = *reinterpret_cast<const float4 *>(static_cast<const float *>(row) + j);
-                v[4 * u] = q.x, v[4 * u + 1] = q.y, v[4 * u + 2] = q.z, v[4 * u + 3] = q.w;
             }
         }
-        return;
     }
-#pragma unroll
-    for (int u = 0; u < PER / G; ++u) {
-        const int64_t j = j0 + static_cast<int64_t>(64 * u + lane) * G;
-#pragma unroll
-        for (int e = 0; e < G; ++e) {
-            float x = -INFINITY;
-            if (j + e < V) {
-                if constexpr (BF16)
-                    x = __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t *>(row)[j + e]) << 16);
-                else
-                    x = static_cast<const float *>(row)[j + e];
-            }
-            v[G * u + e] = x;
-        }
-    }
-}
+};
 
-// One wave per (row, segment of 64 PER columns).  Bound by the one read of the
-// logits: the wave keeps its segment in registers, so the maximum, the
-// exponentials and the candidates cost no second read, and nothing is shared
-// between waves (no barrier).
-// Candidates: the n_out-th largest of the 64 lane maxima is a lower bound of
-// the segment's n_out-th largest value (that many lanes hold a value at least
-// as large), cut to its upper 16 bits so that 16 ballots find it; the few
-// values at or above it are collected in LDS and ranked by counting.  Lists
-// are in descending value, equal values in ascending column.
-template <bool BF16, int PER>
+// One wave per (row, segment of 2048 columns).  Bound by the one read of the
+// logits: the segment sits in registers, so the sum, the maximum and the
+// candidates cost no second read; nothing is shared between waves (no
+// barrier), and six waves per SIMD cover each other's loads.
+// Candidates: the k-th largest of the 64 lane maxima is a lower bound of the
+// segment's k-th largest value (that many lanes hold a value at least as
+// large), cut to its upper 16 bits so that 16 ballots find it; the few values
+// at or above it are collected in LDS and ranked by counting.  The list is in
+// descending value, equal values in ascending column.
+template <bool BF16>
 __global__ __launch_bounds__(kScanWaves * 64) void beam_scan_kernel(
     const void *__restrict__ logits, int64_t ld, int64_t n_rows, int64_t V, int32_t nseg,
     const float *__restrict__ scores, const uint8_t *__restrict__ finished, int32_t k,
     SegRecord *__restrict__ rec, uint64_t *__restrict__ lists)
 {
-    constexpr int G = BF16 ? 8 : 4;
+    constexpr int G = Segment<BF16>::G;
     __shared__ uint64_t cand[kScanWaves][kCandCap];
-    __shared__ uint32_t count[kScanWaves];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int64_t id = static_cast<int64_t>(blockIdx.x) * kScanWaves + wave;
     if (id >= n_rows * nseg)
         return;
     const int64_t row = id / nseg;
-    const int64_t j0 = (id - row * nseg) * (64 * PER);
     if (!score_alive(scores[row]) || (finished && finished[row]))
         return;  // the merge does not read this beam's records
-
-    float v[PER];
-    load_segment<BF16, PER>(static_cast<const char *>(logits) + row * ld * (BF16 ? 2 : 4), V, j0, lane, v);
-
-    float lm = v[0];
+    const int64_t j0 = (id - row * nseg) * kSegCols;
+    float v[32];
+    {
+        Segment<BF16> sg;
+        sg.load(static_cast<const char *>(logits) + row * ld * (16 / G), V, j0, lane);
+        sg.values(v);
+    }
+    float gm[8], lm = -INFINITY;
 #pragma unroll
-    for (int i = 1; i < PER; ++i)
-        lm = __builtin_elementwise_maximum(lm, v[i]);  // NaN stays NaN
-    float m = lm;
-#pragma unroll
-    for (int off = 32; off >= 1; off >>= 1)
-        m = __builtin_elementwise_maximum(m, __shfl_xor(m, off, 64));
+    for (int u = 0; u < 8; ++u) {
+        gm[u] = __builtin_elementwise_maximum(__builtin_elementwise_maximum(v[4 * u], v[4 * u + 1]),
+                                              __builtin_elementwise_maximum(v[4 * u + 2], v[4 * u + 3]));
+        lm = __builtin_elementwise_maximum(lm, gm[u]);  // NaN stays NaN
+    }
+    const float m = wave_maximum(lm);
     uint64_t *out = lists + id * k;
     if (!(m < INFINITY) || m == -INFINITY) {
         // NaN or +inf somewhere (the whole row then offers nothing), or only
         // -inf: no candidates.
         if (lane == 0) {
-            rec[id].m = m;
             rec[id].d = (m == -INFINITY) ? 0.0 : static_cast<double>(NAN);
+            rec[id].base = (m == -INFINITY) ? -INFINITY : 0.0;
         }
-        for (int i = lane; i < k; i += 64)
-            out[i] = 0;
+        if (lane < k)
+            out[lane] = 0;
         return;
     }
 
-    const double md = static_cast<double>(m);
-    double d = 0.0;
+    double base = m, d = 0.0;
+    if (fabsf(m) < 268435456.0f) {
+        const double n0 = rint(base * 1.4426950408889634);
+        base = n0 * 0.6931471805599453;
+        d = sum_exp(v, m - 600.0f, n0);
+    } else {
+        // Beyond 2^28 other values lie at least 16 below.
 #pragma unroll
-    for (int i = 0; i < PER; ++i)
-        d += exp_nonpos(static_cast<double>(v[i]) - md);
-#pragma unroll
-    for (int off = 32; off >= 1; off >>= 1)
-        d += shfl_xor_f64(d, off);
+        for (int i = 0; i < 32; ++i)
+            d += exp_nonpos(static_cast<double>(v[i]) - base);
+    }
+    d = wave_sum(d);
     if (lane == 0) {
-        rec[id].m = m;
         rec[id].d = d;
+        rec[id].base = base;
     }
 
-    // Largest t (upper 16 bits) that at least k lane maxima reach, but above
-    // the key of -inf.
     const uint32_t mykey = order_key(lm);
     uint32_t t = 0;
 #pragma unroll
@@ -212,27 +291,29 @@ __global__ __launch_bounds__(kScanWaves * 64) void beam_scan_kernel(
         if (__popcll(__ballot(mykey >= c)) >= k)
             t = c;
     }
-    t = max(t, order_key(-INFINITY) + 1u);
-    const float tv = key_value(t);
-
-    if (lane == 0)
-        count[wave] = 0;
-    __builtin_amdgcn_wave_barrier();
-    uint64_t *mine = cand[wave];
-    if (lm >= tv) {
+    const float bound = key_value(max(t, order_key(-INFINITY) + 1u));
+    const uint32_t rest = 0xffffffffu - (static_cast<uint32_t>(j0) + static_cast<uint32_t>(lane * G));
+    auto key_of = [&](int i) {
+        return (static_cast<uint64_t>(order_key(v[i])) << 32) | (rest - static_cast<uint32_t>(64 * (i / G) * G + i % G));
+    };
+    uint64_t *const mine = cand[wave];
+    int n = 0;  // the same in every lane
 #pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            if (v[i] >= tv) {
-                const uint32_t at = atomicAdd(&count[wave], 1u);
-                const uint32_t col = static_cast<uint32_t>(j0) + (64 * (i / G) + lane) * G + i % G;
+    for (int u = 0; u < 8; ++u) {
+        if (!__ballot(gm[u] >= bound))
+            continue;
+#pragma unroll
+        for (int i = 4 * u; i < 4 * u + 4; ++i) {
+            const uint64_t mask = __ballot(v[i] >= bound);
+            if (v[i] >= bound) {
+                const int at = n + __popcll(mask & ((1ull << lane) - 1ull));
                 if (at < kCandCap)
-                    mine[at] = (static_cast<uint64_t>(order_key(v[i])) << 32) | (0xffffffffu - col);
+                    mine[at] = key_of(i);
             }
+            n += __popcll(mask);
         }
     }
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-    const int n = static_cast<int>(__builtin_amdgcn_readfirstlane(count[wave]));
     if (n <= kCandCap) {
         for (int i = lane; i < n; i += 64) {
             const uint64_t key = mine[i];
@@ -242,19 +323,18 @@ __global__ __launch_bounds__(kScanWaves * 64) void beam_scan_kernel(
             if (rank < k)
                 out[rank] = key;
         }
-        for (int i = n + lane; i < k; i += 64)
-            out[i] = 0;
+        if (n + lane < k)
+            out[n + lane] = 0;
         return;
     }
-    // Too many equal values at the bound (rows of ties): k rounds, each taking
-    // the largest key below the last one.
+    // Many equal values at the bound: k rounds, each taking the largest key
+    // below the last one.
     uint64_t last = ~0ull;
-    for (int rank = 0; rank < k; ++rank) {
+    for (int r = 0; r < k; ++r) {
         uint64_t best = 0;
 #pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            const uint32_t col = static_cast<uint32_t>(j0) + (64 * (i / G) + lane) * G + i % G;
-            const uint64_t key = (static_cast<uint64_t>(order_key(v[i])) << 32) | (0xffffffffu - col);
+        for (int i = 0; i < 32; ++i) {
+            const uint64_t key = key_of(i);
             if (v[i] > -INFINITY && key < last && key > best)
                 best = key;
         }
@@ -262,7 +342,7 @@ __global__ __launch_bounds__(kScanWaves * 64) void beam_scan_kernel(
         for (int off = 32; off >= 1; off >>= 1)
             best = max(best, shfl_xor_u64(best, off));
         if (lane == 0)
-            out[rank] = best;
+            out[r] = best;
         last = best;
     }
 }
@@ -273,7 +353,7 @@ __device__ __forceinline__ bool before(double a, uint32_t fa, double b, uint32_t
     return a > b || (a == b && fa < fb);
 }
 
-constexpr int kMergeThreads = 256;
+constexpr int kMergeThreads = 512;
 constexpr int kMergeCap = 1024;
 
 // One workgroup per request: logZ of every beam from its segments' records,
@@ -302,6 +382,13 @@ __global__ __launch_bounds__(kMergeThreads) void beam_merge_kernel(
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int64_t row0 = b * W;
+    // Lists 0 .. W nseg - 1 (beam l / nseg) and one candidate per finished beam;
+    // list l is walked by thread (l % 64) * 8 + (l / 64) % 8, so that the 64
+    // groups of eight threads share the lists evenly.  The head of the thread's
+    // first list is on its way while the sums are folded.
+    const int64_t n_lists = static_cast<int64_t>(W) * nseg;
+    const int64_t l0 = (tid >> 3) + 64 * (tid & 7);
+    const uint64_t head0 = l0 < n_lists ? lists[(row0 * nseg + l0) * k] : 0;
     if (tid < W) {
         sc[tid] = scores[row0 + tid];
         fin[tid] = finished ? (finished[row0 + tid] != 0) : 0;
@@ -316,20 +403,17 @@ __global__ __launch_bounds__(kMergeThreads) void beam_merge_kernel(
         double lz = static_cast<double>(NAN);
         if (!fin[w] && score_alive(sc[w])) {
             const SegRecord *r = rec + (row0 + w) * nseg;
-            float m = -INFINITY;
+            double m = -INFINITY;
             for (int s = lane; s < nseg; s += 64)
-                m = __builtin_elementwise_maximum(m, r[s].m);
+                m = fmax(m, r[s].base);
 #pragma unroll
             for (int off = 32; off >= 1; off >>= 1)
-                m = __builtin_elementwise_maximum(m, __shfl_xor(m, off, 64));
-            if (m > -INFINITY && m < INFINITY) {
-                double d = 0.0;
+                m = fmax(m, shfl_xor_f64(m, off));
+            if (m > -INFINITY) {
+                double d = 0.0;  // NaN from any segment that holds NaN or +inf
                 for (int s = lane; s < nseg; s += 64)
-                    d += r[s].d * exp_nonpos(static_cast<double>(r[s].m) - static_cast<double>(m));
-#pragma unroll
-                for (int off = 32; off >= 1; off >>= 1)
-                    d += shfl_xor_f64(d, off);
-                lz = static_cast<double>(m) + log(d);
+                    d += r[s].d * exp_nonpos(r[s].base - m);
+                lz = m + log(wave_sum(d));
             }
         }
         if (lane == 0)
@@ -337,11 +421,6 @@ __global__ __launch_bounds__(kMergeThreads) void beam_merge_kernel(
     }
     __syncthreads();
 
-    // Lists 0 .. W nseg - 1 (beam l / nseg), then one per finished beam; list l
-    // is walked by thread (l % 64) * 4 + (l / 64) % 4, so that the 64 groups of
-    // four threads share the lists evenly.
-    const int64_t n_lists = static_cast<int64_t>(W) * nseg;
-    const int64_t l0 = (tid >> 2) + 64 * (tid & 3);
     auto score_of = [&](int w, uint64_t key) {
         return static_cast<double>(sc[w]) +
                (static_cast<double>(key_value(static_cast<uint32_t>(key >> 32))) - logz[w]);
@@ -356,7 +435,7 @@ __global__ __launch_bounds__(kMergeThreads) void beam_merge_kernel(
     for (int64_t l = l0; l < n_lists; l += kMergeThreads) {
         const int w = static_cast<int>(l / nseg);
         if (logz[w] == logz[w]) {
-            const uint64_t key = lists[(row0 * nseg + l) * k];
+            const uint64_t key = l == l0 ? head0 : lists[(row0 * nseg + l) * k];
             if (key)
                 head = fmax(head, score_of(w, key));
         }
@@ -365,7 +444,7 @@ __global__ __launch_bounds__(kMergeThreads) void beam_merge_kernel(
         head = fmax(head, static_cast<double>(sc[tid]));
     // Rounded down, so that a bound on the rounded heads bounds the scores.
     if (head > -INFINITY)
-        atomicMax(&group[tid >> 2], order_key(__double2float_rd(head)));
+        atomicMax(&group[tid >> 3], order_key(__double2float_rd(head)));
     __syncthreads();
     uint32_t t = 0;
     {
@@ -392,14 +471,22 @@ __global__ __launch_bounds__(kMergeThreads) void beam_merge_kernel(
             if (!(logz[w] == logz[w]))
                 continue;
             const uint64_t *q = lists + (row0 * nseg + l) * k;
-            for (int i = 0; i < k; ++i) {
-                const uint64_t key = q[i];
-                if (!key)
+            // Four keys at a time: one wait for most lists.
+            for (int i = 0; i < k; i += 4) {
+                uint64_t key[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    key[e] = i + e < k ? q[i + e] : 0;
+                bool more = true;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const double c = score_of(w, key[e]);
+                    more = more && key[e] && c >= tv;
+                    if (more)
+                        append(c, flat_of(w, key[e]));
+                }
+                if (!more)
                     break;
-                const double c = score_of(w, key);
-                if (c < tv)
-                    break;
-                append(c, flat_of(w, key));
             }
         }
         if (tid < W && held(tid) && static_cast<double>(sc[tid]) >= tv)
@@ -638,9 +725,6 @@ hipError_t launch_reorder(const ReorderArgs &a, int64_t n_outer, hipStream_t s)
 
 }  // namespace
 
-// Columns per scan segment (64 lanes x PER).
-constexpr int kSegCols = 2048;
-
 int64_t beam_segments(int64_t V)
 {
     return (V + kSegCols - 1) / kSegCols;
@@ -660,19 +744,19 @@ hipError_t launch_beam_select(const void *logits, int64_t ld, bool bf16, int64_t
     const int64_t nseg = beam_segments(V), waves = B * W * nseg;
     SegRecord *rec = static_cast<SegRecord *>(workspace);
     uint64_t *lists = reinterpret_cast<uint64_t *>(rec + waves);
-    const unsigned blocks = static_cast<unsigned>((waves + kScanWaves - 1) / kScanWaves);
-    const int32_t k = static_cast<int32_t>(n_out), ns = static_cast<int32_t>(nseg);
+    const dim3 grid(static_cast<unsigned>((waves + kScanWaves - 1) / kScanWaves)), block(kScanWaves * 64);
+    const int32_t k = static_cast<int32_t>(n_out), nc = static_cast<int32_t>(nseg);
     if (bf16)
-        hipLaunchKernelGGL((beam_scan_kernel<true, kSegCols / 64>), dim3(blocks), dim3(kScanWaves * 64), 0, s,
-                           logits, ld, B * W, V, ns, scores, finished, k, rec, lists);
+        hipLaunchKernelGGL((beam_scan_kernel<true>), grid, block, 0, s, logits, ld, B * W, V, nc,
+                           scores, finished, k, rec, lists);
     else
-        hipLaunchKernelGGL((beam_scan_kernel<false, kSegCols / 64>), dim3(blocks), dim3(kScanWaves * 64), 0, s,
-                           logits, ld, B * W, V, ns, scores, finished, k, rec, lists);
+        hipLaunchKernelGGL((beam_scan_kernel<false>), grid, block, 0, s, logits, ld, B * W, V, nc,
+                           scores, finished, k, rec, lists);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess)
         return e;
     hipLaunchKernelGGL(beam_merge_kernel, dim3(static_cast<unsigned>(B)), dim3(kMergeThreads), 0, s, logits,
-                       ld, bf16 ? 1 : 0, static_cast<int32_t>(W), V, ns, scores, finished, eos, k, rec,
+                       ld, bf16 ? 1 : 0, static_cast<int32_t>(W), V, nc, scores, finished, eos, k, rec,
                        lists, out_scores, out_parent, out_token, out_finished);
     return hipGetLastError();
 }
