@@ -103,39 +103,109 @@ __host__ __device__ constexpr int piece_row(int RP)
     return RP == 16 ? 64 : 3 * RP;
 }
 
+// Batches of at most kFewTokens tokens are walked by adapter instead of by
+// blocks of 16 neighbouring tokens: each adapter's weights are then read once
+// per tile however the batch mixes its requests, and the adapters spread over
+// workgroups.
+constexpr int kFewTokens = 256;
+
+// The groups of such a batch, in order of first use: group g holds adapter
+// g[].id's tokens order[start .. start + count), ascending; count 0 past the
+// last.  Tokens on none form a group of id -1, all those whose id is no adapter
+// one of id n.
+struct FewGroup {
+    int32_t id, start, count, pad;
+};
+struct FewGroups {
+    FewGroup g[kFewTokens];
+    int32_t order[kFewTokens];
+};
+
+// Fills `t` (LDS) from the ids; 1024 threads.  Every token's id is compared with
+// all others, a quarter of them per thread (walking the distinct ids one after
+// another took 0.5 us each).
+__device__ __forceinline__ void group_few(const LoraAdapters &ad, int64_t M, FewGroups &t, int tid)
+{
+    __shared__ __attribute__((aligned(16))) int32_t ids[kFewTokens];
+    __shared__ int32_t cnt[4][kFewTokens], ahead[4][kFewTokens], first[4][kFewTokens];
+    __shared__ int32_t lead_start[kFewTokens], sums[4];
+    if (tid < kFewTokens) {
+        const int32_t v = tid < M ? ad.adapter[tid] : 0;
+        ids[tid] = tid >= M ? -2 : v < 0 ? -1 : v >= ad.n ? static_cast<int32_t>(ad.n) : v;
+        t.g[tid] = FewGroup{-1, 0, 0, 0};
+    }
+    __syncthreads();
+    const int m = tid & (kFewTokens - 1), part = tid / kFewTokens, lane = tid & 63;
+    const int32_t id = ids[m];
+    int c = 0, before = 0, f = kFewTokens;
+    for (int i = 64 * part; i < min(64 * part + 64, static_cast<int>(M)); i += 4) {
+        const int4 o = *reinterpret_cast<const int4 *>(ids + i);
+        const int32_t w[4] = {o.x, o.y, o.z, o.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const bool same = w[e] == id;
+            c += same;
+            before += same && i + e < m;
+            f = same ? min(f, i + e) : f;
+        }
+    }
+    cnt[part][m] = c, ahead[part][m] = before, first[part][m] = f;
+    __syncthreads();
+    int lead = 0, excl = 0;
+    if (tid < kFewTokens) {
+        c = cnt[0][m] + cnt[1][m] + cnt[2][m] + cnt[3][m];
+        before = ahead[0][m] + ahead[1][m] + ahead[2][m] + ahead[3][m];
+        f = min(min(first[0][m], first[1][m]), min(first[2][m], first[3][m]));
+        // Scan over the groups' first tokens: tokens in the upper half, groups
+        // in the lower.
+        lead = id != -2 && before == 0 ? (c << 16) | 1 : 0;
+        int incl = lead;
+#pragma unroll
+        for (int off = 1; off < 64; off <<= 1) {
+            const int o = __shfl_up(incl, off, 64);
+            incl += lane >= off ? o : 0;
+        }
+        excl = incl - lead;
+        if (lane == 63)
+            sums[tid >> 6] = incl;
+    }
+    __syncthreads();
+    if (tid < kFewTokens) {
+        for (int w = 0; w < (tid >> 6); ++w)
+            excl += sums[w];
+        if (lead) {
+            const int g = excl & 0xffff;
+            t.g[g] = FewGroup{id, excl >> 16, c, 0};
+            lead_start[m] = excl >> 16;
+        }
+    }
+    __syncthreads();
+    if (tid < kFewTokens && id != -2)
+        t.order[lead_start[f] + before] = m;
+    __syncthreads();
+}
+
 // ---------------------------------------------------------------------------
-// u = s_a A_a x for 16 tokens, one of the adapters they use (blockIdx.y: the
-// slot-th distinct one, in token order) and 16 of its ranks (blockIdx.z).  The
-// 16 waves split K and are summed in order through LDS.  Latency-bound: a few
-// hundred KiB per workgroup, so all of K runs in one workgroup (a second
-// launch to join parts would cost more) and slots spread over the chip.
-// Written as pieces: rows [token][piece_row] (u3), or ranks by grouped
-// position [3][RP][Mp] (uT, for the gradients).
+// u = s_a A_a x for 16 tokens of one adapter and 16 of its ranks.  The 16 waves
+// split K and are summed in order through LDS.  Latency-bound (a few hundred
+// KiB per workgroup), so all of K runs in one workgroup: a second launch to
+// join parts would cost more.  Written as pieces: rows [token][piece_row]
+// (u3), or ranks by grouped position [3][RP][Mp] (uT, for the gradients).
 constexpr int kShrinkThreads = 1024;
 
-__global__ __launch_bounds__(kShrinkThreads) void lora_shrink_kernel(
-    const uint16_t *__restrict__ x, int64_t ldx, int64_t M, int64_t K, LoraAdapters ad, int64_t blk0,
-    int RP, uint16_t *__restrict__ u3, uint16_t *__restrict__ uT, int64_t Mp,
-    const int32_t *__restrict__ ppos)
+struct ShrinkOut {
+    uint16_t *u3, *uT;
+    int64_t Mp;
+    const int32_t *ppos;
+    int RP;
+};
+
+// This wave's part of the 16 x 16 result: rows of A from pa (lane's row, its
+// eight columns of a step), of x from px.
+__device__ __forceinline__ f32x4 shrink_wave(const uint16_t *pa, const uint16_t *px, int64_t K, int wave,
+                                             int q)
 {
     constexpr int NW = kShrinkThreads / 64;
-    __shared__ f32x4 red[NW][64];
-    const int tid = threadIdx.x, lane = tid & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int t16 = lane & 15, q = lane >> 4;
-    const int64_t tok = (blk0 + blockIdx.x) * 16 + t16;
-    const int32_t id = tok < M ? ad.adapter[tok] : -1;
-    const bool valid = id >= 0 && id < ad.n;
-    uint32_t todo = static_cast<uint32_t>(__ballot(valid)) & 0xffffu;
-    for (unsigned s = 0; s < blockIdx.y && todo; ++s)
-        todo &= ~tokens_of(id, first_id(id, todo));
-    if (!todo)
-        return;  // uniform over the workgroup: every wave holds the same tokens
-    const int32_t a = first_id(id, todo);
-
-    const int j0 = blockIdx.z * 16;
-    const uint16_t *pa = ad.A + a * ad.stride_a + static_cast<int64_t>(min(j0 + t16, ad.r - 1)) * ad.lda;
-    const uint16_t *px = x + min(tok, M - 1) * ldx;
     const int64_t per_wave = (K + 32 * NW - 1) / (32 * NW) * 32;
     int64_t k = wave * per_wave;
     const int64_t kend = min(K, k + per_wave);
@@ -144,157 +214,394 @@ __global__ __launch_bounds__(kShrinkThreads) void lora_shrink_kernel(
         uint4 va[8], vx[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            va[i] = *reinterpret_cast<const uint4 *>(pa + k + 32 * i + 8 * q);
-            vx[i] = *reinterpret_cast<const uint4 *>(px + k + 32 * i + 8 * q);
+            va[i] = *reinterpret_cast<const uint4 *>(pa + k + 32 * i);
+            vx[i] = *reinterpret_cast<const uint4 *>(px + k + 32 * i);
         }
+        __builtin_amdgcn_sched_barrier(0);  // all sixteen in flight
 #pragma unroll
         for (int i = 0; i < 8; ++i)
             acc = mfma16(as_frag(va[i]), as_frag(vx[i]), acc);
     }
     for (; k < kend; k += 32) {
-        const int64_t kk = k + 8 * q;
-        acc = mfma16(as_frag(load8(pa + kk, K - kk)), as_frag(load8(px + kk, K - kk)), acc);
+        const int64_t left = K - k - 8 * q;
+        acc = mfma16(as_frag(load8(pa + k, left)), as_frag(load8(px + k, left)), acc);
     }
-    red[wave][lane] = acc;
+    return acc;
+}
+
+// Sums the waves' parts and writes the pieces of rank j0 + tid / 16 of the
+// thread's token (tid % 16 of the tile) where `mine`.
+__device__ __forceinline__ void shrink_join(f32x4 (&red)[kShrinkThreads / 64][64], f32x4 acc, bool mine,
+                                            int64_t tok, float scale, int64_t pos, int j0, int r,
+                                            const ShrinkOut &o, int tid)
+{
+    const int lane = tid & 63, t16 = tid & 15;
+    red[tid >> 6][lane] = acc;
     __syncthreads();
-    if (tid >= 256)
-        return;
-    // Thread: token tid % 16 (= t16), rank j0 + tid / 16.
-    const int jj = tid >> 4, j = j0 + jj;
-    float sum = 0.0f;
+    if (tid < 256 && mine) {
+        const int jj = tid >> 4, j = j0 + jj;
+        float sum = 0.0f;
 #pragma unroll
-    for (int w = 0; w < NW; ++w)
-        sum += red[w][(jj >> 2) * 16 + t16][jj & 3];
-    if (id != a || tok >= M)
-        return;
-    sum = j < ad.r ? sum * (ad.scale ? ad.scale[a] : 1.0f) : 0.0f;
-    uint32_t p[3];
-    split3(sum, p);
-    if (u3) {
-        uint16_t *row = u3 + tok * piece_row(RP) + j;
-        row[0] = static_cast<uint16_t>(p[0]);
-        row[RP] = static_cast<uint16_t>(p[1]);
-        row[2 * RP] = static_cast<uint16_t>(p[2]);
-        if (RP == 16)
-            row[48] = 0;
+        for (int w = 0; w < kShrinkThreads / 64; ++w)
+            sum += red[w][(jj >> 2) * 16 + t16][jj & 3];
+        uint32_t p[3];
+        split3(j < r ? sum * scale : 0.0f, p);
+        if (o.u3) {
+            uint16_t *row = o.u3 + tok * piece_row(o.RP) + j;
+            row[0] = static_cast<uint16_t>(p[0]);
+            row[o.RP] = static_cast<uint16_t>(p[1]);
+            row[2 * o.RP] = static_cast<uint16_t>(p[2]);
+            if (o.RP == 16)
+                row[48] = 0;
+        }
+        if (o.uT) {
+            uint16_t *col = o.uT + j * o.Mp + pos;
+            col[0] = static_cast<uint16_t>(p[0]);
+            col[o.RP * o.Mp] = static_cast<uint16_t>(p[1]);
+            col[2 * o.RP * o.Mp] = static_cast<uint16_t>(p[2]);
+        }
     }
-    if (uT) {
-        uint16_t *col = uT + j * Mp + ppos[tok];
-        col[0] = static_cast<uint16_t>(p[0]);
-        col[RP * Mp] = static_cast<uint16_t>(p[1]);
-        col[2 * RP * Mp] = static_cast<uint16_t>(p[2]);
+    __syncthreads();
+}
+
+// At most kFewTokens tokens: blockIdx.x takes the groups in turn, 16 tokens at
+// a time.  Leaves the groups in `table` for the next kernel.
+__global__ void __launch_bounds__(kShrinkThreads) __attribute__((amdgpu_waves_per_eu(4, 4)))
+lora_shrink_few_kernel(const uint16_t *__restrict__ x, int64_t ldx, int64_t M, int64_t K,
+                       LoraAdapters ad, ShrinkOut o, FewGroups *__restrict__ table)
+{
+    __shared__ f32x4 red[kShrinkThreads / 64][64];
+    __shared__ FewGroups t;
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int t16 = lane & 15, q = lane >> 4;
+    const int j0 = blockIdx.y * 16;
+    group_few(ad, M, t, tid);
+    if (table && blockIdx.x == 0 && blockIdx.y == 0) {
+        if (tid < kFewTokens) {
+            table->g[tid] = t.g[tid];
+            table->order[tid] = t.order[tid];
+        }
+    }
+    for (int g = blockIdx.x; g < kFewTokens; g += gridDim.x) {
+        const int32_t a = t.g[g].id;
+        const int count = t.g[g].count;
+        if (count == 0)
+            return;
+        if (a < 0 || a >= ad.n)
+            continue;
+        const float scale = ad.scale ? ad.scale[a] : 1.0f;
+        const int32_t *list = t.order + t.g[g].start;
+        const uint16_t *pa = ad.A + a * ad.stride_a +
+                             static_cast<int64_t>(min(j0 + t16, ad.r - 1)) * ad.lda + 8 * q;
+        for (int c = 0; c < count; c += 16) {
+            const int64_t tok = list[min(c + t16, count - 1)];
+            const int64_t pos = o.uT ? o.ppos[tok] : 0;
+            const f32x4 acc = shrink_wave(pa, x + tok * ldx + 8 * q, K, wave, q);
+            shrink_join(red, acc, c + t16 < count, tok, scale, pos, j0, ad.r, o, tid);
+        }
+    }
+}
+
+// Any number of tokens: 16 neighbouring ones per blockIdx.x; the distinct
+// adapters they use, in token order, go round the blockIdx.y slots.
+__global__ void __launch_bounds__(kShrinkThreads) __attribute__((amdgpu_waves_per_eu(4, 4)))
+lora_shrink_kernel(const uint16_t *__restrict__ x, int64_t ldx, int64_t M, int64_t K, LoraAdapters ad,
+                   int64_t blk0, ShrinkOut o)
+{
+    __shared__ f32x4 red[kShrinkThreads / 64][64];
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int t16 = lane & 15, q = lane >> 4;
+    const int64_t tok = (blk0 + blockIdx.x) * 16 + t16;
+    const int32_t id = tok < M ? ad.adapter[tok] : -1;
+    const bool valid = id >= 0 && id < ad.n;
+    const float scale = valid && ad.scale ? ad.scale[id] : 1.0f;
+    const int64_t pos = valid && o.uT ? o.ppos[tok] : 0;
+    const int j0 = blockIdx.z * 16;
+    // todo is the same in every wave: they hold the same tokens.
+    uint32_t todo = static_cast<uint32_t>(__ballot(valid)) & 0xffffu;
+    for (unsigned slot = 0; todo; ++slot) {
+        const int32_t a = first_id(id, todo);
+        todo &= ~tokens_of(id, a);
+        if (slot % gridDim.y != blockIdx.y)
+            continue;
+        const uint16_t *pa = ad.A + a * ad.stride_a +
+                             static_cast<int64_t>(min(j0 + t16, ad.r - 1)) * ad.lda + 8 * q;
+        const f32x4 acc = shrink_wave(pa, x + min(tok, M - 1) * ldx + 8 * q, K, wave, q);
+        shrink_join(red, acc, id == a, tok, scale, pos, j0, ad.r, o, tid);
+    }
+}
+
+// 8 words of a matrix row from column j (a multiple of 8), the row's length r
+// (a row pitch is at least r rounded up to 8): words past r are zero.  Only the
+// last row of the matrix may end where its storage does, so the others are read
+// whole.
+__device__ __forceinline__ uint4 load8_row(const uint16_t *row, int j, int r, bool last)
+{
+    if (j >= r)
+        return make_uint4(0u, 0u, 0u, 0u);
+    if (j + 8 <= r)
+        return *reinterpret_cast<const uint4 *>(row + j);
+    return last ? load8(row + j, r - j) : keep8(*reinterpret_cast<const uint4 *>(row + j), r - j);
+}
+
+// 16 tokens x 64 vocabulary rows of one adapter's part, turned from the matrix
+// layout (lane: token t16, rows 16 i + 4 q ..) into row pieces (lane: token
+// 4 i + q of the 16, columns 4 t16 ..) through 4 KiB of the wave's LDS: 16-byte
+// chunk c of token t's 64 values sits at c ^ t.
+__device__ __forceinline__ void turn_rows(f32x4 (&d)[4], float *own, int t16, int q)
+{
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        *reinterpret_cast<f32x4 *>(own + t16 * 64 + (((4 * i + q) ^ t16) << 2)) = d[i];
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        d[i] = *reinterpret_cast<const f32x4 *>(own + (4 * i + q) * 64 + ((t16 ^ (4 * i + q)) << 2));
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+}
+
+// Four values of an FP32 row at column v, zero past V.
+__device__ __forceinline__ f32x4 load_piece(const float *p, int64_t v, int64_t V)
+{
+    if (v + 4 <= V)
+        return *reinterpret_cast<const f32x4 *>(p + v);
+    f32x4 r = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int e = 0; e < 4 && v + e < V; ++e)
+        r[e] = p[v + e];
+    return r;
+}
+
+template <bool BF16>
+__device__ __forceinline__ void store_piece(void *out, int64_t row, int64_t v, int64_t V, f32x4 r)
+{
+    if constexpr (BF16) {
+        uint16_t *p = static_cast<uint16_t *>(out) + row + v;
+        uint32_t h[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            h[e] = f32_to_bf16_bits(r[e]);
+        if (v + 4 <= V)
+            store8(p, make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16)), false);
+        else
+            for (int e = 0; e < 4 && v + e < V; ++e)
+                p[e] = static_cast<uint16_t>(h[e]);
+    } else {
+        float *p = static_cast<float *>(out) + row + v;
+        if (v + 4 <= V)
+            *reinterpret_cast<f32x4 *>(p) = r;
+        else
+            for (int e = 0; e < 4 && v + e < V; ++e)
+                p[e] = r[e];
+    }
+}
+
+// logits += u B^T for at most kFewTokens tokens: one workgroup per 256
+// vocabulary rows and part (blockIdx.y) of the adapters in use; 16 tokens of an
+// adapter at a time, their B rows read once.  Bound by B of the adapters in use
+// and by z, read and written once; many small workgroups hide the latency.
+#ifndef LMH_FEW_EU
+#define LMH_FEW_EU 5
+#endif
+template <int RP, bool BF16>
+__global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(RP <= 32 ? LMH_FEW_EU : 3)))
+lora_expand_few_kernel(const float *z, int64_t ldz, void *out,
+                                                              int64_t ldo, int64_t M, int64_t V,
+                                                              LoraAdapters ad,
+                                                              const uint16_t *__restrict__ u3,
+                                                              const FewGroups *__restrict__ table)
+{
+    constexpr int U = RP < 32 ? 1 : RP / 32, S = piece_row(RP) / 32;
+    __shared__ __attribute__((aligned(16))) float turn[4][16 * 64];
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int t16 = lane & 15, q = lane >> 4;
+    const int64_t v0 = static_cast<int64_t>(blockIdx.x) * 256 + wave * 64;
+    if (v0 >= V)
+        return;
+    const int jq = RP == 16 ? 8 * (q & 1) : 8 * q;  // the lane's first rank of a step
+    const int64_t v = v0 + 4 * t16;
+    for (int g = blockIdx.y; g < kFewTokens; g += gridDim.y) {
+        const FewGroup info = table->g[g];
+        const int32_t a = info.id;
+        const int count = info.count;
+        if (count == 0)
+            return;
+        const int32_t *list = table->order + info.start;
+        const bool live = a >= 0 && a < ad.n;
+        if (!BF16 && a < 0)
+            continue;  // z is in place
+        bf16x8 fb[U][4];
+        if (live) {
+            const uint16_t *pb = ad.B + a * ad.stride_b;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int64_t vr = min(v0 + 16 * i + t16, V - 1);
+#pragma unroll
+                for (int uu = 0; uu < U; ++uu)
+                    fb[uu][i] = as_frag(load8_row(pb + vr * ad.ldb, 32 * uu + jq, ad.r, vr == V - 1));
+            }
+        }
+        for (int c = 0; c < count; c += 16) {
+            f32x4 zr[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                zr[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+                if (c + 4 * i + q < count)
+                    zr[i] = load_piece(z + list[c + 4 * i + q] * ldz, v, V);
+            }
+            f32x4 d[4];
+            const float fill = a >= ad.n ? NAN : 0.0f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                d[i] = f32x4{fill, fill, fill, fill};
+            if (live) {
+                const uint16_t *pu = u3 + list[min(c + t16, count - 1)] * piece_row(RP) + 8 * q;
+                bf16x8 fu[S];
+#pragma unroll
+                for (int s = 0; s < S; ++s)
+                    fu[s] = as_frag(*reinterpret_cast<const uint4 *>(pu + 32 * s));
+#pragma unroll
+                for (int s = 0; s < S; ++s)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        d[i] = mfma16(fb[s % U][i], fu[s], d[i]);
+            }
+            turn_rows(d, turn[wave], t16, q);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (c + 4 * i + q < count)
+                    store_piece<BF16>(out, list[c + 4 * i + q] * ldo, v, V, zr[i] + d[i]);
+        }
     }
 }
 
 // ---------------------------------------------------------------------------
-// logits += u B^T for 16 tokens x 256 vocabulary rows: reads the FP32 product
-// z, adds each token's adapter, stores FP32 (in place) or BF16 (rounded once).
-// Wave w holds rows 64 w .. + 63 as four 16 x 16 results; B rows go straight
-// from memory into matrix operands (the fragment is 16 contiguous bytes of a
-// row).  Bound by B of the adapters in use and by z, read and written once.
+// logits += u B^T: reads the FP32 product z, adds each token's adapter, stores
+// FP32 (in place) or BF16 (rounded once).  A workgroup covers 256 vocabulary
+// rows and `nb` blocks of 16 tokens, one after another; wave w holds rows
+// 64 w .. + 63 as four 16 x 16 results per block.  B rows go straight from
+// memory into matrix operands (a fragment is 16 contiguous bytes of a row) and
+// stay there while the next block uses the same adapter; z and the result move
+// in whole 256-byte row pieces, the products turned through 4 KiB of LDS per
+// wave.  Bound by z, read and written once, and by B of the adapters in use.
 template <int RP, bool BF16>
 __global__ __launch_bounds__(256) void lora_expand_kernel(const float *z, int64_t ldz, void *out,
                                                           int64_t ldo, int64_t M, int64_t V,
                                                           LoraAdapters ad,
-                                                          const uint16_t *__restrict__ u3,
-                                                          int64_t tok_blocks, int64_t blk0)
+                                                          const uint16_t *__restrict__ u3, int nb,
+                                                          int64_t tok_groups, int64_t wg0)
 {
     constexpr int U = RP < 32 ? 1 : RP / 32;     // distinct 32-deep steps over a rank
     constexpr int S = piece_row(RP) / 32;        // steps over the three pieces
+    __shared__ __attribute__((aligned(16))) float turn[4][16 * 64];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int t16 = lane & 15, q = lane >> 4;
-    const int64_t id_blk = blk0 + blockIdx.x;
-    const int64_t vt = id_blk / tok_blocks;
-    const int64_t tok = (id_blk - vt * tok_blocks) * 16 + t16;
-    const int32_t id = tok < M ? ad.adapter[tok] : -1;
-    const bool valid = id >= 0 && id < ad.n;
-    uint32_t todo = static_cast<uint32_t>(__ballot(valid)) & 0xffffu;
-    const bool bad = id >= ad.n;
-    if (!BF16 && !todo && !__ballot(bad))
-        return;
+    // Workgroups b, b + 8, ... share an XCD: they take the token groups of one
+    // vocabulary tile in turn, so that its B rows are read into one L2.
+    const int64_t wg = wg0 + blockIdx.x;
+    const int64_t vt = wg / 8 / tok_groups * 8 + wg % 8;
+    const int64_t tg = wg / 8 % tok_groups;
     const int64_t v0 = vt * 256 + wave * 64;
     if (v0 >= V)
         return;
-    bf16x8 fu[S];
-    const uint16_t *pu = u3 + min(tok, M - 1) * piece_row(RP) + 8 * q;
-    if (todo) {
+    float *const own = turn[wave];
+    const int jq = RP == 16 ? 8 * (q & 1) : 8 * q;  // the lane's first rank of a step
+    bf16x8 fb[U][4];
+    int32_t held = -1;  // the adapter whose B rows fb holds
+    auto load_b = [&](int32_t a, bf16x8 (&f)[U][4]) {
+        const uint16_t *pb = ad.B + a * ad.stride_b;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int64_t v = min(v0 + 16 * i + t16, V - 1);
+            const bool last = v == V - 1;
+#pragma unroll
+            for (int uu = 0; uu < U; ++uu)
+                f[uu][i] = as_frag(load8_row(pb + v * ad.ldb, 32 * uu + jq, ad.r, last));
+        }
+    };
+    // One block of 16 tokens: ids, pieces of u, and row pieces of z (this lane's
+    // four are tokens tok0 + 4 i + q, columns v0 + 4 t16 .. + 3).  The next
+    // block's are on their way before this one's results are stored: a wait for
+    // loads issued after stores would wait for the stores too.
+    const int64_t v = v0 + 4 * t16;
+    struct Block {
+        int32_t id;
+        bf16x8 u[S];
+        f32x4 z[4];
+    };
+    auto load_block = [&](Block &t, int64_t tok0) {
+        const int64_t tok = tok0 + t16;
+        t.id = tok < M ? ad.adapter[tok] : -1;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int64_t rt = tok0 + 4 * i + q;
+            t.z[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+            if (rt < M)
+                t.z[i] = load_piece(z + rt * ldz, v, V);
+        }
+        const uint16_t *pu = u3 + min(tok, M - 1) * piece_row(RP) + 8 * q;
 #pragma unroll
         for (int s = 0; s < S; ++s)
-            fu[s] = as_frag(*reinterpret_cast<const uint4 *>(pu + 32 * s));
-    }
-    f32x4 acc[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int64_t v = v0 + 16 * i + 4 * q;
-        acc[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-        if (tok < M) {
-            const float *p = z + tok * ldz + v;
-            if (v + 4 <= V)
-                acc[i] = *reinterpret_cast<const f32x4 *>(p);
-            else
-                for (int e = 0; e < 4 && v + e < V; ++e)
-                    acc[i][e] = p[e];
+            t.u[s] = as_frag(*reinterpret_cast<const uint4 *>(pu + 32 * s));
+    };
+    Block cur;
+    if (tg * nb * 16 < M)
+        load_block(cur, tg * nb * 16);
+    for (int b = 0; b < nb; ++b) {
+        const int64_t tok0 = (tg * nb + b) * 16;
+        if (tok0 >= M)
+            return;
+        Block nxt;
+        if (b + 1 < nb && tok0 + 16 < M)
+            load_block(nxt, tok0 + 16);
+        const int32_t id = cur.id;
+        const bool bad = id >= ad.n;
+        uint32_t todo = static_cast<uint32_t>(__ballot(id >= 0 && id < ad.n)) & 0xffffu;
+        if (!BF16 && !todo && !__ballot(bad)) {
+            cur = nxt;
+            continue;
         }
-    }
-    while (todo) {
-        const int32_t a = first_id(id, todo);
-        todo &= ~tokens_of(id, a);
-        const uint16_t *pb = ad.B + a * ad.stride_b;
-        f32x4 tmp[4];
+        f32x4 acc[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            tmp[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-        for (int uu = 0; uu < U; ++uu) {
-            const int j = RP == 16 ? 8 * (q & 1) : 32 * uu + 8 * q;
-            bf16x8 fb[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int64_t v = min(v0 + 16 * i + t16, V - 1);
-                fb[i] = as_frag(load8(pb + v * ad.ldb + j, ad.r - j));
-            }
-#pragma unroll
-            for (int s = uu; s < S; s += U)
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    tmp[i] = mfma16(fb[i], fu[s], tmp[i]);
-        }
-        if (id == a) {
+            acc[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        while (todo) {
+            const int32_t a = first_id(id, todo);
+            todo &= ~tokens_of(id, a);
+            if (a != held)
+                load_b(a, fb);
+            held = a;
+            f32x4 tmp[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                acc[i] += tmp[i];
+                tmp[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int s = 0; s < S; ++s)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    tmp[i] = mfma16(fb[s % U][i], cur.u[s], tmp[i]);
+            if (id == a) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    acc[i] = tmp[i];
+            }
         }
-    }
-    if (tok >= M)
-        return;
-    if (bad) {
+        if (bad) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            acc[i] = f32x4{NAN, NAN, NAN, NAN};
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int64_t v = v0 + 16 * i + 4 * q;
-        if constexpr (BF16) {
-            uint16_t *p = static_cast<uint16_t *>(out) + tok * ldo + v;
-            uint32_t h[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                h[e] = f32_to_bf16_bits(acc[i][e]);
-            if (v + 4 <= V)
-                store8(p, make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16)), false);
-            else
-                for (int e = 0; e < 4 && v + e < V; ++e)
-                    p[e] = static_cast<uint16_t>(h[e]);
-        } else {
-            float *p = static_cast<float *>(out) + tok * ldo + v;
-            if (v + 4 <= V)
-                *reinterpret_cast<f32x4 *>(p) = acc[i];
-            else
-                for (int e = 0; e < 4 && v + e < V; ++e)
-                    p[e] = acc[i][e];
+            for (int i = 0; i < 4; ++i)
+                acc[i] = f32x4{NAN, NAN, NAN, NAN};
         }
+        turn_rows(acc, own, t16, q);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int64_t rt = tok0 + 4 * i + q;
+            if (rt < M)
+                store_piece<BF16>(out, rt * ldo, v, V, cur.z[i] + acc[i]);
+        }
+        cur = nxt;
     }
 }
 
@@ -759,17 +1066,30 @@ int64_t grouped_length(int64_t M, int64_t n)
 }
 
 hipError_t launch_shrink(const uint16_t *x, int64_t ldx, int64_t M, int64_t K, const LoraAdapters &ad,
-                         uint16_t *u3, uint16_t *uT, int64_t Mp, const int32_t *ppos, hipStream_t s)
+                         uint16_t *u3, uint16_t *uT, int64_t Mp, const int32_t *ppos, FewGroups *table,
+                         hipStream_t s)
 {
     const int RP = rank_bucket(ad.r);
+    const ShrinkOut o = {u3, uT, Mp, ppos, RP};
+    const int64_t zr = RP / 16;
+    if (M <= kFewTokens) {
+        // One workgroup per group there can be (n adapters, none, no adapter).
+        const dim3 grid(static_cast<unsigned>(std::min<int64_t>(ad.n + 2, M)), static_cast<unsigned>(zr));
+        hipLaunchKernelGGL(lora_shrink_few_kernel, grid, dim3(kShrinkThreads), 0, s, x, ldx, M, K, ad, o,
+                           table);
+        return hipGetLastError();
+    }
+    if (ad.n == 0)
+        return hipSuccess;
     const int64_t blocks = (M + 15) / 16;
-    const int64_t slots = std::min<int64_t>(std::min<int64_t>(ad.n, 16), M), zr = RP / 16;
+    // Slots to fill the chip twice over, at most one per distinct adapter.
+    const int64_t slots =
+        std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(ad.n, 16), 512 / (blocks * zr)));
     const int64_t most = kMaxItems / kShrinkThreads / (slots * zr);
     for (int64_t b0 = 0; b0 < blocks; b0 += most) {
         const dim3 grid(static_cast<unsigned>(std::min(most, blocks - b0)), static_cast<unsigned>(slots),
                         static_cast<unsigned>(zr));
-        hipLaunchKernelGGL(lora_shrink_kernel, grid, dim3(kShrinkThreads), 0, s, x, ldx, M, K, ad, b0, RP,
-                           u3, uT, Mp, ppos);
+        hipLaunchKernelGGL(lora_shrink_kernel, grid, dim3(kShrinkThreads), 0, s, x, ldx, M, K, ad, b0, o);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess)
             return e;
@@ -779,17 +1099,44 @@ hipError_t launch_shrink(const uint16_t *x, int64_t ldx, int64_t M, int64_t K, c
 
 template <int RP>
 hipError_t launch_expand(const float *z, int64_t ldz, void *out, int64_t ldo, bool bf16, int64_t M,
-                         int64_t V, const LoraAdapters &ad, const uint16_t *u3, hipStream_t s)
+                         int64_t V, const LoraAdapters &ad, const uint16_t *u3,
+                         const FewGroups *table, hipStream_t s)
 {
-    const int64_t tb = (M + 15) / 16, blocks = (V + 255) / 256 * tb, most = kMaxItems / 256;
-    for (int64_t b0 = 0; b0 < blocks; b0 += most) {
-        const dim3 grid(static_cast<unsigned>(std::min(most, blocks - b0)));
+    if (M <= kFewTokens) {
+        // Parts of the groups: as many as make 4096 workgroups.
+#ifndef LMH_FEW_WGS
+#define LMH_FEW_WGS 4096
+#endif
+        const int64_t vts = (V + 255) / 256;
+        const int64_t parts = std::max<int64_t>(1, std::min(std::min(ad.n + 2, M), LMH_FEW_WGS / vts));
+        const dim3 grid(static_cast<unsigned>(vts), static_cast<unsigned>(parts));
+        if (bf16)
+            hipLaunchKernelGGL((lora_expand_few_kernel<RP, true>), grid, dim3(256), 0, s, z, ldz, out, ldo, M, V,
+                               ad, u3, table);
+        else
+            hipLaunchKernelGGL((lora_expand_few_kernel<RP, false>), grid, dim3(256), 0, s, z, ldz, out, ldo, M,
+                               V, ad, u3, table);
+        return hipGetLastError();
+    }
+    // Token blocks per workgroup: up to eight (B rows kept across a request's
+    // tokens, loads ahead of stores) while 1024 workgroups remain.
+#ifndef LMH_EXPAND_NB
+#define LMH_EXPAND_NB 8
+#endif
+    const int64_t tb = (M + 15) / 16, vts = (V + 255) / 256;
+    const int nb = static_cast<int>(
+        std::max<int64_t>(1, std::min<int64_t>(LMH_EXPAND_NB, tb * vts / 1024)));
+    const int64_t groups = (tb + nb - 1) / nb;
+    // Whole groups of eight vocabulary tiles (the tiles past V exit).
+    const int64_t wgs = (vts + 7) / 8 * 8 * groups, most = kMaxItems / 256;
+    for (int64_t w0 = 0; w0 < wgs; w0 += most) {
+        const dim3 grid(static_cast<unsigned>(std::min(most, wgs - w0)));
         if (bf16)
             hipLaunchKernelGGL((lora_expand_kernel<RP, true>), grid, dim3(256), 0, s, z, ldz, out, ldo, M, V,
-                               ad, u3, tb, b0);
+                               ad, u3, nb, groups, w0);
         else
             hipLaunchKernelGGL((lora_expand_kernel<RP, false>), grid, dim3(256), 0, s, z, ldz, out, ldo, M,
-                               V, ad, u3, tb, b0);
+                               V, ad, u3, nb, groups, w0);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess)
             return e;
@@ -845,9 +1192,15 @@ hipError_t launch_bwd_k(const LoraBwd &p, const BwdLayout &l, char *ws, hipStrea
 
 }  // namespace
 
+// Room for the groups of a small batch, ahead of u.
+static int64_t few_bytes(int64_t M)
+{
+    return M <= kFewTokens ? round256(sizeof(FewGroups)) : 0;
+}
+
 int64_t lora_logits_workspace_bytes(int64_t M, int64_t V, int64_t r, bool bf16)
 {
-    const int64_t u = round256(2 * piece_row(rank_bucket(r)) * M);
+    const int64_t u = few_bytes(M) + round256(2 * piece_row(rank_bucket(r)) * M);
     return u + (bf16 ? round256(4 * M * ((V + 3) / 4 * 4)) : 0);
 }
 
@@ -860,26 +1213,26 @@ hipError_t launch_logits_lora(const GemmProblem &p, bool bf16, const LoraAdapter
                               hipStream_t s)
 {
     const int64_t M = p.C, K = p.P, V = p.R;
-    uint16_t *u3 = static_cast<uint16_t *>(workspace);
+    char *ws = static_cast<char *>(workspace);
+    FewGroups *table = reinterpret_cast<FewGroups *>(ws);  // M <= kFewTokens
+    uint16_t *u3 = reinterpret_cast<uint16_t *>(ws + few_bytes(M));
     GemmProblem f = p;  // the shared product, FP32: in place, or in the workspace for BF16 logits
     if (bf16) {
-        f.D = static_cast<char *>(workspace) + round256(2 * piece_row(rank_bucket(ad.r)) * M);
+        f.D = reinterpret_cast<char *>(u3) + round256(2 * piece_row(rank_bucket(ad.r)) * M);
         f.ldd = (V + 3) / 4 * 4;
     }
     f.stream_out = false;  // read back at once
-    hipError_t e = hipSuccess;
-    if (ad.n > 0)
-        e = launch_shrink(p.B, p.ldb, M, K, ad, u3, nullptr, 0, nullptr, s);
+    hipError_t e = launch_shrink(p.B, p.ldb, M, K, ad, u3, nullptr, 0, nullptr, table, s);
     if (e == hipSuccess)
         e = launch_gemm_logits(f, Epi::kStoreF32, s);
     if (e != hipSuccess)
         return e;
     const float *z = static_cast<const float *>(f.D);
     switch (rank_bucket(ad.r)) {
-    case 16: return launch_expand<16>(z, f.ldd, p.D, p.ldd, bf16, M, V, ad, u3, s);
-    case 32: return launch_expand<32>(z, f.ldd, p.D, p.ldd, bf16, M, V, ad, u3, s);
-    case 64: return launch_expand<64>(z, f.ldd, p.D, p.ldd, bf16, M, V, ad, u3, s);
-    default: return launch_expand<128>(z, f.ldd, p.D, p.ldd, bf16, M, V, ad, u3, s);
+    case 16: return launch_expand<16>(z, f.ldd, p.D, p.ldd, bf16, M, V, ad, u3, table, s);
+    case 32: return launch_expand<32>(z, f.ldd, p.D, p.ldd, bf16, M, V, ad, u3, table, s);
+    case 64: return launch_expand<64>(z, f.ldd, p.D, p.ldd, bf16, M, V, ad, u3, table, s);
+    default: return launch_expand<128>(z, f.ldd, p.D, p.ldd, bf16, M, V, ad, u3, table, s);
     }
 }
 
@@ -897,7 +1250,7 @@ hipError_t launch_lora_bwd(const LoraBwd &p, void *workspace, hipStream_t s)
     hipError_t e = hipGetLastError();
     if (e == hipSuccess && p.dB && p.ad.n > 0 && p.M > 0)
         e = launch_shrink(p.x, p.ldx, p.M, p.K, p.ad, nullptr, reinterpret_cast<uint16_t *>(ws + l.uT), Mp,
-                          ppos, s);
+                          ppos, nullptr, s);
     if (e == hipSuccess && p.ad.n > 0 && p.V > 0) {
         switch (RP) {
         case 16: e = launch_bwd_v<16>(p, l, ws, s); break;
