@@ -262,13 +262,13 @@ bool adapter_sizes_ok(int64_t M, int64_t K, int64_t V, int64_t rank, int64_t n)
            rank <= kMaxRank && n >= 0 && n <= (kMaxLaunchItems / 256) - 2;
 }
 
-// The gradients' launches: one workgroup of 256 per (256 columns, group), and
-// 4 work-items per rank of every token; positions are kept in 32 bits.
+// The gradients' launches: one workgroup of 256 per (256 columns, adapter or
+// chunk of 64 tokens), and 4 work-items per rank of every token.
 bool lora_bwd_fits(int64_t M, int64_t K, int64_t V, int64_t rank, int64_t n)
 {
     const int64_t most = kMaxLaunchItems / 256;
-    return ceil_div(V, 256) <= most / std::max<int64_t>(n, 1) && ceil_div(K, 256) <= most / (n + 2) &&
-           M <= kMaxLaunchItems / (4 * kMaxRank) && M + 64 * (n + 1) <= kMaxDim;
+    return ceil_div(V, 256) <= most / std::max<int64_t>(n, 1) &&
+           ceil_div(K, 256) <= most / (2 * n + M / 64 + 2) && M <= kMaxLaunchItems / (4 * kMaxRank);
 }
 
 constexpr int64_t kMaxBeams = 64;

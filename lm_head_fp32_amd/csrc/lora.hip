@@ -138,7 +138,8 @@ __device__ __forceinline__ void group_few(const LoraAdapters &ad, int64_t M, Few
     const int m = tid & (kFewTokens - 1), part = tid / kFewTokens, lane = tid & 63;
     const int32_t id = ids[m];
     int c = 0, before = 0, f = kFewTokens;
-    for (int i = 64 * part; i < min(64 * part + 64, static_cast<int>(M)); i += 4) {
+    const int quarter = (static_cast<int>(M) + 15) / 16 * 4;  // whole vectors; past M no id matches
+    for (int i = quarter * part; i < min(quarter * part + quarter, kFewTokens); i += 4) {
         const int4 o = *reinterpret_cast<const int4 *>(ids + i);
         const int32_t w[4] = {o.x, o.y, o.z, o.w};
 #pragma unroll
@@ -189,16 +190,8 @@ __device__ __forceinline__ void group_few(const LoraAdapters &ad, int64_t M, Few
 // u = s_a A_a x for 16 tokens of one adapter and 16 of its ranks.  The 16 waves
 // split K and are summed in order through LDS.  Latency-bound (a few hundred
 // KiB per workgroup), so all of K runs in one workgroup: a second launch to
-// join parts would cost more.  Written as pieces: rows [token][piece_row]
-// (u3), or ranks by grouped position [3][RP][Mp] (uT, for the gradients).
+// join parts would cost more.  Written as pieces, rows [token][piece_row].
 constexpr int kShrinkThreads = 1024;
-
-struct ShrinkOut {
-    uint16_t *u3, *uT;
-    int64_t Mp;
-    const int32_t *ppos;
-    int RP;
-};
 
 // This wave's part of the 16 x 16 result: rows of A from pa (lane's row, its
 // eight columns of a step), of x from px.
@@ -232,8 +225,8 @@ __device__ __forceinline__ f32x4 shrink_wave(const uint16_t *pa, const uint16_t 
 // Sums the waves' parts and writes the pieces of rank j0 + tid / 16 of the
 // thread's token (tid % 16 of the tile) where `mine`.
 __device__ __forceinline__ void shrink_join(f32x4 (&red)[kShrinkThreads / 64][64], f32x4 acc, bool mine,
-                                            int64_t tok, float scale, int64_t pos, int j0, int r,
-                                            const ShrinkOut &o, int tid)
+                                            int64_t tok, float scale, int j0, int r, uint16_t *u3, int RP,
+                                            int tid)
 {
     const int lane = tid & 63, t16 = tid & 15;
     red[tid >> 6][lane] = acc;
@@ -246,20 +239,12 @@ __device__ __forceinline__ void shrink_join(f32x4 (&red)[kShrinkThreads / 64][64
             sum += red[w][(jj >> 2) * 16 + t16][jj & 3];
         uint32_t p[3];
         split3(j < r ? sum * scale : 0.0f, p);
-        if (o.u3) {
-            uint16_t *row = o.u3 + tok * piece_row(o.RP) + j;
-            row[0] = static_cast<uint16_t>(p[0]);
-            row[o.RP] = static_cast<uint16_t>(p[1]);
-            row[2 * o.RP] = static_cast<uint16_t>(p[2]);
-            if (o.RP == 16)
-                row[48] = 0;
-        }
-        if (o.uT) {
-            uint16_t *col = o.uT + j * o.Mp + pos;
-            col[0] = static_cast<uint16_t>(p[0]);
-            col[o.RP * o.Mp] = static_cast<uint16_t>(p[1]);
-            col[2 * o.RP * o.Mp] = static_cast<uint16_t>(p[2]);
-        }
+        uint16_t *row = u3 + tok * piece_row(RP) + j;
+        row[0] = static_cast<uint16_t>(p[0]);
+        row[RP] = static_cast<uint16_t>(p[1]);
+        row[2 * RP] = static_cast<uint16_t>(p[2]);
+        if (RP == 16)
+            row[48] = 0;
     }
     __syncthreads();
 }
@@ -268,7 +253,8 @@ __device__ __forceinline__ void shrink_join(f32x4 (&red)[kShrinkThreads / 64][64
 // a time.  Leaves the groups in `table` for the next kernel.
 __global__ void __launch_bounds__(kShrinkThreads) __attribute__((amdgpu_waves_per_eu(4, 4)))
 lora_shrink_few_kernel(const uint16_t *__restrict__ x, int64_t ldx, int64_t M, int64_t K,
-                       LoraAdapters ad, ShrinkOut o, FewGroups *__restrict__ table)
+                       LoraAdapters ad, int RP, uint16_t *__restrict__ u3,
+                       FewGroups *__restrict__ table)
 {
     __shared__ f32x4 red[kShrinkThreads / 64][64];
     __shared__ FewGroups t;
@@ -296,9 +282,8 @@ lora_shrink_few_kernel(const uint16_t *__restrict__ x, int64_t ldx, int64_t M, i
                              static_cast<int64_t>(min(j0 + t16, ad.r - 1)) * ad.lda + 8 * q;
         for (int c = 0; c < count; c += 16) {
             const int64_t tok = list[min(c + t16, count - 1)];
-            const int64_t pos = o.uT ? o.ppos[tok] : 0;
             const f32x4 acc = shrink_wave(pa, x + tok * ldx + 8 * q, K, wave, q);
-            shrink_join(red, acc, c + t16 < count, tok, scale, pos, j0, ad.r, o, tid);
+            shrink_join(red, acc, c + t16 < count, tok, scale, j0, ad.r, u3, RP, tid);
         }
     }
 }
@@ -307,7 +292,7 @@ lora_shrink_few_kernel(const uint16_t *__restrict__ x, int64_t ldx, int64_t M, i
 // adapters they use, in token order, go round the blockIdx.y slots.
 __global__ void __launch_bounds__(kShrinkThreads) __attribute__((amdgpu_waves_per_eu(4, 4)))
 lora_shrink_kernel(const uint16_t *__restrict__ x, int64_t ldx, int64_t M, int64_t K, LoraAdapters ad,
-                   int64_t blk0, ShrinkOut o)
+                   int64_t blk0, int RP, uint16_t *__restrict__ u3)
 {
     __shared__ f32x4 red[kShrinkThreads / 64][64];
     const int tid = threadIdx.x, lane = tid & 63;
@@ -317,7 +302,6 @@ lora_shrink_kernel(const uint16_t *__restrict__ x, int64_t ldx, int64_t M, int64
     const int32_t id = tok < M ? ad.adapter[tok] : -1;
     const bool valid = id >= 0 && id < ad.n;
     const float scale = valid && ad.scale ? ad.scale[id] : 1.0f;
-    const int64_t pos = valid && o.uT ? o.ppos[tok] : 0;
     const int j0 = blockIdx.z * 16;
     // todo is the same in every wave: they hold the same tokens.
     uint32_t todo = static_cast<uint32_t>(__ballot(valid)) & 0xffffu;
@@ -329,7 +313,7 @@ lora_shrink_kernel(const uint16_t *__restrict__ x, int64_t ldx, int64_t M, int64
         const uint16_t *pa = ad.A + a * ad.stride_a +
                              static_cast<int64_t>(min(j0 + t16, ad.r - 1)) * ad.lda + 8 * q;
         const f32x4 acc = shrink_wave(pa, x + min(tok, M - 1) * ldx + 8 * q, K, wave, q);
-        shrink_join(red, acc, id == a, tok, scale, pos, j0, ad.r, o, tid);
+        shrink_join(red, acc, id == a, tok, scale, j0, ad.r, u3, RP, tid);
     }
 }
 
@@ -608,75 +592,94 @@ __global__ __launch_bounds__(256) void lora_expand_kernel(const float *z, int64_
 // ---------------------------------------------------------------------------
 // Gradients.  The tokens are grouped by adapter first (stable): group g < n
 // holds adapter g's tokens, group n the tokens on none, group n + 1 those
-// whose id is not an adapter.  offset[g] is the group's first place in
-// order[]; a second numbering starts every group at a multiple of 64
-// (group_base), so that a chunk of 64 tokens of one group is 128 contiguous,
-// aligned bytes of a rank's row in uT and tT.
-__host__ __device__ __forceinline__ int64_t group_base(int64_t offset, int64_t g)
+// whose id is not an adapter.  offset[g] is the group's first place in order[].
+// Chunks of up to 64 tokens of one group are numbered too: those of group g
+// start at chunk_base(offset[g], g), with some numbers unused, so that a
+// workgroup can be given a chunk without knowing the counts.
+__host__ __device__ __forceinline__ int64_t chunk_base(int64_t offset, int64_t g)
 {
-    // Room enough: floor64(o + c) - floor64(o) + 64 >= ceil64(c).
-    return offset / 64 * 64 + 64 * g;
+    // Room enough: floor((o + c) / 64) - floor(o / 64) + 1 >= ceil(c / 64).
+    return offset / 64 + g;
 }
 
+struct Chunk {
+    int32_t group, first, count, pad;  // its tokens are order[first .. first + count); group -1: unused
+};
+
 // One workgroup per group: counts the ids below and in its group, then writes
-// its tokens in order.  Reads the ids n + 2 times in all (they stay in L2);
-// no workgroup waits for another.
+// its tokens in order, and its chunks.  Reads the ids n + 2 times in all (they
+// stay in L2); no workgroup waits for another.
 __global__ __launch_bounds__(256) void lora_group_kernel(const int32_t *__restrict__ adapter, int64_t M,
                                                          int64_t n, int32_t *__restrict__ offset,
                                                          int32_t *__restrict__ order,
-                                                         int32_t *__restrict__ ppos)
+                                                         Chunk *__restrict__ chunks)
 {
-    __shared__ int32_t part[4];
-    __shared__ int32_t total;
+    __shared__ int32_t part[2][4];
     const int64_t g = blockIdx.x;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     auto cls = [&](int32_t id) { return id < 0 ? n : id >= n ? n + 1 : static_cast<int64_t>(id); };
-    int32_t less = 0;
-    for (int64_t m = tid; m < M; m += 256)
-        less += cls(adapter[m]) < g;
+    int32_t less = 0, same = 0;
+    for (int64_t m = tid; m < M; m += 256) {
+        const int64_t c = cls(adapter[m]);
+        less += c < g;
+        same += c == g;
+    }
 #pragma unroll
-    for (int off = 32; off >= 1; off >>= 1)
+    for (int off = 32; off >= 1; off >>= 1) {
         less += __shfl_xor(less, off, 64);
+        same += __shfl_xor(same, off, 64);
+    }
     if (lane == 0)
-        part[wave] = less;
+        part[0][wave] = less, part[1][wave] = same;
     __syncthreads();
-    const int32_t first = part[0] + part[1] + part[2] + part[3];
+    const int32_t first = part[0][0] + part[0][1] + part[0][2] + part[0][3];
+    const int32_t count = part[1][0] + part[1][1] + part[1][2] + part[1][3];
     if (tid == 0) {
         offset[g] = first;
         if (g == n + 1)
             offset[n + 2] = static_cast<int32_t>(M);
-        total = 0;
     }
-    const int32_t base = static_cast<int32_t>(group_base(first, g));
-    for (int64_t m0 = 0; m0 < M; m0 += 256) {
+    const int64_t c0 = chunk_base(first, g), c1 = chunk_base(first + count, g + 1);
+    for (int64_t c = c0 + tid; c < c1; c += 256) {
+        const int32_t at = static_cast<int32_t>(64 * (c - c0));
+        chunks[c] = at < count ? Chunk{static_cast<int32_t>(g), first + at, min(64, count - at), 0}
+                               : Chunk{-1, 0, 0, 0};
+    }
+    if (count == 0)
+        return;
+    int32_t done = 0;
+    for (int64_t m0 = 0; m0 < M && done < count; m0 += 256) {
         const int64_t m = m0 + tid;
         const bool mine = m < M && cls(adapter[m]) == g;
         const uint64_t mask = __ballot(mine);
-        __syncthreads();  // part[] and total of the round before are read
+        __syncthreads();  // the round before has read part[0]
         if (lane == 0)
-            part[wave] = __popcll(mask);
+            part[0][wave] = __popcll(mask);
         __syncthreads();
-        int32_t at = total + __popcll(mask & ((1ull << lane) - 1ull));
+        int32_t at = done + __popcll(mask & ((1ull << lane) - 1ull));
         for (int w = 0; w < wave; ++w)
-            at += part[w];
-        if (mine) {
+            at += part[0][w];
+        if (mine)
             order[first + at] = static_cast<int32_t>(m);
-            if (g < n)
-                ppos[m] = base + at;
-        }
-        __syncthreads();
-        if (tid == 0)
-            total += part[0] + part[1] + part[2] + part[3];
+        done += part[0][0] + part[0][1] + part[0][2] + part[0][3];
     }
 }
 
-// A staged tile: 64 rows (tokens, or ranks) of 256 BF16 words, 16-byte chunk c
-// of row p at chunk c ^ tile_key(p).  The key separates the eight rows that a
-// quarter of a row-wise fragment read touches, and the two groups of four rows
-// that half of a transposing read touches.
-__device__ __forceinline__ int tile_key(int p)
+// Staged tiles: 64 rows (tokens, or ranks) of PITCH BF16 words, 16-byte chunk c
+// of row p at chunk c ^ key(p).  Wide rows (16 chunks or more): the key
+// separates the eight rows that a quarter of a row-wise fragment read touches,
+// and the two groups of four rows that half of a transposing read touches.
+// Rows of pieces take the three low bits only, so that a chunk stays within
+// its eight.
+template <int PITCH, bool PIECES>
+__device__ __forceinline__ int tile_at(int p, int chunk)
 {
-    return ((p & 3) << 2) ^ ((p >> 2) & 1) ^ (((p >> 3) & 1) << 1);
+    int key;
+    if constexpr (PIECES)
+        key = ((p & 3) << 1) ^ ((p >> 2) & 1);
+    else
+        key = ((p & 3) << 2) ^ ((p >> 2) & 1) ^ (((p >> 3) & 1) << 1);
+    return p * PITCH + ((chunk ^ key) << 3);
 }
 
 typedef short v4i16 __attribute__((ext_vector_type(4)));
@@ -686,13 +689,12 @@ typedef short v8i16 __attribute__((ext_vector_type(8)));
 // p = the lane group's first row (a multiple of 8).  Within a group of 16
 // lanes, lane 4 b + a addresses row b, columns 4 a .. 4 a + 3, and the
 // transposing read hands lane i column i of the four rows.
+template <int PITCH, bool PIECES>
 __device__ __forceinline__ bf16x8 tile_column_frag(const uint16_t *tile, int p, int n0, int lane)
 {
     typedef __attribute__((address_space(3))) v4i16 lds_v4;
     const int b = (lane >> 2) & 3, col = n0 + 4 * (lane & 3);
-    auto at = [&](int row) {
-        return tile + row * 256 + (((col >> 3) ^ tile_key(row)) << 3) + (col & 7);
-    };
+    auto at = [&](int row) { return tile + tile_at<PITCH, PIECES>(row, col >> 3) + (col & 7); };
     const v4i16 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4 *)(at(p + b)));
     const v4i16 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4 *)(at(p + 4 + b)));
     const v8i16 c = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
@@ -700,37 +702,93 @@ __device__ __forceinline__ bf16x8 tile_column_frag(const uint16_t *tile, int p, 
 }
 
 // Row fragment: 8 columns from n (a multiple of 8) of row p.
+template <int PITCH, bool PIECES>
 __device__ __forceinline__ bf16x8 tile_row_frag(const uint16_t *tile, int p, int n)
 {
-    return *reinterpret_cast<const bf16x8 *>(tile + p * 256 + (((n >> 3) ^ tile_key(p)) << 3));
+    return *reinterpret_cast<const bf16x8 *>(tile + tile_at<PITCH, PIECES>(p, n >> 3));
 }
 
-// The registers of one tile on its way from memory: 64 tokens x 256 columns by
-// 256 threads, thread = (row 8 i + tid / 32, chunk tid % 32).
-struct TokenTile {
-    uint4 v[8];
-    __device__ __forceinline__ void load(const uint16_t *base, int64_t ld, const int32_t *order,
-                                         int64_t first, int64_t count, int64_t col0, int64_t ncols,
+// LDS pitch of a row of pieces: whole groups of eight chunks.
+__host__ __device__ constexpr int piece_pitch(int RP)
+{
+    return RP == 32 ? 128 : piece_row(RP);
+}
+
+// One chunk of tokens on its way from memory in a workgroup of 256: 64 rows of
+// 256 columns of a matrix, and the tokens' pieces.  Rows past the count are
+// zero.  Row numbers come from LDS, two chunks ahead, so that no wait for a
+// number or a piece stands behind the rows in flight (a wave's loads retire in
+// order).
+template <int RP>
+struct ChunkLoad {
+    static constexpr int PL = piece_row(RP), PP = piece_pitch(RP), NP = PL / 32;
+    uint4 v[8], u[NP];
+
+    __device__ __forceinline__ void load(const uint16_t *base, int64_t ld, int64_t col0, int64_t ncols,
+                                         const uint16_t *pieces, const int32_t *rows, int64_t count,
                                          int tid)
     {
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
+            const int at = 256 * i + tid, row = at / (PL / 8);
+            u[i] = make_uint4(0u, 0u, 0u, 0u);
+            if (row < count)
+                u[i] = *reinterpret_cast<const uint4 *>(
+                    pieces + static_cast<int64_t>(rows[row]) * PL + 8 * (at - row * (PL / 8)));
+        }
         const int64_t col = col0 + 8 * (tid & 31);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const int64_t row = 8 * i + (tid >> 5);
+            const int row = 8 * i + (tid >> 5);
             v[i] = make_uint4(0u, 0u, 0u, 0u);
             if (row < count && col < ncols)
-                v[i] = load8(base + static_cast<int64_t>(order[first + row]) * ld + col, ncols - col);
+                v[i] = load8(base + static_cast<int64_t>(rows[row]) * ld + col, ncols - col);
         }
     }
-    __device__ __forceinline__ void store(uint16_t *tile, int tid) const
+    __device__ __forceinline__ void store(uint16_t *tile, uint16_t *pieces, int tid) const
     {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int row = 8 * i + (tid >> 5);
-            *reinterpret_cast<uint4 *>(tile + row * 256 + (((tid & 31) ^ tile_key(row)) << 3)) = v[i];
+        for (int i = 0; i < NP; ++i) {
+            const int at = 256 * i + tid, row = at / (PL / 8);
+            *reinterpret_cast<uint4 *>(pieces + tile_at<PP, true>(row, at - row * (PL / 8))) = u[i];
         }
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            *reinterpret_cast<uint4 *>(tile + tile_at<256, false>(8 * i + (tid >> 5), tid & 31)) = v[i];
     }
 };
+
+// Walks a group's tokens 64 at a time through `tile` [64][256] and `pieces`
+// [64][PP] in LDS: f(chunk's token numbers, count) between barriers.  rows:
+// 2 x 64 numbers in LDS.
+template <int RP, typename F>
+__device__ __forceinline__ void for_each_chunk(const uint16_t *base, int64_t ld, int64_t col0, int64_t ncols,
+                                               const uint16_t *pieces, const int32_t *order, int64_t count,
+                                               uint16_t *tile, uint16_t *ptile, int32_t (&rows)[2][64],
+                                               int tid, F &&f)
+{
+    auto number = [&](int64_t c) { return tid < 64 && c + tid < count ? order[c + tid] : 0; };
+    if (tid < 64) {
+        rows[0][tid] = number(0);
+        rows[1][tid] = number(64);
+    }
+    __syncthreads();
+    ChunkLoad<RP> nxt;
+    nxt.load(base, ld, col0, ncols, pieces, rows[0], count, tid);
+    int32_t ahead = 0;
+    for (int64_t c = 0; c < count; c += 64) {
+        const int b = (c >> 6) & 1;
+        __syncthreads();  // the chunk before is read
+        if (c > 0 && tid < 64)
+            rows[b ^ 1][tid] = ahead;  // the chunk after this one
+        nxt.store(tile, ptile, tid);
+        __syncthreads();
+        ahead = number(c + 128);
+        if (c + 64 < count)
+            nxt.load(base, ld, col0, ncols, pieces, rows[b ^ 1], count - c - 64, tid);
+        f(rows[b], c, count - c);
+    }
+}
 
 __device__ __forceinline__ void store_f32x4(float *p, f32x4 v, int64_t n, bool add)
 {
@@ -753,31 +811,29 @@ template <int RP>
 __global__ __launch_bounds__(256) void lora_bwd_v_kernel(
     const uint16_t *__restrict__ g, int64_t ldg, int64_t M, int64_t V, LoraAdapters ad,
     const int32_t *__restrict__ offset, const int32_t *__restrict__ order,
-    const uint16_t *__restrict__ uT, int64_t Mp, float *__restrict__ tpart, float *__restrict__ dB,
-    int64_t lddb, int64_t stride_db, int accumulate, int64_t nvb)
+    const uint16_t *__restrict__ u3, float *__restrict__ tpart, float *__restrict__ dB, int64_t lddb,
+    int64_t stride_db, int accumulate, int64_t nvb)
 {
-    constexpr int JF = RP / 16, LDB = 256 + 8;
+    constexpr int JF = RP / 16, LDB = 256 + 8, PP = piece_pitch(RP);
     __shared__ __attribute__((aligned(16))) uint16_t sG[64 * 256];
+    __shared__ __attribute__((aligned(16))) uint16_t sU[64 * PP];
     __shared__ __attribute__((aligned(16))) uint16_t sBT[RP * LDB];
+    __shared__ int32_t rows[2][64];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int t16 = lane & 15, q = lane >> 4;
     const int64_t a = blockIdx.x / nvb, vb = blockIdx.x - a * nvb;
     const int64_t v0 = vb * 256;
     const int64_t o0 = offset[a], cnt = offset[a + 1] - o0;
-    const int64_t pp0 = group_base(o0, a);
     if (cnt == 0 && (accumulate || !dB))
         return;
 
-    TokenTile nxt;
-    if (cnt > 0)
-        nxt.load(g, ldg, order, o0, cnt, v0, V, tid);
     if (tpart && cnt > 0) {
         const int64_t v = v0 + tid;
         const uint16_t *pb = ad.B + a * ad.stride_b + v * ad.ldb;
 #pragma unroll
         for (int j = 0; j < RP; j += 8) {
-            const uint4 w = (v < V && j < ad.r) ? load8(pb + j, ad.r - j) : make_uint4(0u, 0u, 0u, 0u);
+            const uint4 w = v < V ? load8_row(pb, j, ad.r, v == V - 1) : make_uint4(0u, 0u, 0u, 0u);
             const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
             for (int e = 0; e < 8; ++e)
@@ -791,60 +847,53 @@ __global__ __launch_bounds__(256) void lora_bwd_v_kernel(
         for (int i = 0; i < 4; ++i)
             accB[jf][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 
-    for (int64_t c = 0; c < cnt; c += 64) {
-        __syncthreads();  // the tile of the chunk before is read
-        nxt.store(sG, tid);
-        __syncthreads();
-        if (c + 64 < cnt)
-            nxt.load(g, ldg, order, o0 + c + 64, cnt - c - 64, v0, V, tid);
-        if (tpart) {
-            // Ranks (rows) x this wave's 16 tokens, over the 256 columns.
-            f32x4 acc[JF];
+    if (cnt > 0)
+        for_each_chunk<RP>(
+            g, ldg, v0, V, u3, order + o0, cnt, sG, sU, rows, tid,
+            [&](const int32_t *toks, int64_t, int64_t left) {
+                if (tpart) {
+                    // Ranks (rows) x this wave's 16 tokens, over the 256 columns.
+                    f32x4 acc[JF];
 #pragma unroll
-            for (int jf = 0; jf < JF; ++jf)
-                acc[jf] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+                    for (int jf = 0; jf < JF; ++jf)
+                        acc[jf] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-            for (int s = 0; s < 8; ++s) {
-                const bf16x8 ft = tile_row_frag(sG, 16 * wave + t16, 32 * s + 8 * q);
+                    for (int s = 0; s < 8; ++s) {
+                        const bf16x8 ft = tile_row_frag<256, false>(sG, 16 * wave + t16, 32 * s + 8 * q);
 #pragma unroll
-                for (int jf = 0; jf < JF; ++jf)
-                    acc[jf] = mfma16(*reinterpret_cast<const bf16x8 *>(
-                                         sBT + (16 * jf + t16) * LDB + 32 * s + 8 * q),
-                                     ft, acc[jf]);
-            }
-            const int64_t at = c + 16 * wave + t16;
-            if (at < cnt) {
-                float *p = tpart + (vb * M + order[o0 + at]) * RP + 4 * q;
+                        for (int jf = 0; jf < JF; ++jf)
+                            acc[jf] = mfma16(*reinterpret_cast<const bf16x8 *>(
+                                                 sBT + (16 * jf + t16) * LDB + 32 * s + 8 * q),
+                                             ft, acc[jf]);
+                    }
+                    if (16 * wave + t16 < left) {
+                        float *p = tpart + (vb * M + toks[16 * wave + t16]) * RP + 4 * q;
 #pragma unroll
-                for (int jf = 0; jf < JF; ++jf)
-                    *reinterpret_cast<f32x4 *>(p + 16 * jf) = acc[jf];
-            }
-        }
-        if (dB) {
-            // Ranks (rows) x this wave's 64 columns, over the 64 tokens.
+                        for (int jf = 0; jf < JF; ++jf)
+                            *reinterpret_cast<f32x4 *>(p + 16 * jf) = acc[jf];
+                    }
+                }
+                if (dB) {
+                    // Ranks (rows) x this wave's 64 columns, over the 64 tokens.
 #pragma unroll
-            for (int ks = 0; ks < 2; ++ks) {
-                bf16x8 fg[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    fg[i] = tile_column_frag(sG, 32 * ks + 8 * q, 64 * wave + 16 * i, lane);
-                const int64_t at = c + 32 * ks + 8 * q;
-#pragma unroll
-                for (int jf = 0; jf < JF; ++jf)
-#pragma unroll
-                    for (int p = 0; p < 3; ++p) {
-                        uint4 w = *reinterpret_cast<const uint4 *>(
-                            uT + (p * RP + 16 * jf + t16) * Mp + pp0 + at);
-                        if (c + 64 > cnt)
-                            w = keep8(w, cnt - at);
-                        const bf16x8 fu = as_frag(w);
+                    for (int ks = 0; ks < 2; ++ks) {
+                        bf16x8 fg[4];
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
-                            accB[jf][i] = mfma16(fu, fg[i], accB[jf][i]);
+                            fg[i] = tile_column_frag<256, false>(sG, 32 * ks + 8 * q, 64 * wave + 16 * i, lane);
+#pragma unroll
+                        for (int jf = 0; jf < JF; ++jf)
+#pragma unroll
+                            for (int p = 0; p < 3; ++p) {
+                                const bf16x8 fu =
+                                    tile_column_frag<PP, true>(sU, 32 * ks + 8 * q, p * RP + 16 * jf, lane);
+#pragma unroll
+                                for (int i = 0; i < 4; ++i)
+                                    accB[jf][i] = mfma16(fu, fg[i], accB[jf][i]);
+                            }
                     }
-            }
-        }
-    }
+                }
+            });
     if (!dB)
         return;
 #pragma unroll
@@ -862,13 +911,10 @@ __global__ __launch_bounds__(256) void lora_bwd_v_kernel(
 }
 
 // t = s_a x the sum of its parts, in block order per lane and then by lane:
-// 16 lanes share one group of four ranks of one token.  Written as pieces in
-// rows (t3) and by rank and grouped position (tT).
+// 16 lanes share one group of four ranks of one token.  Written as pieces.
 __global__ __launch_bounds__(256) void lora_t_kernel(const float *__restrict__ tpart, int64_t nvb,
                                                      int64_t M, int RP, LoraAdapters ad,
-                                                     const int32_t *__restrict__ ppos,
-                                                     uint16_t *__restrict__ t3,
-                                                     uint16_t *__restrict__ tT, int64_t Mp)
+                                                     uint16_t *__restrict__ t3)
 {
     __shared__ f32x4 red[16][16];
     const int tid = threadIdx.x, col = tid & 15, part = tid >> 4;
@@ -894,158 +940,147 @@ __global__ __launch_bounds__(256) void lora_t_kernel(const float *__restrict__ t
     if (a < 0 || a >= ad.n)
         return;  // its parts were never written, and t is not read
     const float s = ad.scale ? ad.scale[a] : 1.0f;
+    uint32_t p[4][3];
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+        split3(j + e < ad.r ? sum[e] * s : 0.0f, p[e]);
     uint16_t *row = t3 + m * piece_row(RP) + j;
-    uint16_t *colp = tT + j * Mp + ppos[m];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        uint32_t p[3];
-        split3(j + e < ad.r ? sum[e] * s : 0.0f, p);
-#pragma unroll
-        for (int k = 0; k < 3; ++k) {
-            row[k * RP + e] = static_cast<uint16_t>(p[k]);
-            colp[(k * RP + e) * Mp] = static_cast<uint16_t>(p[k]);
-        }
-        if (RP == 16)
-            row[48 + e] = 0;
-    }
+    for (int k = 0; k < 3; ++k)
+        *reinterpret_cast<uint2 *>(row + k * RP) =
+            make_uint2(p[0][k] | (p[1][k] << 16), p[2][k] | (p[3][k] << 16));
+    if (RP == 16)
+        *reinterpret_cast<uint2 *>(row + 48) = make_uint2(0u, 0u);
 }
 
-// One workgroup per (256 columns of K, group): walks the group's tokens 64 at
-// a time; dX = t A from A_a's block in LDS, dA accumulated over the tokens from
-// one read of x.  The group of tokens on no adapter gets zeros in dX, that of
-// ids that are no adapter NaN.  Bound by writing dX.
+// dX and dA, 256 columns of K per workgroup.  The first nkb n workgroups
+// accumulate dA of one adapter over its tokens, 64 at a time, from one read of
+// x; the others write dX = t A of one chunk of up to 64 tokens, A_a's block in
+// LDS (tokens on no adapter get zeros, those whose id is none NaN).  One launch,
+// so that the two share the chip: dA has few workgroups, dX many short ones.
+// Bound by writing dX.
 template <int RP>
 __global__ __launch_bounds__(256) void lora_bwd_k_kernel(
     const uint16_t *__restrict__ x, int64_t ldx, int64_t K, LoraAdapters ad,
     const int32_t *__restrict__ offset, const int32_t *__restrict__ order,
-    const uint16_t *__restrict__ t3, const uint16_t *__restrict__ tT, int64_t Mp,
-    float *__restrict__ dX, int64_t lddx, float *__restrict__ dA, int64_t ldda, int64_t stride_da,
-    int accumulate, int64_t nkb)
+    const Chunk *__restrict__ chunks, const uint16_t *__restrict__ t3, float *__restrict__ dX,
+    int64_t lddx, float *__restrict__ dA, int64_t ldda, int64_t stride_da, int accumulate, int64_t nkb)
 {
-    constexpr int JF = RP / 16;
-    constexpr int U = RP < 32 ? 1 : RP / 32, S = piece_row(RP) / 32;
-    __shared__ __attribute__((aligned(16))) uint16_t sX[64 * 256];
-    __shared__ __attribute__((aligned(16))) uint16_t sA[RP * 256];
+    constexpr int JF = RP / 16, PP = piece_pitch(RP), PL = piece_row(RP);
+    constexpr int U = RP < 32 ? 1 : RP / 32, S = PL / 32;
+    constexpr int WIDE = RP > 64 ? RP * 256 : 64 * 256;  // x [64][256] or A [RP][256]
+    __shared__ __attribute__((aligned(16))) uint16_t wide[WIDE];
+    __shared__ __attribute__((aligned(16))) uint16_t pieces[64 * PP];
+    __shared__ __attribute__((aligned(16))) float turn[4][16 * 64];
+    __shared__ int32_t rows[2][64];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int t16 = lane & 15, q = lane >> 4;
-    const int64_t a = blockIdx.x / nkb, kb = blockIdx.x - a * nkb;
+    const int64_t unit = blockIdx.x / nkb, kb = blockIdx.x - unit * nkb;
     const int64_t k0 = kb * 256;
-    const int64_t o0 = offset[a], cnt = offset[a + 1] - o0;
-    if (a >= ad.n) {
-        if (!dX || (a == ad.n && accumulate))
+    const int64_t n_da = dA ? ad.n : 0;
+
+    if (unit < n_da) {
+        const int64_t a = unit;
+        const int64_t o0 = offset[a], cnt = offset[a + 1] - o0;
+        if (cnt == 0 && accumulate)
             return;
-        const float fill = a == ad.n ? 0.0f : NAN;
-        const int64_t k = k0 + 4 * lane;
-        for (int64_t i = wave; i < cnt; i += 4)
-            store_f32x4(dX + static_cast<int64_t>(order[o0 + i]) * lddx + k,
-                        f32x4{fill, fill, fill, fill}, K - k, false);
+        f32x4 acc[4][JF];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int jf = 0; jf < JF; ++jf)
+                acc[i][jf] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        if (cnt > 0)
+            for_each_chunk<RP>(
+                x, ldx, k0, K, t3, order + o0, cnt, wide, pieces, rows, tid,
+                [&](const int32_t *, int64_t, int64_t) {
+#pragma unroll
+                    for (int ks = 0; ks < 2; ++ks) {
+                        bf16x8 fx[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            fx[i] = tile_column_frag<256, false>(wide, 32 * ks + 8 * q, 64 * wave + 16 * i, lane);
+#pragma unroll
+                        for (int jf = 0; jf < JF; ++jf)
+#pragma unroll
+                            for (int p = 0; p < 3; ++p) {
+                                const bf16x8 ft =
+                                    tile_column_frag<PP, true>(pieces, 32 * ks + 8 * q, p * RP + 16 * jf, lane);
+#pragma unroll
+                                for (int i = 0; i < 4; ++i)
+                                    acc[i][jf] = mfma16(fx[i], ft, acc[i][jf]);
+                            }
+                    }
+                });
+#pragma unroll
+        for (int jf = 0; jf < JF; ++jf) {
+            const int j = 16 * jf + t16;
+            if (j >= ad.r)
+                continue;
+            float *p = dA + a * stride_da + j * ldda;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int64_t k = k0 + 64 * wave + 16 * i + 4 * q;
+                store_f32x4(p + k, acc[i][jf], K - k, accumulate != 0);
+            }
+        }
         return;
     }
-    const int64_t pp0 = group_base(o0, a);
-    if (cnt == 0 && (accumulate || !dA))
-        return;
 
-    TokenTile nxt;
-    if (dA && cnt > 0)
-        nxt.load(x, ldx, order, o0, cnt, k0, K, tid);
-    if (dX && cnt > 0) {
+    const Chunk ch = chunks[unit - n_da];
+    if (ch.group < 0 || (ch.group == ad.n && accumulate))
+        return;
+    const int64_t kw = k0 + 64 * wave + 4 * t16;  // this lane's columns of a row piece
+    if (ch.group >= ad.n) {
+        const float fill = ch.group == ad.n ? 0.0f : NAN;
+        for (int i = q; i < ch.count; i += 4)
+            store_f32x4(dX + static_cast<int64_t>(order[ch.first + i]) * lddx + kw,
+                        f32x4{fill, fill, fill, fill}, K - kw, false);
+        return;
+    }
+    const int64_t a = ch.group;
+    if (tid < 64)
+        rows[0][tid] = tid < ch.count ? order[ch.first + tid] : 0;
+    {
         const int64_t col = k0 + 8 * (tid & 31);
-        for (int j = tid >> 5; j < RP; j += 8) {
-            const uint4 w = (j < ad.r && col < K)
-                                ? load8(ad.A + a * ad.stride_a + j * ad.lda + col, K - col)
-                                : make_uint4(0u, 0u, 0u, 0u);
-            *reinterpret_cast<uint4 *>(sA + j * 256 + (((tid & 31) ^ tile_key(j)) << 3)) = w;
+        const uint16_t *pa = ad.A + a * ad.stride_a;
+#pragma unroll
+        for (int i = 0; i < RP / 8; ++i) {
+            const int j = 8 * i + (tid >> 5);
+            const uint4 w = (j < ad.r && col < K) ? load8(pa + j * ad.lda + col, K - col)
+                                                  : make_uint4(0u, 0u, 0u, 0u);
+            *reinterpret_cast<uint4 *>(wide + tile_at<256, false>(j, tid & 31)) = w;
         }
     }
-    f32x4 accA[4][JF];
+    __syncthreads();
+    bf16x8 fa[U][4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int uu = 0; uu < U; ++uu)
 #pragma unroll
-        for (int jf = 0; jf < JF; ++jf)
-            accA[i][jf] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-
-    for (int64_t c = 0; c < cnt; c += 64) {
-        __syncthreads();
-        if (dA)
-            nxt.store(sX, tid);
-        __syncthreads();
-        if (dA && c + 64 < cnt)
-            nxt.load(x, ldx, order, o0 + c + 64, cnt - c - 64, k0, K, tid);
-        if (dX) {
-            // This wave's 64 columns (rows) x 16 tokens at a time.
+        for (int i = 0; i < 4; ++i)
+            fa[uu][i] = tile_column_frag<256, false>(wide, RP == 16 ? 8 * (q & 1) : 32 * uu + 8 * q,
+                                                     64 * wave + 16 * i, lane);
+    // This wave's 64 columns (rows) x 16 tokens at a time.
+    for (int t0 = 0; t0 < ch.count; t0 += 16) {
+        const uint16_t *pt = t3 + static_cast<int64_t>(rows[0][min(t0 + t16, ch.count - 1)]) * PL + 8 * q;
+        f32x4 d[4];
 #pragma unroll
-            for (int tf = 0; tf < 4; ++tf) {
-                const int64_t at = c + 16 * tf + t16;
-                if (c + 16 * tf >= cnt)
-                    break;
-                const int64_t m = order[o0 + min(at, cnt - 1)];
-                const uint16_t *pt = t3 + m * piece_row(RP) + 8 * q;
-                f32x4 acc[4];
+        for (int i = 0; i < 4; ++i)
+            d[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    acc[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        for (int s = 0; s < S; ++s) {
+            const bf16x8 ft = as_frag(*reinterpret_cast<const uint4 *>(pt + 32 * s));
 #pragma unroll
-                for (int uu = 0; uu < U; ++uu) {
-                    const int p = RP == 16 ? 8 * (q & 1) : 32 * uu + 8 * q;
-                    bf16x8 fa[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        fa[i] = tile_column_frag(sA, p, 64 * wave + 16 * i, lane);
-#pragma unroll
-                    for (int s = uu; s < S; s += U) {
-                        const bf16x8 ft = as_frag(*reinterpret_cast<const uint4 *>(pt + 32 * s));
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            acc[i] = mfma16(fa[i], ft, acc[i]);
-                    }
-                }
-                if (at < cnt) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int64_t k = k0 + 64 * wave + 16 * i + 4 * q;
-                        store_f32x4(dX + m * lddx + k, acc[i], K - k, accumulate != 0);
-                    }
-                }
-            }
+            for (int i = 0; i < 4; ++i)
+                d[i] = mfma16(fa[s % U][i], ft, d[i]);
         }
-        if (dA) {
+        turn_rows(d, turn[wave], t16, q);
 #pragma unroll
-            for (int ks = 0; ks < 2; ++ks) {
-                bf16x8 fx[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    fx[i] = tile_column_frag(sX, 32 * ks + 8 * q, 64 * wave + 16 * i, lane);
-                const int64_t at = c + 32 * ks + 8 * q;
-#pragma unroll
-                for (int jf = 0; jf < JF; ++jf)
-#pragma unroll
-                    for (int p = 0; p < 3; ++p) {
-                        uint4 w = *reinterpret_cast<const uint4 *>(
-                            tT + (p * RP + 16 * jf + t16) * Mp + pp0 + at);
-                        if (c + 64 > cnt)
-                            w = keep8(w, cnt - at);
-                        const bf16x8 ft = as_frag(w);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            accA[i][jf] = mfma16(fx[i], ft, accA[i][jf]);
-                    }
-            }
-        }
-    }
-    if (!dA)
-        return;
-#pragma unroll
-    for (int jf = 0; jf < JF; ++jf) {
-        const int j = 16 * jf + t16;
-        if (j >= ad.r)
-            continue;
-        float *p = dA + a * stride_da + j * ldda;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int64_t k = k0 + 64 * wave + 16 * i + 4 * q;
-            store_f32x4(p + k, accA[i][jf], K - k, accumulate != 0);
-        }
+        for (int i = 0; i < 4; ++i)
+            if (t0 + 4 * i + q < ch.count)
+                store_f32x4(dX + static_cast<int64_t>(rows[0][t0 + 4 * i + q]) * lddx + kw, d[i], K - kw,
+                            accumulate != 0);
     }
 }
 
@@ -1059,24 +1094,16 @@ int64_t round256(int64_t b)
     return (b + 255) / 256 * 256;
 }
 
-// Grouped positions: every group starts at a multiple of 64 (group_base).
-int64_t grouped_length(int64_t M, int64_t n)
-{
-    return M / 64 * 64 + 64 * (n + 1);
-}
-
 hipError_t launch_shrink(const uint16_t *x, int64_t ldx, int64_t M, int64_t K, const LoraAdapters &ad,
-                         uint16_t *u3, uint16_t *uT, int64_t Mp, const int32_t *ppos, FewGroups *table,
-                         hipStream_t s)
+                         uint16_t *u3, FewGroups *table, hipStream_t s)
 {
     const int RP = rank_bucket(ad.r);
-    const ShrinkOut o = {u3, uT, Mp, ppos, RP};
     const int64_t zr = RP / 16;
     if (M <= kFewTokens) {
         // One workgroup per group there can be (n adapters, none, no adapter).
         const dim3 grid(static_cast<unsigned>(std::min<int64_t>(ad.n + 2, M)), static_cast<unsigned>(zr));
-        hipLaunchKernelGGL(lora_shrink_few_kernel, grid, dim3(kShrinkThreads), 0, s, x, ldx, M, K, ad, o,
-                           table);
+        hipLaunchKernelGGL(lora_shrink_few_kernel, grid, dim3(kShrinkThreads), 0, s, x, ldx, M, K, ad, RP,
+                           u3, table);
         return hipGetLastError();
     }
     if (ad.n == 0)
@@ -1089,7 +1116,8 @@ hipError_t launch_shrink(const uint16_t *x, int64_t ldx, int64_t M, int64_t K, c
     for (int64_t b0 = 0; b0 < blocks; b0 += most) {
         const dim3 grid(static_cast<unsigned>(std::min(most, blocks - b0)), static_cast<unsigned>(slots),
                         static_cast<unsigned>(zr));
-        hipLaunchKernelGGL(lora_shrink_kernel, grid, dim3(kShrinkThreads), 0, s, x, ldx, M, K, ad, b0, o);
+        hipLaunchKernelGGL(lora_shrink_kernel, grid, dim3(kShrinkThreads), 0, s, x, ldx, M, K, ad, b0, RP,
+                           u3);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess)
             return e;
@@ -1146,20 +1174,26 @@ hipError_t launch_expand(const float *z, int64_t ldz, void *out, int64_t ldo, bo
 
 // The gradients' workspace, in order.
 struct BwdLayout {
-    int64_t offset, order, ppos, uT, t3, tT, tpart, end;
+    int64_t offset, order, chunks, u3, t3, tpart, end;
 };
+
+// Numbers of chunks: every group's start at chunk_base.
+int64_t chunk_numbers(int64_t M, int64_t n)
+{
+    return chunk_base(M, n + 2);
+}
 
 BwdLayout bwd_layout(int64_t M, int64_t V, int64_t r, int64_t n)
 {
-    const int64_t RP = rank_bucket(r), Mp = grouped_length(M, n), nvb = (V + 255) / 256;
+    const int64_t RP = rank_bucket(r), nvb = (V + 255) / 256;
+    const int64_t pieces = round256(2 * piece_row(static_cast<int>(RP)) * M);
     BwdLayout l;
     l.offset = 0;
     l.order = l.offset + round256(4 * (n + 3));
-    l.ppos = l.order + round256(4 * M);
-    l.uT = l.ppos + round256(4 * M);
-    l.t3 = l.uT + round256(2 * 3 * RP * Mp);
-    l.tT = l.t3 + round256(2 * piece_row(static_cast<int>(RP)) * M);
-    l.tpart = l.tT + round256(2 * 3 * RP * Mp);
+    l.chunks = l.order + round256(4 * M);
+    l.u3 = l.chunks + round256(static_cast<int64_t>(sizeof(Chunk)) * chunk_numbers(M, n));
+    l.t3 = l.u3 + pieces;
+    l.tpart = l.t3 + pieces;
     l.end = l.tpart + round256(4 * nvb * M * RP);
     return l;
 }
@@ -1171,7 +1205,7 @@ hipError_t launch_bwd_v(const LoraBwd &p, const BwdLayout &l, char *ws, hipStrea
     hipLaunchKernelGGL((lora_bwd_v_kernel<RP>), dim3(static_cast<unsigned>(nvb * p.ad.n)), dim3(256), 0, s,
                        p.g, p.ldg, p.M, p.V, p.ad, reinterpret_cast<const int32_t *>(ws + l.offset),
                        reinterpret_cast<const int32_t *>(ws + l.order),
-                       reinterpret_cast<const uint16_t *>(ws + l.uT), grouped_length(p.M, p.ad.n),
+                       reinterpret_cast<const uint16_t *>(ws + l.u3),
                        (p.dX || p.dA) ? reinterpret_cast<float *>(ws + l.tpart) : nullptr, p.dB, p.lddb,
                        p.stride_db, p.accumulate ? 1 : 0, nvb);
     return hipGetLastError();
@@ -1181,12 +1215,13 @@ template <int RP>
 hipError_t launch_bwd_k(const LoraBwd &p, const BwdLayout &l, char *ws, hipStream_t s)
 {
     const int64_t nkb = (p.K + 255) / 256;
-    hipLaunchKernelGGL((lora_bwd_k_kernel<RP>), dim3(static_cast<unsigned>(nkb * (p.ad.n + 2))), dim3(256),
-                       0, s, p.x, p.ldx, p.K, p.ad, reinterpret_cast<const int32_t *>(ws + l.offset),
+    const int64_t units = (p.dA ? p.ad.n : 0) + (p.dX ? chunk_numbers(p.M, p.ad.n) : 0);
+    hipLaunchKernelGGL((lora_bwd_k_kernel<RP>), dim3(static_cast<unsigned>(nkb * units)), dim3(256), 0, s,
+                       p.x, p.ldx, p.K, p.ad, reinterpret_cast<const int32_t *>(ws + l.offset),
                        reinterpret_cast<const int32_t *>(ws + l.order),
-                       reinterpret_cast<const uint16_t *>(ws + l.t3),
-                       reinterpret_cast<const uint16_t *>(ws + l.tT), grouped_length(p.M, p.ad.n), p.dX,
-                       p.lddx, p.dA, p.ldda, p.stride_da, p.accumulate ? 1 : 0, nkb);
+                       reinterpret_cast<const Chunk *>(ws + l.chunks),
+                       reinterpret_cast<const uint16_t *>(ws + l.t3), p.dX, p.lddx, p.dA, p.ldda,
+                       p.stride_da, p.accumulate ? 1 : 0, nkb);
     return hipGetLastError();
 }
 
@@ -1222,7 +1257,7 @@ hipError_t launch_logits_lora(const GemmProblem &p, bool bf16, const LoraAdapter
         f.ldd = (V + 3) / 4 * 4;
     }
     f.stream_out = false;  // read back at once
-    hipError_t e = launch_shrink(p.B, p.ldb, M, K, ad, u3, nullptr, 0, nullptr, table, s);
+    hipError_t e = launch_shrink(p.B, p.ldb, M, K, ad, u3, table, s);
     if (e == hipSuccess)
         e = launch_gemm_logits(f, Epi::kStoreF32, s);
     if (e != hipSuccess)
@@ -1241,16 +1276,14 @@ hipError_t launch_lora_bwd(const LoraBwd &p, void *workspace, hipStream_t s)
     const BwdLayout l = bwd_layout(p.M, p.V, p.ad.r, p.ad.n);
     char *ws = static_cast<char *>(workspace);
     const int RP = rank_bucket(p.ad.r);
-    int32_t *offset = reinterpret_cast<int32_t *>(ws + l.offset);
-    int32_t *order = reinterpret_cast<int32_t *>(ws + l.order);
-    int32_t *ppos = reinterpret_cast<int32_t *>(ws + l.ppos);
-    const int64_t Mp = grouped_length(p.M, p.ad.n), nvb = (p.V + 255) / 256;
+    uint16_t *t3 = reinterpret_cast<uint16_t *>(ws + l.t3);
+    const int64_t nvb = (p.V + 255) / 256;
     hipLaunchKernelGGL(lora_group_kernel, dim3(static_cast<unsigned>(p.ad.n + 2)), dim3(256), 0, s,
-                       p.ad.adapter, p.M, p.ad.n, offset, order, ppos);
+                       p.ad.adapter, p.M, p.ad.n, reinterpret_cast<int32_t *>(ws + l.offset),
+                       reinterpret_cast<int32_t *>(ws + l.order), reinterpret_cast<Chunk *>(ws + l.chunks));
     hipError_t e = hipGetLastError();
     if (e == hipSuccess && p.dB && p.ad.n > 0 && p.M > 0)
-        e = launch_shrink(p.x, p.ldx, p.M, p.K, p.ad, nullptr, reinterpret_cast<uint16_t *>(ws + l.uT), Mp,
-                          ppos, nullptr, s);
+        e = launch_shrink(p.x, p.ldx, p.M, p.K, p.ad, reinterpret_cast<uint16_t *>(ws + l.u3), nullptr, s);
     if (e == hipSuccess && p.ad.n > 0 && p.V > 0) {
         switch (RP) {
         case 16: e = launch_bwd_v<16>(p, l, ws, s); break;
@@ -1264,9 +1297,7 @@ hipError_t launch_lora_bwd(const LoraBwd &p, void *workspace, hipStream_t s)
     if (p.ad.n > 0 && p.M > 0) {
         const int64_t n4 = p.M * RP / 4;
         hipLaunchKernelGGL(lora_t_kernel, dim3(static_cast<unsigned>((n4 + 15) / 16)), dim3(256), 0, s,
-                           reinterpret_cast<const float *>(ws + l.tpart), nvb, p.M, RP, p.ad, ppos,
-                           reinterpret_cast<uint16_t *>(ws + l.t3),
-                           reinterpret_cast<uint16_t *>(ws + l.tT), Mp);
+                           reinterpret_cast<const float *>(ws + l.tpart), nvb, p.M, RP, p.ad, t3);
         e = hipGetLastError();
         if (e != hipSuccess)
             return e;
