@@ -394,18 +394,19 @@ int32_t lmhead_wgrad(const void *dlogits, int64_t ldd, const void *x, int64_t ld
  *           none (the row equals lmhead_logits' up to rounding).  A value >=
  *           n_adapters cannot be reported from the kernel: that row is NaN.
  *  scale    FP32 [n_adapters] or NULL (1).
- *  rank     1 .. 128, n_adapters >= 0.
+ *  rank     1 .. 128, n_adapters >= 0 (at most 2^23 - 2), M <= 2^22.
  *  One token's result depends on its own x and adapter only: a NaN or infinity
  *  in another token or another adapter of the batch does not reach it.
  *  A x is an FP32 sum and enters the second product unrounded (in three BF16
  *  pieces of 8 bits).
  *  workspace: device memory of at least lmhead_logits_lora_workspace_bytes(M,
- *  V, rank, out_dtype) bytes (negative LMH_ERR_* for bad sizes), 16-byte
+ *  K, V, rank, out_dtype) bytes (negative LMH_ERR_* for bad sizes), 16-byte
  *  aligned; its contents do not matter on entry.  Two calls that share one
  *  must be ordered on one stream.  out and workspace must not overlap each
  *  other or an input.
  */
-int64_t lmhead_logits_lora_workspace_bytes(int64_t M, int64_t V, int64_t rank, int32_t out_dtype);
+int64_t lmhead_logits_lora_workspace_bytes(int64_t M, int64_t K, int64_t V, int64_t rank,
+                                           int32_t out_dtype);
 int32_t lmhead_logits_lora(const void *x, int64_t ldx, const void *W, int64_t ldw, const void *A,
                            int64_t lda, int64_t stride_a, const void *B, int64_t ldb,
                            int64_t stride_b, const int32_t *adapter, const float *scale,

@@ -65,7 +65,7 @@ _SIGNATURES = {
                          _vp], _i32),
     "lmhead_dgrad_noalloc": ([_vp, _i64, _vp, _i64, _vp, _i64, _i32, _i64, _i64, _i64, _i32,
                               _vp], _i32),
-    "lmhead_logits_lora_workspace_bytes": ([_i64, _i64, _i64, _i32], _i64),
+    "lmhead_logits_lora_workspace_bytes": ([_i64, _i64, _i64, _i64, _i32], _i64),
     "lmhead_logits_lora": ([_vp, _i64, _vp, _i64, _vp, _i64, _i64, _vp, _i64, _i64, _vp, _vp, _i64,
                             _i64, _vp, _i64, _i32, _i64, _i64, _i64, _vp, _i64, _vp], _i32),
     "lmhead_lora_bwd_workspace_bytes": ([_i64, _i64, _i64, _i64, _i64], _i64),
@@ -604,9 +604,9 @@ def _adapter_args(x, A, B, adapter, scale, V):
     return (pa, lda, sa, pb, ldb, sb, pi, ps, n, r)
 
 
-def lmhead_logits_lora_workspace_bytes(M, V, rank, out_dtype="fp32"):
+def lmhead_logits_lora_workspace_bytes(M, K, V, rank, out_dtype="fp32"):
     """Workspace bytes lmhead_logits_lora needs."""
-    need = int(lib().lmhead_logits_lora_workspace_bytes(int(M), int(V), int(rank), _dtype_code(out_dtype)))
+    need = int(lib().lmhead_logits_lora_workspace_bytes(int(M), int(K), int(V), int(rank), _dtype_code(out_dtype)))
     if need < 0:
         _check("lmhead_logits_lora_workspace_bytes", -need)
     return need
@@ -636,7 +636,7 @@ def lmhead_logits_lora(x, W, A, B, adapter, scale=None, out=None, out_dtype=None
     po, ldo = _mat(out, "out", out.dtype)
     if out.shape != (M, V):
         raise ValueError("out must be [M, V]")
-    ws, nbytes = _workspace("lmhead_logits_lora", lmhead_logits_lora_workspace_bytes(M, V, ad[9], code),
+    ws, nbytes = _workspace("lmhead_logits_lora", lmhead_logits_lora_workspace_bytes(M, K, V, ad[9], code),
                             workspace, x, stream)
     _check("lmhead_logits_lora",
            lib().lmhead_logits_lora(px, ldx, pw, ldw, *ad, po, ldo, code, M, K, V, ws.data_ptr(), nbytes,

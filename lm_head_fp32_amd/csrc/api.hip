@@ -255,20 +255,21 @@ Span bytes_span(const void *p, int64_t bytes)
     return span_of(p, 1, bytes, bytes, 1);
 }
 
-// Sizes shared by the adapter calls.
+// Sizes shared by the adapter calls: 4 work-items per rank of every token in
+// one launch.
 bool adapter_sizes_ok(int64_t M, int64_t K, int64_t V, int64_t rank, int64_t n)
 {
-    return M >= 0 && K >= 0 && V >= 0 && M <= kMaxDim && K <= kMaxDim && V <= kMaxDim && rank >= 1 &&
-           rank <= kMaxRank && n >= 0 && n <= (kMaxLaunchItems / 256) - 2;
+    return M >= 0 && K >= 0 && V >= 0 && M <= kMaxLaunchItems / (4 * kMaxRank) && K <= kMaxDim &&
+           V <= kMaxDim && rank >= 1 && rank <= kMaxRank && n >= 0 && n <= (kMaxLaunchItems / 256) - 2;
 }
 
 // The gradients' launches: one workgroup of 256 per (256 columns, adapter or
-// chunk of 64 tokens), and 4 work-items per rank of every token.
-bool lora_bwd_fits(int64_t M, int64_t K, int64_t V, int64_t rank, int64_t n)
+// chunk of 64 tokens).
+bool lora_bwd_fits(int64_t M, int64_t K, int64_t V, int64_t n)
 {
     const int64_t most = kMaxLaunchItems / 256;
     return ceil_div(V, 256) <= most / std::max<int64_t>(n, 1) &&
-           ceil_div(K, 256) <= most / (2 * n + M / 64 + 2) && M <= kMaxLaunchItems / (4 * kMaxRank);
+           ceil_div(K, 256) <= most / (2 * n + M / 64 + 2);
 }
 
 constexpr int64_t kMaxBeams = 64;
@@ -717,13 +718,14 @@ int32_t lmhead_wgrad(const void *dlogits, int64_t ldd, const void *x, int64_t ld
         static_cast<hipStream_t>(stream)));
 }
 
-int64_t lmhead_logits_lora_workspace_bytes(int64_t M, int64_t V, int64_t rank, int32_t out_dtype)
+int64_t lmhead_logits_lora_workspace_bytes(int64_t M, int64_t K, int64_t V, int64_t rank,
+                                           int32_t out_dtype)
 {
     if (check_dtype_out(out_dtype) != LMH_OK)
         return -static_cast<int64_t>(LMH_ERR_DTYPE);
-    if (!adapter_sizes_ok(M, 0, V, rank, 0) || !span_fits(M, V + 3, V + 3))
+    if (!adapter_sizes_ok(M, K, V, rank, 0) || !span_fits(M, V + 3, V + 3))
         return -static_cast<int64_t>(LMH_ERR_SHAPE);
-    return lmh::lora_logits_workspace_bytes(M, V, rank, out_dtype == LMH_BF16);
+    return lmh::lora_logits_workspace_bytes(M, K, V, rank, out_dtype == LMH_BF16);
 }
 
 int32_t lmhead_logits_lora(const void *x, int64_t ldx, const void *W, int64_t ldw, const void *A,
@@ -749,7 +751,7 @@ int32_t lmhead_logits_lora(const void *x, int64_t ldx, const void *W, int64_t ld
         return LMH_ERR_NULL;
     if (!aligned4(adapter) || (scale && !aligned4(scale)) || !aligned16(workspace))
         return LMH_ERR_ALIGN;
-    const int64_t need = lmh::lora_logits_workspace_bytes(M, V, rank, bf16);
+    const int64_t need = lmh::lora_logits_workspace_bytes(M, K, V, rank, bf16);
     if (workspace_bytes < need || !gemm_grid_fits(V, M, false))
         return LMH_ERR_SHAPE;
     const Span outs[] = {span_of(out, M, V, ldo, osz), bytes_span(workspace, need)};
@@ -785,10 +787,10 @@ int32_t lmhead_logits_lora(const void *x, int64_t ldx, const void *W, int64_t ld
 int64_t lmhead_lora_bwd_workspace_bytes(int64_t M, int64_t K, int64_t V, int64_t rank,
                                         int64_t n_adapters)
 {
-    if (!adapter_sizes_ok(M, K, V, rank, n_adapters) || !lora_bwd_fits(M, K, V, rank, n_adapters) ||
+    if (!adapter_sizes_ok(M, K, V, rank, n_adapters) || !lora_bwd_fits(M, K, V, n_adapters) ||
         !span_fits(M, V + 3, V + 3))
         return -static_cast<int64_t>(LMH_ERR_SHAPE);
-    return lmh::lora_bwd_workspace_bytes(M, V, rank, n_adapters);
+    return lmh::lora_bwd_workspace_bytes(M, K, V, rank, n_adapters);
 }
 
 int32_t lmhead_lora_bwd(const void *dlogits, int64_t ldd, const void *x, int64_t ldx, const void *A,
@@ -798,7 +800,7 @@ int32_t lmhead_lora_bwd(const void *dlogits, int64_t ldd, const void *x, int64_t
                         float *dB, int64_t lddb, int64_t stride_db, int32_t accumulate, int64_t M,
                         int64_t K, int64_t V, void *workspace, int64_t workspace_bytes, void *stream)
 {
-    if (!adapter_sizes_ok(M, K, V, rank, n_adapters) || !lora_bwd_fits(M, K, V, rank, n_adapters) ||
+    if (!adapter_sizes_ok(M, K, V, rank, n_adapters) || !lora_bwd_fits(M, K, V, n_adapters) ||
         workspace_bytes < 0 || !span_fits(M, V + 3, V + 3))
         return LMH_ERR_SHAPE;
     if (!dX && !dA && !dB)
@@ -817,7 +819,7 @@ int32_t lmhead_lora_bwd(const void *dlogits, int64_t ldd, const void *x, int64_t
         return LMH_ERR_NULL;
     if (!aligned4(adapter) || (scale && !aligned4(scale)) || !aligned16(workspace))
         return LMH_ERR_ALIGN;
-    const int64_t need = lmh::lora_bwd_workspace_bytes(M, V, rank, n_adapters);
+    const int64_t need = lmh::lora_bwd_workspace_bytes(M, K, V, rank, n_adapters);
     if (workspace_bytes < need)
         return LMH_ERR_SHAPE;
     const Span outs[] = {bytes_span(workspace, need), span_of(dX, dX ? M : 0, K, lddx, 4),

@@ -149,8 +149,8 @@ struct LoraBwd {
     int64_t M, K, V;
 };
 
-int64_t lora_logits_workspace_bytes(int64_t M, int64_t V, int64_t r, bool bf16);
-int64_t lora_bwd_workspace_bytes(int64_t M, int64_t V, int64_t r, int64_t n);
+int64_t lora_logits_workspace_bytes(int64_t M, int64_t K, int64_t V, int64_t r, bool bf16);
+int64_t lora_bwd_workspace_bytes(int64_t M, int64_t K, int64_t V, int64_t r, int64_t n);
 // p as for launch_gemm_logits (R = V, C = M, P = K), with D the final logits.
 hipError_t launch_logits_lora(const GemmProblem &p, bool bf16, const LoraAdapters &ad, void *workspace,
                               hipStream_t s);

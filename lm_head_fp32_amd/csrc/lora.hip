@@ -109,30 +109,30 @@ __host__ __device__ constexpr int piece_row(int RP)
 // workgroups.
 constexpr int kFewTokens = 256;
 
-// The groups of such a batch, in order of first use: group g holds adapter
-// g[].id's tokens order[start .. start + count), ascending; count 0 past the
-// last.  Tokens on none form a group of id -1, all those whose id is no adapter
-// one of id n.
-struct FewGroup {
-    int32_t id, start, count, pad;
+// Such a batch in units of up to 16 tokens of one adapter: unit i holds tokens
+// order[first .. first + count), ascending, of adapter id; count 0 past the
+// last unit.  Tokens on none form units of id -1, all those whose id is no
+// adapter units of id n.
+struct FewUnit {
+    int32_t id, first, count, pad;
 };
-struct FewGroups {
-    FewGroup g[kFewTokens];
+struct FewUnits {
+    FewUnit u[kFewTokens];
     int32_t order[kFewTokens];
 };
 
 // Fills `t` (LDS) from the ids; 1024 threads.  Every token's id is compared with
 // all others, a quarter of them per thread (walking the distinct ids one after
 // another took 0.5 us each).
-__device__ __forceinline__ void group_few(const LoraAdapters &ad, int64_t M, FewGroups &t, int tid)
+__device__ __forceinline__ void group_few(const LoraAdapters &ad, int64_t M, FewUnits &t, int tid)
 {
     __shared__ __attribute__((aligned(16))) int32_t ids[kFewTokens];
     __shared__ int32_t cnt[4][kFewTokens], ahead[4][kFewTokens], first[4][kFewTokens];
-    __shared__ int32_t lead_start[kFewTokens], sums[4];
+    __shared__ int32_t lead_start[kFewTokens], sums[2][4];
     if (tid < kFewTokens) {
         const int32_t v = tid < M ? ad.adapter[tid] : 0;
         ids[tid] = tid >= M ? -2 : v < 0 ? -1 : v >= ad.n ? static_cast<int32_t>(ad.n) : v;
-        t.g[tid] = FewGroup{-1, 0, 0, 0};
+        t.u[tid] = FewUnit{-1, 0, 0, 0};
     }
     __syncthreads();
     const int m = tid & (kFewTokens - 1), part = tid / kFewTokens, lane = tid & 63;
@@ -152,56 +152,53 @@ __device__ __forceinline__ void group_few(const LoraAdapters &ad, int64_t M, Few
     }
     cnt[part][m] = c, ahead[part][m] = before, first[part][m] = f;
     __syncthreads();
-    int lead = 0, excl = 0;
+    // Two scans in token order: the tokens of groups that began earlier (at a
+    // group's first token), and the units that began earlier (at every 16th
+    // token of a group).
+    int lead = 0, unit = 0, lead_sum = 0, unit_sum = 0;
     if (tid < kFewTokens) {
         c = cnt[0][m] + cnt[1][m] + cnt[2][m] + cnt[3][m];
         before = ahead[0][m] + ahead[1][m] + ahead[2][m] + ahead[3][m];
         f = min(min(first[0][m], first[1][m]), min(first[2][m], first[3][m]));
-        // Scan over the groups' first tokens: tokens in the upper half, groups
-        // in the lower.
-        lead = id != -2 && before == 0 ? (c << 16) | 1 : 0;
-        int incl = lead;
+        lead_sum = lead = id != -2 && before == 0 ? c : 0;
+        unit_sum = unit = id != -2 && before % 16 == 0 ? 1 : 0;
 #pragma unroll
         for (int off = 1; off < 64; off <<= 1) {
-            const int o = __shfl_up(incl, off, 64);
-            incl += lane >= off ? o : 0;
+            const int ol = __shfl_up(lead_sum, off, 64), ou = __shfl_up(unit_sum, off, 64);
+            lead_sum += lane >= off ? ol : 0;
+            unit_sum += lane >= off ? ou : 0;
         }
-        excl = incl - lead;
         if (lane == 63)
-            sums[tid >> 6] = incl;
+            sums[0][tid >> 6] = lead_sum, sums[1][tid >> 6] = unit_sum;
     }
     __syncthreads();
     if (tid < kFewTokens) {
+        lead_sum -= lead, unit_sum -= unit;
         for (int w = 0; w < (tid >> 6); ++w)
-            excl += sums[w];
-        if (lead) {
-            const int g = excl & 0xffff;
-            t.g[g] = FewGroup{id, excl >> 16, c, 0};
-            lead_start[m] = excl >> 16;
-        }
+            lead_sum += sums[0][w], unit_sum += sums[1][w];
+        if (lead)
+            lead_start[m] = lead_sum;
     }
     __syncthreads();
-    if (tid < kFewTokens && id != -2)
-        t.order[lead_start[f] + before] = m;
+    if (tid < kFewTokens && id != -2) {
+        const int at = lead_start[f] + before;
+        t.order[at] = m;
+        if (unit)
+            t.u[unit_sum] = FewUnit{id, at, min(16, c - before), 0};
+    }
     __syncthreads();
 }
 
 // ---------------------------------------------------------------------------
-// u = s_a A_a x for 16 tokens of one adapter and 16 of its ranks.  The 16 waves
-// split K and are summed in order through LDS.  Latency-bound (a few hundred
-// KiB per workgroup), so all of K runs in one workgroup: a second launch to
-// join parts would cost more.  Written as pieces, rows [token][piece_row].
-constexpr int kShrinkThreads = 1024;
-
-// This wave's part of the 16 x 16 result: rows of A from pa (lane's row, its
-// eight columns of a step), of x from px.
-__device__ __forceinline__ f32x4 shrink_wave(const uint16_t *pa, const uint16_t *px, int64_t K, int wave,
-                                             int q)
+// u = s_a A_a x, 16 tokens by 16 ranks at a time; NW waves of a workgroup split
+// K and are summed in order through LDS.  Written as pieces, rows
+// [token][piece_row].
+//
+// The wave's part of the 16 x 16 result over K range [k, kend) (k a multiple of
+// 32): pa and px point at the lane's row, its eight columns of a step.
+__device__ __forceinline__ f32x4 shrink_wave(const uint16_t *pa, const uint16_t *px, int64_t k, int64_t kend,
+                                             int64_t K, int q)
 {
-    constexpr int NW = kShrinkThreads / 64;
-    const int64_t per_wave = (K + 32 * NW - 1) / (32 * NW) * 32;
-    int64_t k = wave * per_wave;
-    const int64_t kend = min(K, k + per_wave);
     f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
     for (; k + 256 <= kend; k += 256) {
         uint4 va[8], vx[8];
@@ -215,6 +212,17 @@ __device__ __forceinline__ f32x4 shrink_wave(const uint16_t *pa, const uint16_t 
         for (int i = 0; i < 8; ++i)
             acc = mfma16(as_frag(va[i]), as_frag(vx[i]), acc);
     }
+    for (; k + 64 <= kend; k += 64) {
+        uint4 va[2], vx[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            va[i] = *reinterpret_cast<const uint4 *>(pa + k + 32 * i);
+            vx[i] = *reinterpret_cast<const uint4 *>(px + k + 32 * i);
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            acc = mfma16(as_frag(va[i]), as_frag(vx[i]), acc);
+    }
     for (; k < kend; k += 32) {
         const int64_t left = K - k - 8 * q;
         acc = mfma16(as_frag(load8(pa + k, left)), as_frag(load8(px + k, left)), acc);
@@ -222,99 +230,142 @@ __device__ __forceinline__ f32x4 shrink_wave(const uint16_t *pa, const uint16_t 
     return acc;
 }
 
-// Sums the waves' parts and writes the pieces of rank j0 + tid / 16 of the
-// thread's token (tid % 16 of the tile) where `mine`.
-__device__ __forceinline__ void shrink_join(f32x4 (&red)[kShrinkThreads / 64][64], f32x4 acc, bool mine,
-                                            int64_t tok, float scale, int j0, int r, uint16_t *u3, int RP,
-                                            int tid)
+// The sum over the waves of rank tid / 16, token tid % 16 (threads below 256).
+template <int NW>
+__device__ __forceinline__ float shrink_sum(const f32x4 (&red)[NW][64], int tid)
 {
-    const int lane = tid & 63, t16 = tid & 15;
-    red[tid >> 6][lane] = acc;
-    __syncthreads();
-    if (tid < 256 && mine) {
-        const int jj = tid >> 4, j = j0 + jj;
-        float sum = 0.0f;
+    const int jj = tid >> 4, t16 = tid & 15;
+    float sum = 0.0f;
 #pragma unroll
-        for (int w = 0; w < kShrinkThreads / 64; ++w)
-            sum += red[w][(jj >> 2) * 16 + t16][jj & 3];
-        uint32_t p[3];
-        split3(j < r ? sum * scale : 0.0f, p);
-        uint16_t *row = u3 + tok * piece_row(RP) + j;
-        row[0] = static_cast<uint16_t>(p[0]);
-        row[RP] = static_cast<uint16_t>(p[1]);
-        row[2 * RP] = static_cast<uint16_t>(p[2]);
-        if (RP == 16)
-            row[48] = 0;
-    }
-    __syncthreads();
+    for (int w = 0; w < NW; ++w)
+        sum += red[w][(jj >> 2) * 16 + t16][jj & 3];
+    return sum;
 }
 
-// At most kFewTokens tokens: blockIdx.x takes the groups in turn, 16 tokens at
-// a time.  Leaves the groups in `table` for the next kernel.
+// At most kFewTokens tokens: one workgroup per unit (blockIdx.x) and 16 ranks,
+// all of K in it -- latency-bound, and a second launch to join parts would cost
+// more.  Leaves the units in `table` for the next kernel.
+constexpr int kShrinkThreads = 1024;
+
 __global__ void __launch_bounds__(kShrinkThreads) __attribute__((amdgpu_waves_per_eu(4, 4)))
 lora_shrink_few_kernel(const uint16_t *__restrict__ x, int64_t ldx, int64_t M, int64_t K,
                        LoraAdapters ad, int RP, uint16_t *__restrict__ u3,
-                       FewGroups *__restrict__ table)
+                       FewUnits *__restrict__ table)
 {
-    __shared__ f32x4 red[kShrinkThreads / 64][64];
-    __shared__ FewGroups t;
+    constexpr int NW = kShrinkThreads / 64;
+    __shared__ f32x4 red[NW][64];
+    __shared__ FewUnits t;
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int t16 = lane & 15, q = lane >> 4;
     const int j0 = blockIdx.y * 16;
     group_few(ad, M, t, tid);
-    if (table && blockIdx.x == 0 && blockIdx.y == 0) {
-        if (tid < kFewTokens) {
-            table->g[tid] = t.g[tid];
-            table->order[tid] = t.order[tid];
-        }
+    if (table && blockIdx.x == 0 && blockIdx.y == 0 && tid < kFewTokens) {
+        table->u[tid] = t.u[tid];
+        table->order[tid] = t.order[tid];
     }
-    for (int g = blockIdx.x; g < kFewTokens; g += gridDim.x) {
-        const int32_t a = t.g[g].id;
-        const int count = t.g[g].count;
-        if (count == 0)
-            return;
-        if (a < 0 || a >= ad.n)
-            continue;
-        const float scale = ad.scale ? ad.scale[a] : 1.0f;
-        const int32_t *list = t.order + t.g[g].start;
-        const uint16_t *pa = ad.A + a * ad.stride_a +
-                             static_cast<int64_t>(min(j0 + t16, ad.r - 1)) * ad.lda + 8 * q;
-        for (int c = 0; c < count; c += 16) {
-            const int64_t tok = list[min(c + t16, count - 1)];
-            const f32x4 acc = shrink_wave(pa, x + tok * ldx + 8 * q, K, wave, q);
-            shrink_join(red, acc, c + t16 < count, tok, scale, j0, ad.r, u3, RP, tid);
-        }
-    }
+    const FewUnit u = t.u[blockIdx.x];
+    if (u.count == 0 || u.id < 0 || u.id >= ad.n)
+        return;
+    const float scale = ad.scale ? ad.scale[u.id] : 1.0f;
+    const int64_t tok = t.order[u.first + min(t16, u.count - 1)];
+    const int64_t per_wave = (K + 32 * NW - 1) / (32 * NW) * 32, k0 = wave * per_wave;
+    red[wave][lane] = shrink_wave(
+        ad.A + u.id * ad.stride_a + static_cast<int64_t>(min(j0 + t16, ad.r - 1)) * ad.lda + 8 * q,
+        x + tok * ldx + 8 * q, k0, min(K, k0 + per_wave), K, q);
+    __syncthreads();
+    if (tid >= 256 || t16 >= u.count)
+        return;
+    const int j = j0 + (tid >> 4);
+    const float sum = shrink_sum(red, tid);
+    uint32_t p[3];
+    split3(j < ad.r ? sum * scale : 0.0f, p);
+    uint16_t *row = u3 + tok * piece_row(RP) + j;
+    row[0] = static_cast<uint16_t>(p[0]);
+    row[RP] = static_cast<uint16_t>(p[1]);
+    row[2 * RP] = static_cast<uint16_t>(p[2]);
+    if (RP == 16)
+        row[48] = 0;
 }
 
-// Any number of tokens: 16 neighbouring ones per blockIdx.x; the distinct
-// adapters they use, in token order, go round the blockIdx.y slots.
-__global__ void __launch_bounds__(kShrinkThreads) __attribute__((amdgpu_waves_per_eu(4, 4)))
+// Any number of tokens: 16 neighbouring ones, 16 ranks and one of the S parts
+// of K (blockIdx.x = (block S + part)); the distinct adapters the tokens use, in
+// token order, go round the blockIdx.y slots.  One CU draws some 50 GB/s, so
+// the 0.5 MiB that a tile reads at K = 8192 are spread over S workgroups, whose
+// sums [S][M][RP] lora_join_kernel adds.
+__global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(4, 4)))
 lora_shrink_kernel(const uint16_t *__restrict__ x, int64_t ldx, int64_t M, int64_t K, LoraAdapters ad,
-                   int64_t blk0, int RP, uint16_t *__restrict__ u3)
+                   int64_t wg0, int RP, int S, int64_t part_k, float *__restrict__ upart)
 {
-    __shared__ f32x4 red[kShrinkThreads / 64][64];
+    __shared__ f32x4 red[4][64];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int t16 = lane & 15, q = lane >> 4;
-    const int64_t tok = (blk0 + blockIdx.x) * 16 + t16;
+    const int64_t wg = wg0 + blockIdx.x, part = wg % S;
+    const int64_t tok = wg / S * 16 + t16;
     const int32_t id = tok < M ? ad.adapter[tok] : -1;
-    const bool valid = id >= 0 && id < ad.n;
-    const float scale = valid && ad.scale ? ad.scale[id] : 1.0f;
     const int j0 = blockIdx.z * 16;
+    const int64_t per_wave = part_k / 4, k0 = part * part_k + wave * per_wave;
     // todo is the same in every wave: they hold the same tokens.
-    uint32_t todo = static_cast<uint32_t>(__ballot(valid)) & 0xffffu;
+    uint32_t todo = static_cast<uint32_t>(__ballot(id >= 0 && id < ad.n)) & 0xffffu;
     for (unsigned slot = 0; todo; ++slot) {
         const int32_t a = first_id(id, todo);
         todo &= ~tokens_of(id, a);
         if (slot % gridDim.y != blockIdx.y)
             continue;
-        const uint16_t *pa = ad.A + a * ad.stride_a +
-                             static_cast<int64_t>(min(j0 + t16, ad.r - 1)) * ad.lda + 8 * q;
-        const f32x4 acc = shrink_wave(pa, x + min(tok, M - 1) * ldx + 8 * q, K, wave, q);
-        shrink_join(red, acc, id == a, tok, scale, j0, ad.r, u3, RP, tid);
+        red[wave][lane] = shrink_wave(
+            ad.A + a * ad.stride_a + static_cast<int64_t>(min(j0 + t16, ad.r - 1)) * ad.lda + 8 * q,
+            x + min(tok, M - 1) * ldx + 8 * q, k0, min(K, k0 + per_wave), K, q);
+        __syncthreads();
+        const float sum = shrink_sum(red, tid);
+        if (id == a)
+            upart[(part * M + tok) * RP + j0 + (tid >> 4)] = sum;
+        __syncthreads();
     }
+}
+
+// u or t = s_a x the sum of its parts [n_parts][M][RP], in order per lane and
+// then by lane: 16 lanes share one group of four ranks of one token.  Written
+// as pieces; ranks past r are zero.
+__global__ __launch_bounds__(256) void lora_join_kernel(const float *__restrict__ parts, int64_t n_parts,
+                                                        int64_t M, int RP, LoraAdapters ad,
+                                                        uint16_t *__restrict__ pieces)
+{
+    __shared__ f32x4 red[16][16];
+    const int tid = threadIdx.x, col = tid & 15, part = tid >> 4;
+    const int64_t n4 = M * RP / 4;
+    const int64_t i4 = static_cast<int64_t>(blockIdx.x) * 16 + col;
+    f32x4 sum = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (i4 < n4) {
+        const f32x4 *p = reinterpret_cast<const f32x4 *>(parts) + i4;
+#pragma unroll 8
+        for (int64_t b = part; b < n_parts; b += 16)
+            sum += p[b * n4];
+    }
+    red[part][col] = sum;
+    __syncthreads();
+    if (part != 0 || i4 >= n4)
+        return;
+#pragma unroll
+    for (int w = 1; w < 16; ++w)
+        sum += red[w][col];
+    const int64_t m = i4 * 4 / RP;
+    const int j = static_cast<int>(i4 * 4 - m * RP);
+    const int32_t a = ad.adapter[m];
+    if (a < 0 || a >= ad.n)
+        return;  // its parts were never written, and nothing reads its pieces
+    const float s = ad.scale ? ad.scale[a] : 1.0f;
+    uint32_t p[4][3];
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+        split3(j + e < ad.r ? sum[e] * s : 0.0f, p[e]);
+    uint16_t *row = pieces + m * piece_row(RP) + j;
+#pragma unroll
+    for (int k = 0; k < 3; ++k)
+        *reinterpret_cast<uint2 *>(row + k * RP) =
+            make_uint2(p[0][k] | (p[1][k] << 16), p[2][k] | (p[3][k] << 16));
+    if (RP == 16)
+        *reinterpret_cast<uint2 *>(row + 48) = make_uint2(0u, 0u);
 }
 
 // 8 words of a matrix row from column j (a multiple of 8), the row's length r
@@ -382,19 +433,15 @@ __device__ __forceinline__ void store_piece(void *out, int64_t row, int64_t v, i
 }
 
 // logits += u B^T for at most kFewTokens tokens: one workgroup per 256
-// vocabulary rows and part (blockIdx.y) of the adapters in use; 16 tokens of an
-// adapter at a time, their B rows read once.  Bound by B of the adapters in use
-// and by z, read and written once; many small workgroups hide the latency.
-#ifndef LMH_FEW_EU
-#define LMH_FEW_EU 5
-#endif
+// vocabulary rows and share (blockIdx.y) of the units.  Bound by B of the
+// adapters in use and by z, read and written once; many small workgroups hide
+// the latency (128 tokens over 32 adapters, V = 32768, rank 16: 18 us at five
+// waves per SIMD for 66 MB; 24 us by blocks of 16 neighbouring tokens).
 template <int RP, bool BF16>
-__global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(RP <= 32 ? LMH_FEW_EU : 3)))
-lora_expand_few_kernel(const float *z, int64_t ldz, void *out,
-                                                              int64_t ldo, int64_t M, int64_t V,
-                                                              LoraAdapters ad,
-                                                              const uint16_t *__restrict__ u3,
-                                                              const FewGroups *__restrict__ table)
+__global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(RP <= 32 ? 5 : 3)))
+lora_expand_few_kernel(const float *z, int64_t ldz, void *out, int64_t ldo, int64_t M, int64_t V,
+                       LoraAdapters ad, const uint16_t *__restrict__ u3,
+                       const FewUnits *__restrict__ table)
 {
     constexpr int U = RP < 32 ? 1 : RP / 32, S = piece_row(RP) / 32;
     __shared__ __attribute__((aligned(16))) float turn[4][16 * 64];
@@ -406,17 +453,16 @@ lora_expand_few_kernel(const float *z, int64_t ldz, void *out,
         return;
     const int jq = RP == 16 ? 8 * (q & 1) : 8 * q;  // the lane's first rank of a step
     const int64_t v = v0 + 4 * t16;
-    for (int g = blockIdx.y; g < kFewTokens; g += gridDim.y) {
-        const FewGroup info = table->g[g];
-        const int32_t a = info.id;
-        const int count = info.count;
-        if (count == 0)
+    for (int i0 = blockIdx.y; i0 < kFewTokens; i0 += gridDim.y) {
+        const FewUnit un = table->u[i0];
+        const int32_t a = un.id;
+        if (un.count == 0)
             return;
-        const int32_t *list = table->order + info.start;
-        const bool live = a >= 0 && a < ad.n;
         if (!BF16 && a < 0)
             continue;  // z is in place
-        bf16x8 fb[U][4];
+        const int32_t *list = table->order + un.first;
+        const bool live = a >= 0 && a < ad.n;
+        bf16x8 fb[U][4], fu[S];
         if (live) {
             const uint16_t *pb = ad.B + a * ad.stride_b;
 #pragma unroll
@@ -427,37 +473,36 @@ lora_expand_few_kernel(const float *z, int64_t ldz, void *out,
                     fb[uu][i] = as_frag(load8_row(pb + vr * ad.ldb, 32 * uu + jq, ad.r, vr == V - 1));
             }
         }
-        for (int c = 0; c < count; c += 16) {
-            f32x4 zr[4];
+        int64_t row[4];  // the tokens of this lane's row pieces, -1 past the unit
+        f32x4 zr[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                zr[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-                if (c + 4 * i + q < count)
-                    zr[i] = load_piece(z + list[c + 4 * i + q] * ldz, v, V);
-            }
-            f32x4 d[4];
-            const float fill = a >= ad.n ? NAN : 0.0f;
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                d[i] = f32x4{fill, fill, fill, fill};
-            if (live) {
-                const uint16_t *pu = u3 + list[min(c + t16, count - 1)] * piece_row(RP) + 8 * q;
-                bf16x8 fu[S];
-#pragma unroll
-                for (int s = 0; s < S; ++s)
-                    fu[s] = as_frag(*reinterpret_cast<const uint4 *>(pu + 32 * s));
-#pragma unroll
-                for (int s = 0; s < S; ++s)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        d[i] = mfma16(fb[s % U][i], fu[s], d[i]);
-            }
-            turn_rows(d, turn[wave], t16, q);
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (c + 4 * i + q < count)
-                    store_piece<BF16>(out, list[c + 4 * i + q] * ldo, v, V, zr[i] + d[i]);
+        for (int i = 0; i < 4; ++i) {
+            row[i] = 4 * i + q < un.count ? list[4 * i + q] : -1;
+            zr[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+            if (row[i] >= 0)
+                zr[i] = load_piece(z + row[i] * ldz, v, V);
         }
+        f32x4 d[4];
+        const float fill = a >= ad.n ? NAN : 0.0f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            d[i] = f32x4{fill, fill, fill, fill};
+        if (live) {
+            const uint16_t *pu = u3 + static_cast<int64_t>(list[min(t16, un.count - 1)]) * piece_row(RP) + 8 * q;
+#pragma unroll
+            for (int s = 0; s < S; ++s)
+                fu[s] = as_frag(*reinterpret_cast<const uint4 *>(pu + 32 * s));
+#pragma unroll
+            for (int s = 0; s < S; ++s)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    d[i] = mfma16(fb[s % U][i], fu[s], d[i]);
+        }
+        turn_rows(d, turn[wave], t16, q);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (row[i] >= 0)
+                store_piece<BF16>(out, row[i] * ldo, v, V, zr[i] + d[i]);
     }
 }
 
@@ -619,6 +664,7 @@ __global__ __launch_bounds__(256) void lora_group_kernel(const int32_t *__restri
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     auto cls = [&](int32_t id) { return id < 0 ? n : id >= n ? n + 1 : static_cast<int64_t>(id); };
     int32_t less = 0, same = 0;
+#pragma unroll 4
     for (int64_t m = tid; m < M; m += 256) {
         const int64_t c = cls(adapter[m]);
         less += c < g;
@@ -910,49 +956,6 @@ __global__ __launch_bounds__(256) void lora_bwd_v_kernel(
     }
 }
 
-// t = s_a x the sum of its parts, in block order per lane and then by lane:
-// 16 lanes share one group of four ranks of one token.  Written as pieces.
-__global__ __launch_bounds__(256) void lora_t_kernel(const float *__restrict__ tpart, int64_t nvb,
-                                                     int64_t M, int RP, LoraAdapters ad,
-                                                     uint16_t *__restrict__ t3)
-{
-    __shared__ f32x4 red[16][16];
-    const int tid = threadIdx.x, col = tid & 15, part = tid >> 4;
-    const int64_t n4 = M * RP / 4;
-    const int64_t i4 = static_cast<int64_t>(blockIdx.x) * 16 + col;
-    f32x4 sum = {0.0f, 0.0f, 0.0f, 0.0f};
-    if (i4 < n4) {
-        const f32x4 *p = reinterpret_cast<const f32x4 *>(tpart) + i4;
-#pragma unroll 8
-        for (int64_t b = part; b < nvb; b += 16)
-            sum += p[b * n4];
-    }
-    red[part][col] = sum;
-    __syncthreads();
-    if (part != 0 || i4 >= n4)
-        return;
-#pragma unroll
-    for (int w = 1; w < 16; ++w)
-        sum += red[w][col];
-    const int64_t m = i4 * 4 / RP;
-    const int j = static_cast<int>(i4 * 4 - m * RP);
-    const int32_t a = ad.adapter[m];
-    if (a < 0 || a >= ad.n)
-        return;  // its parts were never written, and t is not read
-    const float s = ad.scale ? ad.scale[a] : 1.0f;
-    uint32_t p[4][3];
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-        split3(j + e < ad.r ? sum[e] * s : 0.0f, p[e]);
-    uint16_t *row = t3 + m * piece_row(RP) + j;
-#pragma unroll
-    for (int k = 0; k < 3; ++k)
-        *reinterpret_cast<uint2 *>(row + k * RP) =
-            make_uint2(p[0][k] | (p[1][k] << 16), p[2][k] | (p[3][k] << 16));
-    if (RP == 16)
-        *reinterpret_cast<uint2 *>(row + 48) = make_uint2(0u, 0u);
-}
-
 // dX and dA, 256 columns of K per workgroup.  The first nkb n workgroups
 // accumulate dA of one adapter over its tokens, 64 at a time, from one read of
 // x; the others write dX = t A of one chunk of up to 64 tokens, A_a's block in
@@ -1094,49 +1097,70 @@ int64_t round256(int64_t b)
     return (b + 255) / 256 * 256;
 }
 
+// Units a batch of M <= kFewTokens tokens can have.
+int64_t few_units(int64_t M, int64_t n)
+{
+    return std::min<int64_t>(M, M / 16 + n + 2);
+}
+
+// Parts of K of the shrink beyond kFewTokens tokens: enough for 1024
+// workgroups, at most 16, at least 256 columns each.
+int64_t shrink_parts(int64_t M, int64_t K, int64_t RP)
+{
+    const int64_t tiles = std::max<int64_t>(1, (M + 15) / 16) * (RP / 16);
+    return std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(16, K / 256), 1024 / tiles));
+}
+
+hipError_t launch_join(const float *parts, int64_t n_parts, int64_t M, int RP, const LoraAdapters &ad,
+                       uint16_t *pieces, hipStream_t s)
+{
+    const int64_t n4 = M * RP / 4;  // blocks of 16; at most 2^31 work-items per launch
+    const int64_t most = kMaxItems / 16;
+    if (n4 > most)
+        return hipErrorInvalidValue;  // refused by the caller's size check
+    hipLaunchKernelGGL(lora_join_kernel, dim3(static_cast<unsigned>((n4 + 15) / 16)), dim3(256), 0, s, parts,
+                       n_parts, M, RP, ad, pieces);
+    return hipGetLastError();
+}
+
+// u3 from x; upart: [shrink_parts][M][RP] FP32 (M > kFewTokens only).
 hipError_t launch_shrink(const uint16_t *x, int64_t ldx, int64_t M, int64_t K, const LoraAdapters &ad,
-                         uint16_t *u3, FewGroups *table, hipStream_t s)
+                         uint16_t *u3, FewUnits *table, float *upart, hipStream_t s)
 {
     const int RP = rank_bucket(ad.r);
     const int64_t zr = RP / 16;
     if (M <= kFewTokens) {
-        // One workgroup per group there can be (n adapters, none, no adapter).
-        const dim3 grid(static_cast<unsigned>(std::min<int64_t>(ad.n + 2, M)), static_cast<unsigned>(zr));
+        const dim3 grid(static_cast<unsigned>(few_units(M, ad.n)), static_cast<unsigned>(zr));
         hipLaunchKernelGGL(lora_shrink_few_kernel, grid, dim3(kShrinkThreads), 0, s, x, ldx, M, K, ad, RP,
                            u3, table);
         return hipGetLastError();
     }
     if (ad.n == 0)
         return hipSuccess;
-    const int64_t blocks = (M + 15) / 16;
-    // Slots to fill the chip twice over, at most one per distinct adapter.
-    const int64_t slots =
-        std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(ad.n, 16), 512 / (blocks * zr)));
-    const int64_t most = kMaxItems / kShrinkThreads / (slots * zr);
-    for (int64_t b0 = 0; b0 < blocks; b0 += most) {
-        const dim3 grid(static_cast<unsigned>(std::min(most, blocks - b0)), static_cast<unsigned>(slots),
+    const int64_t S = shrink_parts(M, K, RP), part_k = (K + 128 * S - 1) / (128 * S) * 128;
+    const int64_t slots = std::min<int64_t>(ad.n, 4);
+    const int64_t wgs = (M + 15) / 16 * S, most = kMaxItems / 256 / (slots * zr);
+    for (int64_t w0 = 0; w0 < wgs; w0 += most) {
+        const dim3 grid(static_cast<unsigned>(std::min(most, wgs - w0)), static_cast<unsigned>(slots),
                         static_cast<unsigned>(zr));
-        hipLaunchKernelGGL(lora_shrink_kernel, grid, dim3(kShrinkThreads), 0, s, x, ldx, M, K, ad, b0, RP,
-                           u3);
+        hipLaunchKernelGGL(lora_shrink_kernel, grid, dim3(256), 0, s, x, ldx, M, K, ad, w0, RP,
+                           static_cast<int>(S), part_k, upart);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess)
             return e;
     }
-    return hipSuccess;
+    return launch_join(upart, S, M, RP, ad, u3, s);
 }
 
 template <int RP>
 hipError_t launch_expand(const float *z, int64_t ldz, void *out, int64_t ldo, bool bf16, int64_t M,
                          int64_t V, const LoraAdapters &ad, const uint16_t *u3,
-                         const FewGroups *table, hipStream_t s)
+                         const FewUnits *table, hipStream_t s)
 {
     if (M <= kFewTokens) {
-        // Parts of the groups: as many as make 4096 workgroups.
-#ifndef LMH_FEW_WGS
-#define LMH_FEW_WGS 4096
-#endif
+        // Shares of the units: as many as make 4096 workgroups.
         const int64_t vts = (V + 255) / 256;
-        const int64_t parts = std::max<int64_t>(1, std::min(std::min(ad.n + 2, M), LMH_FEW_WGS / vts));
+        const int64_t parts = std::max<int64_t>(1, std::min<int64_t>(few_units(M, ad.n), 4096 / vts));
         const dim3 grid(static_cast<unsigned>(vts), static_cast<unsigned>(parts));
         if (bf16)
             hipLaunchKernelGGL((lora_expand_few_kernel<RP, true>), grid, dim3(256), 0, s, z, ldz, out, ldo, M, V,
@@ -1174,7 +1198,7 @@ hipError_t launch_expand(const float *z, int64_t ldz, void *out, int64_t ldo, bo
 
 // The gradients' workspace, in order.
 struct BwdLayout {
-    int64_t offset, order, chunks, u3, t3, tpart, end;
+    int64_t offset, order, chunks, u3, t3, parts, end;  // parts: of u, then of t
 };
 
 // Numbers of chunks: every group's start at chunk_base.
@@ -1183,7 +1207,7 @@ int64_t chunk_numbers(int64_t M, int64_t n)
     return chunk_base(M, n + 2);
 }
 
-BwdLayout bwd_layout(int64_t M, int64_t V, int64_t r, int64_t n)
+BwdLayout bwd_layout(int64_t M, int64_t K, int64_t V, int64_t r, int64_t n)
 {
     const int64_t RP = rank_bucket(r), nvb = (V + 255) / 256;
     const int64_t pieces = round256(2 * piece_row(static_cast<int>(RP)) * M);
@@ -1193,8 +1217,8 @@ BwdLayout bwd_layout(int64_t M, int64_t V, int64_t r, int64_t n)
     l.chunks = l.order + round256(4 * M);
     l.u3 = l.chunks + round256(static_cast<int64_t>(sizeof(Chunk)) * chunk_numbers(M, n));
     l.t3 = l.u3 + pieces;
-    l.tpart = l.t3 + pieces;
-    l.end = l.tpart + round256(4 * nvb * M * RP);
+    l.parts = l.t3 + pieces;
+    l.end = l.parts + round256(4 * std::max(nvb, shrink_parts(M, K, RP)) * M * RP);
     return l;
 }
 
@@ -1206,7 +1230,7 @@ hipError_t launch_bwd_v(const LoraBwd &p, const BwdLayout &l, char *ws, hipStrea
                        p.g, p.ldg, p.M, p.V, p.ad, reinterpret_cast<const int32_t *>(ws + l.offset),
                        reinterpret_cast<const int32_t *>(ws + l.order),
                        reinterpret_cast<const uint16_t *>(ws + l.u3),
-                       (p.dX || p.dA) ? reinterpret_cast<float *>(ws + l.tpart) : nullptr, p.dB, p.lddb,
+                       (p.dX || p.dA) ? reinterpret_cast<float *>(ws + l.parts) : nullptr, p.dB, p.lddb,
                        p.stride_db, p.accumulate ? 1 : 0, nvb);
     return hipGetLastError();
 }
@@ -1227,21 +1251,33 @@ hipError_t launch_bwd_k(const LoraBwd &p, const BwdLayout &l, char *ws, hipStrea
 
 }  // namespace
 
-// Room for the groups of a small batch, ahead of u.
-static int64_t few_bytes(int64_t M)
+// The forward's workspace, in order: a small batch's units, u, and the FP32
+// product of BF16 logits; the parts of u share the last one's place (they are
+// joined before the product runs).
+struct FwdLayout {
+    int64_t table, u3, z, end;
+};
+
+static FwdLayout fwd_layout(int64_t M, int64_t K, int64_t V, int64_t r, bool bf16)
 {
-    return M <= kFewTokens ? round256(sizeof(FewGroups)) : 0;
+    const int64_t RP = rank_bucket(r);
+    FwdLayout l;
+    l.table = 0;
+    l.u3 = M <= kFewTokens ? round256(sizeof(FewUnits)) : 0;
+    l.z = l.u3 + round256(2 * piece_row(static_cast<int>(RP)) * M);
+    l.end = l.z + round256(std::max<int64_t>(bf16 ? 4 * M * ((V + 3) / 4 * 4) : 0,
+                                             M <= kFewTokens ? 0 : 4 * shrink_parts(M, K, RP) * M * RP));
+    return l;
 }
 
-int64_t lora_logits_workspace_bytes(int64_t M, int64_t V, int64_t r, bool bf16)
+int64_t lora_logits_workspace_bytes(int64_t M, int64_t K, int64_t V, int64_t r, bool bf16)
 {
-    const int64_t u = few_bytes(M) + round256(2 * piece_row(rank_bucket(r)) * M);
-    return u + (bf16 ? round256(4 * M * ((V + 3) / 4 * 4)) : 0);
+    return fwd_layout(M, K, V, r, bf16).end;
 }
 
-int64_t lora_bwd_workspace_bytes(int64_t M, int64_t V, int64_t r, int64_t n)
+int64_t lora_bwd_workspace_bytes(int64_t M, int64_t K, int64_t V, int64_t r, int64_t n)
 {
-    return bwd_layout(M, V, r, n).end;
+    return bwd_layout(M, K, V, r, n).end;
 }
 
 hipError_t launch_logits_lora(const GemmProblem &p, bool bf16, const LoraAdapters &ad, void *workspace,
@@ -1249,15 +1285,16 @@ hipError_t launch_logits_lora(const GemmProblem &p, bool bf16, const LoraAdapter
 {
     const int64_t M = p.C, K = p.P, V = p.R;
     char *ws = static_cast<char *>(workspace);
-    FewGroups *table = reinterpret_cast<FewGroups *>(ws);  // M <= kFewTokens
-    uint16_t *u3 = reinterpret_cast<uint16_t *>(ws + few_bytes(M));
+    const FwdLayout l = fwd_layout(M, K, V, ad.r, bf16);
+    FewUnits *table = reinterpret_cast<FewUnits *>(ws + l.table);  // M <= kFewTokens
+    uint16_t *u3 = reinterpret_cast<uint16_t *>(ws + l.u3);
     GemmProblem f = p;  // the shared product, FP32: in place, or in the workspace for BF16 logits
     if (bf16) {
-        f.D = reinterpret_cast<char *>(u3) + round256(2 * piece_row(rank_bucket(ad.r)) * M);
+        f.D = ws + l.z;
         f.ldd = (V + 3) / 4 * 4;
     }
     f.stream_out = false;  // read back at once
-    hipError_t e = launch_shrink(p.B, p.ldb, M, K, ad, u3, table, s);
+    hipError_t e = launch_shrink(p.B, p.ldb, M, K, ad, u3, table, reinterpret_cast<float *>(ws + l.z), s);
     if (e == hipSuccess)
         e = launch_gemm_logits(f, Epi::kStoreF32, s);
     if (e != hipSuccess)
@@ -1273,7 +1310,7 @@ hipError_t launch_logits_lora(const GemmProblem &p, bool bf16, const LoraAdapter
 
 hipError_t launch_lora_bwd(const LoraBwd &p, void *workspace, hipStream_t s)
 {
-    const BwdLayout l = bwd_layout(p.M, p.V, p.ad.r, p.ad.n);
+    const BwdLayout l = bwd_layout(p.M, p.K, p.V, p.ad.r, p.ad.n);
     char *ws = static_cast<char *>(workspace);
     const int RP = rank_bucket(p.ad.r);
     uint16_t *t3 = reinterpret_cast<uint16_t *>(ws + l.t3);
@@ -1283,7 +1320,8 @@ hipError_t launch_lora_bwd(const LoraBwd &p, void *workspace, hipStream_t s)
                        reinterpret_cast<int32_t *>(ws + l.order), reinterpret_cast<Chunk *>(ws + l.chunks));
     hipError_t e = hipGetLastError();
     if (e == hipSuccess && p.dB && p.ad.n > 0 && p.M > 0)
-        e = launch_shrink(p.x, p.ldx, p.M, p.K, p.ad, reinterpret_cast<uint16_t *>(ws + l.u3), nullptr, s);
+        e = launch_shrink(p.x, p.ldx, p.M, p.K, p.ad, reinterpret_cast<uint16_t *>(ws + l.u3), nullptr,
+                          reinterpret_cast<float *>(ws + l.parts), s);
     if (e == hipSuccess && p.ad.n > 0 && p.V > 0) {
         switch (RP) {
         case 16: e = launch_bwd_v<16>(p, l, ws, s); break;
@@ -1295,10 +1333,7 @@ hipError_t launch_lora_bwd(const LoraBwd &p, void *workspace, hipStream_t s)
     if (e != hipSuccess || (!p.dX && !p.dA) || p.K == 0)
         return e;
     if (p.ad.n > 0 && p.M > 0) {
-        const int64_t n4 = p.M * RP / 4;
-        hipLaunchKernelGGL(lora_t_kernel, dim3(static_cast<unsigned>((n4 + 15) / 16)), dim3(256), 0, s,
-                           reinterpret_cast<const float *>(ws + l.tpart), nvb, p.M, RP, p.ad, t3);
-        e = hipGetLastError();
+        e = launch_join(reinterpret_cast<const float *>(ws + l.parts), nvb, p.M, RP, p.ad, t3, s);
         if (e != hipSuccess)
             return e;
     }

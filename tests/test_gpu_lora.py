@@ -365,7 +365,7 @@ def test_streams_workspaces_and_graphs():
     assert torch.equal(out1, want) and torch.equal(out2, want2)
     with pytest.raises(ValueError):  # a raw handle needs the caller's workspace
         lmh.lmhead_logits_lora(x, W, A, B, ids, out=out1, stream=s1.cuda_stream)
-    ws = torch.empty(max(lmh.lmhead_logits_lora_workspace_bytes(M, V, r, "bf16"),
+    ws = torch.empty(max(lmh.lmhead_logits_lora_workspace_bytes(M, K, V, r, "bf16"),
                          lmh.lmhead_lora_bwd_workspace_bytes(M, K, V, r, n)), dtype=torch.uint8,
                      device="cuda")
     outs = [torch.empty_like(want)] + [torch.empty_like(t) for t in back]

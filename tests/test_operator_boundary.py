@@ -144,6 +144,21 @@ def test_beam_reorder_refusals(L):
         assert f(**{none: 0}) == OK, none
 
 
+def test_workspace_sizes(L):
+    """Every size, zero included, has a workspace size (no division by a size)."""
+    for M in (0, 1, 16, 17, 256, 257, 4096, 2 ** 22):
+        for K in (0, 1, 255, 8192):
+            for V in (0, 1, 257, 32768):
+                for r in (1, 16, 17, 64, 128):
+                    for dt in (FP32, BF16):
+                        assert L.lmhead_logits_lora_workspace_bytes(M, K, V, r, dt) >= 0
+                    for n in (0, 1, 300):
+                        assert L.lmhead_lora_bwd_workspace_bytes(M, K, V, r, n) > 0
+    assert L.lmhead_logits_lora_workspace_bytes(2 ** 22 + 1, 8, 8, 8, FP32) == -SHAPE
+    assert L.lmhead_logits_lora_workspace_bytes(8, 8, 8, 8, FP16) == -DTYPE
+    assert L.lmhead_lora_bwd_workspace_bytes(8, 8, 2 ** 31 - 1, 8, 2) == -SHAPE
+
+
 def test_python_arguments():
     """What the binding refuses before it reaches the library."""
     cpu = torch.zeros(4, 8, dtype=torch.bfloat16)
@@ -164,7 +179,7 @@ def test_python_arguments():
     with pytest.raises(ValueError):
         lmh.lmhead_beam_reorder(cpu, torch.zeros(2, 2, dtype=torch.int32), lengths=torch.zeros(2))
     with pytest.raises(lmh.LmheadError):
-        lmh.lmhead_logits_lora_workspace_bytes(4, 8, 200)
+        lmh.lmhead_logits_lora_workspace_bytes(4, 8, 8, 200)
     with pytest.raises(lmh.LmheadError):
         lmh.lmhead_lora_bwd_workspace_bytes(-1, 8, 8, 4, 1)
     with pytest.raises(lmh.LmheadError):
