@@ -288,39 +288,71 @@ lora_shrink_few_kernel(const uint16_t *__restrict__ x, int64_t ldx, int64_t M, i
         row[48] = 0;
 }
 
-// Any number of tokens: 16 neighbouring ones, 16 ranks and one of the S parts
-// of K (blockIdx.x = (block S + part)); the distinct adapters the tokens use, in
-// token order, go round the blockIdx.y slots.  One CU draws some 50 GB/s, so
-// the 0.5 MiB that a tile reads at K = 8192 are spread over S workgroups, whose
-// sums [S][M][RP] lora_join_kernel adds.
-__global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(4, 4)))
-lora_shrink_kernel(const uint16_t *__restrict__ x, int64_t ldx, int64_t M, int64_t K, LoraAdapters ad,
-                   int64_t wg0, int RP, int S, int64_t part_k, float *__restrict__ upart)
+// Any number of tokens: each wave takes 16 neighbouring ones, all ranks and one
+// of the S parts of K (blockIdx.x = (block S + part), four waves a block); the
+// distinct adapters the tokens use, in token order, go round the blockIdx.y
+// slots.  A CU draws some 20 - 50 GB/s, so what counts is how few bytes reach
+// it and that every CU has some: x once for all ranks, A shared by the four
+// waves through L1, K in parts whose sums [S][M][RP] lora_join_kernel adds.
+// (M = 1024, K = 8192: rank 64 read 16 x 16 at a time 22 - 30 us.)
+template <int RP>
+__global__ __launch_bounds__(256) void lora_shrink_kernel(const uint16_t *__restrict__ x, int64_t ldx,
+                                                          int64_t M, int64_t K, LoraAdapters ad,
+                                                          int64_t wg0, int S, int64_t part_k,
+                                                          float *__restrict__ upart)
 {
-    __shared__ f32x4 red[4][64];
-    const int tid = threadIdx.x, lane = tid & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    constexpr int RB = RP / 16, UN = RB <= 2 ? 8 : RB == 4 ? 4 : 2;
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int t16 = lane & 15, q = lane >> 4;
     const int64_t wg = wg0 + blockIdx.x, part = wg % S;
-    const int64_t tok = wg / S * 16 + t16;
+    const int64_t tok = (wg / S * 4 + wave) * 16 + t16;
     const int32_t id = tok < M ? ad.adapter[tok] : -1;
-    const int j0 = blockIdx.z * 16;
-    const int64_t per_wave = part_k / 4, k0 = part * part_k + wave * per_wave;
-    // todo is the same in every wave: they hold the same tokens.
     uint32_t todo = static_cast<uint32_t>(__ballot(id >= 0 && id < ad.n)) & 0xffffu;
+    const int64_t k0 = part * part_k, kend = min(K, k0 + part_k);
+    const uint16_t *px = x + min(tok, M - 1) * ldx + 8 * q;
     for (unsigned slot = 0; todo; ++slot) {
         const int32_t a = first_id(id, todo);
         todo &= ~tokens_of(id, a);
         if (slot % gridDim.y != blockIdx.y)
             continue;
-        red[wave][lane] = shrink_wave(
-            ad.A + a * ad.stride_a + static_cast<int64_t>(min(j0 + t16, ad.r - 1)) * ad.lda + 8 * q,
-            x + min(tok, M - 1) * ldx + 8 * q, k0, min(K, k0 + per_wave), K, q);
-        __syncthreads();
-        const float sum = shrink_sum(red, tid);
-        if (id == a)
-            upart[(part * M + tok) * RP + j0 + (tid >> 4)] = sum;
-        __syncthreads();
+        const uint16_t *pa[RB];
+        f32x4 acc[RB];
+#pragma unroll
+        for (int b = 0; b < RB; ++b) {
+            pa[b] = ad.A + a * ad.stride_a + static_cast<int64_t>(min(16 * b + t16, ad.r - 1)) * ad.lda + 8 * q;
+            acc[b] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        }
+        int64_t k = k0;
+        for (; k + 32 * UN <= kend; k += 32 * UN) {
+            uint4 vx[UN], va[UN][RB];
+#pragma unroll
+            for (int i = 0; i < UN; ++i) {
+                vx[i] = *reinterpret_cast<const uint4 *>(px + k + 32 * i);
+#pragma unroll
+                for (int b = 0; b < RB; ++b)
+                    va[i][b] = *reinterpret_cast<const uint4 *>(pa[b] + k + 32 * i);
+            }
+            __builtin_amdgcn_sched_barrier(0);  // all of them in flight
+#pragma unroll
+            for (int i = 0; i < UN; ++i)
+#pragma unroll
+                for (int b = 0; b < RB; ++b)
+                    acc[b] = mfma16(as_frag(va[i][b]), as_frag(vx[i]), acc[b]);
+        }
+        for (; k < kend; k += 32) {
+            const int64_t left = K - k - 8 * q;
+            const bf16x8 fx = as_frag(load8(px + k, left));
+#pragma unroll
+            for (int b = 0; b < RB; ++b)
+                acc[b] = mfma16(as_frag(load8(pa[b] + k, left)), fx, acc[b]);
+        }
+        if (id == a) {
+            float *p = upart + (part * M + tok) * RP + 4 * q;
+#pragma unroll
+            for (int b = 0; b < RB; ++b)
+                *reinterpret_cast<f32x4 *>(p + 16 * b) = acc[b];
+        }
     }
 }
 
@@ -1103,12 +1135,15 @@ int64_t few_units(int64_t M, int64_t n)
     return std::min<int64_t>(M, M / 16 + n + 2);
 }
 
-// Parts of K of the shrink beyond kFewTokens tokens: enough for 1024
-// workgroups, at most 16, at least 256 columns each.
-int64_t shrink_parts(int64_t M, int64_t K, int64_t RP)
+// Parts of K of the shrink beyond kFewTokens tokens: enough for 512
+// workgroups, at most 32, at least 256 columns each.
+#ifndef LMH_SHRINK_WGS
+#define LMH_SHRINK_WGS 512
+#endif
+int64_t shrink_parts(int64_t M, int64_t K)
 {
-    const int64_t tiles = std::max<int64_t>(1, (M + 15) / 16) * (RP / 16);
-    return std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(16, K / 256), 1024 / tiles));
+    const int64_t blocks = std::max<int64_t>(1, (M + 63) / 64);
+    return std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(32, K / 256), LMH_SHRINK_WGS / blocks));
 }
 
 hipError_t launch_join(const float *parts, int64_t n_parts, int64_t M, int RP, const LoraAdapters &ad,
@@ -1137,14 +1172,21 @@ hipError_t launch_shrink(const uint16_t *x, int64_t ldx, int64_t M, int64_t K, c
     }
     if (ad.n == 0)
         return hipSuccess;
-    const int64_t S = shrink_parts(M, K, RP), part_k = (K + 128 * S - 1) / (128 * S) * 128;
+    const int64_t S = shrink_parts(M, K), part_k = (K + 32 * S - 1) / (32 * S) * 32;
     const int64_t slots = std::min<int64_t>(ad.n, 4);
-    const int64_t wgs = (M + 15) / 16 * S, most = kMaxItems / 256 / (slots * zr);
+    const int64_t wgs = (M + 63) / 64 * S, most = kMaxItems / 256 / slots;
     for (int64_t w0 = 0; w0 < wgs; w0 += most) {
-        const dim3 grid(static_cast<unsigned>(std::min(most, wgs - w0)), static_cast<unsigned>(slots),
-                        static_cast<unsigned>(zr));
-        hipLaunchKernelGGL(lora_shrink_kernel, grid, dim3(256), 0, s, x, ldx, M, K, ad, w0, RP,
-                           static_cast<int>(S), part_k, upart);
+        const dim3 grid(static_cast<unsigned>(std::min(most, wgs - w0)), static_cast<unsigned>(slots));
+        auto run = [&](auto kernel) {
+            hipLaunchKernelGGL(kernel, grid, dim3(256), 0, s, x, ldx, M, K, ad, w0, static_cast<int>(S),
+                               part_k, upart);
+        };
+        switch (RP) {
+        case 16: run(lora_shrink_kernel<16>); break;
+        case 32: run(lora_shrink_kernel<32>); break;
+        case 64: run(lora_shrink_kernel<64>); break;
+        default: run(lora_shrink_kernel<128>); break;
+        }
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess)
             return e;
@@ -1218,7 +1260,7 @@ BwdLayout bwd_layout(int64_t M, int64_t K, int64_t V, int64_t r, int64_t n)
     l.u3 = l.chunks + round256(static_cast<int64_t>(sizeof(Chunk)) * chunk_numbers(M, n));
     l.t3 = l.u3 + pieces;
     l.parts = l.t3 + pieces;
-    l.end = l.parts + round256(4 * std::max(nvb, shrink_parts(M, K, RP)) * M * RP);
+    l.end = l.parts + round256(4 * std::max(nvb, shrink_parts(M, K)) * M * RP);
     return l;
 }
 
@@ -1266,7 +1308,7 @@ static FwdLayout fwd_layout(int64_t M, int64_t K, int64_t V, int64_t r, bool bf1
     l.u3 = M <= kFewTokens ? round256(sizeof(FewUnits)) : 0;
     l.z = l.u3 + round256(2 * piece_row(static_cast<int>(RP)) * M);
     l.end = l.z + round256(std::max<int64_t>(bf16 ? 4 * M * ((V + 3) / 4 * 4) : 0,
-                                             M <= kFewTokens ? 0 : 4 * shrink_parts(M, K, RP) * M * RP));
+                                             M <= kFewTokens ? 0 : 4 * shrink_parts(M, K) * M * RP));
     return l;
 }
 
