@@ -608,9 +608,8 @@ struct ReorderArgs {
     int64_t dst_so, dst_sr, dst_sh;
     const int32_t *parent;
     const int32_t *lengths;
-    int64_t B;
     int32_t W_in, W_out;
-    int64_t H, T, pos_bytes;
+    int64_t T, pos_bytes;
 };
 
 template <int BYTES>
@@ -632,65 +631,76 @@ struct VecOf<1> {
     typedef uint8_t type;
 };
 
+// The result is not read again by this kernel: its stores are marked as
+// streamed once (1 GB cache: 250 -> 236 us; marking the loads as well lost what
+// a small state's rows gain from the caches, 7 -> 10 us).
+template <int VB>
+__device__ __forceinline__ void store_vec(char *p, typename VecOf<VB>::type v)
+{
+    __builtin_nontemporal_store(v, reinterpret_cast<typename VecOf<VB>::type *>(p));
+}
+
+// VB bytes of every beam.
 template <int WMAX, int VB, bool IN_PLACE>
-__device__ __forceinline__ void move_column(const char *s, char *d, int64_t ssr, int64_t dsr,
-                                            const int32_t *par, int32_t W_in, int32_t W_out)
+__device__ __forceinline__ void move_column(const char *s, char *d, int64_t ssr, int64_t dsr, const int32_t *par,
+                                            int32_t W_in, int32_t W_out)
 {
     typedef typename VecOf<VB>::type vec;
     if constexpr (IN_PLACE) {
+        // All rows are read before any is written; those that stay (or have no
+        // parent) are neither.
         vec r[WMAX];
+        uint64_t moves = 0;
 #pragma unroll
         for (int i = 0; i < WMAX; ++i) {
             const int32_t p = i < W_out ? par[i] : -1;
-            if (p >= 0 && p < W_in && p != i)
+            if (p >= 0 && p < W_in && p != i) {
+                moves |= uint64_t{1} << i;
                 r[i] = *reinterpret_cast<const vec *>(s + p * ssr);
+            }
         }
 #pragma unroll
-        for (int i = 0; i < WMAX; ++i) {
-            const int32_t p = i < W_out ? par[i] : -1;
-            if (p >= 0 && p < W_in && p != i)
-                *reinterpret_cast<vec *>(d + i * dsr) = r[i];
-        }
+        for (int i = 0; i < WMAX; ++i)
+            if ((moves >> i) & 1)
+                store_vec<VB>(d + i * dsr, r[i]);
     } else {
-        for (int i0 = 0; i0 < W_out; i0 += 4) {
-            vec r[4];
+        for (int i0 = 0; i0 < W_out; i0 += WMAX) {
+            vec r[WMAX];
+            uint64_t moves = 0;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < WMAX; ++i) {
                 const int32_t p = i0 + i < W_out ? par[i0 + i] : -1;
-                if (p >= 0 && p < W_in)
+                if (p >= 0 && p < W_in) {
+                    moves |= uint64_t{1} << i;
                     r[i] = *reinterpret_cast<const vec *>(s + p * ssr);
+                }
             }
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int32_t p = i0 + i < W_out ? par[i0 + i] : -1;
-                if (p >= 0 && p < W_in)
-                    *reinterpret_cast<vec *>(d + (i0 + i) * dsr) = r[i];
-            }
+            for (int i = 0; i < WMAX; ++i)
+                if ((moves >> i) & 1)
+                    store_vec<VB>(d + (i0 + i) * dsr, r[i]);
         }
     }
 }
 
 template <int WMAX, int VB, bool IN_PLACE>
-__global__ __launch_bounds__(256) void beam_reorder_kernel(ReorderArgs a, int64_t blocks_per_row)
+__global__ __launch_bounds__(256) void beam_reorder_kernel(ReorderArgs a, uint32_t blocks_per_row,
+                                                           uint32_t B, uint32_t H)
 {
-    // blockIdx.x = ((o * H + h) * B + b) * blocks_per_row + block
-    const int64_t id = blockIdx.x;
-    const int64_t slab = id / blocks_per_row;
-    const int64_t blk = id - slab * blocks_per_row;
-    const int64_t oh = slab / a.B;
-    const int64_t b = slab - oh * a.B;
-    const int64_t o = oh / a.H;
-    const int64_t h = oh - o * a.H;
+    // blockIdx.x = ((o * H + h) * B + b) * blocks_per_row + block, below 2^23
+    const uint32_t slab = blockIdx.x / blocks_per_row, blk = blockIdx.x - slab * blocks_per_row;
+    const uint32_t oh = slab / B, b = slab - oh * B;
+    const uint32_t o = oh / H, h = oh - o * H;
     int64_t len = a.T;
     if (a.lengths)
         len = min(max(static_cast<int64_t>(a.lengths[b]), int64_t{0}), a.T);
     const int64_t live = len * a.pos_bytes;
-    const int64_t at = (blk * 256 + threadIdx.x) * VB;
+    const int64_t at = (static_cast<int64_t>(blk) * 256 + threadIdx.x) * VB;
     if (at >= live)
         return;
-    const int32_t *par = a.parent + b * a.W_out;
-    const char *s = a.src + o * a.src_so + b * a.W_in * a.src_sr + h * a.src_sh + at;
-    char *d = a.dst + o * a.dst_so + b * a.W_out * a.dst_sr + h * a.dst_sh + at;
+    const int32_t *par = a.parent + static_cast<int64_t>(b) * a.W_out;
+    const char *s = a.src + o * a.src_so + static_cast<int64_t>(b) * a.W_in * a.src_sr + h * a.src_sh + at;
+    char *d = a.dst + o * a.dst_so + static_cast<int64_t>(b) * a.W_out * a.dst_sr + h * a.dst_sh + at;
     if (at + VB <= live) {
         move_column<WMAX, VB, IN_PLACE>(s, d, a.src_sr, a.dst_sr, par, a.W_in, a.W_out);
     } else {
@@ -700,22 +710,22 @@ __global__ __launch_bounds__(256) void beam_reorder_kernel(ReorderArgs a, int64_
 }
 
 template <int WMAX, int VB, bool IN_PLACE>
-hipError_t launch_reorder(const ReorderArgs &a, int64_t n_outer, hipStream_t s)
+hipError_t launch_reorder(const ReorderArgs &a, int64_t B, int64_t H, int64_t n_outer, hipStream_t s)
 {
     const int64_t per_row = (a.T * a.pos_bytes + 256 * VB - 1) / (256 * VB);
-    const int64_t slabs = n_outer * a.H * a.B;
     constexpr int64_t kMaxBlocks = (int64_t{1} << 31) / 256;
     // Several launches over outer blocks where one would pass 2^31 work-items.
-    if (per_row > kMaxBlocks || slabs / n_outer > kMaxBlocks / per_row)
+    if (per_row > kMaxBlocks || B * H > kMaxBlocks / per_row)
         return hipErrorInvalidValue;  // refused by the caller's size check
-    const int64_t per_launch = std::max<int64_t>(1, kMaxBlocks / (per_row * a.H * a.B));
+    const int64_t per_launch = std::max<int64_t>(1, kMaxBlocks / (per_row * H * B));
     for (int64_t o = 0; o < n_outer; o += per_launch) {
         const int64_t no = std::min(per_launch, n_outer - o);
         ReorderArgs q = a;
         q.src += o * a.src_so;
         q.dst += o * a.dst_so;
         hipLaunchKernelGGL((beam_reorder_kernel<WMAX, VB, IN_PLACE>),
-                           dim3(static_cast<unsigned>(no * a.H * a.B * per_row)), dim3(256), 0, s, q, per_row);
+                           dim3(static_cast<unsigned>(no * H * B * per_row)), dim3(256), 0, s, q,
+                           static_cast<uint32_t>(per_row), static_cast<uint32_t>(B), static_cast<uint32_t>(H));
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess)
             return e;
@@ -773,25 +783,23 @@ hipError_t launch_beam_reorder(const void *src, void *dst, const int64_t (&src_s
     a.dst_so = dst_strides[0], a.dst_sr = dst_strides[1], a.dst_sh = dst_strides[2];
     a.parent = parent;
     a.lengths = lengths;
-    a.B = B;
     a.W_in = static_cast<int32_t>(W_in);
     a.W_out = static_cast<int32_t>(W_out);
-    a.H = H;
     a.T = T;
     a.pos_bytes = pos_bytes;
     if (src != dst)
-        return launch_reorder<4, 16, false>(a, n_outer, s);
+        return launch_reorder<4, 16, false>(a, B, H, n_outer, s);
     // In place the rows of one column stay in registers: narrower columns for
     // more beams.
     if (W_out <= 4)
-        return launch_reorder<4, 16, true>(a, n_outer, s);
+        return launch_reorder<4, 16, true>(a, B, H, n_outer, s);
     if (W_out <= 8)
-        return launch_reorder<8, 16, true>(a, n_outer, s);
+        return launch_reorder<8, 16, true>(a, B, H, n_outer, s);
     if (W_out <= 16)
-        return launch_reorder<16, 16, true>(a, n_outer, s);
+        return launch_reorder<16, 16, true>(a, B, H, n_outer, s);
     if (W_out <= 32)
-        return launch_reorder<32, 8, true>(a, n_outer, s);
-    return launch_reorder<64, 4, true>(a, n_outer, s);
+        return launch_reorder<32, 8, true>(a, B, H, n_outer, s);
+    return launch_reorder<64, 4, true>(a, B, H, n_outer, s);
 }
 
 }  // namespace lmh
