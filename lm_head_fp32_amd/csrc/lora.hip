@@ -1137,13 +1137,11 @@ int64_t few_units(int64_t M, int64_t n)
 
 // Parts of K of the shrink beyond kFewTokens tokens: enough for 512
 // workgroups, at most 32, at least 256 columns each.
-#ifndef LMH_SHRINK_WGS
-#define LMH_SHRINK_WGS 512
-#endif
+constexpr int64_t kShrinkWorkgroups = 512;
 int64_t shrink_parts(int64_t M, int64_t K)
 {
     const int64_t blocks = std::max<int64_t>(1, (M + 63) / 64);
-    return std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(32, K / 256), LMH_SHRINK_WGS / blocks));
+    return std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(32, K / 256), kShrinkWorkgroups / blocks));
 }
 
 hipError_t launch_join(const float *parts, int64_t n_parts, int64_t M, int RP, const LoraAdapters &ad,
@@ -1214,12 +1212,10 @@ hipError_t launch_expand(const float *z, int64_t ldz, void *out, int64_t ldo, bo
     }
     // Token blocks per workgroup: up to eight (B rows kept across a request's
     // tokens, loads ahead of stores) while 1024 workgroups remain.
-#ifndef LMH_EXPAND_NB
-#define LMH_EXPAND_NB 8
-#endif
+    constexpr int64_t kMostBlocks = 8;
     const int64_t tb = (M + 15) / 16, vts = (V + 255) / 256;
     const int nb = static_cast<int>(
-        std::max<int64_t>(1, std::min<int64_t>(LMH_EXPAND_NB, tb * vts / 1024)));
+        std::max<int64_t>(1, std::min<int64_t>(kMostBlocks, tb * vts / 1024)));
     const int64_t groups = (tb + nb - 1) / nb;
     // Whole groups of eight vocabulary tiles (the tiles past V exit).
     const int64_t wgs = (vts + 7) / 8 * 8 * groups, most = kMaxItems / 256;
