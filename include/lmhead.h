@@ -398,7 +398,8 @@ int32_t lmhead_wgrad(const void *dlogits, int64_t ldd, const void *x, int64_t ld
  *  One token's result depends on its own x and adapter only: a NaN or infinity
  *  in another token or another adapter of the batch does not reach it.
  *  A x is an FP32 sum and enters the second product unrounded (in three BF16
- *  pieces of 8 bits).
+ *  pieces of 8 bits, some of them zero: an infinity in a token's own row of B
+ *  gives an infinity or NaN).
  *  workspace: device memory of at least lmhead_logits_lora_workspace_bytes(M,
  *  K, V, rank, out_dtype) bytes (negative LMH_ERR_* for bad sizes), 16-byte
  *  aligned; its contents do not matter on entry.  Two calls that share one
@@ -431,7 +432,8 @@ int32_t lmhead_logits_lora(const void *x, int64_t ldx, const void *W, int64_t ld
  *  computed).  accumulate == 0 overwrites them (an adapter without tokens and
  *  a token without an adapter get zeros), accumulate != 0 adds to them.  A
  *  token whose id is >= n_adapters gets a NaN row in dX and enters no other
- *  gradient.  u and t are FP32 sums, not rounded before the second product.
+ *  gradient.  u and t are FP32 sums, not rounded before the second product (an
+ *  infinity that meets them gives an infinity or NaN, as in the forward).
  *  Results are deterministic.
  *  workspace as lmhead_logits_lora, of lmhead_lora_bwd_workspace_bytes(M, K,
  *  V, rank, n_adapters) bytes.  Limits (LMH_ERR_SHAPE): M <= 2^22,
@@ -458,8 +460,9 @@ int32_t lmhead_lora_bwd(const void *dlogits, int64_t ldd, const void *x, int64_t
  *  except that a finished beam has c = scores[b][w] at v = eos and -inf
  *  elsewhere.  A NaN c counts as -inf, as does every candidate of a beam whose
  *  score is NaN or +inf.  The n_out largest are returned in descending order,
- *  equal ones by ascending w n_cols + v:
- *    out_scores[b][i] = c (computed in FP64, rounded once to FP32),
+ *  equal ones by ascending w, then descending logit, then ascending v:
+ *    out_scores[b][i] = c (computed in FP64, the sum of exponentials with a
+ *    relative error below 4e-9; rounded once to FP32),
  *    out_parent[b][i] = w, out_token[b][i] = v,
  *    out_finished[b][i] = 1 if beam w was finished or v == eos, else 0.
  *  The logits are read once; rows of finished beams and of beams whose score
@@ -501,8 +504,8 @@ int32_t lmhead_beam_select(const void *logits, int64_t ld, int32_t logits_dtype,
  *  In place: dst == src with equal strides and beams_out == beams_in; any
  *  parent map, rows that stay are not touched.  Any other overlap of dst with
  *  src, parent or lengths is LMH_ERR_ALIAS.  The runs of dst must be disjoint
- *  (LMH_ERR_SHAPE).  Limits: beams <= 64; n_requests n_heads ceil(n_positions
- *  position_bytes / 1024) <= 2^23; spans up to 2^44 bytes.
+ *  (LMH_ERR_SHAPE).  Limits: beams <= 64; n_requests n_heads (n_positions
+ *  position_bytes / 1024 + 2) <= 2^23; spans up to 2^44 bytes.
  */
 int32_t lmhead_beam_reorder(const void *src, int64_t src_outer, int64_t src_row, int64_t src_head,
                             void *dst, int64_t dst_outer, int64_t dst_row, int64_t dst_head,

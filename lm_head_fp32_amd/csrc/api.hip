@@ -963,8 +963,9 @@ int32_t lmhead_beam_reorder(const void *src, int64_t src_outer, int64_t src_row,
         return LMH_ERR_NULL;
     if (!aligned4(parent) || (lengths && !aligned4(lengths)))
         return LMH_ERR_ALIGN;
-    // One launch covers at least one outer block.
-    const int64_t per_row = ceil_div(run, 256 * 4);
+    // One launch in place covers at least one outer block (rows take an odd
+    // number of workgroups).
+    const int64_t per_row = ceil_div(run, 256 * 4) | 1;
     if (per_row > kMaxLaunchItems / 256 || n_requests > kMaxLaunchItems / 256 / per_row ||
         n_heads > kMaxLaunchItems / 256 / per_row / n_requests)
         return LMH_ERR_SHAPE;

@@ -4,8 +4,9 @@
 //
 // Selection, per request b with W beams over V tokens:
 //   c(w, v) = s_w + (z_wv - logZ_w),  logZ_w = m_w + log sum_v exp(z_wv - m_w)
-// and the n_out largest c in descending order, equal ones by ascending
-// w V + v.  Within a beam the order of c is the order of z, so one pass over
+// and the n_out largest c in descending order, equal ones by ascending w, then
+// descending z, then ascending v (by w V + v, then, unless logits differ by less
+// than c resolves).  Within a beam the order of c is the order of z, so one pass over
 // the logits suffices: every wave reads one segment of a row into registers
 // and leaves the segment's {max, sum of exponentials} and its n_out largest
 // logits; a second kernel folds the sums, turns the kept logits into scores
@@ -347,10 +348,23 @@ __global__ __launch_bounds__(kScanWaves * 64) void beam_scan_kernel(
     }
 }
 
-// (a, fa) before (b, fb): larger score, equal scores by ascending position.
-__device__ __forceinline__ bool before(double a, uint32_t fa, double b, uint32_t fb)
+// A candidate: its score, its beam and its key in the beam's lists (larger: a
+// larger logit, or an equal one of an earlier token).  `before`: larger score,
+// equal scores by ascending beam, then descending key.  The scores of a beam
+// whose logits are tiny can be equal where the logits are not; the lists hold
+// the largest logits, so the logits decide.
+struct Pick {
+    double c;
+    uint64_t key;
+    int32_t w;
+};
+__device__ __forceinline__ bool before(const Pick &a, const Pick &b)
 {
-    return a > b || (a == b && fa < fb);
+    return a.c > b.c || (a.c == b.c && (a.w < b.w || (a.w == b.w && a.key > b.key)));
+}
+__device__ __forceinline__ uint32_t key_token(uint64_t key)
+{
+    return 0xffffffffu - static_cast<uint32_t>(key);
 }
 
 constexpr int kMergeThreads = 512;
@@ -373,10 +387,10 @@ __global__ __launch_bounds__(kMergeThreads) void beam_merge_kernel(
     __shared__ uint8_t fin[kBeamMax];
     __shared__ uint32_t group[64];
     __shared__ double cs[kMergeCap];
-    __shared__ uint32_t cf[kMergeCap];
+    __shared__ uint64_t ck[kMergeCap];
+    __shared__ int32_t cw[kMergeCap];
     __shared__ uint32_t n_cand;
-    __shared__ double red_c[NW];
-    __shared__ uint32_t red_f[NW];
+    __shared__ Pick red[NW];
 
     const int64_t b = blockIdx.x;
     const int tid = threadIdx.x, lane = tid & 63;
@@ -425,10 +439,8 @@ __global__ __launch_bounds__(kMergeThreads) void beam_merge_kernel(
         return static_cast<double>(sc[w]) +
                (static_cast<double>(key_value(static_cast<uint32_t>(key >> 32))) - logz[w]);
     };
-    auto flat_of = [&](int w, uint64_t key) {
-        return static_cast<uint32_t>(w * V) + (0xffffffffu - static_cast<uint32_t>(key));
-    };
-    // A finished beam's one candidate.
+    // A finished beam's one candidate, at `eos`.
+    const uint64_t held_key = 0xffffffffu - static_cast<uint32_t>(eos);
     auto held = [&](int w) { return fin[w] && score_alive(sc[w]) && eos >= 0 && eos < V; };
 
     double head = -INFINITY;
@@ -458,11 +470,12 @@ __global__ __launch_bounds__(kMergeThreads) void beam_merge_kernel(
     }
     t = max(t, order_key(-INFINITY) + 1u);
     const double tv = static_cast<double>(key_value(t));
-    auto append = [&](double c, uint32_t f) {
+    auto append = [&](double c, int w, uint64_t key) {
         const uint32_t at = atomicAdd(&n_cand, 1u);
         if (at < kMergeCap) {
             cs[at] = c;
-            cf[at] = f;
+            ck[at] = key;
+            cw[at] = w;
         }
     };
     if (head >= tv) {
@@ -483,20 +496,18 @@ __global__ __launch_bounds__(kMergeThreads) void beam_merge_kernel(
                     const double c = score_of(w, key[e]);
                     more = more && key[e] && c >= tv;
                     if (more)
-                        append(c, flat_of(w, key[e]));
+                        append(c, w, key[e]);
                 }
                 if (!more)
                     break;
             }
         }
         if (tid < W && held(tid) && static_cast<double>(sc[tid]) >= tv)
-            append(static_cast<double>(sc[tid]), static_cast<uint32_t>(tid * V) + static_cast<uint32_t>(eos));
+            append(static_cast<double>(sc[tid]), tid, held_key);
     }
     __syncthreads();
 
-    auto emit = [&](int i, double c, uint32_t f) {
-        const int w = static_cast<int>(f / V);
-        const int32_t tok = static_cast<int32_t>(f - static_cast<uint32_t>(w * V));
+    auto emit = [&](int i, double c, int w, int32_t tok) {
         const int64_t o = b * k + i;
         out_scores[o] = static_cast<float>(c);
         out_parent[o] = w;
@@ -507,27 +518,24 @@ __global__ __launch_bounds__(kMergeThreads) void beam_merge_kernel(
     int found;
     if (n <= kMergeCap) {
         for (int i = tid; i < n; i += kMergeThreads) {
-            const double c = cs[i];
-            const uint32_t f = cf[i];
+            const Pick me = {cs[i], ck[i], cw[i]};
             int rank = 0;
             for (int q = 0; q < n; ++q)
-                rank += before(cs[q], cf[q], c, f);
+                rank += before(Pick{cs[q], ck[q], cw[q]}, me);
             if (rank < k)
-                emit(rank, c, f);
+                emit(rank, me.c, me.w, static_cast<int32_t>(key_token(me.key)));
         }
         found = min(n, k);
     } else {
         // Rows of ties: k rounds over every kept candidate, each taking the
         // best one after the last.
-        double lc = INFINITY;
-        uint32_t lf = 0;
+        Pick last = {INFINITY, 0, -1};
         found = 0;
         for (int rank = 0; rank < k; ++rank) {
-            double bc = -INFINITY;
-            uint32_t bf = 0xffffffffu;
-            auto offer = [&](double c, uint32_t f) {
-                if ((rank == 0 || before(lc, lf, c, f)) && before(c, f, bc, bf))
-                    bc = c, bf = f;
+            Pick best = {-INFINITY, 0, kBeamMax};
+            auto offer = [&](const Pick &p) {
+                if (before(last, p) && before(p, best))
+                    best = p;
             };
             for (int64_t l = l0; l < n_lists; l += kMergeThreads) {
                 const int w = static_cast<int>(l / nseg);
@@ -535,30 +543,30 @@ __global__ __launch_bounds__(kMergeThreads) void beam_merge_kernel(
                     continue;
                 const uint64_t *q = lists + (row0 * nseg + l) * k;
                 for (int i = 0; i < k && q[i]; ++i)
-                    offer(score_of(w, q[i]), flat_of(w, q[i]));
+                    offer(Pick{score_of(w, q[i]), q[i], w});
             }
             if (tid < W && held(tid))
-                offer(static_cast<double>(sc[tid]), static_cast<uint32_t>(tid * V) + static_cast<uint32_t>(eos));
+                offer(Pick{static_cast<double>(sc[tid]), held_key, tid});
 #pragma unroll
             for (int off = 32; off >= 1; off >>= 1) {
-                const double oc = shfl_xor_f64(bc, off);
-                const uint32_t of = __shfl_xor(bf, off, 64);
-                if (before(oc, of, bc, bf))
-                    bc = oc, bf = of;
+                const Pick o = {shfl_xor_f64(best.c, off), shfl_xor_u64(best.key, off),
+                                __shfl_xor(best.w, off, 64)};
+                if (before(o, best))
+                    best = o;
             }
             if (lane == 0)
-                red_c[wave] = bc, red_f[wave] = bf;
+                red[wave] = best;
             __syncthreads();
-            bc = red_c[0], bf = red_f[0];
+            best = red[0];
             for (int q = 1; q < NW; ++q)
-                if (before(red_c[q], red_f[q], bc, bf))
-                    bc = red_c[q], bf = red_f[q];
+                if (before(red[q], best))
+                    best = red[q];
             __syncthreads();
-            if (bc == -INFINITY)
+            if (best.c == -INFINITY)
                 break;
             if (tid == 0)
-                emit(rank, bc, bf);
-            lc = bc, lf = bf;
+                emit(rank, best.c, best.w, static_cast<int32_t>(key_token(best.key)));
+            last = best;
             ++found;
         }
     }
@@ -569,9 +577,9 @@ __global__ __launch_bounds__(kMergeThreads) void beam_merge_kernel(
     for (uint32_t f0 = 0; f0 < total && found < k; f0 += 64) {
         const uint32_t f = f0 + lane;
         bool none = false;
+        const int w = f < total ? static_cast<int>(f / V) : 0;
+        const int64_t v = f - static_cast<uint32_t>(w * V);
         if (f < total) {
-            const int w = static_cast<int>(f / V);
-            const int64_t v = f - static_cast<uint32_t>(w * V);
             if (fin[w]) {
                 none = v != eos || !score_alive(sc[w]);
             } else if (!(logz[w] == logz[w])) {
@@ -587,7 +595,7 @@ __global__ __launch_bounds__(kMergeThreads) void beam_merge_kernel(
         const uint64_t mask = __ballot(none);
         const int pos = found + __popcll(mask & ((1ull << lane) - 1ull));
         if (none && pos < k)
-            emit(pos, -INFINITY, f);
+            emit(pos, -INFINITY, w, static_cast<int32_t>(v));
         found += __popcll(mask);
     }
 }
@@ -595,12 +603,14 @@ __global__ __launch_bounds__(kMergeThreads) void beam_merge_kernel(
 // ---------------------------------------------------------------------------
 // Reordering.  dst row (o, b W_out + i, h) <- src row (o, b W_in + parent[b][i],
 // h), the first live_b bytes of it (live_b = positions x bytes per position).
-// One thread moves the same 16 (8, 4) bytes of every beam of a request: in
-// place it reads all the rows it needs before it writes any, so rows may trade
-// places with no second buffer, and rows that stay are neither read nor
-// written.  A copy, bound by the bytes of the rows that move.  Rows need no
-// alignment: a vector starts at any byte (the hardware takes unaligned
-// global accesses), and the last live_b % 16 bytes go one by one.
+// A copy, bound by the bytes of the rows that move.  Rows need no alignment: a
+// vector starts at any byte (the hardware takes unaligned global accesses),
+// and the last live_b % 16 bytes go one by one.
+//
+// A row takes an odd number of workgroups.  Workgroups go round the eight XCDs
+// in turn, so with an even number the same XCDs would always hold the rows'
+// ends, which a request's length often cuts off (1 GB of [16][64][8][1024][64]
+// BF16 with lengths of 1 .. 1024: 230 -> 159 us).
 struct ReorderArgs {
     const char *src;
     char *dst;
@@ -632,59 +642,87 @@ struct VecOf<1> {
 };
 
 // The result is not read again by this kernel: its stores are marked as
-// streamed once (1 GB cache: 250 -> 236 us; marking the loads as well lost what
-// a small state's rows gain from the caches, 7 -> 10 us).
+// streamed once (1 GB cache: 219 -> 200 us; marking the loads as well lost what
+// a small state's rows gain from the caches, 6.0 -> 8.5 us).
 template <int VB>
 __device__ __forceinline__ void store_vec(char *p, typename VecOf<VB>::type v)
 {
     __builtin_nontemporal_store(v, reinterpret_cast<typename VecOf<VB>::type *>(p));
 }
 
-// VB bytes of every beam.
-template <int WMAX, int VB, bool IN_PLACE>
-__device__ __forceinline__ void move_column(const char *s, char *d, int64_t ssr, int64_t dsr, const int32_t *par,
-                                            int32_t W_in, int32_t W_out)
+// Into other memory: a workgroup moves 8 KiB of one destination row, two
+// vectors a thread.  The destination rows of a request that may share a parent
+// are eight workgroups apart, on one XCD, whose L2 then serves the second
+// reader.  Unit u = ((o H + h) B + b) blocks_per_row + block; each has W_out
+// workgroups.  (1 GB as above: 150 us, 5.9 TB/s; 7 requests x 5 beams of some
+// 6 MB: 6.4 us.  All rows of a request in one thread, as in place: 159 and
+// 6.9 us; one vector a thread 260 and 8.8 us, four 161 and 6.1 us.)
+constexpr int kCopyVecs = 2;
+
+__global__ __launch_bounds__(256) void beam_copy_kernel(ReorderArgs a, uint32_t unit0, uint32_t units,
+                                                        uint32_t blocks_per_row, uint32_t B, uint32_t H)
 {
-    typedef typename VecOf<VB>::type vec;
-    if constexpr (IN_PLACE) {
-        // All rows are read before any is written; those that stay (or have no
-        // parent) are neither.
-        vec r[WMAX];
-        uint64_t moves = 0;
+    typedef typename VecOf<16>::type vec;
+    constexpr int kStep = 256 * 16;
+    const uint32_t W = static_cast<uint32_t>(a.W_out);
+    const uint32_t eight = blockIdx.x / (8 * W), at8 = blockIdx.x - eight * 8 * W;
+    const uint32_t i = at8 / 8, unit = unit0 + eight * 8 + at8 % 8;
+    if (unit >= units)
+        return;
+    const uint32_t ohb = unit / blocks_per_row, blk = unit - ohb * blocks_per_row;
+    const uint32_t oh = ohb / B, b = ohb - oh * B;
+    const uint32_t o = oh / H, h = oh - o * H;
+    const int32_t p = a.parent[static_cast<int64_t>(b) * W + i];
+    int64_t len = a.T;
+    if (a.lengths)
+        len = min(max(static_cast<int64_t>(a.lengths[b]), int64_t{0}), a.T);
+    const int64_t at = static_cast<int64_t>(blk) * kStep * kCopyVecs + threadIdx.x * 16;
+    const int64_t left = len * a.pos_bytes - at;
+    if (left <= 0 || p < 0 || p >= a.W_in)
+        return;
+    const char *s = a.src + o * a.src_so + (static_cast<int64_t>(b) * a.W_in + p) * a.src_sr + h * a.src_sh + at;
+    char *d = a.dst + o * a.dst_so + (static_cast<int64_t>(b) * W + i) * a.dst_sr + h * a.dst_sh + at;
+    vec r[kCopyVecs];
 #pragma unroll
-        for (int i = 0; i < WMAX; ++i) {
-            const int32_t p = i < W_out ? par[i] : -1;
-            if (p >= 0 && p < W_in && p != i) {
-                moves |= uint64_t{1} << i;
-                r[i] = *reinterpret_cast<const vec *>(s + p * ssr);
-            }
-        }
+    for (int u = 0; u < kCopyVecs; ++u)
+        if (kStep * u + 16 <= left)
+            r[u] = *reinterpret_cast<const vec *>(s + kStep * u);
 #pragma unroll
-        for (int i = 0; i < WMAX; ++i)
-            if ((moves >> i) & 1)
-                store_vec<VB>(d + i * dsr, r[i]);
-    } else {
-        for (int i0 = 0; i0 < W_out; i0 += WMAX) {
-            vec r[WMAX];
-            uint64_t moves = 0;
-#pragma unroll
-            for (int i = 0; i < WMAX; ++i) {
-                const int32_t p = i0 + i < W_out ? par[i0 + i] : -1;
-                if (p >= 0 && p < W_in) {
-                    moves |= uint64_t{1} << i;
-                    r[i] = *reinterpret_cast<const vec *>(s + p * ssr);
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < WMAX; ++i)
-                if ((moves >> i) & 1)
-                    store_vec<VB>(d + (i0 + i) * dsr, r[i]);
-        }
+    for (int u = 0; u < kCopyVecs; ++u) {
+        if (kStep * u + 16 <= left)
+            store_vec<16>(d + kStep * u, r[u]);
+        else
+            for (int64_t e = kStep * u; e < kStep * u + 16 && e < left; ++e)
+                d[e] = s[e];
     }
 }
 
-template <int WMAX, int VB, bool IN_PLACE>
-__global__ __launch_bounds__(256) void beam_reorder_kernel(ReorderArgs a, uint32_t blocks_per_row,
+// In place: one thread moves the same VB bytes of every beam of a request.  It
+// reads all the rows it needs before it writes any, so rows may trade places
+// with no second buffer, and rows that stay (or have no parent) are neither
+// read nor written.
+template <int WMAX, int VB>
+__device__ __forceinline__ void move_column(char *d, int64_t sr, const int32_t *par, int32_t W)
+{
+    typedef typename VecOf<VB>::type vec;
+    vec r[WMAX];
+    uint64_t moves = 0;
+#pragma unroll
+    for (int i = 0; i < WMAX; ++i) {
+        const int32_t p = i < W ? par[i] : -1;
+        if (p >= 0 && p < W && p != i) {
+            moves |= uint64_t{1} << i;
+            r[i] = *reinterpret_cast<const vec *>(d + p * sr);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < WMAX; ++i)
+        if ((moves >> i) & 1)
+            store_vec<VB>(d + i * sr, r[i]);
+}
+
+template <int WMAX, int VB>
+__global__ __launch_bounds__(256) void beam_permute_kernel(ReorderArgs a, uint32_t blocks_per_row,
                                                            uint32_t B, uint32_t H)
 {
     // blockIdx.x = ((o * H + h) * B + b) * blocks_per_row + block, below 2^23
@@ -699,32 +737,60 @@ __global__ __launch_bounds__(256) void beam_reorder_kernel(ReorderArgs a, uint32
     if (at >= live)
         return;
     const int32_t *par = a.parent + static_cast<int64_t>(b) * a.W_out;
-    const char *s = a.src + o * a.src_so + static_cast<int64_t>(b) * a.W_in * a.src_sr + h * a.src_sh + at;
     char *d = a.dst + o * a.dst_so + static_cast<int64_t>(b) * a.W_out * a.dst_sr + h * a.dst_sh + at;
     if (at + VB <= live) {
-        move_column<WMAX, VB, IN_PLACE>(s, d, a.src_sr, a.dst_sr, par, a.W_in, a.W_out);
+        move_column<WMAX, VB>(d, a.dst_sr, par, a.W_out);
     } else {
         for (int64_t e = 0; at + e < live; ++e)
-            move_column<WMAX, 1, IN_PLACE>(s + e, d + e, a.src_sr, a.dst_sr, par, a.W_in, a.W_out);
+            move_column<WMAX, 1>(d + e, a.dst_sr, par, a.W_out);
     }
 }
 
-template <int WMAX, int VB, bool IN_PLACE>
-hipError_t launch_reorder(const ReorderArgs &a, int64_t B, int64_t H, int64_t n_outer, hipStream_t s)
+constexpr int64_t kMaxBlocks = (int64_t{1} << 31) / 256;  // workgroups of 256 per launch
+
+// Workgroups of `bytes` each that a row takes (odd, see above).
+int64_t row_blocks(const ReorderArgs &a, int64_t bytes)
 {
-    const int64_t per_row = (a.T * a.pos_bytes + 256 * VB - 1) / (256 * VB);
-    constexpr int64_t kMaxBlocks = (int64_t{1} << 31) / 256;
-    // Several launches over outer blocks where one would pass 2^31 work-items.
-    if (per_row > kMaxBlocks || B * H > kMaxBlocks / per_row)
+    return ((a.T * a.pos_bytes + bytes - 1) / bytes) | 1;
+}
+
+hipError_t launch_copy(const ReorderArgs &a, int64_t B, int64_t H, int64_t n_outer, hipStream_t s)
+{
+    const int64_t per_row = row_blocks(a, 256 * 16 * kCopyVecs), per_outer = per_row * B * H;
+    if (per_outer > kMaxBlocks)
         return hipErrorInvalidValue;  // refused by the caller's size check
-    const int64_t per_launch = std::max<int64_t>(1, kMaxBlocks / (per_row * H * B));
-    for (int64_t o = 0; o < n_outer; o += per_launch) {
-        const int64_t no = std::min(per_launch, n_outer - o);
+    const int64_t outers = kMaxBlocks / per_outer, most = kMaxBlocks / (8 * a.W_out) * 8;
+    for (int64_t o = 0; o < n_outer; o += outers) {
         ReorderArgs q = a;
         q.src += o * a.src_so;
         q.dst += o * a.dst_so;
-        hipLaunchKernelGGL((beam_reorder_kernel<WMAX, VB, IN_PLACE>),
-                           dim3(static_cast<unsigned>(no * H * B * per_row)), dim3(256), 0, s, q,
+        const int64_t units = std::min(outers, n_outer - o) * per_outer;
+        for (int64_t u = 0; u < units; u += most) {
+            const int64_t eights = (std::min(most, units - u) + 7) / 8;
+            hipLaunchKernelGGL(beam_copy_kernel, dim3(static_cast<unsigned>(eights * 8 * a.W_out)), dim3(256), 0, s,
+                               q, static_cast<uint32_t>(u), static_cast<uint32_t>(units),
+                               static_cast<uint32_t>(per_row), static_cast<uint32_t>(B),
+                               static_cast<uint32_t>(H));
+            const hipError_t e = hipGetLastError();
+            if (e != hipSuccess)
+                return e;
+        }
+    }
+    return hipSuccess;
+}
+
+template <int WMAX, int VB>
+hipError_t launch_permute(const ReorderArgs &a, int64_t B, int64_t H, int64_t n_outer, hipStream_t s)
+{
+    const int64_t per_row = row_blocks(a, 256 * VB), per_outer = per_row * B * H;
+    if (per_outer > kMaxBlocks)
+        return hipErrorInvalidValue;  // refused by the caller's size check
+    const int64_t outers = kMaxBlocks / per_outer;
+    for (int64_t o = 0; o < n_outer; o += outers) {
+        ReorderArgs q = a;
+        q.dst += o * a.dst_so;
+        hipLaunchKernelGGL((beam_permute_kernel<WMAX, VB>),
+                           dim3(static_cast<unsigned>(std::min(outers, n_outer - o) * per_outer)), dim3(256), 0, s, q,
                            static_cast<uint32_t>(per_row), static_cast<uint32_t>(B), static_cast<uint32_t>(H));
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess)
@@ -788,18 +854,17 @@ hipError_t launch_beam_reorder(const void *src, void *dst, const int64_t (&src_s
     a.T = T;
     a.pos_bytes = pos_bytes;
     if (src != dst)
-        return launch_reorder<4, 16, false>(a, B, H, n_outer, s);
-    // In place the rows of one column stay in registers: narrower columns for
-    // more beams.
+        return launch_copy(a, B, H, n_outer, s);
+    // The rows of one column stay in registers: narrower columns for more beams.
     if (W_out <= 4)
-        return launch_reorder<4, 16, true>(a, B, H, n_outer, s);
+        return launch_permute<4, 16>(a, B, H, n_outer, s);
     if (W_out <= 8)
-        return launch_reorder<8, 16, true>(a, B, H, n_outer, s);
+        return launch_permute<8, 16>(a, B, H, n_outer, s);
     if (W_out <= 16)
-        return launch_reorder<16, 16, true>(a, B, H, n_outer, s);
+        return launch_permute<16, 16>(a, B, H, n_outer, s);
     if (W_out <= 32)
-        return launch_reorder<32, 8, true>(a, B, H, n_outer, s);
-    return launch_reorder<64, 4, true>(a, B, H, n_outer, s);
+        return launch_permute<32, 8>(a, B, H, n_outer, s);
+    return launch_permute<64, 4>(a, B, H, n_outer, s);
 }
 
 }  // namespace lmh

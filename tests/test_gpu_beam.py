@@ -120,6 +120,26 @@ def test_select_ties_go_to_the_lowest_position():
     _check(_rows(zero), s, 10)
 
 
+@pytest.mark.parametrize("W,V,k", [(1, 100, 5), (2, 5000, 8), (3, 2049, 64), (32, 2100, 64)])
+def test_select_logits_apart_by_less_than_a_score_resolves(W, V, k):
+    # Every logit lies below 2^-60, so every score is -log V in 64 bits: the
+    # logits decide within a beam, the lower beam between two.
+    g = torch.Generator(device="cuda").manual_seed(V)
+    z = _rows(1e-19 * torch.rand(W, V, device="cuda", generator=g).add_(1.0))
+    z[:, V // 3] = z[:, V // 2]  # an equal pair
+    got = lmh.lmhead_beam_select(z, torch.zeros(1, W, device="cuda"), n_out=k)
+    want = np.lexsort((np.arange(V), -z[0].cpu().numpy()))[:k]
+    assert not got[1].any() and got[2][0].tolist() == want.tolist()
+    assert (got[0].double().cpu() + np.log(V)).abs().max() <= np.log(V) * 2.0 ** -24 + 4e-9
+
+
+def test_select_eos_outside_32_bits_is_refused():
+    z, s, _ = _random(1, 2, 100, torch.float32, 0)
+    for eos in (2 ** 31, -2 ** 31 - 1, 2 ** 32 + 3):
+        with pytest.raises(ValueError):
+            lmh.lmhead_beam_select(z, s, eos=eos)
+
+
 def test_select_masked_and_bad_rows():
     inf, nan = float("inf"), float("nan")
     for dtype in (torch.float32, torch.bfloat16):
@@ -333,6 +353,20 @@ def test_reorder_past_32_bit_offsets():
     assert st[:, 7].tolist() == [1, 0, 2, 3, 5, 3]
     assert st[:, -1].tolist() == [2, 1, 3, 4, 6, 4] and st[:, T - 3].tolist() == [2, 1, 3, 4, 6, 4]
     assert not st[:, 8:1024].any()
+
+
+@pytest.mark.parametrize("n_outer,B,W", [(1, 140001, 64), (3, 2 ** 22 - 1, 2)])
+def test_reorder_of_many_short_rows(n_outer, B, W):
+    """More rows than one launch covers."""
+    g = torch.Generator(device="cuda").manual_seed(B)
+    st = torch.randint(0, 256, (n_outer, B * W, 1), device="cuda", generator=g, dtype=torch.uint8)
+    par = torch.randint(0, W, (B, W), device="cuda", generator=g, dtype=torch.int32)
+    rows = (torch.arange(B, device="cuda")[:, None] * W + par).view(-1)
+    want = st.index_select(1, rows)
+    out = lmh.lmhead_beam_reorder(st, par, out=torch.zeros_like(st), beam_dim=1)
+    assert torch.equal(out, want)
+    lmh.lmhead_beam_reorder(st, par, beam_dim=1)
+    assert torch.equal(st, want)
 
 
 def test_decode_with_adapters_and_beams():
