@@ -190,6 +190,98 @@ __device__ __forceinline__ void group_few(const LoraAdapters &ad, int64_t M, Few
 }
 
 // ---------------------------------------------------------------------------
+// The gradients' grouping of the tokens by adapter (stable): group g < n
+// holds adapter g's tokens, group n the tokens on none, group n + 1 those
+// whose id is not an adapter.  offset[g] is the group's first place in order[].
+// Chunks of up to 64 tokens of one group are numbered too: those of group g
+// start at chunk_base(offset[g], g), with some numbers unused, so that a
+// workgroup can be given a chunk without knowing the counts.
+__host__ __device__ __forceinline__ int64_t chunk_base(int64_t offset, int64_t g)
+{
+    // Room enough: floor((o + c) / 64) - floor(o / 64) + 1 >= ceil(c / 64).
+    return offset / 64 + g;
+}
+
+struct Chunk {
+    int32_t group, first, count, pad;  // its tokens are order[first .. first + count); group -1: unused
+};
+
+struct Grouping {
+    int32_t *offset, *order;
+    Chunk *chunks;
+};
+
+// The work of one workgroup of NT threads for group g: counts the ids below and
+// in its group, then writes its tokens in order, and its chunks.  All groups
+// together read the ids n + 2 times (they stay in L2); no workgroup waits for
+// another.
+template <int NT>
+__device__ __forceinline__ void group_tokens(const int32_t *__restrict__ adapter, int64_t M, int64_t n,
+                                             const Grouping &out, int64_t g)
+{
+    constexpr int NW = NT / 64;
+    __shared__ int32_t part[2][NW];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    auto cls = [&](int32_t id) { return id < 0 ? n : id >= n ? n + 1 : static_cast<int64_t>(id); };
+    int32_t less = 0, same = 0;
+#pragma unroll 4
+    for (int64_t m = tid; m < M; m += NT) {
+        const int64_t c = cls(adapter[m]);
+        less += c < g;
+        same += c == g;
+    }
+#pragma unroll
+    for (int off = 32; off >= 1; off >>= 1) {
+        less += __shfl_xor(less, off, 64);
+        same += __shfl_xor(same, off, 64);
+    }
+    if (lane == 0)
+        part[0][wave] = less, part[1][wave] = same;
+    __syncthreads();
+    int32_t first = 0, count = 0;
+#pragma unroll
+    for (int w = 0; w < NW; ++w)
+        first += part[0][w], count += part[1][w];
+    if (tid == 0) {
+        out.offset[g] = first;
+        if (g == n + 1)
+            out.offset[n + 2] = static_cast<int32_t>(M);
+    }
+    const int64_t c0 = chunk_base(first, g), c1 = chunk_base(first + count, g + 1);
+    for (int64_t c = c0 + tid; c < c1; c += NT) {
+        const int32_t at = static_cast<int32_t>(64 * (c - c0));
+        out.chunks[c] = at < count ? Chunk{static_cast<int32_t>(g), first + at, min(64, count - at), 0}
+                                   : Chunk{-1, 0, 0, 0};
+    }
+    if (count == 0)
+        return;
+    int32_t done = 0;
+    for (int64_t m0 = 0; m0 < M && done < count; m0 += NT) {
+        const int64_t m = m0 + tid;
+        const bool mine = m < M && cls(adapter[m]) == g;
+        const uint64_t mask = __ballot(mine);
+        __syncthreads();  // the round before has read part[0]
+        if (lane == 0)
+            part[0][wave] = __popcll(mask);
+        __syncthreads();
+        int32_t at = done + __popcll(mask & ((1ull << lane) - 1ull));
+#pragma unroll
+        for (int w = 0; w < NW; ++w) {
+            at += w < wave ? part[0][w] : 0;
+            done += part[0][w];
+        }
+        if (mine)
+            out.order[first + at] = static_cast<int32_t>(m);
+    }
+}
+
+__global__ __launch_bounds__(256) void lora_group_kernel(const int32_t *__restrict__ adapter, int64_t M,
+                                                         int64_t n, Grouping out)
+{
+    group_tokens<256>(adapter, M, n, out, blockIdx.x);
+}
+
+// ---------------------------------------------------------------------------
 // u = s_a A_a x, 16 tokens by 16 ranks at a time; NW waves of a workgroup split
 // K and are summed in order through LDS.  Written as pieces, rows
 // [token][piece_row].
@@ -244,14 +336,20 @@ __device__ __forceinline__ float shrink_sum(const f32x4 (&red)[NW][64], int tid)
 
 // At most kFewTokens tokens: one workgroup per unit (blockIdx.x) and 16 ranks,
 // all of K in it -- latency-bound, and a second launch to join parts would cost
-// more.  Leaves the units in `table` for the next kernel.
+// more.  Leaves the units in `table` for the next kernel.  The first n_groups
+// workgroups group the tokens for the gradients instead.
 constexpr int kShrinkThreads = 1024;
 
 __global__ void __launch_bounds__(kShrinkThreads) __attribute__((amdgpu_waves_per_eu(4, 4)))
 lora_shrink_few_kernel(const uint16_t *__restrict__ x, int64_t ldx, int64_t M, int64_t K,
                        LoraAdapters ad, int RP, uint16_t *__restrict__ u3,
-                       FewUnits *__restrict__ table)
+                       FewUnits *__restrict__ table, Grouping groups, unsigned n_groups)
 {
+    if (blockIdx.x < n_groups) {
+        if (blockIdx.y == 0)
+            group_tokens<kShrinkThreads>(ad.adapter, M, ad.n, groups, blockIdx.x);
+        return;
+    }
     constexpr int NW = kShrinkThreads / 64;
     __shared__ f32x4 red[NW][64];
     __shared__ FewUnits t;
@@ -264,7 +362,7 @@ lora_shrink_few_kernel(const uint16_t *__restrict__ x, int64_t ldx, int64_t M, i
         table->u[tid] = t.u[tid];
         table->order[tid] = t.order[tid];
     }
-    const FewUnit u = t.u[blockIdx.x];
+    const FewUnit u = t.u[blockIdx.x - n_groups];
     if (u.count == 0 || u.id < 0 || u.id >= ad.n)
         return;
     const float scale = ad.scale ? ad.scale[u.id] : 1.0f;
@@ -294,18 +392,25 @@ lora_shrink_few_kernel(const uint16_t *__restrict__ x, int64_t ldx, int64_t M, i
 // slots.  A CU draws some 20 - 50 GB/s, so what counts is how few bytes reach
 // it and that every CU has some: x once for all ranks, A shared by the four
 // waves through L1, K in parts whose sums [S][M][RP] lora_join_kernel adds.
-// (M = 1024, K = 8192: rank 64 read 16 x 16 at a time 22 - 30 us.)
+// (M = 1024, K = 8192: rank 64 read 16 x 16 at a time 22 - 30 us.)  The first
+// n_groups workgroups group the tokens for the gradients instead.
 template <int RP>
 __global__ __launch_bounds__(256) void lora_shrink_kernel(const uint16_t *__restrict__ x, int64_t ldx,
                                                           int64_t M, int64_t K, LoraAdapters ad,
-                                                          int64_t wg0, int S, int64_t part_k,
-                                                          float *__restrict__ upart)
+                                                          int S, int64_t part_k,
+                                                          float *__restrict__ upart, Grouping groups,
+                                                          unsigned n_groups)
 {
+    if (blockIdx.x < n_groups) {
+        if (blockIdx.y == 0)
+            group_tokens<256>(ad.adapter, M, ad.n, groups, blockIdx.x);
+        return;
+    }
     constexpr int RB = RP / 16, UN = RB <= 2 ? 8 : RB == 4 ? 4 : 2;
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int t16 = lane & 15, q = lane >> 4;
-    const int64_t wg = wg0 + blockIdx.x, part = wg % S;
+    const int64_t wg = blockIdx.x - n_groups, part = wg % S;
     const int64_t tok = (wg / S * 4 + wave) * 16 + t16;
     const int32_t id = tok < M ? ad.adapter[tok] : -1;
     uint32_t todo = static_cast<uint32_t>(__ballot(id >= 0 && id < ad.n)) & 0xffffu;
@@ -667,82 +772,8 @@ __global__ __launch_bounds__(256) void lora_expand_kernel(const float *z, int64_
 }
 
 // ---------------------------------------------------------------------------
-// Gradients.  The tokens are grouped by adapter first (stable): group g < n
-// holds adapter g's tokens, group n the tokens on none, group n + 1 those
-// whose id is not an adapter.  offset[g] is the group's first place in order[].
-// Chunks of up to 64 tokens of one group are numbered too: those of group g
-// start at chunk_base(offset[g], g), with some numbers unused, so that a
-// workgroup can be given a chunk without knowing the counts.
-__host__ __device__ __forceinline__ int64_t chunk_base(int64_t offset, int64_t g)
-{
-    // Room enough: floor((o + c) / 64) - floor(o / 64) + 1 >= ceil(c / 64).
-    return offset / 64 + g;
-}
-
-struct Chunk {
-    int32_t group, first, count, pad;  // its tokens are order[first .. first + count); group -1: unused
-};
-
-// One workgroup per group: counts the ids below and in its group, then writes
-// its tokens in order, and its chunks.  Reads the ids n + 2 times in all (they
-// stay in L2); no workgroup waits for another.
-__global__ __launch_bounds__(256) void lora_group_kernel(const int32_t *__restrict__ adapter, int64_t M,
-                                                         int64_t n, int32_t *__restrict__ offset,
-                                                         int32_t *__restrict__ order,
-                                                         Chunk *__restrict__ chunks)
-{
-    __shared__ int32_t part[2][4];
-    const int64_t g = blockIdx.x;
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    auto cls = [&](int32_t id) { return id < 0 ? n : id >= n ? n + 1 : static_cast<int64_t>(id); };
-    int32_t less = 0, same = 0;
-#pragma unroll 4
-    for (int64_t m = tid; m < M; m += 256) {
-        const int64_t c = cls(adapter[m]);
-        less += c < g;
-        same += c == g;
-    }
-#pragma unroll
-    for (int off = 32; off >= 1; off >>= 1) {
-        less += __shfl_xor(less, off, 64);
-        same += __shfl_xor(same, off, 64);
-    }
-    if (lane == 0)
-        part[0][wave] = less, part[1][wave] = same;
-    __syncthreads();
-    const int32_t first = part[0][0] + part[0][1] + part[0][2] + part[0][3];
-    const int32_t count = part[1][0] + part[1][1] + part[1][2] + part[1][3];
-    if (tid == 0) {
-        offset[g] = first;
-        if (g == n + 1)
-            offset[n + 2] = static_cast<int32_t>(M);
-    }
-    const int64_t c0 = chunk_base(first, g), c1 = chunk_base(first + count, g + 1);
-    for (int64_t c = c0 + tid; c < c1; c += 256) {
-        const int32_t at = static_cast<int32_t>(64 * (c - c0));
-        chunks[c] = at < count ? Chunk{static_cast<int32_t>(g), first + at, min(64, count - at), 0}
-                               : Chunk{-1, 0, 0, 0};
-    }
-    if (count == 0)
-        return;
-    int32_t done = 0;
-    for (int64_t m0 = 0; m0 < M && done < count; m0 += 256) {
-        const int64_t m = m0 + tid;
-        const bool mine = m < M && cls(adapter[m]) == g;
-        const uint64_t mask = __ballot(mine);
-        __syncthreads();  // the round before has read part[0]
-        if (lane == 0)
-            part[0][wave] = __popcll(mask);
-        __syncthreads();
-        int32_t at = done + __popcll(mask & ((1ull << lane) - 1ull));
-        for (int w = 0; w < wave; ++w)
-            at += part[0][w];
-        if (mine)
-            order[first + at] = static_cast<int32_t>(m);
-        done += part[0][0] + part[0][1] + part[0][2] + part[0][3];
-    }
-}
-
+// Gradients.
+//
 // Staged tiles: 64 rows (tokens, or ranks) of PITCH BF16 words, 16-byte chunk c
 // of row p at chunk c ^ key(p).  Wide rows (16 chunks or more): the key
 // separates the eight rows that a quarter of a row-wise fragment read touches,
@@ -1156,39 +1187,39 @@ hipError_t launch_join(const float *parts, int64_t n_parts, int64_t M, int RP, c
     return hipGetLastError();
 }
 
-// u3 from x; upart: [shrink_parts][M][RP] FP32 (M > kFewTokens only).
+// u3 from x; upart: [shrink_parts][M][RP] FP32 (M > kFewTokens only).  n_groups:
+// groups of tokens to write beside it (ad.n + 2, or 0: none).
 hipError_t launch_shrink(const uint16_t *x, int64_t ldx, int64_t M, int64_t K, const LoraAdapters &ad,
-                         uint16_t *u3, FewUnits *table, float *upart, hipStream_t s)
+                         uint16_t *u3, FewUnits *table, float *upart, const Grouping &groups,
+                         int64_t n_groups, hipStream_t s)
 {
     const int RP = rank_bucket(ad.r);
     const int64_t zr = RP / 16;
     if (M <= kFewTokens) {
-        const dim3 grid(static_cast<unsigned>(few_units(M, ad.n)), static_cast<unsigned>(zr));
+        const dim3 grid(static_cast<unsigned>(n_groups + few_units(M, ad.n)), static_cast<unsigned>(zr));
         hipLaunchKernelGGL(lora_shrink_few_kernel, grid, dim3(kShrinkThreads), 0, s, x, ldx, M, K, ad, RP,
-                           u3, table);
+                           u3, table, groups, static_cast<unsigned>(n_groups));
         return hipGetLastError();
     }
     if (ad.n == 0)
         return hipSuccess;
     const int64_t S = shrink_parts(M, K), part_k = (K + 32 * S - 1) / (32 * S) * 32;
     const int64_t slots = std::min<int64_t>(ad.n, 4);
-    const int64_t wgs = (M + 63) / 64 * S, most = kMaxItems / 256 / slots;
-    for (int64_t w0 = 0; w0 < wgs; w0 += most) {
-        const dim3 grid(static_cast<unsigned>(std::min(most, wgs - w0)), static_cast<unsigned>(slots));
-        auto run = [&](auto kernel) {
-            hipLaunchKernelGGL(kernel, grid, dim3(256), 0, s, x, ldx, M, K, ad, w0, static_cast<int>(S),
-                               part_k, upart);
-        };
-        switch (RP) {
-        case 16: run(lora_shrink_kernel<16>); break;
-        case 32: run(lora_shrink_kernel<32>); break;
-        case 64: run(lora_shrink_kernel<64>); break;
-        default: run(lora_shrink_kernel<128>); break;
-        }
-        const hipError_t e = hipGetLastError();
-        if (e != hipSuccess)
-            return e;
+    const int64_t wgs = (M + 63) / 64 * S;  // < 2^17
+    const dim3 grid(static_cast<unsigned>(n_groups + wgs), static_cast<unsigned>(slots));
+    auto run = [&](auto kernel) {
+        hipLaunchKernelGGL(kernel, grid, dim3(256), 0, s, x, ldx, M, K, ad, static_cast<int>(S), part_k, upart,
+                           groups, static_cast<unsigned>(n_groups));
+    };
+    switch (RP) {
+    case 16: run(lora_shrink_kernel<16>); break;
+    case 32: run(lora_shrink_kernel<32>); break;
+    case 64: run(lora_shrink_kernel<64>); break;
+    default: run(lora_shrink_kernel<128>); break;
     }
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess)
+        return e;
     return launch_join(upart, S, M, RP, ad, u3, s);
 }
 
@@ -1233,6 +1264,8 @@ hipError_t launch_expand(const float *z, int64_t ldz, void *out, int64_t ldo, bo
     }
     return hipSuccess;
 }
+
+constexpr int64_t kGroupsBeside = 1024;
 
 // The gradients' workspace, in order.
 struct BwdLayout {
@@ -1332,7 +1365,8 @@ hipError_t launch_logits_lora(const GemmProblem &p, bool bf16, const LoraAdapter
         f.ldd = (V + 3) / 4 * 4;
     }
     f.stream_out = false;  // read back at once
-    hipError_t e = launch_shrink(p.B, p.ldb, M, K, ad, u3, table, reinterpret_cast<float *>(ws + l.z), s);
+    hipError_t e = launch_shrink(p.B, p.ldb, M, K, ad, u3, table, reinterpret_cast<float *>(ws + l.z),
+                                 Grouping{}, 0, s);
     if (e == hipSuccess)
         e = launch_gemm_logits(f, Epi::kStoreF32, s);
     if (e != hipSuccess)
@@ -1353,13 +1387,23 @@ hipError_t launch_lora_bwd(const LoraBwd &p, void *workspace, hipStream_t s)
     const int RP = rank_bucket(p.ad.r);
     uint16_t *t3 = reinterpret_cast<uint16_t *>(ws + l.t3);
     const int64_t nvb = (p.V + 255) / 256;
-    hipLaunchKernelGGL(lora_group_kernel, dim3(static_cast<unsigned>(p.ad.n + 2)), dim3(256), 0, s,
-                       p.ad.adapter, p.M, p.ad.n, reinterpret_cast<int32_t *>(ws + l.offset),
-                       reinterpret_cast<int32_t *>(ws + l.order), reinterpret_cast<Chunk *>(ws + l.chunks));
-    hipError_t e = hipGetLastError();
-    if (e == hipSuccess && p.dB && p.ad.n > 0 && p.M > 0)
+    const Grouping groups = {reinterpret_cast<int32_t *>(ws + l.offset),
+                             reinterpret_cast<int32_t *>(ws + l.order),
+                             reinterpret_cast<Chunk *>(ws + l.chunks)};
+    const int64_t n_groups = p.ad.n + 2;
+    const bool shrink = p.dB && p.ad.n > 0 && p.M > 0;
+    // One launch for the grouping and u, neither of which needs the other (M =
+    // 1024, K = 8192: FILL); many groups take longer than u and go by themselves.
+    const bool beside = shrink && n_groups <= kGroupsBeside;
+    hipError_t e = hipSuccess;
+    if (!beside) {
+        hipLaunchKernelGGL(lora_group_kernel, dim3(static_cast<unsigned>(n_groups)), dim3(256), 0, s,
+                           p.ad.adapter, p.M, p.ad.n, groups);
+        e = hipGetLastError();
+    }
+    if (e == hipSuccess && shrink)
         e = launch_shrink(p.x, p.ldx, p.M, p.K, p.ad, reinterpret_cast<uint16_t *>(ws + l.u3), nullptr,
-                          reinterpret_cast<float *>(ws + l.parts), s);
+                          reinterpret_cast<float *>(ws + l.parts), groups, beside ? n_groups : 0, s);
     if (e == hipSuccess && p.ad.n > 0 && p.V > 0) {
         switch (RP) {
         case 16: e = launch_bwd_v<16>(p, l, ws, s); break;

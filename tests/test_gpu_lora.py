@@ -241,6 +241,12 @@ def test_bwd_integers_exact(M, K, V, r, n, order):
         assert _untouched(one[i])
 
 
+@pytest.mark.parametrize("M,n", [(90, 1022), (90, 1023), (400, 1022), (400, 1200)])
+def test_bwd_many_adapters(M, n):
+    """More adapters than are grouped beside the first product, and just as many."""
+    test_bwd_integers_exact(M, 40, 30, 2, n, "mixed")
+
+
 @pytest.mark.parametrize("M,K,V,r,n", [(101, 2048, 3003, 8, 3), (256, 1024, 2048, 64, 2),
                                        (40, 512, 1000, 128, 2)])
 def test_bwd_random(M, K, V, r, n):
