@@ -913,9 +913,12 @@ __device__ __forceinline__ void store_f32x4(float *p, f32x4 v, int64_t n, bool a
 
 // One workgroup per (256 vocabulary columns, adapter): walks the adapter's
 // tokens 64 at a time and takes both products from one read of g: its part of
-// t (over these 256 columns; joined by lora_t_kernel) and dB (accumulated over
-// the tokens in registers).  B^T sits in LDS.  Bound by the one read of g;
-// the parts of t cost 8 RP bytes per token and block against 512 of g.
+// t (over these 256 columns; joined by lora_join_kernel) and dB (accumulated over
+// the tokens in registers).  B^T sits in LDS.  Bound by the one read of g (M =
+// 1024, V = 32768, 4 adapters of rank 16: 20 us, 3.4 TB/s with 3 us to start and
+// drain and 4 us of dependent loads -- group, token numbers, rows -- before the
+// stream); a second chunk in flight gained nothing (22 us).  The parts of t cost
+// 8 RP bytes per token and block against 512 of g.
 template <int RP>
 __global__ __launch_bounds__(256) void lora_bwd_v_kernel(
     const uint16_t *__restrict__ g, int64_t ldg, int64_t M, int64_t V, LoraAdapters ad,
@@ -1024,7 +1027,8 @@ __global__ __launch_bounds__(256) void lora_bwd_v_kernel(
 // x; the others write dX = t A of one chunk of up to 64 tokens, A_a's block in
 // LDS (tokens on no adapter get zeros, those whose id is none NaN).  One launch,
 // so that the two share the chip: dA has few workgroups, dX many short ones.
-// Bound by writing dX.
+// Bound by writing dX (M = 1024, K = 8192, 4 adapters of rank 16: 13 us for 17 MB
+// read and 34 MB written, 3.8 TB/s).
 template <int RP>
 __global__ __launch_bounds__(256) void lora_bwd_k_kernel(
     const uint16_t *__restrict__ x, int64_t ldx, int64_t K, LoraAdapters ad,
@@ -1242,7 +1246,9 @@ hipError_t launch_expand(const float *z, int64_t ldz, void *out, int64_t ldo, bo
         return hipGetLastError();
     }
     // Token blocks per workgroup: up to eight (B rows kept across a request's
-    // tokens, loads ahead of stores) while 1024 workgroups remain.
+    // tokens, loads ahead of stores) while 1024 workgroups remain.  M = 1024, V =
+    // 32768, 16 adapters of rank 64: 70 us; one block 105 us, two to sixteen within 4 % of
+    // eight.
     constexpr int64_t kMostBlocks = 8;
     const int64_t tb = (M + 15) / 16, vts = (V + 255) / 256;
     const int nb = static_cast<int>(
@@ -1393,7 +1399,8 @@ hipError_t launch_lora_bwd(const LoraBwd &p, void *workspace, hipStream_t s)
     const int64_t n_groups = p.ad.n + 2;
     const bool shrink = p.dB && p.ad.n > 0 && p.M > 0;
     // One launch for the grouping and u, neither of which needs the other (M =
-    // 1024, K = 8192: FILL); many groups take longer than u and go by themselves.
+    // 1024, K = 8192: 4.5 + 7.6 -> 8 us); beyond kGroupsBeside groups the
+    // grouping is the longer of the two and goes by itself.
     const bool beside = shrink && n_groups <= kGroupsBeside;
     hipError_t e = hipSuccess;
     if (!beside) {
