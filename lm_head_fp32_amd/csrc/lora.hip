@@ -104,9 +104,12 @@ __host__ __device__ constexpr int piece_row(int RP)
 }
 
 // Batches of at most kFewTokens tokens are walked by adapter instead of by
-// blocks of 16 neighbouring tokens: each adapter's weights are then read once
-// per tile however the batch mixes its requests, and the adapters spread over
-// workgroups.
+// blocks of 16 tokens: each adapter's weights are then read once per tile however
+// the batch mixes its requests, the adapters spread over workgroups, and two
+// launches do instead of three.  Shrink (and join) + expand at 256 tokens this
+// way and at 257 the other, K = 4096, V = 32768: 32 mixed adapters of rank 16 40
+// and 51 us, 4 in runs 34 and 33 us; 16 mixed of rank 64 50 and 65 us, 4 in runs
+// 43 and 41 us.
 constexpr int kFewTokens = 256;
 
 // Such a batch in units of up to 16 tokens of one adapter: unit i holds tokens
@@ -275,6 +278,43 @@ __device__ __forceinline__ void group_tokens(const int32_t *__restrict__ adapter
     }
 }
 
+// The logits' order of more than kFewTokens tokens: by adapter within windows of
+// kWindow tokens (then by place), tokens on none last, so that a block of 16 in
+// that order has one adapter or two however the batch mixes its requests (320
+// tokens mixing 16 adapters of rank 64, V = 32768: expand 131 -> 38 us; runs as
+// before).  One
+// workgroup of 256 per 64 tokens (lane: token), each wave counting the keys ahead
+// of them in a quarter of the window.
+constexpr int kWindow = 1024;
+
+__device__ __forceinline__ void order_tokens(const int32_t *__restrict__ adapter, int64_t M,
+                                             int32_t *__restrict__ order, int64_t block)
+{
+    __shared__ __attribute__((aligned(16))) uint32_t key[kWindow];
+    __shared__ int32_t part[4][64];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int64_t w0 = block * 64 / kWindow * kWindow;
+    for (int i = tid; i < kWindow; i += 256)  // none: 2^31 and up; past M: the last
+        key[i] = w0 + i < M ? static_cast<uint32_t>(adapter[w0 + i]) : 0xffffffffu;
+    __syncthreads();
+    const int me = static_cast<int>(block * 64 - w0) + lane;
+    const uint32_t k = key[me];
+    int ahead = 0;
+#pragma unroll 4
+    for (int i = wave * (kWindow / 4); i < (wave + 1) * (kWindow / 4); i += 4) {
+        const uint4 o = *reinterpret_cast<const uint4 *>(key + i);
+        const uint32_t v[4] = {o.x, o.y, o.z, o.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            ahead += v[e] < k || (v[e] == k && i + e < me);
+    }
+    part[wave][lane] = ahead;
+    __syncthreads();
+    if (wave == 0 && w0 + me < M)
+        order[w0 + part[0][lane] + part[1][lane] + part[2][lane] + part[3][lane]] =
+            static_cast<int32_t>(w0 + me);
+}
+
 __global__ __launch_bounds__(256) void lora_group_kernel(const int32_t *__restrict__ adapter, int64_t M,
                                                          int64_t n, Grouping out)
 {
@@ -393,7 +433,8 @@ lora_shrink_few_kernel(const uint16_t *__restrict__ x, int64_t ldx, int64_t M, i
 // it and that every CU has some: x once for all ranks, A shared by the four
 // waves through L1, K in parts whose sums [S][M][RP] lora_join_kernel adds.
 // (M = 1024, K = 8192: rank 64 read 16 x 16 at a time 22 - 30 us.)  The first
-// n_groups workgroups group the tokens for the gradients instead.
+// n_groups workgroups group the tokens for the gradients, or (no `offset`) put
+// them in the logits' order, instead.
 template <int RP>
 __global__ __launch_bounds__(256) void lora_shrink_kernel(const uint16_t *__restrict__ x, int64_t ldx,
                                                           int64_t M, int64_t K, LoraAdapters ad,
@@ -402,8 +443,12 @@ __global__ __launch_bounds__(256) void lora_shrink_kernel(const uint16_t *__rest
                                                           unsigned n_groups)
 {
     if (blockIdx.x < n_groups) {
-        if (blockIdx.y == 0)
+        if (blockIdx.y != 0)
+            return;
+        if (groups.offset)
             group_tokens<256>(ad.adapter, M, ad.n, groups, blockIdx.x);
+        else
+            order_tokens(ad.adapter, M, groups.order, blockIdx.x);
         return;
     }
     constexpr int RB = RP / 16, UN = RB <= 2 ? 8 : RB == 4 ? 4 : 2;
@@ -646,24 +691,30 @@ lora_expand_few_kernel(const float *z, int64_t ldz, void *out, int64_t ldo, int6
 // ---------------------------------------------------------------------------
 // logits += u B^T: reads the FP32 product z, adds each token's adapter, stores
 // FP32 (in place) or BF16 (rounded once).  A workgroup covers 256 vocabulary
-// rows and `nb` blocks of 16 tokens, one after another; wave w holds rows
-// 64 w .. + 63 as four 16 x 16 results per block.  B rows go straight from
-// memory into matrix operands (a fragment is 16 contiguous bytes of a row) and
-// stay there while the next block uses the same adapter; z and the result move
-// in whole 256-byte row pieces, the products turned through 4 KiB of LDS per
-// wave.  Bound by z, read and written once, and by B of the adapters in use.
+// rows and `nb` blocks of 16 tokens of the logits' order, one after another;
+// wave w holds rows 64 w .. + 63 as four 16 x 16 results per block.  B rows go
+// straight from memory into matrix operands (a fragment is 16 contiguous bytes
+// of a row) and stay there while the next block uses the same adapter; z and
+// the result move in whole 256-byte row pieces, the products turned through 4
+// KiB of LDS per wave.  Bound by z, read and written once, and by B of the
+// adapters in use (M = 1024, V = 32768, four adapters of rank 64: 72 us for 285
+// MB, 4.0 TB/s; a copy of these bytes reaches 4.7).
+constexpr int kMostBlocks = 8;
+
 template <int RP, bool BF16>
 __global__ __launch_bounds__(256) void lora_expand_kernel(const float *z, int64_t ldz, void *out,
                                                           int64_t ldo, int64_t M, int64_t V,
                                                           LoraAdapters ad,
-                                                          const uint16_t *__restrict__ u3, int nb,
+                                                          const uint16_t *__restrict__ u3,
+                                                          const int32_t *__restrict__ order, int nb,
                                                           int64_t tok_groups, int64_t wg0)
 {
     constexpr int U = RP < 32 ? 1 : RP / 32;     // distinct 32-deep steps over a rank
     constexpr int S = piece_row(RP) / 32;        // steps over the three pieces
     __shared__ __attribute__((aligned(16))) float turn[4][16 * 64];
-    const int lane = threadIdx.x & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    __shared__ int32_t toks[16 * kMostBlocks], ids[16 * kMostBlocks];
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int t16 = lane & 15, q = lane >> 4;
     // Workgroups b, b + 8, ... share an XCD: they take the token groups of one
     // vocabulary tile in turn, so that its B rows are read into one L2.
@@ -671,6 +722,15 @@ __global__ __launch_bounds__(256) void lora_expand_kernel(const float *z, int64_
     const int64_t vt = wg / 8 / tok_groups * 8 + wg % 8;
     const int64_t tg = wg / 8 % tok_groups;
     const int64_t v0 = vt * 256 + wave * 64;
+    // The workgroup's tokens: toks -1 where z stays as it is or there is none.
+    if (tid < 16 * nb) {
+        const int64_t at = tg * nb * 16 + tid;
+        const int32_t tok = at < M ? order[at] : -1;
+        const int32_t id = tok >= 0 ? ad.adapter[tok] : -1;
+        toks[tid] = BF16 || id >= 0 ? tok : -1;
+        ids[tid] = id;
+    }
+    __syncthreads();
     if (v0 >= V)
         return;
     float *const own = turn[wave];
@@ -689,7 +749,7 @@ __global__ __launch_bounds__(256) void lora_expand_kernel(const float *z, int64_
         }
     };
     // One block of 16 tokens: ids, pieces of u, and row pieces of z (this lane's
-    // four are tokens tok0 + 4 i + q, columns v0 + 4 t16 .. + 3).  The next
+    // four are tokens 4 i + q, columns v0 + 4 t16 .. + 3).  The next
     // block's are on their way before this one's results are stored: a wait for
     // loads issued after stores would wait for the stores too.
     const int64_t v = v0 + 4 * t16;
@@ -698,31 +758,28 @@ __global__ __launch_bounds__(256) void lora_expand_kernel(const float *z, int64_
         bf16x8 u[S];
         f32x4 z[4];
     };
-    auto load_block = [&](Block &t, int64_t tok0) {
-        const int64_t tok = tok0 + t16;
-        t.id = tok < M ? ad.adapter[tok] : -1;
+    auto load_block = [&](Block &t, int b) {
+        t.id = ids[16 * b + t16];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int64_t rt = tok0 + 4 * i + q;
+            const int32_t tok = toks[16 * b + 4 * i + q];
             t.z[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-            if (rt < M)
-                t.z[i] = load_piece(z + rt * ldz, v, V);
+            if (tok >= 0)
+                t.z[i] = load_piece(z + tok * ldz, v, V);
         }
-        const uint16_t *pu = u3 + min(tok, M - 1) * piece_row(RP) + 8 * q;
+        const uint16_t *pu = u3 + static_cast<int64_t>(max(toks[16 * b + t16], 0)) * piece_row(RP) + 8 * q;
 #pragma unroll
         for (int s = 0; s < S; ++s)
             t.u[s] = as_frag(*reinterpret_cast<const uint4 *>(pu + 32 * s));
     };
     Block cur;
-    if (tg * nb * 16 < M)
-        load_block(cur, tg * nb * 16);
+    load_block(cur, 0);
     for (int b = 0; b < nb; ++b) {
-        const int64_t tok0 = (tg * nb + b) * 16;
-        if (tok0 >= M)
+        if ((tg * nb + b) * 16 >= M)
             return;
         Block nxt;
-        if (b + 1 < nb && tok0 + 16 < M)
-            load_block(nxt, tok0 + 16);
+        if (b + 1 < nb)
+            load_block(nxt, b + 1);
         const int32_t id = cur.id;
         const bool bad = id >= ad.n;
         uint32_t todo = static_cast<uint32_t>(__ballot(id >= 0 && id < ad.n)) & 0xffffu;
@@ -763,9 +820,9 @@ __global__ __launch_bounds__(256) void lora_expand_kernel(const float *z, int64_
         turn_rows(acc, own, t16, q);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int64_t rt = tok0 + 4 * i + q;
-            if (rt < M)
-                store_piece<BF16>(out, rt * ldo, v, V, cur.z[i] + acc[i]);
+            const int32_t tok = toks[16 * b + 4 * i + q];
+            if (tok >= 0)
+                store_piece<BF16>(out, tok * ldo, v, V, cur.z[i] + acc[i]);
         }
         cur = nxt;
     }
@@ -1192,7 +1249,8 @@ hipError_t launch_join(const float *parts, int64_t n_parts, int64_t M, int RP, c
 }
 
 // u3 from x; upart: [shrink_parts][M][RP] FP32 (M > kFewTokens only).  n_groups:
-// groups of tokens to write beside it (ad.n + 2, or 0: none).
+// workgroups that write `groups` beside it (ad.n + 2, one per group; (M + 63) /
+// 64 where only the order is wanted, M > kFewTokens; 0: none).
 hipError_t launch_shrink(const uint16_t *x, int64_t ldx, int64_t M, int64_t K, const LoraAdapters &ad,
                          uint16_t *u3, FewUnits *table, float *upart, const Grouping &groups,
                          int64_t n_groups, hipStream_t s)
@@ -1205,10 +1263,8 @@ hipError_t launch_shrink(const uint16_t *x, int64_t ldx, int64_t M, int64_t K, c
                            u3, table, groups, static_cast<unsigned>(n_groups));
         return hipGetLastError();
     }
-    if (ad.n == 0)
-        return hipSuccess;
     const int64_t S = shrink_parts(M, K), part_k = (K + 32 * S - 1) / (32 * S) * 32;
-    const int64_t slots = std::min<int64_t>(ad.n, 4);
+    const int64_t slots = std::max<int64_t>(1, std::min<int64_t>(ad.n, 4));
     const int64_t wgs = (M + 63) / 64 * S;  // < 2^17
     const dim3 grid(static_cast<unsigned>(n_groups + wgs), static_cast<unsigned>(slots));
     auto run = [&](auto kernel) {
@@ -1230,7 +1286,7 @@ hipError_t launch_shrink(const uint16_t *x, int64_t ldx, int64_t M, int64_t K, c
 template <int RP>
 hipError_t launch_expand(const float *z, int64_t ldz, void *out, int64_t ldo, bool bf16, int64_t M,
                          int64_t V, const LoraAdapters &ad, const uint16_t *u3,
-                         const FewUnits *table, hipStream_t s)
+                         const FewUnits *table, const int32_t *order, hipStream_t s)
 {
     if (M <= kFewTokens) {
         // Shares of the units: as many as make 4096 workgroups.
@@ -1247,9 +1303,7 @@ hipError_t launch_expand(const float *z, int64_t ldz, void *out, int64_t ldo, bo
     }
     // Token blocks per workgroup: up to eight (B rows kept across a request's
     // tokens, loads ahead of stores) while 1024 workgroups remain.  M = 1024, V =
-    // 32768, 16 adapters of rank 64: 70 us; one block 105 us, two to sixteen within 4 % of
-    // eight.
-    constexpr int64_t kMostBlocks = 8;
+    // 32768, four adapters of rank 64 in runs: 71 us; four blocks 81 us.
     const int64_t tb = (M + 15) / 16, vts = (V + 255) / 256;
     const int nb = static_cast<int>(
         std::max<int64_t>(1, std::min<int64_t>(kMostBlocks, tb * vts / 1024)));
@@ -1260,10 +1314,10 @@ hipError_t launch_expand(const float *z, int64_t ldz, void *out, int64_t ldo, bo
         const dim3 grid(static_cast<unsigned>(std::min(most, wgs - w0)));
         if (bf16)
             hipLaunchKernelGGL((lora_expand_kernel<RP, true>), grid, dim3(256), 0, s, z, ldz, out, ldo, M, V,
-                               ad, u3, nb, groups, w0);
+                               ad, u3, order, nb, groups, w0);
         else
             hipLaunchKernelGGL((lora_expand_kernel<RP, false>), grid, dim3(256), 0, s, z, ldz, out, ldo, M,
-                               V, ad, u3, nb, groups, w0);
+                               V, ad, u3, order, nb, groups, w0);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess)
             return e;
@@ -1328,11 +1382,12 @@ hipError_t launch_bwd_k(const LoraBwd &p, const BwdLayout &l, char *ws, hipStrea
 
 }  // namespace
 
-// The forward's workspace, in order: a small batch's units, u, and the FP32
+// The forward's workspace, in order: a small batch's units or a larger one's
+// order, u, and the FP32
 // product of BF16 logits; the parts of u share the last one's place (they are
 // joined before the product runs).
 struct FwdLayout {
-    int64_t table, u3, z, end;
+    int64_t table, u3, z, end;  // table: FewUnits, or the order of more tokens
 };
 
 static FwdLayout fwd_layout(int64_t M, int64_t K, int64_t V, int64_t r, bool bf16)
@@ -1340,7 +1395,7 @@ static FwdLayout fwd_layout(int64_t M, int64_t K, int64_t V, int64_t r, bool bf1
     const int64_t RP = rank_bucket(r);
     FwdLayout l;
     l.table = 0;
-    l.u3 = M <= kFewTokens ? round256(sizeof(FewUnits)) : 0;
+    l.u3 = round256(M <= kFewTokens ? sizeof(FewUnits) : 4 * M);
     l.z = l.u3 + round256(2 * piece_row(static_cast<int>(RP)) * M);
     l.end = l.z + round256(std::max<int64_t>(bf16 ? 4 * M * ((V + 3) / 4 * 4) : 0,
                                              M <= kFewTokens ? 0 : 4 * shrink_parts(M, K) * M * RP));
@@ -1364,6 +1419,7 @@ hipError_t launch_logits_lora(const GemmProblem &p, bool bf16, const LoraAdapter
     char *ws = static_cast<char *>(workspace);
     const FwdLayout l = fwd_layout(M, K, V, ad.r, bf16);
     FewUnits *table = reinterpret_cast<FewUnits *>(ws + l.table);  // M <= kFewTokens
+    int32_t *order = reinterpret_cast<int32_t *>(ws + l.table);    // M > kFewTokens
     uint16_t *u3 = reinterpret_cast<uint16_t *>(ws + l.u3);
     GemmProblem f = p;  // the shared product, FP32: in place, or in the workspace for BF16 logits
     if (bf16) {
@@ -1372,17 +1428,17 @@ hipError_t launch_logits_lora(const GemmProblem &p, bool bf16, const LoraAdapter
     }
     f.stream_out = false;  // read back at once
     hipError_t e = launch_shrink(p.B, p.ldb, M, K, ad, u3, table, reinterpret_cast<float *>(ws + l.z),
-                                 Grouping{}, 0, s);
+                                 Grouping{nullptr, order, nullptr}, M <= kFewTokens ? 0 : (M + 63) / 64, s);
     if (e == hipSuccess)
         e = launch_gemm_logits(f, Epi::kStoreF32, s);
     if (e != hipSuccess)
         return e;
     const float *z = static_cast<const float *>(f.D);
     switch (rank_bucket(ad.r)) {
-    case 16: return launch_expand<16>(z, f.ldd, p.D, p.ldd, bf16, M, V, ad, u3, table, s);
-    case 32: return launch_expand<32>(z, f.ldd, p.D, p.ldd, bf16, M, V, ad, u3, table, s);
-    case 64: return launch_expand<64>(z, f.ldd, p.D, p.ldd, bf16, M, V, ad, u3, table, s);
-    default: return launch_expand<128>(z, f.ldd, p.D, p.ldd, bf16, M, V, ad, u3, table, s);
+    case 16: return launch_expand<16>(z, f.ldd, p.D, p.ldd, bf16, M, V, ad, u3, table, order, s);
+    case 32: return launch_expand<32>(z, f.ldd, p.D, p.ldd, bf16, M, V, ad, u3, table, order, s);
+    case 64: return launch_expand<64>(z, f.ldd, p.D, p.ldd, bf16, M, V, ad, u3, table, order, s);
+    default: return launch_expand<128>(z, f.ldd, p.D, p.ldd, bf16, M, V, ad, u3, table, order, s);
     }
 }
 

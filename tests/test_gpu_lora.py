@@ -117,6 +117,24 @@ def test_logits_integers_exact(M, K, V, r, n, order, out):
     assert _untouched(dst)
 
 
+@pytest.mark.parametrize("out", ["fp32", "bf16"])
+@pytest.mark.parametrize("M,n,r", [(257, 1, 16), (1023, 40, 20), (1025, 200, 16), (2100, 3, 70), (5000, 700, 3)])
+def test_logits_of_large_mixed_batches(M, n, r, out):
+    """Batches beyond one window of the tokens' order, none of it in runs."""
+    test_logits_integers_exact(M, 64, 270, r, n, "mixed", out)
+
+
+def test_logits_of_large_batches_without_adapters():
+    x, W, A, B, ids, scale, _ = _case(300, 64, 270, 8, 0, "mixed", 3, 0)
+    ids[7], ids[299] = 0, 5  # no adapters, so none with these numbers
+    want = x.double() @ W.double().t()
+    want[7] = want[299] = float("nan")
+    for dt in (torch.float32, torch.bfloat16):
+        out = torch.empty((300, 272), dtype=dt, device="cuda")[:, :270]
+        lmh.lmhead_logits_lora(x, W, A, B, ids, scale=scale, out=out)
+        assert torch.equal(torch.nan_to_num(out, nan=1e30), torch.nan_to_num(want.float().to(dt), nan=1e30))
+
+
 @pytest.mark.parametrize("M,K,V,r,n", [(1, 4096, 2000, 16, 8), (37, 2040, 3003, 12, 5),
                                        (128, 1024, 2048, 64, 32), (513, 2048, 1025, 128, 4)])
 def test_logits_random(M, K, V, r, n):
