@@ -772,6 +772,10 @@ def lmhead_beam_select(logits, scores, n_out=None, finished=None, eos=-1, out_sc
 
 def _merged(shape, strides, name):
     """(size, stride) of several dimensions walked as one."""
+    if not shape:
+        return 1, 0
+    if len(shape) == 1:
+        return (shape[0], strides[0]) if shape[0] > 1 else (shape[0], 0)
     if 0 in shape:
         return 0, 0
     size, stride = 1, 0
@@ -793,7 +797,7 @@ def _runs(t, name, beam_dim, len_dim):
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name}: expected a GPU tensor")
     _on_current_device(t, name)
-    shape, strides, esz = list(t.shape), list(t.stride()), t.element_size()
+    shape, strides, esz = t.shape, t.stride(), t.element_size()
     tail = len(shape) if len_dim is None else len_dim + 1
     # The contiguous run from the end: with lengths exactly the dimensions
     # after len_dim, else as far as it goes.
@@ -854,6 +858,9 @@ def lmhead_beam_reorder(state, parent, out=None, beam_dim=0, len_dim=None, lengt
                          (": in place needs as many beams as before" if out is None else ""))
     if out is None:
         pd, ds = ps, ss
+    elif out.is_cuda and out.stride() == state.stride() and out.shape == state.shape:
+        _on_current_device(out, "out")
+        pd, ds = out.data_ptr(), ss  # laid out as the state is
     else:
         pd, ds, *same = _runs(dst, "out", beam_dim, len_dim)
         if [same[0]] + same[2:] != [n_outer, n_heads, positions, pos_bytes]:
