@@ -32,7 +32,6 @@ namespace lmh {
 namespace {
 
 constexpr int kBeamMax = 64;       // beams per request, and beams selected
-constexpr int kScanWaves = 4;      // waves per scan workgroup
 constexpr int kSegCols = 2048;     // columns a wave holds at a time, 32 a lane
 constexpr int kCandCap = 512;      // candidates a wave can hold
 
@@ -89,7 +88,7 @@ __device__ __forceinline__ double sum_exp(const float (&v)[PER], float low, doub
     double d = 0.0;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-        const double z = static_cast<double>(__builtin_amdgcn_fmed3f(v[i], low, INFINITY));
+        const double z = static_cast<double>(__builtin_elementwise_maximum(v[i], low));
         const double t = fma(z, kLog2E, c);
         const double f = fma(z, kLog2E, c - t);
         double p = 0.0001534581202420037;
@@ -214,36 +213,38 @@ struct Segment {
     }
 };
 
-// One wave per (row, segment of 2048 columns).  Bound by the one read of the
-// logits: the segment sits in registers, so the sum, the maximum and the
-// candidates cost no second read; nothing is shared between waves (no
-// barrier), and six waves per SIMD cover each other's loads.
+// One wave, a workgroup of its own, per (row, segment of 2048 columns).  Bound by
+// the one read of the logits: the segment sits in registers, so the sum, the
+// maximum and the candidates cost no second read; nothing is shared between
+// waves, and six per SIMD cover each other's loads.  A wave goes first (priority)
+// until its loads are out, so that they do not wait behind the some 600
+// instructions with which the others treat theirs.  461 rows of 131072 FP32
+// columns, 242 MB: 50 - 54 us, 4.5 - 4.8 TB/s; without the priority 53 - 54, in
+// workgroups of four waves 56 - 59.
 // Candidates: the k-th largest of the 64 lane maxima is a lower bound of the
 // segment's k-th largest value (that many lanes hold a value at least as
 // large), cut to its upper 16 bits so that 16 ballots find it; the few values
 // at or above it are collected in LDS and ranked by counting.  The list is in
 // descending value, equal values in ascending column.
 template <bool BF16>
-__global__ __launch_bounds__(kScanWaves * 64) void beam_scan_kernel(
-    const void *__restrict__ logits, int64_t ld, int64_t n_rows, int64_t V, int32_t nseg,
+__global__ __launch_bounds__(64) void beam_scan_kernel(
+    const void *__restrict__ logits, int64_t ld, int64_t V, uint32_t nseg,
     const float *__restrict__ scores, const uint8_t *__restrict__ finished, int32_t k,
     SegRecord *__restrict__ rec, uint64_t *__restrict__ lists)
 {
     constexpr int G = Segment<BF16>::G;
-    __shared__ uint64_t cand[kScanWaves][kCandCap];
-    const int lane = threadIdx.x & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int64_t id = static_cast<int64_t>(blockIdx.x) * kScanWaves + wave;
-    if (id >= n_rows * nseg)
-        return;
-    const int64_t row = id / nseg;
+    __shared__ uint64_t mine[kCandCap];
+    __builtin_amdgcn_s_setprio(3);
+    const int lane = threadIdx.x;
+    const uint32_t id = blockIdx.x, row = id / nseg;  // below 2^25
     if (!score_alive(scores[row]) || (finished && finished[row]))
         return;  // the merge does not read this beam's records
-    const int64_t j0 = (id - row * nseg) * kSegCols;
+    const int64_t j0 = static_cast<int64_t>(id - row * nseg) * kSegCols;
     float v[32];
     {
         Segment<BF16> sg;
-        sg.load(static_cast<const char *>(logits) + row * ld * (16 / G), V, j0, lane);
+        sg.load(static_cast<const char *>(logits) + static_cast<int64_t>(row) * ld * (16 / G), V, j0, lane);
+        __builtin_amdgcn_s_setprio(0);
         sg.values(v);
     }
     float gm[8], lm = -INFINITY;
@@ -254,7 +255,7 @@ __global__ __launch_bounds__(kScanWaves * 64) void beam_scan_kernel(
         lm = __builtin_elementwise_maximum(lm, gm[u]);  // NaN stays NaN
     }
     const float m = wave_maximum(lm);
-    uint64_t *out = lists + id * k;
+    uint64_t *out = lists + static_cast<int64_t>(id) * k;
     if (!(m < INFINITY) || m == -INFINITY) {
         // NaN or +inf somewhere (the whole row then offers nothing), or only
         // -inf: no candidates.
@@ -297,7 +298,6 @@ __global__ __launch_bounds__(kScanWaves * 64) void beam_scan_kernel(
     auto key_of = [&](int i) {
         return (static_cast<uint64_t>(order_key(v[i])) << 32) | (rest - static_cast<uint32_t>(64 * (i / G) * G + i % G));
     };
-    uint64_t *const mine = cand[wave];
     int n = 0;  // the same in every lane
 #pragma unroll
     for (int u = 0; u < 8; ++u) {
@@ -820,13 +820,13 @@ hipError_t launch_beam_select(const void *logits, int64_t ld, bool bf16, int64_t
     const int64_t nseg = beam_segments(V), waves = B * W * nseg;
     SegRecord *rec = static_cast<SegRecord *>(workspace);
     uint64_t *lists = reinterpret_cast<uint64_t *>(rec + waves);
-    const dim3 grid(static_cast<unsigned>((waves + kScanWaves - 1) / kScanWaves)), block(kScanWaves * 64);
+    const dim3 grid(static_cast<unsigned>(waves)), block(64);
     const int32_t k = static_cast<int32_t>(n_out), nc = static_cast<int32_t>(nseg);
     if (bf16)
-        hipLaunchKernelGGL((beam_scan_kernel<true>), grid, block, 0, s, logits, ld, B * W, V, nc,
+        hipLaunchKernelGGL((beam_scan_kernel<true>), grid, block, 0, s, logits, ld, V, static_cast<uint32_t>(nseg),
                            scores, finished, k, rec, lists);
     else
-        hipLaunchKernelGGL((beam_scan_kernel<false>), grid, block, 0, s, logits, ld, B * W, V, nc,
+        hipLaunchKernelGGL((beam_scan_kernel<false>), grid, block, 0, s, logits, ld, V, static_cast<uint32_t>(nseg),
                            scores, finished, k, rec, lists);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess)
