@@ -133,6 +133,40 @@ def test_select_logits_apart_by_less_than_a_score_resolves(W, V, k):
     assert (got[0].double().cpu() + np.log(V)).abs().max() <= np.log(V) * 2.0 ** -24 + 4e-9
 
 
+def test_select_of_the_largest_vocabulary():
+    """Tokens up to the last that 31 bits number."""
+    V = 2 ** 31 - 9
+    z = torch.zeros((1, V + 1), dtype=torch.bfloat16, device="cuda")[:, :V]
+    at = [V - 1, 0, 2 ** 30 + 7, V - 2049, 2047]
+    for i, j in enumerate(at):
+        z[0, j] = 9.0 - i
+    got = lmh.lmhead_beam_select(z, torch.zeros(1, 1, device="cuda"), n_out=7, eos=V - 1)
+    assert got[2][0].tolist() == at + [1, 2] and got[3][0].tolist() == [True] + 6 * [False]
+    logz = np.log(V - 5 + sum(np.exp(9.0 - i) for i in range(5)))
+    want = np.array([9.0, 8.0, 7.0, 6.0, 5.0, 0.0, 0.0]) - logz
+    assert np.abs(got[0][0].double().cpu().numpy() - want).max() <= np.abs(want).max() * 2.0 ** -24 + 4e-9
+
+
+def test_two_searches_at_once():
+    """Calls on two streams, each with results and workspaces of its own."""
+    z, s, fin = _random(16, 4, 40000, torch.float32, 21)
+    want = lmh.lmhead_beam_select(z, s, finished=fin, eos=5)
+    par = want[1]
+    st = torch.randint(0, 99, (2, 64, 3, 500, 16), device="cuda", dtype=torch.int16)
+    moved = lmh.lmhead_beam_reorder(st, par, out=torch.empty_like(st), beam_dim=1)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = []
+    for _ in range(10):
+        for q in streams:
+            with torch.cuda.stream(q):
+                got.append((lmh.lmhead_beam_select(z, s, finished=fin, eos=5),
+                            lmh.lmhead_beam_reorder(st, par, out=torch.empty_like(st), beam_dim=1)))
+    torch.cuda.synchronize()
+    for sel, mv in got:
+        assert all(torch.equal(a, b) for a, b in zip(sel, want)) and torch.equal(mv, moved)
+
+
 def test_select_eos_outside_32_bits_is_refused():
     z, s, _ = _random(1, 2, 100, torch.float32, 0)
     for eos in (2 ** 31, -2 ** 31 - 1, 2 ** 32 + 3):

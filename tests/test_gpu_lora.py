@@ -291,6 +291,35 @@ def test_bwd_random(M, K, V, r, n):
         assert torch.equal(q, p)
 
 
+@pytest.mark.parametrize("M,K,V,r,n", [(1, 1, 1, 1, 1), (5, 1, 9, 3, 2), (2, 7, 3, 2, 1), (300, 3, 5, 128, 2),
+                                       (70001, 32, 40, 4, 3)])
+def test_smallest_and_longest_batches(M, K, V, r, n):
+    test_logits_integers_exact(M, K, V, r, n, "mixed", "fp32")
+    test_logits_integers_exact(M, K, V, r, n, "runs", "bf16")
+    test_bwd_integers_exact(M, K, V, r, n, "mixed")
+
+
+def test_offsets_past_32_bits():
+    """Logits and gradients of more than 2^31 elements: the last tokens' results
+    are those of a call that holds them alone."""
+    M, K, V, r, n, last = 66000, 64, 32800, 4, 2, 40
+    x, W, A, B, ids, scale, g = _case(M, K, V, r, n, "mixed", 11, 0)
+    ids[:M - last] = -1  # they alone have adapters
+    rows = slice(M - last, M)
+    tail = _padded(x[rows].clone(), 0), ids[rows].clone()
+    for dt in ("fp32", "bf16"):
+        z = lmh.lmhead_logits_lora(x, W, A, B, ids, scale=scale, out_dtype=dt)
+        # integers of at most 9 K + 18 r K, far below 2^24, so every sum is exact
+        assert torch.equal(z[rows], lmh.lmhead_logits_lora(tail[0], W, A, B, tail[1], scale=scale, out_dtype=dt))
+        del z
+    gr = torch.zeros((M, V), dtype=torch.bfloat16, device="cuda")
+    gr[rows] = _ints(g, (last, V), 1)
+    got = lmh.lmhead_lora_bwd(gr, x, A, B, ids, scale=scale)
+    want = lmh.lmhead_lora_bwd(gr[rows].clone(), tail[0], A, B, tail[1], scale=scale)
+    assert torch.equal(got[0][rows], want[0]) and not got[0][:M - last].any()
+    assert torch.equal(got[1], want[1]) and torch.equal(got[2], want[2])
+
+
 def test_bwd_empty_sizes():
     x, W, A, B, ids, scale, g = _case(20, 64, 72, 8, 3, "mixed", 5, 0)
     gr = _ints(g, (20, 72), 1)
