@@ -689,6 +689,89 @@ lora_expand_few_kernel(const float *z, int64_t ldz, void *out, int64_t ldo, int6
 }
 
 // ---------------------------------------------------------------------------
+// z = x W^T for outputs of few tiles, where the shared product's kernels leave
+// most of the chip idle: a workgroup forms a T x T tile (tokens x vocabulary
+// rows), its eight waves an eighth of K each, summed in order through LDS.
+// Fragments come straight from memory, a batch of steps at a time; what bounds
+// it is how fast they reach the CU (218 tokens, K = 8192, V = 1070: the whole call
+// 41 us, 134 with the kernels of lmhead_logits).
+constexpr int kBaseWaves = 8;
+
+template <int T>
+__global__ __launch_bounds__(kBaseWaves * 64) void lora_base_kernel(const uint16_t *__restrict__ x, int64_t ldx,
+                                                                    const uint16_t *__restrict__ W, int64_t ldw,
+                                                                    float *__restrict__ z, int64_t ldz, int64_t M,
+                                                                    int64_t K, int64_t V)
+{
+    constexpr int NF = T / 16, UN = T == 32 ? 8 : 4;
+    __shared__ f32x4 red[kBaseWaves][NF * NF][64];
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int t16 = lane & 15, q = lane >> 4;
+    const int64_t v0 = static_cast<int64_t>(blockIdx.x) * T, m0 = static_cast<int64_t>(blockIdx.y) * T;
+    const uint16_t *pw[NF], *px[NF];
+    f32x4 acc[NF][NF];
+#pragma unroll
+    for (int i = 0; i < NF; ++i) {
+        pw[i] = W + min(v0 + 16 * i + t16, V - 1) * ldw + 8 * q;
+        px[i] = x + min(m0 + 16 * i + t16, M - 1) * ldx + 8 * q;
+#pragma unroll
+        for (int j = 0; j < NF; ++j)
+            acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    }
+    const int64_t per_wave = (K + 32 * kBaseWaves - 1) / (32 * kBaseWaves) * 32;
+    int64_t k = wave * per_wave;
+    const int64_t kend = min(K, k + per_wave);
+    for (; k + 32 * UN <= kend; k += 32 * UN) {
+        uint4 vw[UN][NF], vx[UN][NF];
+#pragma unroll
+        for (int u = 0; u < UN; ++u)
+#pragma unroll
+            for (int i = 0; i < NF; ++i) {
+                vw[u][i] = *reinterpret_cast<const uint4 *>(pw[i] + k + 32 * u);
+                vx[u][i] = *reinterpret_cast<const uint4 *>(px[i] + k + 32 * u);
+            }
+        __builtin_amdgcn_sched_barrier(0);  // all of them in flight
+#pragma unroll
+        for (int u = 0; u < UN; ++u)
+#pragma unroll
+            for (int i = 0; i < NF; ++i)
+#pragma unroll
+                for (int j = 0; j < NF; ++j)
+                    acc[i][j] = mfma16(as_frag(vw[u][i]), as_frag(vx[u][j]), acc[i][j]);
+    }
+    for (; k < kend; k += 32) {
+        const int64_t left = K - k - 8 * q;
+        uint4 vw[NF], vx[NF];
+#pragma unroll
+        for (int i = 0; i < NF; ++i) {
+            vw[i] = load8(pw[i] + k, left);
+            vx[i] = load8(px[i] + k, left);
+        }
+#pragma unroll
+        for (int i = 0; i < NF; ++i)
+#pragma unroll
+            for (int j = 0; j < NF; ++j)
+                acc[i][j] = mfma16(as_frag(vw[i]), as_frag(vx[j]), acc[i][j]);
+    }
+#pragma unroll
+    for (int i = 0; i < NF; ++i)
+#pragma unroll
+        for (int j = 0; j < NF; ++j)
+            red[wave][i * NF + j][lane] = acc[i][j];
+    __syncthreads();
+    for (int f = wave; f < NF * NF; f += kBaseWaves) {
+        f32x4 sum = red[0][f][lane];
+#pragma unroll
+        for (int w = 1; w < kBaseWaves; ++w)
+            sum += red[w][f][lane];
+        const int64_t m = m0 + 16 * (f % NF) + t16, v = v0 + 16 * (f / NF) + 4 * q;
+        if (m < M)
+            store_piece<false>(z, m * ldz, v, V, sum);
+    }
+}
+
+// ---------------------------------------------------------------------------
 // logits += u B^T: reads the FP32 product z, adds each token's adapter, stores
 // FP32 (in place) or BF16 (rounded once).  A workgroup covers 256 vocabulary
 // rows and `nb` blocks of 16 tokens of the logits' order, one after another;
@@ -1414,6 +1497,46 @@ int64_t lora_bwd_workspace_bytes(int64_t M, int64_t K, int64_t V, int64_t r, int
     return bwd_layout(M, K, V, r, n).end;
 }
 
+// Tile of lora_base_kernel for outputs of few tiles, or 0: the kernels of
+// lmhead_logits, whose tiles are larger and whose workgroups walk all of K.  The
+// whole call, theirs and this one's:
+//   32 x 32, at most one workgroup per CU.  M 12, V 5000, K 7976: 58 and 25 us;
+//     218, 1070, 8192: 134 and 41 us; 58, 3000, 976: 20.8 and 21.1 us.  Up to 16
+//     tokens at K >= 8192 theirs split K as well: 16, 2549, 8192: 29.8 and 31.4.
+//   64 x 64, M > 128, at most two per CU.  410, 2989, 7304: 188 and 112 us; 654,
+//     2549, 2048: 55 and 49 us; past it 400, 5000, 2048: 54 and 61 us.
+//   64 x 64 for fewer tokens, at most one per CU.  128, 5000, 4632: 65 and 39 us;
+//     past it 128, 9000, 2048: 33 and 42 us.  Up to 64 tokens theirs are as fast
+//     where K is long and a multiple of 64: 45, 9000, 8000: 49 and 59 us, but
+//     45, 9000, 7976: 71 and 52 us.
+static int64_t base_tile(int64_t M, int64_t K, int64_t V)
+{
+    auto tiles = [&](int64_t T) { return (M + T - 1) / T * ((V + T - 1) / T); };
+    if (tiles(32) <= 256)
+        return M <= 16 && K >= 8192 ? 0 : 32;
+    if (M > 128)
+        return tiles(64) <= 512 ? 64 : 0;
+    return tiles(64) <= 256 && (M > 64 || K < 5120 || K % 64 != 0) ? 64 : 0;
+}
+
+// The shared product, FP32.
+static hipError_t launch_base(const GemmProblem &f, hipStream_t s)
+{
+    const int64_t M = f.C, K = f.P, V = f.R, T = base_tile(M, K, V);
+    if (T == 0)
+        return launch_gemm_logits(f, Epi::kStoreF32, s);
+    const dim3 grid(static_cast<unsigned>((V + T - 1) / T), static_cast<unsigned>((M + T - 1) / T));
+    auto run = [&](auto kernel) {
+        hipLaunchKernelGGL(kernel, grid, dim3(kBaseWaves * 64), 0, s, f.B, f.ldb, f.A, f.lda,
+                           static_cast<float *>(f.D), f.ldd, M, K, V);
+    };
+    if (T == 32)
+        run(lora_base_kernel<32>);
+    else
+        run(lora_base_kernel<64>);
+    return hipGetLastError();
+}
+
 hipError_t launch_logits_lora(const GemmProblem &p, bool bf16, const LoraAdapters &ad, void *workspace,
                               hipStream_t s)
 {
@@ -1432,7 +1555,7 @@ hipError_t launch_logits_lora(const GemmProblem &p, bool bf16, const LoraAdapter
     hipError_t e = launch_shrink(p.B, p.ldb, M, K, ad, u3, table, reinterpret_cast<float *>(ws + l.z),
                                  Grouping{nullptr, order, nullptr}, M <= kFewTokens ? 0 : (M + 63) / 64, s);
     if (e == hipSuccess)
-        e = launch_gemm_logits(f, Epi::kStoreF32, s);
+        e = launch_base(f, s);
     if (e != hipSuccess)
         return e;
     const float *z = static_cast<const float *>(f.D);

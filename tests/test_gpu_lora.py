@@ -291,6 +291,15 @@ def test_bwd_random(M, K, V, r, n):
         assert torch.equal(q, p)
 
 
+@pytest.mark.parametrize("M,K,V,r,n", [
+    (12, 7976, 1000, 4, 3), (16, 8192, 1000, 4, 3), (45, 5112, 2601, 8, 5), (45, 5120, 2601, 8, 5),
+    (100, 1000, 4000, 16, 2), (200, 520, 3001, 8, 4), (257, 264, 5000, 8, 4), (900, 4632, 1001, 4, 3)])
+def test_logits_of_few_tiles(M, K, V, r, n):
+    """Outputs that one workgroup per tile and all of K would leave most CUs out of."""
+    for out in ("fp32", "bf16"):
+        test_logits_integers_exact(M, K, V, r, n, "mixed", out)
+
+
 @pytest.mark.parametrize("M,K,V,r,n", [(1, 1, 1, 1, 1), (5, 1, 9, 3, 2), (2, 7, 3, 2, 1), (300, 3, 5, 128, 2),
                                        (70001, 32, 40, 4, 3)])
 def test_smallest_and_longest_batches(M, K, V, r, n):
