@@ -600,7 +600,7 @@ def _adapter_args(x, A, B, adapter, scale, V):
     pa, lda, sa = _stack(A, "A", torch.bfloat16)
     pb, ldb, sb = _stack(B, "B", torch.bfloat16)
     n, r, K = A.shape
-    if K != x.shape[1] or tuple(B.shape) != (n, V, r):
+    if K != x.shape[1] or B.shape != (n, V, r):
         raise ValueError("A must be [n, r, K] and B [n, V, r]")
     pi = _vec(adapter, "adapter", torch.int32, x.shape[0])
     ps = None if scale is None else _vec(scale, "scale", torch.float32, n)
@@ -609,7 +609,7 @@ def _adapter_args(x, A, B, adapter, scale, V):
 
 def lmhead_logits_lora_workspace_bytes(M, K, V, rank, out_dtype="fp32"):
     """Workspace bytes lmhead_logits_lora needs."""
-    need = int(lib().lmhead_logits_lora_workspace_bytes(int(M), int(K), int(V), int(rank), _dtype_code(out_dtype)))
+    need = lib().lmhead_logits_lora_workspace_bytes(int(M), int(K), int(V), int(rank), _dtype_code(out_dtype))
     if need < 0:
         _check("lmhead_logits_lora_workspace_bytes", -need)
     return need
@@ -636,9 +636,11 @@ def lmhead_logits_lora(x, W, A, B, adapter, scale=None, out=None, out_dtype=None
         if code not in (LMH_BF16, LMH_FP32):
             _check("lmhead_logits_lora", 1)
         out = _empty_rows(M, V, _TORCH_DT[code], x)
-    po, ldo = _mat(out, "out", out.dtype)
-    if out.shape != (M, V):
-        raise ValueError("out must be [M, V]")
+        po, ldo = out.data_ptr(), out.stride(0)
+    else:
+        po, ldo = _mat(out, "out", out.dtype)
+        if out.shape != (M, V):
+            raise ValueError("out must be [M, V]")
     ws, nbytes = _workspace("lmhead_logits_lora", lmhead_logits_lora_workspace_bytes(M, K, V, ad[9], code),
                             workspace, x, stream)
     _check("lmhead_logits_lora",
@@ -649,7 +651,7 @@ def lmhead_logits_lora(x, W, A, B, adapter, scale=None, out=None, out_dtype=None
 
 def lmhead_lora_bwd_workspace_bytes(M, K, V, rank, n_adapters):
     """Workspace bytes lmhead_lora_bwd needs."""
-    need = int(lib().lmhead_lora_bwd_workspace_bytes(int(M), int(K), int(V), int(rank), int(n_adapters)))
+    need = lib().lmhead_lora_bwd_workspace_bytes(int(M), int(K), int(V), int(rank), int(n_adapters))
     if need < 0:
         _check("lmhead_lora_bwd_workspace_bytes", -need)
     return need
@@ -674,39 +676,41 @@ def lmhead_lora_bwd(dlogits, x, A, B, adapter, scale=None, dX=None, dA=None, dB=
     n, r = ad[8], ad[9]
     if accumulate and (dX is None or dA is None or dB is None):
         raise ValueError("accumulate=True needs existing dX, dA and dB (or False)")
+    outs = []
     if dX is None:
         dX = _empty_rows(M, K, torch.float32, x)
-    if dA is None:
-        dA = _empty_stack(n, r, K, x)
-    if dB is None:
-        dB = _empty_stack(n, V, r, x)
-    outs = []
-    if dX is False:
-        outs += [None, 0]
+        outs += dX.data_ptr(), dX.stride(0)
+    elif dX is False:
+        outs += None, 0
     else:
         outs += _mat(dX, "dX", torch.float32)
         if dX.shape != (M, K):
             raise ValueError("dX must be [M, K]")
-    for t, name, shape in ((dA, "dA", (n, r, K)), (dB, "dB", (n, V, r))):
-        if t is False:
-            outs += [None, 0, 0]
-            continue
-        outs += _stack(t, name, torch.float32)
-        if tuple(t.shape) != shape:
-            raise ValueError(f"{name} must be {list(shape)}")
+    grads = []
+    for t, name, rows, cols in ((dA, "dA", r, K), (dB, "dB", V, r)):
+        if t is None:
+            t = _empty_stack(n, rows, cols, x)
+            outs += t.data_ptr(), t.stride(1), t.stride(0)
+        elif t is False:
+            outs += None, 0, 0
+        else:
+            outs += _stack(t, name, torch.float32)
+            if t.shape != (n, rows, cols):
+                raise ValueError(f"{name} must be [{n}, {rows}, {cols}]")
+        grads.append(t)
     ws, nbytes = _workspace("lmhead_lora_bwd", lmhead_lora_bwd_workspace_bytes(M, K, V, r, n), workspace,
                             x, stream)
     _check("lmhead_lora_bwd",
            lib().lmhead_lora_bwd(pg, ldg, px, ldx, *ad, *outs, int(bool(accumulate)), M, K, V,
                                  ws.data_ptr(), nbytes, _stream(stream)))
-    return tuple(None if t is False else t for t in (dX, dA, dB))
+    return tuple(None if t is False else t for t in (dX, *grads))
 
 
 # ------------------------------------------------------------- beam search
 
 def lmhead_beam_select_workspace_bytes(n_requests, n_beams, n_cols, n_out):
     """Workspace bytes lmhead_beam_select needs."""
-    need = lib().lmhead_beam_select_workspace_bytes(n_requests, n_beams, n_cols, n_out)
+    need = lib().lmhead_beam_select_workspace_bytes(int(n_requests), int(n_beams), int(n_cols), int(n_out))
     if need < 0:
         _check("lmhead_beam_select_workspace_bytes", -need)
     return need
