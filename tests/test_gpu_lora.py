@@ -462,3 +462,40 @@ def test_streams_workspaces_and_graphs():
     graphs[0].replay()
     torch.cuda.synchronize()
     assert torch.equal(outs[0], fresh)
+
+
+@pytest.mark.parametrize("M,V,out", [(600, 1000, "fp32"), (600, 20000, "fp32"), (1500, 3000, "bf16"), (40, 20000, "bf16")])
+def test_captured_batches_of_other_adapters(M, V, out):
+    """A captured step replayed with other ids in place, over a workspace of NaNs."""
+    K, r, n = 136, 16, 7
+    x, W, A, B, ids, scale, g = _case(M, K, V, r, n, "mixed", 41, 0)
+    gr = _ints(g, (M, V), 1)
+    if V % 8:
+        gr = _padded(gr, 0)
+    ws = torch.empty(max(lmh.lmhead_logits_lora_workspace_bytes(M, K, V, r, out),
+                         lmh.lmhead_lora_bwd_workspace_bytes(M, K, V, r, n)), dtype=torch.uint8, device="cuda")
+    z = torch.empty((M, V), dtype=torch.float32 if out == "fp32" else torch.bfloat16, device="cuda")
+    grads = [torch.empty(t.shape, device="cuda") for t in (x, A, B)]
+
+    def step():
+        lmh.lmhead_logits_lora(x, W, A, B, ids, scale=scale, out=z, workspace=ws)
+        lmh.lmhead_lora_bwd(gr, x, A, B, ids, scale=scale, dX=grads[0], dA=grads[1], dB=grads[2], workspace=ws)
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for rep in range(4):
+        ids.copy_(_ids(g, M, n, "runs" if rep % 2 else "mixed", invalid=rep == 2))
+        step()
+        torch.cuda.synchronize()
+        want = [t.clone() for t in (z, *grads)]
+        for t in (z, *grads):
+            t.fill_(7.0)
+        ws.fill_(0xff)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        for t, w in zip((z, *grads), want):
+            assert torch.equal(torch.nan_to_num(t, nan=1e30), torch.nan_to_num(w, nan=1e30)), rep
