@@ -438,7 +438,7 @@ int32_t lmhead_logits_lora(const void *x, int64_t ldx, const void *W, int64_t ld
  *  workspace as lmhead_logits_lora, of lmhead_lora_bwd_workspace_bytes(M, K,
  *  V, rank, n_adapters) bytes.  Limits (LMH_ERR_SHAPE): M <= 2^22,
  *  ceil(V / 256) n_adapters and ceil(K / 256) (2 n_adapters + M / 64 + 2) <=
- *  2^23.
+ *  2^23, ceil(M / 256) (n_adapters + 2) <= 2^31.
  */
 int64_t lmhead_lora_bwd_workspace_bytes(int64_t M, int64_t K, int64_t V, int64_t rank,
                                         int64_t n_adapters);

@@ -264,12 +264,14 @@ bool adapter_sizes_ok(int64_t M, int64_t K, int64_t V, int64_t rank, int64_t n)
 }
 
 // The gradients' launches: one workgroup of 256 per (256 columns, adapter or
-// chunk of 64 tokens).
+// chunk of 64 tokens); and the grouping, which reads every id for each adapter
+// (2^31 rounds of 256 ids take some tenths of a second).
 bool lora_bwd_fits(int64_t M, int64_t K, int64_t V, int64_t n)
 {
     const int64_t most = kMaxLaunchItems / 256;
     return ceil_div(V, 256) <= most / std::max<int64_t>(n, 1) &&
-           ceil_div(K, 256) <= most / (2 * n + M / 64 + 2);
+           ceil_div(K, 256) <= most / (2 * n + M / 64 + 2) &&
+           ceil_div(M, 256) <= (int64_t{1} << 31) / (n + 2);
 }
 
 constexpr int64_t kMaxBeams = 64;

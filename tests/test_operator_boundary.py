@@ -157,6 +157,9 @@ def test_workspace_sizes(L):
     assert L.lmhead_logits_lora_workspace_bytes(2 ** 22 + 1, 8, 8, 8, FP32) == -SHAPE
     assert L.lmhead_logits_lora_workspace_bytes(8, 8, 8, 8, FP16) == -DTYPE
     assert L.lmhead_lora_bwd_workspace_bytes(8, 8, 2 ** 31 - 1, 8, 2) == -SHAPE
+    # the grouping of the tokens reads every id for every adapter
+    assert L.lmhead_lora_bwd_workspace_bytes(2 ** 22, 8, 8, 8, 2 ** 17 - 2) > 0
+    assert L.lmhead_lora_bwd_workspace_bytes(2 ** 22, 8, 8, 8, 2 ** 17 - 1) == -SHAPE
 
 
 def test_python_arguments():
