@@ -462,7 +462,9 @@ int32_t lmhead_lora_bwd(const void *dlogits, int64_t ldd, const void *x, int64_t
  *  score is NaN or +inf.  The n_out largest are returned in descending order,
  *  equal ones by ascending w, then descending logit, then ascending v:
  *    out_scores[b][i] = c (computed in FP64, the sum of exponentials with a
- *    relative error below 4e-9; rounded once to FP32),
+ *    relative error below 4e-9; rounded once to FP32: a candidate below its
+    range, such as a beam at -FLT_MAX over a logit masked with it, comes after
+    those in it and before those at -inf, and is returned as -inf),
  *    out_parent[b][i] = w, out_token[b][i] = v,
  *    out_finished[b][i] = 1 if beam w was finished or v == eos, else 0.
  *  The logits are read once; rows of finished beams and of beams whose score

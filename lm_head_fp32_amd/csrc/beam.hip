@@ -454,7 +454,8 @@ __global__ __launch_bounds__(kMergeThreads) void beam_merge_kernel(
     }
     if (tid < W && held(tid))
         head = fmax(head, static_cast<double>(sc[tid]));
-    // Rounded down, so that a bound on the rounded heads bounds the scores.
+    // Rounded down, so that a bound on the rounded heads bounds the scores; what
+    // lies below the FP32 range becomes -inf, which is no bound.
     if (head > -INFINITY)
         atomicMax(&group[tid >> 3], order_key(__double2float_rd(head)));
     __syncthreads();
@@ -468,8 +469,11 @@ __global__ __launch_bounds__(kMergeThreads) void beam_merge_kernel(
                 t = c;
         }
     }
-    t = max(t, order_key(-INFINITY) + 1u);
-    const double tv = static_cast<double>(key_value(t));
+    // The bound is a finite FP32 value that k heads reach, or there is none: the
+    // FP64 scores of fewer than k heads may lie in the FP32 range (or be all there
+    // are), and one below it, -FLT_MAX plus a masked logit's -FLT_MAX say, still
+    // comes before -inf.
+    const double tv = t > order_key(-INFINITY) ? static_cast<double>(key_value(t)) : -INFINITY;
     auto append = [&](double c, int w, uint64_t key) {
         const uint32_t at = atomicAdd(&n_cand, 1u);
         if (at < kMergeCap) {
@@ -478,7 +482,7 @@ __global__ __launch_bounds__(kMergeThreads) void beam_merge_kernel(
             cw[at] = w;
         }
     };
-    if (head >= tv) {
+    if (head > -INFINITY && head >= tv) {
         for (int64_t l = l0; l < n_lists; l += kMergeThreads) {
             const int w = static_cast<int>(l / nseg);
             if (!(logz[w] == logz[w]))
