@@ -456,17 +456,23 @@ int32_t lmhead_lora_bwd(const void *dlogits, int64_t ldd, const void *x, int64_t
  *  Request b holds beams w < n_beams; row b n_beams + w of the logits and
  *  scores[b][w] (the beam's summed log-probability) belong to beam w.  Every
  *  (w, v) is a candidate with
- *    c = scores[b][w] + log softmax(logits row)[v],
+ *    c = scores[b][w] + ((z[v] - max z) - log sum_v exp(z[v] - max z)),
  *  except that a finished beam has c = scores[b][w] at v = eos and -inf
  *  elsewhere.  A NaN c counts as -inf, as does every candidate of a beam whose
  *  score is NaN or +inf.  The n_out largest are returned in descending order,
  *  equal ones by ascending w, then descending logit, then ascending v:
- *    out_scores[b][i] = c (computed in FP64, the sum of exponentials with a
- *    relative error below 4e-9; rounded once to FP32: a candidate below its
-    range, such as a beam at -FLT_MAX over a logit masked with it, comes after
-    those in it and before those at -inf, and is returned as -inf),
+ *    out_scores[b][i] = c (computed in FP64; the terms of the sum below the
+ *    largest, which is exactly 1, have a relative error below 4e-9; rounded
+ *    once to FP32: a candidate below its range, such as a beam at -FLT_MAX
+ *    over a logit masked with it, comes after those in it and before those at
+ *    -inf, and is returned as -inf),
  *    out_parent[b][i] = w, out_token[b][i] = v,
  *    out_finished[b][i] = 1 if beam w was finished or v == eos, else 0.
+ *  No c is above its beam's score; a row with one finite logit has c equal to
+ *  it; rows that differ by a constant (each z - max z exact) have equal c.  A
+ *  row whose largest logit lies below -2^126 holds only masks of the type's
+ *  lowest value: it is not normalised, the logarithm counting as 0 (it would
+ *  be lost beside max z in 64 bits).
  *  The logits are read once; rows of finished beams and of beams whose score
  *  is -inf, NaN or +inf are not read (but for at most 2 n_out values where
  *  fewer than n_out candidates lie above -inf).

@@ -3,7 +3,7 @@
 // states that follows it.
 //
 // Selection, per request b with W beams over V tokens:
-//   c(w, v) = s_w + (z_wv - logZ_w),  logZ_w = m_w + log sum_v exp(z_wv - m_w)
+//   c(w, v) = s_w + (z_wv - m_w) - log d_w,  m_w = max_v z_wv,  d_w = sum_v exp(z_wv - m_w)
 // and the n_out largest c in descending order, equal ones by ascending w, then
 // descending z, then ascending v (by w V + v, then, unless logits differ by less
 // than c resolves).  Within a beam the order of c is the order of z, so one pass over
@@ -11,8 +11,14 @@
 // and leaves the segment's {max, sum of exponentials} and its n_out largest
 // logits; a second kernel folds the sums, turns the kept logits into scores
 // and picks the winners.  Which candidate wins must not depend on rounding,
-// so sums, logZ and scores are FP64 (the logits enter exactly); only the
-// returned score is rounded, once, to FP32.
+// so sums, logarithms and scores are FP64 (the logits enter exactly); only the
+// returned score is rounded, once, to FP32.  The exponentials are taken about the
+// row's maximum and log of their sum is kept apart from it, c = s_w + ((z_wv -
+// m_w) - log d_w): the largest logit then adds exactly 1, so no candidate scores
+// above its beam, a token that is the only one left scores exactly as its beam,
+// and rows that differ by a constant (in FP32 exactly) give equal scores.  Scores
+// that are equal by the mathematics alone, the same terms in another order say,
+// can differ by the last bits of the sum.
 //
 // A candidate that is NaN counts as -inf.  The scan keeps values above -inf
 // only; beams whose every candidate is -inf (a score that is not below +inf
@@ -37,8 +43,8 @@ constexpr int kCandCap = 512;      // candidates a wave can hold
 
 // What a wave leaves of its segment of a row, besides its list.
 struct SegRecord {
-    double d;     // sum over the segment of exp(z - base); NaN: it holds NaN or +inf
-    double base;  // about the segment's maximum; -inf: nothing above -inf
+    double d;  // sum over the segment of exp(z - m); NaN: it holds NaN or +inf
+    double m;  // the segment's maximum; -inf: nothing above -inf
 };
 static_assert(sizeof(SegRecord) == 16, "one 16-byte record per segment");
 
@@ -73,31 +79,33 @@ __device__ __forceinline__ double exp_nonpos(double x)
     return ldexp(p, static_cast<int>(n));
 }
 
-// Sum of exp(v[i] - N ln 2) for an integer N, as 2^(z log2 e - N): one FP64
-// product per value, split into integer n and fraction f by adding 1.5 x 2^52
-// (n is then in the low word), 2^f from a polynomial whose relative error
-// alternates below 1.9e-9 on [-1/2, 1/2] (fitted by exchange), 2^n by an integer
-// add to the exponent: 12 full-rate instructions a value and one conversion.
-// Values below `low` count as that; z log2 e - N must lie within +-1000 and |N|
-// below 2^30.
+// Sum of exp(v[i] - m) for a finite m at least every v[i], in FP64.  y = (m - v[i]) /
+// 512, one product and sum cut to [0, 1] by the instruction (a difference of 512
+// and more, -inf too, counts as 512: e^-512 is nothing beside 1); 2^(-512 y log2 e)
+// split into integer n and fraction f by adding 1.5 x 2^52 (n is then in the low
+// word); 2^f from a polynomial that is 1 at f = 0 and whose relative error
+// alternates below 2.0e-9 on [-1/2, 1/2] (fitted under that condition); 2^n by an
+// integer add to the exponent: 12 full-rate instructions a value and one
+// conversion.  The largest value adds exactly 1, and the same row moved by a
+// constant has the same sum.
 template <int PER>
-__device__ __forceinline__ double sum_exp(const float (&v)[PER], float low, double n0)
+__device__ __forceinline__ double sum_exp(const float (&v)[PER], double m)
 {
     constexpr double kLog2E = 1.4426950408889634, kMagic = 6755399441055744.0;
-    const double c = kMagic - n0;
+    const double m512 = m / 512.0;
     double d = 0.0;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-        const double z = static_cast<double>(__builtin_elementwise_maximum(v[i], low));
-        const double t = fma(z, kLog2E, c);
-        const double f = fma(z, kLog2E, c - t);
-        double p = 0.0001534581202420037;
-        p = fma(p, f, 0.0013399931219698897);
-        p = fma(p, f, 0.009618488957041028);
-        p = fma(p, f, 0.055503287769636304);
-        p = fma(p, f, 0.24022646890634677);
-        p = fma(p, f, 0.6931472057372686);
-        p = fma(p, f, 1.0000000005541663);
+        const double y = fmin(fmax(fma(static_cast<double>(v[i]), -1.0 / 512.0, m512), 0.0), 1.0);
+        const double t = fma(y, -512.0 * kLog2E, kMagic);
+        const double f = fma(y, -512.0 * kLog2E, kMagic - t);
+        double p = 0.00015353362227507272;
+        p = fma(p, f, 0.0013398874406550455);
+        p = fma(p, f, 0.009618437356465498);
+        p = fma(p, f, 0.055503324711486945);
+        p = fma(p, f, 0.2402264791363921);
+        p = fma(p, f, 0.6931472028550582);
+        p = fma(p, f, 1.0);
         const int n = static_cast<int>(__double_as_longlong(t));  // the low word
         d += __hiloint2double(__double2hiint(p) + (n << 20), __double2loint(p));
     }
@@ -261,28 +269,17 @@ __global__ __launch_bounds__(64) void beam_scan_kernel(
         // -inf: no candidates.
         if (lane == 0) {
             rec[id].d = (m == -INFINITY) ? 0.0 : static_cast<double>(NAN);
-            rec[id].base = (m == -INFINITY) ? -INFINITY : 0.0;
+            rec[id].m = (m == -INFINITY) ? -INFINITY : 0.0;
         }
         if (lane < k)
             out[lane] = 0;
         return;
     }
 
-    double base = m, d = 0.0;
-    if (fabsf(m) < 268435456.0f) {
-        const double n0 = rint(base * 1.4426950408889634);
-        base = n0 * 0.6931471805599453;
-        d = sum_exp(v, m - 600.0f, n0);
-    } else {
-        // Beyond 2^28 other values lie at least 16 below.
-#pragma unroll
-        for (int i = 0; i < 32; ++i)
-            d += exp_nonpos(static_cast<double>(v[i]) - base);
-    }
-    d = wave_sum(d);
+    const double d = wave_sum(sum_exp(v, m));
     if (lane == 0) {
         rec[id].d = d;
-        rec[id].base = base;
+        rec[id].m = m;
     }
 
     const uint32_t mykey = order_key(lm);
@@ -369,8 +366,9 @@ __device__ __forceinline__ uint32_t key_token(uint64_t key)
 
 constexpr int kMergeThreads = 512;
 constexpr int kMergeCap = 1024;
+constexpr double kMaskedOut = -0x1p126;
 
-// One workgroup per request: logZ of every beam from its segments' records,
+// One workgroup per request: the sum of every beam from its segments' records,
 // then the n_out best of the W nseg sorted lists.  Latency-bound (a few
 // thousand candidates): a lower bound on the n_out-th best score, from the
 // lists' heads as in the scan, leaves a few dozen candidates to rank.
@@ -382,7 +380,8 @@ __global__ __launch_bounds__(kMergeThreads) void beam_merge_kernel(
     int32_t *__restrict__ out_token, uint8_t *__restrict__ out_finished)
 {
     constexpr int NW = kMergeThreads / 64;
-    __shared__ double logz[kBeamMax];     // NaN: no candidate above -inf
+    __shared__ double logd[kBeamMax];     // NaN: no candidate above -inf
+    __shared__ float top[kBeamMax];       // the row's maximum
     __shared__ float sc[kBeamMax];
     __shared__ uint8_t fin[kBeamMax];
     __shared__ uint32_t group[64];
@@ -414,30 +413,35 @@ __global__ __launch_bounds__(kMergeThreads) void beam_merge_kernel(
     __syncthreads();
 
     for (int w = wave; w < W; w += NW) {
-        double lz = static_cast<double>(NAN);
+        double log_d = static_cast<double>(NAN), m = -INFINITY;
         if (!fin[w] && score_alive(sc[w])) {
             const SegRecord *r = rec + (row0 + w) * nseg;
-            double m = -INFINITY;
             for (int s = lane; s < nseg; s += 64)
-                m = fmax(m, r[s].base);
+                m = fmax(m, r[s].m);
 #pragma unroll
             for (int off = 32; off >= 1; off >>= 1)
                 m = fmax(m, shfl_xor_f64(m, off));
             if (m > -INFINITY) {
                 double d = 0.0;  // NaN from any segment that holds NaN or +inf
                 for (int s = lane; s < nseg; s += 64)
-                    d += r[s].d * exp_nonpos(r[s].base - m);
-                lz = m + log(wave_sum(d));
+                    d += r[s].d * exp_nonpos(r[s].m - m);
+                log_d = log(wave_sum(d));
+                // Nothing but masks of the type's lowest value: not normalised
+                // (m + log d is m in 64 bits).
+                if (m < kMaskedOut && log_d == log_d)
+                    log_d = 0.0;
             }
         }
-        if (lane == 0)
-            logz[w] = lz;
+        if (lane == 0) {
+            logd[w] = log_d;
+            top[w] = static_cast<float>(m);
+        }
     }
     __syncthreads();
 
     auto score_of = [&](int w, uint64_t key) {
-        return static_cast<double>(sc[w]) +
-               (static_cast<double>(key_value(static_cast<uint32_t>(key >> 32))) - logz[w]);
+        const double z = static_cast<double>(key_value(static_cast<uint32_t>(key >> 32)));
+        return static_cast<double>(sc[w]) + ((z - static_cast<double>(top[w])) - logd[w]);
     };
     // A finished beam's one candidate, at `eos`.
     const uint64_t held_key = 0xffffffffu - static_cast<uint32_t>(eos);
@@ -446,7 +450,7 @@ __global__ __launch_bounds__(kMergeThreads) void beam_merge_kernel(
     double head = -INFINITY;
     for (int64_t l = l0; l < n_lists; l += kMergeThreads) {
         const int w = static_cast<int>(l / nseg);
-        if (logz[w] == logz[w]) {
+        if (logd[w] == logd[w]) {
             const uint64_t key = l == l0 ? head0 : lists[(row0 * nseg + l) * k];
             if (key)
                 head = fmax(head, score_of(w, key));
@@ -485,7 +489,7 @@ __global__ __launch_bounds__(kMergeThreads) void beam_merge_kernel(
     if (head > -INFINITY && head >= tv) {
         for (int64_t l = l0; l < n_lists; l += kMergeThreads) {
             const int w = static_cast<int>(l / nseg);
-            if (!(logz[w] == logz[w]))
+            if (!(logd[w] == logd[w]))
                 continue;
             const uint64_t *q = lists + (row0 * nseg + l) * k;
             // Four keys at a time: one wait for most lists.
@@ -543,7 +547,7 @@ __global__ __launch_bounds__(kMergeThreads) void beam_merge_kernel(
             };
             for (int64_t l = l0; l < n_lists; l += kMergeThreads) {
                 const int w = static_cast<int>(l / nseg);
-                if (!(logz[w] == logz[w]))
+                if (!(logd[w] == logd[w]))
                     continue;
                 const uint64_t *q = lists + (row0 * nseg + l) * k;
                 for (int i = 0; i < k && q[i]; ++i)
@@ -586,7 +590,7 @@ __global__ __launch_bounds__(kMergeThreads) void beam_merge_kernel(
         if (f < total) {
             if (fin[w]) {
                 none = v != eos || !score_alive(sc[w]);
-            } else if (!(logz[w] == logz[w])) {
+            } else if (!(logd[w] == logd[w])) {
                 none = true;
             } else {
                 const int64_t at = (row0 + w) * ld + v;
