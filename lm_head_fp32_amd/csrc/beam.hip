@@ -37,6 +37,7 @@ namespace lmh {
 
 namespace {
 
+constexpr int64_t kMaxItems = int64_t{1} << 31;  // work-items per launch
 constexpr int kBeamMax = 64;       // beams per request, and beams selected
 constexpr int kSegCols = 2048;     // columns a wave holds at a time, 32 a lane
 constexpr int kCandCap = 512;      // candidates a wave can hold
@@ -754,7 +755,7 @@ __global__ __launch_bounds__(256) void beam_permute_kernel(ReorderArgs a, uint32
     }
 }
 
-constexpr int64_t kMaxBlocks = (int64_t{1} << 31) / 256;  // workgroups of 256 per launch
+constexpr int64_t kMaxBlocks = kMaxItems / 256;  // workgroups of 256 per launch
 
 // Workgroups of `bytes` each that a row takes (odd, see above).
 int64_t row_blocks(const ReorderArgs &a, int64_t bytes)
@@ -839,10 +840,21 @@ hipError_t launch_beam_select(const void *logits, int64_t ld, bool bf16, int64_t
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess)
         return e;
-    hipLaunchKernelGGL(beam_merge_kernel, dim3(static_cast<unsigned>(B)), dim3(kMergeThreads), 0, s, logits,
-                       ld, bf16 ? 1 : 0, static_cast<int32_t>(W), V, nc, scores, finished, eos, k, rec,
-                       lists, out_scores, out_parent, out_token, out_finished);
-    return hipGetLastError();
+    // A workgroup per request: more requests than one launch's work-items cover
+    // take several.
+    const int64_t most = kMaxItems / kMergeThreads, esz = bf16 ? 2 : 4;
+    for (int64_t b = 0; b < B; b += most) {
+        const int64_t r = b * W, o = b * n_out;
+        hipLaunchKernelGGL(beam_merge_kernel, dim3(static_cast<unsigned>(std::min(most, B - b))),
+                           dim3(kMergeThreads), 0, s, static_cast<const char *>(logits) + r * ld * esz, ld,
+                           bf16 ? 1 : 0, static_cast<int32_t>(W), V, nc, scores + r,
+                           finished ? finished + r : nullptr, eos, k, rec + r * nseg, lists + r * nseg * n_out,
+                           out_scores + o, out_parent + o, out_token + o, out_finished + o);
+        const hipError_t em = hipGetLastError();
+        if (em != hipSuccess)
+            return em;
+    }
+    return hipSuccess;
 }
 
 hipError_t launch_beam_reorder(const void *src, void *dst, const int64_t (&src_strides)[3],

@@ -147,3 +147,32 @@ def test_constrained_search_with_finite_masks():
         sc, _, _, ended = lmh.lmhead_beam_select(_rows(z.cuda()), s.cuda(), n_out=2 * W, finished=fin.cuda(),
                                                  eos=3)
         s, fin = sc[:, :W].cpu().contiguous(), ended[:, :W].cpu().contiguous()
+
+
+@pytest.mark.parametrize("W,B", [(1, 2 ** 23), (3, 2 ** 22 + 5)])
+def test_as_many_requests_as_allowed(W, B):
+    """More requests than one launch of the merge covers, in place; the best of
+    one or two tokens per beam and the beams' ends."""
+    g = torch.Generator(device="cuda").manual_seed(W)
+    z = torch.zeros((B * W, 4), device="cuda")[:, :2]
+    z[:, 1] = torch.where(torch.rand(B * W, device="cuda", generator=g) < 0.5, -2.0, 1.0)
+    s = -torch.arange(B, device="cuda").remainder(1000)[:, None] - 8.0 * torch.rand(B, W, device="cuda", generator=g)
+    fin = torch.rand(B, W, device="cuda", generator=g) < 0.25
+    a, m = z.double(), z.double().amax(1, keepdim=True)
+    c = ((a - m) - torch.log(torch.exp(a - m).sum(1, keepdim=True))).view(B, W, 2) + s.double()[:, :, None]
+    held = torch.stack([torch.full_like(s.double(), -INF), s.double()], 2)  # eos is token 1
+    c = torch.where(fin[:, :, None], held, c).view(B, 2 * W)
+    best, at = torch.sort(c, dim=1, descending=True, stable=True)
+    best, at = best[:, :W], at[:, :W].int()
+    if W > 1:  # no two of a request's scores closer than the kernel's bound on them
+        gap = best[:, :-1] - best[:, 1:]
+        sure = (gap > 1e-8).all(1) & (c.sort(1, descending=True).values[:, W] < best[:, -1] - 1e-8)
+    else:
+        sure = torch.ones(B, dtype=torch.bool, device="cuda")
+    assert sure.float().mean() > 0.99 and sure[-3:].any()
+    ended = torch.gather(fin, 1, (at // 2).long()) | (at % 2 == 1)
+    sc, par, tok, end = lmh.lmhead_beam_select(z, s, finished=fin, eos=1, out_scores=s, out_finished=fin)
+    torch.cuda.synchronize()
+    assert torch.equal(par[sure], (at // 2)[sure]) and torch.equal(tok[sure], (at % 2)[sure])
+    assert torch.equal(end[sure], ended[sure])
+    assert ((sc.double() - best).abs() <= best.abs() * 2.0 ** -24 + 4e-9)[torch.isfinite(best)].all()
