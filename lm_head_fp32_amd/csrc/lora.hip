@@ -1456,6 +1456,8 @@ hipError_t launch_bwd_k(const LoraBwd &p, const BwdLayout &l, char *ws, hipStrea
 {
     const int64_t nkb = (p.K + 255) / 256;
     const int64_t units = (p.dA ? p.ad.n : 0) + (p.dX ? chunk_numbers(p.M, p.ad.n) : 0);
+    if (units == 0)
+        return hipSuccess;  // dA of no adapters
     hipLaunchKernelGGL((lora_bwd_k_kernel<RP>), dim3(static_cast<unsigned>(nkb * units)), dim3(256), 0, s,
                        p.x, p.ldx, p.K, p.ad, reinterpret_cast<const int32_t *>(ws + l.offset),
                        reinterpret_cast<const int32_t *>(ws + l.order),
