@@ -512,8 +512,9 @@ int32_t lmhead_beam_select(const void *logits, int64_t ld, int32_t logits_dtype,
  *  In place: dst == src with equal strides and beams_out == beams_in; any
  *  parent map, rows that stay are not touched.  Any other overlap of dst with
  *  src, parent or lengths is LMH_ERR_ALIAS.  The runs of dst must be disjoint
- *  (LMH_ERR_SHAPE).  Limits: beams <= 64; n_requests n_heads (n_positions
- *  position_bytes / 1024 + 2) <= 2^23; spans up to 2^44 bytes.
+ *  (LMH_ERR_SHAPE).  Limits: beams <= 64; every count below 2^31; n_requests
+ *  n_heads (n_positions position_bytes / 1024 + 2) <= 2^23; spans up to 2^44
+ *  bytes (a run of one position may be as long as these allow, 8 GiB).
  */
 int32_t lmhead_beam_reorder(const void *src, int64_t src_outer, int64_t src_row, int64_t src_head,
                             void *dst, int64_t dst_outer, int64_t dst_row, int64_t dst_head,

@@ -915,15 +915,14 @@ int32_t lmhead_beam_reorder(const void *src, int64_t src_outer, int64_t src_row,
 {
     if (n_outer < 0 || n_requests < 0 || beams_in < 0 || beams_out < 0 || n_heads < 0 ||
         n_positions < 0 || position_bytes < 0 || n_outer > kMaxDim || n_requests > kMaxDim ||
-        beams_in > kMaxBeams || beams_out > kMaxBeams || n_heads > kMaxDim || n_positions > kMaxDim ||
-        position_bytes > kMaxDim)
+        beams_in > kMaxBeams || beams_out > kMaxBeams || n_heads > kMaxDim || n_positions > kMaxDim)
         return LMH_ERR_SHAPE;
     if (n_outer == 0 || n_requests == 0 || beams_out == 0 || n_heads == 0 || n_positions == 0 ||
         position_bytes == 0)
         return LMH_OK;
-    if (beams_in == 0)
+    if (beams_in == 0 || position_bytes > kMaxSpanElems / n_positions)
         return LMH_ERR_SHAPE;
-    const int64_t run = n_positions * position_bytes;  // < 2^62
+    const int64_t run = n_positions * position_bytes;  // <= 2^44
     const int64_t rows_in = n_requests * beams_in, rows_out = n_requests * beams_out;
     // Bytes a tensor of [outer][rows][heads] runs spans; -1 when a stride is
     // negative or the span passes 2^44 bytes.

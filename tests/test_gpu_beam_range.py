@@ -176,3 +176,20 @@ def test_as_many_requests_as_allowed(W, B):
     assert torch.equal(par[sure], (at // 2)[sure]) and torch.equal(tok[sure], (at % 2)[sure])
     assert torch.equal(end[sure], ended[sure])
     assert ((sc.double() - best).abs() <= best.abs() * 2.0 ** -24 + 4e-9)[torch.isfinite(best)].all()
+
+
+def test_reorder_rows_of_more_than_31_bits():
+    """Rows of 2 GiB and more that move whole, to other memory and in place."""
+    T = 2 ** 31 + 4099
+    st = torch.zeros((4, T), dtype=torch.uint8, device="cuda")
+    at = torch.tensor([0, 1, 4097, 2 ** 31 - 1, 2 ** 31, 2 ** 31 + 4096, T - 1], device="cuda")
+    marks = torch.arange(28, dtype=torch.uint8, device="cuda").view(4, 7) + 1
+    st[:, at] = marks
+    par = torch.tensor([[2, 0, 0, 3], [1, 3, 2, 0]], dtype=torch.int32, device="cuda")
+    out = lmh.lmhead_beam_reorder(st, par[:1], out=torch.full_like(st, 99))
+    assert torch.equal(out[:, at], marks[par[0].long()])
+    assert int(out[:, :2 ** 20].sum()) == int(out[:, at[:3]].sum()) and not out[:, -4000:-3].any()
+    del out
+    lmh.lmhead_beam_reorder(st, par[1:])
+    assert torch.equal(st[:, at], marks[par[1].long()])
+    assert not st[:, 8192:2 ** 20].any() and not st[:, -4000:-3].any()

@@ -144,6 +144,24 @@ def test_beam_reorder_refusals(L):
         assert f(**{none: 0}) == OK, none
 
 
+def test_beam_reorder_of_long_runs(L):
+    """A run of one position (a whole row of a state without lengths) is bound
+    by the launch and the spans, not by 31 bits."""
+    def f(pb, **kw):
+        far = dict(no=1, h=1, T=1, sr=pb, dr=pb, so=0, do=0, d=X + 2 ** 46, p=2 ** 50, l=None, pb=pb)
+        return _call(L.lmhead_beam_reorder, RE, RE_OK, **{**far, **kw})
+
+    # the sizes pass: what is refused is the missing parent, or the overlap
+    for pb in (2 ** 31 - 1, 2 ** 31, 2 ** 31 + 1, 2 ** 33 - 4096, 2 ** 39):
+        assert f(pb, p=None) == NULL, pb
+    assert f(2 ** 31, B=1, d=X + 2 ** 31) == ALIAS
+    assert f(2 ** 31, B=1, p=X + 2 ** 46 + 2 ** 33 - 8) == ALIAS
+    # past the launch, past the spans, past 64 bits
+    assert f(2 ** 34, B=1) == SHAPE
+    for pb, T in ((2 ** 44 + 1, 1), (2 ** 43, 3), (2 ** 62, 2), (2 ** 62, 2 ** 31 - 1), (MAX, 1), (MAX, MAX)):
+        assert f(pb, T=T, B=1) == SHAPE, (pb, T)
+
+
 def test_workspace_sizes(L):
     """Every size, zero included, has a workspace size (no division by a size)."""
     for M in (0, 1, 16, 17, 256, 257, 4096, 2 ** 22):
