@@ -575,23 +575,36 @@ def _empty_stack(n, rows, cols, like):
     return t if ld == cols else t[:, :, :cols]
 
 
-def _workspace(fn, need, workspace, like, stream):
+def _workspace(need, workspace, like):
     """(tensor, bytes) of a workspace of at least `need` bytes: the caller's, or
-    one from torch's caching allocator, marked as in use on the launch stream
-    (a raw stream handle needs an explicit workspace)."""
+    one from torch's caching allocator."""
     if workspace is None:
-        if stream is not None and not isinstance(stream, torch.cuda.Stream):
-            raise ValueError(f"{fn} on a raw stream handle needs an explicit workspace")
-        workspace = like.new_empty((max(need, 16),), dtype=torch.uint8)
-        if stream is not None:
-            # freed on return: keep the allocator from reusing it before the
-            # kernels on `stream` are done
-            workspace.record_stream(stream)
-        return workspace, max(need, 16)
+        return like.new_empty((max(need, 16),), dtype=torch.uint8), max(need, 16)
     if not isinstance(workspace, torch.Tensor) or not workspace.is_cuda or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous GPU tensor")
     _on_current_device(workspace, "workspace")
     return workspace, workspace.numel() * workspace.element_size()
+
+
+def _on_stream(fn, stream, workspace, *args):
+    """fn(*args, workspace) with `stream` current, so that the results and the
+    workspace that the call allocates belong to the stream that its kernels run
+    on: memory of the calling stream may still be in use by that stream's
+    earlier work, and a result dropped at once would be handed out there again
+    while the kernels write it.  The calling stream, which is to read them, is
+    noted as a user of the results.  A raw stream handle needs an explicit
+    workspace."""
+    if not isinstance(stream, torch.cuda.Stream):
+        if workspace is None:
+            raise ValueError(f"{fn.__name__} on a raw stream handle needs an explicit workspace")
+        stream = torch.cuda.ExternalStream(int(getattr(stream, "cuda_stream", stream)))
+    caller = torch.cuda.current_stream()
+    with torch.cuda.stream(stream):
+        results = fn(*args, workspace)
+    for t in results if isinstance(results, tuple) else (results,):
+        if t is not None:
+            t.record_stream(caller)
+    return results
 
 
 def _adapter_args(x, A, B, adapter, scale, V):
@@ -624,6 +637,8 @@ def lmhead_logits_lora(x, W, A, B, adapter, scale=None, out=None, out_dtype=None
     order, negative: none, >= n: a NaN row; scale fp32 [n] or None (1).  out
     and out_dtype as in lmhead_logits ('bf16' unless stated).  The adapters'
     part is as exact as the FP32 logits."""
+    if stream is not None and (out is None or workspace is None):
+        return _on_stream(lmhead_logits_lora, stream, workspace, x, W, A, B, adapter, scale, out, out_dtype)
     code = _out_code("lmhead_logits_lora", out, out_dtype, "bf16")
     px, ldx = _mat(x, "x", torch.bfloat16)
     pw, ldw = _mat(W, "W", torch.bfloat16)
@@ -641,8 +656,7 @@ def lmhead_logits_lora(x, W, A, B, adapter, scale=None, out=None, out_dtype=None
         po, ldo = _mat(out, "out", out.dtype)
         if out.shape != (M, V):
             raise ValueError("out must be [M, V]")
-    ws, nbytes = _workspace("lmhead_logits_lora", lmhead_logits_lora_workspace_bytes(M, K, V, ad[9], code),
-                            workspace, x, stream)
+    ws, nbytes = _workspace(lmhead_logits_lora_workspace_bytes(M, K, V, ad[9], code), workspace, x)
     _check("lmhead_logits_lora",
            lib().lmhead_logits_lora(px, ldx, pw, ldw, *ad, po, ldo, code, M, K, V, ws.data_ptr(), nbytes,
                                     _stream(stream)))
@@ -666,6 +680,9 @@ def lmhead_lora_bwd(dlogits, x, A, B, adapter, scale=None, dX=None, dA=None, dB=
     in the place of an output skips it.  accumulate=True adds to the given
     ones (dX: to the shared part that lmhead_dgrad wrote), all of which must
     then be passed or False."""
+    if stream is not None and (dX is None or dA is None or dB is None or workspace is None):
+        return _on_stream(lmhead_lora_bwd, stream, workspace, dlogits, x, A, B, adapter, scale, dX, dA, dB,
+                          accumulate)
     pg, ldg = _mat(dlogits, "dlogits", torch.bfloat16)
     px, ldx = _mat(x, "x", torch.bfloat16)
     M, V = dlogits.shape
@@ -698,8 +715,7 @@ def lmhead_lora_bwd(dlogits, x, A, B, adapter, scale=None, dX=None, dA=None, dB=
             if t.shape != (n, rows, cols):
                 raise ValueError(f"{name} must be [{n}, {rows}, {cols}]")
         grads.append(t)
-    ws, nbytes = _workspace("lmhead_lora_bwd", lmhead_lora_bwd_workspace_bytes(M, K, V, r, n), workspace,
-                            x, stream)
+    ws, nbytes = _workspace(lmhead_lora_bwd_workspace_bytes(M, K, V, r, n), workspace, x)
     _check("lmhead_lora_bwd",
            lib().lmhead_lora_bwd(pg, ldg, px, ldx, *ad, *outs, int(bool(accumulate)), M, K, V,
                                  ws.data_ptr(), nbytes, _stream(stream)))
@@ -745,6 +761,10 @@ def lmhead_beam_select(logits, scores, n_out=None, finished=None, eos=-1, out_sc
     n_out: W unless stated, at most 64.  Returns (scores [B, n_out] fp32,
     parent [B, n_out] int32, token [B, n_out] int32, finished [B, n_out]
     bool); out_scores and out_finished may be `scores` and `finished`."""
+    if stream is not None and (out_scores is None or out_parent is None or out_token is None or
+                               out_finished is None or workspace is None):
+        return _on_stream(lmhead_beam_select, stream, workspace, logits, scores, n_out, finished, eos, out_scores,
+                          out_parent, out_token, out_finished)
     if not isinstance(scores, torch.Tensor) or scores.dim() != 2:
         raise ValueError("scores: expected a [B, W] tensor")
     if not isinstance(logits, torch.Tensor) or logits.dtype not in (torch.float32, torch.bfloat16):
@@ -766,8 +786,7 @@ def lmhead_beam_select(logits, scores, n_out=None, finished=None, eos=-1, out_sc
     out_token, pt = _beam_out(out_token, "out_token", torch.int32, shape, scores)
     out_finished, pe = _beam_out(out_finished, "out_finished", torch.bool, shape, scores)
     code = _DT[logits.dtype]
-    need = lmhead_beam_select_workspace_bytes(B, W, V, k)
-    ws, nbytes = _workspace("lmhead_beam_select", need, workspace, logits, stream)
+    ws, nbytes = _workspace(lmhead_beam_select_workspace_bytes(B, W, V, k), workspace, logits)
     _check("lmhead_beam_select",
            lib().lmhead_beam_select(pz, ld, code, B, W, V, ps, pf, eos, k, po, pp, pt, pe,
                                     ws.data_ptr(), nbytes, _stream(stream)))
