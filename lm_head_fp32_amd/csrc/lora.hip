@@ -694,7 +694,7 @@ lora_expand_few_kernel(const float *z, int64_t ldz, void *out, int64_t ldo, int6
 // rows), its eight waves an eighth of K each, summed in order through LDS.
 // Fragments come straight from memory, a batch of steps at a time; what bounds
 // it is how fast they reach the CU (218 tokens, K = 8192, V = 1070: the whole call
-// 41 us, 134 with the kernels of lmhead_logits).
+// 59 us, 151 with the kernels of lmhead_logits).
 constexpr int kBaseWaves = 8;
 
 template <int T>
@@ -1060,7 +1060,10 @@ __device__ __forceinline__ void store_f32x4(float *p, f32x4 v, int64_t n, bool a
 // 1024, V = 32768, 4 adapters of rank 16: 18 us, 3.7 TB/s with 3 us to start and
 // drain and 4 us of dependent loads -- group, token numbers, rows -- before the
 // stream); a second chunk in flight gained nothing (22 against 20.7 us).  The parts of t cost
-// 8 RP bytes per token and block against 512 of g.
+// 8 RP bytes per token and block against 512 of g.  An adapter's tokens are not split
+// over workgroups: few columns and few adapters leave most CUs idle.  u3 is written
+// only for a call that wants dB: without it sU holds whatever the workspace did and
+// must not be used.
 template <int RP>
 __global__ __launch_bounds__(256) void lora_bwd_v_kernel(
     const uint16_t *__restrict__ g, int64_t ldg, int64_t M, int64_t V, LoraAdapters ad,
@@ -1502,15 +1505,15 @@ int64_t lora_bwd_workspace_bytes(int64_t M, int64_t K, int64_t V, int64_t r, int
 // Tile of lora_base_kernel for outputs of few tiles, or 0: the kernels of
 // lmhead_logits, whose tiles are larger and whose workgroups walk all of K.  The
 // whole call, theirs and this one's:
-//   32 x 32, at most one workgroup per CU.  M 12, V 5000, K 7976: 58 and 25 us;
-//     218, 1070, 8192: 134 and 41 us; 58, 3000, 976: 20.8 and 21.1 us.  Up to 16
-//     tokens at K >= 8192 theirs split K as well: 16, 2549, 8192: 29.8 and 31.4.
-//   64 x 64, M > 128, at most two per CU.  410, 2989, 7304: 188 and 112 us; 654,
-//     2549, 2048: 55 and 49 us; past it 400, 5000, 2048: 54 and 61 us.
-//   64 x 64 for fewer tokens, at most one per CU.  128, 5000, 4632: 65 and 39 us;
-//     past it 128, 9000, 2048: 33 and 42 us.  Up to 64 tokens theirs are as fast
-//     where K is long and a multiple of 64: 45, 9000, 8000: 49 and 59 us, but
-//     45, 9000, 7976: 71 and 52 us.
+//   32 x 32, at most one workgroup per CU.  M 12, V 5000, K 7976: 67 and 35 us;
+//     218, 1070, 8192: 151 and 59 us; 58, 3000, 976: 25 and 18 us.  Up to 16
+//     tokens at K >= 8192 theirs split K as well: 16, 2549, 8192: 41.7 and 43.6.
+//   64 x 64, M > 128, at most two per CU.  410, 2989, 7304: 192 and 114 us; 654,
+//     2549, 2048: 59 and 53 us; past it 400, 5000, 2048: 59 and 65 us.
+//   64 x 64 for fewer tokens, at most one per CU.  128, 5000, 4632: 74 and 49 us;
+//     past it 128, 9000, 2048: 41 and 50 us.  Up to 64 tokens theirs are as fast
+//     where K is long and a multiple of 64 and W is in the caches: 45, 9000, 8000:
+//     64 and 76 us (from memory 90 and 80), but 45, 9000, 7976: 83 and 63 us.
 static int64_t base_tile(int64_t M, int64_t K, int64_t V)
 {
     auto tiles = [&](int64_t T) { return (M + T - 1) / T * ((V + T - 1) / T); };
