@@ -1,0 +1,214 @@
+// rows.h -- device helpers of the kernels that read rows of logits by segments
+// of 2048 columns, one wave each: loads, wave reductions, and the largest values
+// of a segment.
+#pragma once
+
+#include "common.h"
+
+namespace lmh {
+
+constexpr int kSegCols = 2048;     // columns a wave holds at a time, 32 a lane
+constexpr int kCandCap = 512;      // candidates a wave can hold
+
+// FP32 -> uint32 with the same order (-0 and +0 equal); 0 lies below -inf.
+__device__ __forceinline__ uint32_t order_key(float f)
+{
+    const uint32_t u = __float_as_uint(f + 0.0f);
+    return u ^ (static_cast<uint32_t>(static_cast<int32_t>(u) >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float key_value(uint32_t k)
+{
+    return __uint_as_float((k & 0x80000000u) ? (k & 0x7fffffffu) : ~k);
+}
+
+__device__ __forceinline__ double shfl_xor_f64(double v, int off)
+{
+    const uint64_t u = __double_as_longlong(v);
+    const uint32_t lo = __shfl_xor(static_cast<uint32_t>(u), off, 64);
+    const uint32_t hi = __shfl_xor(static_cast<uint32_t>(u >> 32), off, 64);
+    return __longlong_as_double((static_cast<uint64_t>(hi) << 32) | lo);
+}
+
+__device__ __forceinline__ uint64_t shfl_xor_u64(uint64_t u, int off)
+{
+    const uint32_t lo = __shfl_xor(static_cast<uint32_t>(u), off, 64);
+    const uint32_t hi = __shfl_xor(static_cast<uint32_t>(u >> 32), off, 64);
+    return (static_cast<uint64_t>(hi) << 32) | lo;
+}
+
+// Reductions over the wave, every lane getting the result: lanes of a row of
+// 16 through DPP (quad permutations, then rotations by 4 and 8), the four rows
+// through LDS permutes.
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp(uint32_t v)
+{
+    return static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(v), CTRL, 0xf, 0xf, true));
+}
+template <int CTRL>
+__device__ __forceinline__ double dpp_f64(double v)
+{
+    const uint64_t u = __double_as_longlong(v);
+    return __longlong_as_double((static_cast<uint64_t>(dpp<CTRL>(static_cast<uint32_t>(u >> 32))) << 32) |
+                                dpp<CTRL>(static_cast<uint32_t>(u)));
+}
+constexpr int kQuadXor1 = 0xb1, kQuadXor2 = 0x4e, kRowRor4 = 0x124, kRowRor8 = 0x128;
+
+__device__ __forceinline__ float wave_maximum(float m)  // NaN if any lane's is
+{
+    m = __builtin_elementwise_maximum(m, __uint_as_float(dpp<kQuadXor1>(__float_as_uint(m))));
+    m = __builtin_elementwise_maximum(m, __uint_as_float(dpp<kQuadXor2>(__float_as_uint(m))));
+    m = __builtin_elementwise_maximum(m, __uint_as_float(dpp<kRowRor4>(__float_as_uint(m))));
+    m = __builtin_elementwise_maximum(m, __uint_as_float(dpp<kRowRor8>(__float_as_uint(m))));
+    m = __builtin_elementwise_maximum(m, __shfl_xor(m, 16, 64));
+    return __builtin_elementwise_maximum(m, __shfl_xor(m, 32, 64));
+}
+
+__device__ __forceinline__ double wave_sum(double d)
+{
+    d += dpp_f64<kQuadXor1>(d);
+    d += dpp_f64<kQuadXor2>(d);
+    d += dpp_f64<kRowRor4>(d);
+    d += dpp_f64<kRowRor8>(d);
+    d += shfl_xor_f64(d, 16);
+    return d + shfl_xor_f64(d, 32);
+}
+
+__device__ __forceinline__ float wave_sum(float d)
+{
+    d += __uint_as_float(dpp<kQuadXor1>(__float_as_uint(d)));
+    d += __uint_as_float(dpp<kQuadXor2>(__float_as_uint(d)));
+    d += __uint_as_float(dpp<kRowRor4>(__float_as_uint(d)));
+    d += __uint_as_float(dpp<kRowRor8>(__float_as_uint(d)));
+    d += __shfl_xor(d, 16, 64);
+    return d + __shfl_xor(d, 32, 64);
+}
+
+// A segment of a row on its way from memory: lane l holds columns
+// j0 + (64 u + l) G + e, G per 16-byte load; columns at or past V read as -inf.
+template <bool BF16>
+struct Segment {
+    static constexpr int G = BF16 ? 8 : 4, NQ = 32 / G;
+    uint4 q[NQ];
+    __device__ __forceinline__ void load(const void *row, int64_t V, int64_t j0, int lane)
+    {
+        if (j0 + kSegCols <= V) {
+#pragma unroll
+            for (int u = 0; u < NQ; ++u)
+                q[u] = *reinterpret_cast<const uint4 *>(static_cast<const char *>(row) +
+                                                        (j0 + (64 * u + lane) * G) * (16 / G));
+            return;
+        }
+#pragma unroll
+        for (int u = 0; u < NQ; ++u) {
+            uint32_t w[4];
+            const int64_t j = j0 + (64 * u + lane) * G;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                if constexpr (BF16) {
+                    const uint16_t *p = static_cast<const uint16_t *>(row) + j + 2 * e;
+                    const uint32_t lo = j + 2 * e < V ? p[0] : 0xff80u;
+                    const uint32_t hi = j + 2 * e + 1 < V ? p[1] : 0xff80u;
+                    w[e] = lo | (hi << 16);
+                } else {
+                    w[e] = j + e < V ? static_cast<const uint32_t *>(row)[j + e] : 0xff800000u;
+                }
+            }
+            q[u] = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+    }
+    __device__ __forceinline__ void values(float (&v)[32]) const
+    {
+#pragma unroll
+        for (int u = 0; u < NQ; ++u) {
+            const uint32_t w[4] = {q[u].x, q[u].y, q[u].z, q[u].w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                if constexpr (BF16) {
+                    v[8 * u + 2 * e] = __uint_as_float(w[e] << 16);
+                    v[8 * u + 2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
+                } else {
+                    v[4 * u + e] = __uint_as_float(w[e]);
+                }
+            }
+        }
+    }
+};
+
+// The k largest of a segment's values (v, held as Segment loads them, some above
+// -inf, none NaN or +inf; gm the maxima of four at a time, lm the lane's) into
+// out[0 .. k), as keys: order_key above the complement of the column, so that a
+// larger key is a larger value or an equal one of an earlier column; 0 where fewer
+// lie above -inf.  Candidates: the k-th largest of the 64 lane maxima is a lower
+// bound of the segment's k-th largest value (that many lanes hold a value at least
+// as large), cut to its upper 16 bits so that 16 ballots find it; the few values
+// at or above it are collected in LDS (mine[kCandCap], the wave's own) and ranked
+// by counting.
+template <int G>
+__device__ __forceinline__ void keep_largest(const float (&v)[32], const float (&gm)[8], float lm,
+                                             uint32_t j0, int lane, int k, uint64_t *mine,
+                                             uint64_t *out)
+{
+    const uint32_t mykey = order_key(lm);
+    uint32_t t = 0;
+#pragma unroll
+    for (int b = 31; b >= 16; --b) {
+        const uint32_t c = t | (1u << b);
+        if (__popcll(__ballot(mykey >= c)) >= k)
+            t = c;
+    }
+    const float bound = key_value(max(t, order_key(-INFINITY) + 1u));
+    const uint32_t rest = 0xffffffffu - (j0 + static_cast<uint32_t>(lane * G));
+    auto key_of = [&](int i) {
+        return (static_cast<uint64_t>(order_key(v[i])) << 32) | (rest - static_cast<uint32_t>(64 * (i / G) * G + i % G));
+    };
+    int n = 0;  // the same in every lane
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+        if (!__ballot(gm[u] >= bound))
+            continue;
+#pragma unroll
+        for (int i = 4 * u; i < 4 * u + 4; ++i) {
+            const uint64_t mask = __ballot(v[i] >= bound);
+            if (v[i] >= bound) {
+                const int at = n + __popcll(mask & ((1ull << lane) - 1ull));
+                if (at < kCandCap)
+                    mine[at] = key_of(i);
+            }
+            n += __popcll(mask);
+        }
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    if (n <= kCandCap) {
+        for (int i = lane; i < n; i += 64) {
+            const uint64_t key = mine[i];
+            int rank = 0;
+            for (int q = 0; q < n; ++q)
+                rank += mine[q] > key;
+            if (rank < k)
+                out[rank] = key;
+        }
+        if (n + lane < k)
+            out[n + lane] = 0;
+        return;
+    }
+    // Many equal values at the bound: k rounds, each taking the largest key
+    // below the last one.
+    uint64_t last = ~0ull;
+    for (int r = 0; r < k; ++r) {
+        uint64_t best = 0;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+            const uint64_t key = key_of(i);
+            if (v[i] > -INFINITY && key < last && key > best)
+                best = key;
+        }
+#pragma unroll
+        for (int off = 32; off >= 1; off >>= 1)
+            best = max(best, shfl_xor_u64(best, off));
+        if (lane == 0)
+            out[r] = best;
+        last = best;
+    }
+}
+
+}  // namespace lmh
