@@ -524,6 +524,139 @@ int32_t lmhead_beam_reorder(const void *src, int64_t src_outer, int64_t src_row,
                             void *stream);
 
 /*
+ * lmhead_logprobs -- log-probabilities of given tokens, with the rows' entropies,
+ * the tokens' ranks and the most likely alternatives
+ *
+ *  With x = (z - max z) / T and p = softmax(z / T), row i of the logits gives
+ *    logprob[i] = log p[token[i]]; 0 for token[i] == ignore_index, NaN for any
+ *                 other token outside [0, n_cols),
+ *    entropy[i] = - sum_j p_j log p_j,
+ *    rank[i]    = the number of columns before the token in descending order of
+ *                 the logits, equal ones by ascending column (0: the likeliest);
+ *                 -1 where the log-probability is 0 by ignore_index or NaN,
+ *    top_logprob[i][l], top_token[i][l] = log p and column of the n_top first
+ *                 columns in that order; columns at -inf are not listed, what
+ *                 they leave free holds -inf and -1,
+ *    stats[i]   = {m = max z, d = sum exp(x), entropy, logprob}: what
+ *                 lmhead_logprobs_bwd needs.
+ *  The logits are read once.  The sums are FP32 within 2048 columns and FP64
+ *  from there on; ranks and alternatives come from the logits, not from rounded
+ *  probabilities.  A row that holds NaN or +inf, one of -inf only, and one whose
+ *  temperature is not positive and finite, is NaN (tokens -1).
+ *
+ *  logits   [n_rows x n_cols], leading dimension ld, FP32 or BF16 (logits_dtype),
+ *           as lmhead_logits writes them.
+ *  token    int32 [n_rows], or NULL: then logprob and rank must be NULL too, and
+ *           stats holds 0 in logprob's place.
+ *  temperature  FP32, stride 0 (one value) or 1 (one per row), or NULL (1).
+ *  logprob, entropy, rank  [n_rows] or NULL (not wanted).
+ *  top_logprob FP32, top_token int32 [n_rows x n_top], contiguous; not used when
+ *           n_top == 0.
+ *  Limits: 1 <= n_cols, n_top <= min(64, n_cols).
+ *  workspace as lmhead_logits_lora, of lmhead_logprobs_workspace_bytes(n_rows,
+ *  n_cols, n_top) bytes.  Outputs overlap neither inputs nor each other.
+ */
+int64_t lmhead_logprobs_workspace_bytes(int64_t n_rows, int64_t n_cols, int64_t n_top);
+int32_t lmhead_logprobs(const void *logits, int64_t ld, int32_t logits_dtype, int64_t n_rows,
+                        int64_t n_cols, const int32_t *token, int32_t ignore_index,
+                        const float *temperature, int64_t temperature_stride, int64_t n_top,
+                        float *logprob, float *entropy, int32_t *rank, float *top_logprob,
+                        int32_t *top_token, float *stats, void *workspace, int64_t workspace_bytes,
+                        void *stream);
+
+/*
+ * lmhead_logprobs_bwd -- gradient of lmhead_logprobs with respect to the logits
+ *
+ *    dlogits[i][j] = (1 / T) [ g_i ([j == token[i]] - p_j) - h_i p_j (log p_j + H_i) ],
+ *  g = dlogprob, h = dentropy (FP32, stride 0 or 1; NULL: 0), H the entropy.
+ *  stats as the forward wrote it for the same logits and temperature.  g counts
+ *  as 0 in rows of ignore_index (token NULL: in all rows).  A row whose g and h
+ *  are 0 gets zeros, whatever its logits; a row whose token is neither
+ *  ignore_index nor a column gets NaN.
+ *  dlogits [n_rows x n_cols], leading dimension ldg, FP32 or BF16 (grad_dtype:
+ *  the FP32 value rounded once); it may be the logits themselves when types and
+ *  leading dimensions agree, and otherwise overlaps no input.
+ */
+int32_t lmhead_logprobs_bwd(const void *logits, int64_t ld, int32_t logits_dtype,
+                            const float *stats, const int32_t *token, int32_t ignore_index,
+                            const float *temperature, int64_t temperature_stride,
+                            const float *dlogprob, int64_t dlogprob_stride,
+                            const float *dentropy, int64_t dentropy_stride, void *dlogits,
+                            int64_t ldg, int32_t grad_dtype, int64_t n_rows, int64_t n_cols,
+                            void *stream);
+
+/*
+ * lmhead_distill_fwd -- cross-entropy against a teacher known by its top tokens
+ *
+ *  Row i has a list of n_list tokens c_l = teacher_token[i][l] with values v_l =
+ *  teacher_value[i][l]; an entry of a negative token or of value -inf is absent
+ *  (so that lists may be shorter, and lmhead_logprobs' alternatives fit).  With
+ *  p = softmax(z / T):
+ *    tail == 0: the values are logits; q = softmax(v / T) over the list,
+ *      loss[i] = sum_l q_l (log q_l - log p_{c_l}).
+ *    tail != 0: the values are log-probabilities (of the teacher at temperature
+ *      T; used as they are), q_l = exp(v_l), and all other columns are one class
+ *      with q_r = max(0, 1 - sum q) and p_r the sum of their p:
+ *      loss[i] = sum_l q_l (log q_l - log p_{c_l}) + q_r (log q_r - log p_r).
+ *      Where every other column is at -inf that class is left out.
+ *  Both are Kullback-Leibler divergences (multiply the upstream gradient by T^2
+ *  to scale them as is common).  A token that is listed twice counts twice in q
+ *  and once in p.  A row whose list is empty has loss 0 and gradient 0.  A row
+ *  with a token >= n_cols, a value of NaN or +inf, a logit of NaN or +inf, no
+ *  logit above -inf or a temperature that is not positive and finite is NaN.  A
+ *  listed column at -inf with q > 0 makes the loss +inf.
+ *    stats[i] = 8 floats: {max z, sum exp((z - max z) / T), loss, sum of q (with
+ *      q_r), o, w, t, u}: off the list the gradient per unit of dloss / T is
+ *      exp((z - o) / T) w, and q_l = exp((v_l - t) / T) / u (tail != 0: t = 0,
+ *      u = 1, without T); all 0 where the list is empty.
+ *  logits, logits_dtype, temperature as lmhead_logprobs.  teacher_token int32 and
+ *  teacher_value FP32 or BF16 (teacher_dtype), [n_rows x n_list], row pitches
+ *  ldt, ldv >= n_list, aligned to their elements.
+ *  loss [n_rows] or NULL.  Limits: n_cols >= 1, 0 <= n_list <= 256.
+ *  workspace as lmhead_logits_lora, of lmhead_distill_workspace_bytes(n_rows,
+ *  n_cols) bytes.  Outputs overlap neither inputs nor each other.
+ */
+int64_t lmhead_distill_workspace_bytes(int64_t n_rows, int64_t n_cols);
+int32_t lmhead_distill_fwd(const void *logits, int64_t ld, int32_t logits_dtype, int64_t n_rows,
+                           int64_t n_cols, const int32_t *teacher_token, int64_t ldt,
+                           const void *teacher_value, int64_t ldv, int32_t teacher_dtype,
+                           int64_t n_list, int32_t tail, const float *temperature,
+                           int64_t temperature_stride, float *loss, float *stats, void *workspace,
+                           int64_t workspace_bytes, void *stream);
+
+/*
+ * lmhead_distill_bwd -- its gradient with respect to the logits
+ *
+ *  With q = 0 off the list, and Q = sum q (+ q_r):
+ *    tail == 0: dlogits[i][j] = (dloss_i / T) (p_j - q_j)
+ *    tail != 0: dlogits[i][j] = (dloss_i / T) (Q p_j - q_j) on the list,
+ *               dlogits[i][j] = (dloss_i / T) p_j (Q - q_r / p_r) off it.
+ *  stats as lmhead_distill_fwd wrote it for the same logits, lists, tail and
+ *  temperature.  dloss FP32, stride 0 or 1; a row whose dloss is 0 gets zeros,
+ *  whatever its logits.  dlogits as lmhead_logprobs_bwd.
+ */
+int32_t lmhead_distill_bwd(const void *logits, int64_t ld, int32_t logits_dtype,
+                           const float *stats, const int32_t *teacher_token, int64_t ldt,
+                           const void *teacher_value, int64_t ldv, int32_t teacher_dtype,
+                           int64_t n_list, int32_t tail, const float *temperature,
+                           int64_t temperature_stride, const float *dloss, int64_t dloss_stride,
+                           void *dlogits, int64_t ldg, int32_t grad_dtype, int64_t n_rows,
+                           int64_t n_cols, void *stream);
+
+/*
+ * lmhead_distill_fused -- lmhead_distill_fwd and lmhead_distill_bwd in one call,
+ * for an upstream gradient known before the forward
+ */
+int32_t lmhead_distill_fused(const void *logits, int64_t ld, int32_t logits_dtype, int64_t n_rows,
+                             int64_t n_cols, const int32_t *teacher_token, int64_t ldt,
+                             const void *teacher_value, int64_t ldv, int32_t teacher_dtype,
+                             int64_t n_list, int32_t tail, const float *temperature,
+                             int64_t temperature_stride, const float *dloss, int64_t dloss_stride,
+                             float *loss, float *stats, void *dlogits, int64_t ldg,
+                             int32_t grad_dtype, void *workspace, int64_t workspace_bytes,
+                             void *stream);
+
+/*
  * lmhead_diag_mfma_loop -- diagnostic: the sustained BF16 matrix-core rate.
  *
  *  Not a step of the method: a register-only loop that the benchmark runs

@@ -16,6 +16,10 @@ Shapes (row-major, last dimension contiguous, rows may be padded):
   wgrad: dlogits [M, V] bf16, x [M, K] bf16 -> dW [V, K] fp32
   adapters: A [n, r, K] bf16, B [n, V, r] bf16, adapter [M] int32, scale [n] fp32
   beams: logits [B * W, V] fp32 or bf16, scores [B, W] fp32, parent [B, n_out] int32
+  log-probabilities: logits [n, V] fp32 or bf16, token [n] int32 -> logprob, entropy [n] fp32,
+  rank [n] int32, top_logprob [n, n_top] fp32, top_token [n, n_top] int32, stats [n, 4] fp32
+  distillation: teacher_token [n, k] int32, teacher_value [n, k] fp32 or bf16 -> loss [n] fp32,
+  stats [n, 8] fp32
 """
 import ctypes
 import os
@@ -30,11 +34,14 @@ __all__ = [
     "lmhead_status_str", "lmhead_version", "lmhead_diag_mfma_loop", "lmhead_dgrad_workspace_bytes",
     "lmhead_logits_lora", "lmhead_logits_lora_workspace_bytes", "lmhead_lora_bwd",
     "lmhead_lora_bwd_workspace_bytes", "lmhead_beam_select", "lmhead_beam_select_workspace_bytes",
-    "lmhead_beam_reorder",
+    "lmhead_beam_reorder", "lmhead_logprobs", "lmhead_logprobs_workspace_bytes", "lmhead_logprobs_bwd",
+    "lmhead_distill_fwd", "lmhead_distill_bwd", "lmhead_distill_fused", "lmhead_distill_workspace_bytes",
+    "DISTILL_STATS_COLS",
 ]
 
 LMH_BF16, LMH_FP32, LMH_FP16 = 0, 1, 2
 STATS_COLS = 4  # {m, d, X_y, loss}
+DISTILL_STATS_COLS = 8  # see lmhead_distill_fwd in lmhead.h
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_HERE, "liblmhead.so")
@@ -77,6 +84,18 @@ _SIGNATURES = {
                             _vp, _vp, _i64, _vp], _i32),
     "lmhead_beam_reorder": ([_vp, _i64, _i64, _i64, _vp, _i64, _i64, _i64, _vp, _vp, _i64, _i64,
                              _i64, _i64, _i64, _i64, _i64, _vp], _i32),
+    "lmhead_logprobs_workspace_bytes": ([_i64, _i64, _i64], _i64),
+    "lmhead_logprobs": ([_vp, _i64, _i32, _i64, _i64, _vp, _i32, _vp, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _vp,
+                         _vp, _i64, _vp], _i32),
+    "lmhead_logprobs_bwd": ([_vp, _i64, _i32, _vp, _vp, _i32, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _i32,
+                             _i64, _i64, _vp], _i32),
+    "lmhead_distill_workspace_bytes": ([_i64, _i64], _i64),
+    "lmhead_distill_fwd": ([_vp, _i64, _i32, _i64, _i64, _vp, _i64, _vp, _i64, _i32, _i64, _i32, _vp, _i64, _vp,
+                            _vp, _vp, _i64, _vp], _i32),
+    "lmhead_distill_bwd": ([_vp, _i64, _i32, _vp, _vp, _i64, _vp, _i64, _i32, _i64, _i32, _vp, _i64, _vp, _i64,
+                            _vp, _i64, _i32, _i64, _i64, _vp], _i32),
+    "lmhead_distill_fused": ([_vp, _i64, _i32, _i64, _i64, _vp, _i64, _vp, _i64, _i32, _i64, _i32, _vp, _i64, _vp,
+                              _i64, _vp, _vp, _vp, _i64, _i32, _vp, _i64, _vp], _i32),
 }
 
 DGRAD_NOALLOC_MAX_BYTES = 64 << 20  # LMH_DGRAD_NOALLOC_MAX_BYTES in lmhead.h
@@ -598,9 +617,20 @@ def _on_stream(fn, stream, workspace, *args):
         if workspace is None:
             raise ValueError(f"{fn.__name__} on a raw stream handle needs an explicit workspace")
         stream = torch.cuda.ExternalStream(int(getattr(stream, "cuda_stream", stream)))
+    return _run_on(stream, fn, *args, workspace)
+
+
+def _on_launch_stream(fn, stream, *args):
+    """_on_stream for a call without a workspace."""
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(getattr(stream, "cuda_stream", stream)))
+    return _run_on(stream, fn, *args)
+
+
+def _run_on(stream, fn, *args):
     caller = torch.cuda.current_stream()
     with torch.cuda.stream(stream):
-        results = fn(*args, workspace)
+        results = fn(*args)
     for t in results if isinstance(results, tuple) else (results,):
         if t is not None:
             t.record_stream(caller)
@@ -894,6 +924,236 @@ def lmhead_beam_reorder(state, parent, out=None, beam_dim=0, len_dim=None, lengt
            lib().lmhead_beam_reorder(ps, *ss, pd, *ds, pp, pl, n_outer, B, W_in, W_out, n_heads, positions,
                                      pos_bytes, _stream(stream)))
     return dst
+
+
+# ------------------------------------- log-probabilities and distillation
+
+def _row_logits(logits):
+    """(pointer, ld, dtype code, n, V) of fp32 or bf16 logits [n, V]."""
+    if not isinstance(logits, torch.Tensor) or logits.dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError("logits: expected a GPU float32 or bfloat16 tensor")
+    pz, ld = _mat(logits, "logits", logits.dtype)
+    return (pz, ld, _DT[logits.dtype], *logits.shape)
+
+
+def _per_row(t, name, n):
+    """(pointer, stride) of an fp32 tensor of 1 element (every row) or n elements
+    (one per row); (None, 0) of None."""
+    if t is None:
+        return None, 0
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.float32:
+        raise TypeError(f"{name}: expected a GPU float32 tensor of 1 or {n} elements")
+    if t.numel() == 1:
+        return _vec(t, name, torch.float32, 1), 0
+    return _vec(t, name, torch.float32, n), 1
+
+
+def _row_out(t, name, dtype, shape, like):
+    """(tensor or None, pointer) of an output: False: skipped, None: a new one,
+    else the caller's."""
+    if t is False:
+        return None, None
+    if t is None:
+        t = like.new_empty(shape, dtype=dtype)
+        return t, t.data_ptr()
+    n = 1
+    for s in shape:
+        n *= s
+    p = _vec(t, name, dtype, n)
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}")
+    return t, p
+
+
+def _row_grad(fn, logits, dlogits, grad_dtype, in_place):
+    """(tensor, pointer, ld, dtype code) of the gradient of logits [n, V]."""
+    code = _out_code(fn, logits if in_place else dlogits, grad_dtype, "fp32")
+    if in_place:
+        dlogits = logits
+    elif dlogits is None:
+        if code not in (LMH_BF16, LMH_FP32):
+            _check(fn, 1)
+        dlogits = _empty_rows(*logits.shape, _TORCH_DT[code], logits)
+    pg, ldg = _mat(dlogits, "dlogits", dlogits.dtype)
+    if dlogits.shape != logits.shape:
+        raise ValueError("dlogits must be [n, V]")
+    return dlogits, pg, ldg, code
+
+
+def lmhead_logprobs_workspace_bytes(n_rows, n_cols, n_top=0):
+    """Workspace bytes lmhead_logprobs needs."""
+    need = lib().lmhead_logprobs_workspace_bytes(int(n_rows), int(n_cols), int(n_top))
+    if need < 0:
+        _check("lmhead_logprobs_workspace_bytes", -need)
+    return need
+
+
+def lmhead_logprobs(logits, token=None, ignore_index=-100, temperature=None, n_top=0, logprob=None,
+                    entropy=None, rank=None, top_logprob=None, top_token=None, stats=None, workspace=None,
+                    stream=None):
+    """Log-probabilities of one token per row under softmax(logits / temperature),
+    with the rows' entropies, the tokens' ranks and the n_top likeliest columns:
+    (logprob [n], entropy [n], rank [n] int32, top_logprob [n, n_top], top_token
+    [n, n_top] int32, stats [n, 4]), None in the place of what is skipped.
+
+    logits [n, V] fp32 or bf16; token int32 [n] (ignore_index: logprob 0, rank
+    -1) or None (no logprob, no rank); temperature a GPU fp32 tensor of 1 or n
+    elements or None (1).  rank: columns ahead of the token, equal logits by
+    ascending column; the alternatives come in the same order (at most 64; -1
+    and -inf where fewer columns lie above -inf).  False for logprob, entropy or
+    rank skips it.  stats = {m, d, entropy, logprob} is what lmhead_logprobs_bwd
+    needs."""
+    if stream is not None and (logprob is None or entropy is None or rank is None or stats is None or
+                               workspace is None or (n_top and (top_logprob is None or top_token is None))):
+        return _on_stream(lmhead_logprobs, stream, workspace, logits, token, ignore_index, temperature, n_top,
+                          logprob, entropy, rank, top_logprob, top_token, stats)
+    pz, ld, code, n, V = _row_logits(logits)
+    k = int(n_top)
+    if token is None:
+        if isinstance(logprob, torch.Tensor) or isinstance(rank, torch.Tensor):
+            raise ValueError("logprob and rank need a token")
+        py, logprob, rank = None, False, False
+    else:
+        py = _vec(token, "token", torch.int32, n)
+    pt, st = _per_row(temperature, "temperature", n)
+    need = lmhead_logprobs_workspace_bytes(n, V, k)
+    logprob, po = _row_out(logprob, "logprob", torch.float32, (n,), logits)
+    entropy, pe = _row_out(entropy, "entropy", torch.float32, (n,), logits)
+    rank, pr = _row_out(rank, "rank", torch.int32, (n,), logits)
+    top_logprob, pa = _row_out(top_logprob if k else False, "top_logprob", torch.float32, (n, k), logits)
+    top_token, pb = _row_out(top_token if k else False, "top_token", torch.int32, (n, k), logits)
+    if k and (top_logprob is None or top_token is None):
+        raise ValueError("the alternatives are not wanted: n_top = 0")
+    stats, ps = _row_out(stats, "stats", torch.float32, (n, STATS_COLS), logits)
+    ws, nbytes = _workspace(need, workspace, logits)
+    _check("lmhead_logprobs",
+           lib().lmhead_logprobs(pz, ld, code, n, V, py, int(ignore_index), pt, st, k, po, pe, pr, pa, pb, ps,
+                                 ws.data_ptr(), nbytes, _stream(stream)))
+    return logprob, entropy, rank, top_logprob, top_token, stats
+
+
+def lmhead_logprobs_bwd(logits, stats, token, dlogprob, dentropy=None, ignore_index=-100, temperature=None,
+                        dlogits=None, grad_dtype=None, in_place=False, stream=None):
+    """Gradient of lmhead_logprobs' log-probabilities and entropies with respect
+    to the logits: dlogits [n, V].
+
+    stats: the forward's, for the same logits and temperature.  dlogprob,
+    dentropy: GPU fp32 tensors of 1 element (every row) or n elements, or None
+    (0); rows where both are 0 get zeros.  token may be None when dlogprob is.
+    grad_dtype as in lmhead_xent_bwd; in_place=True writes over `logits` (in
+    their type)."""
+    if stream is not None and dlogits is None and not in_place:
+        return _on_launch_stream(lmhead_logprobs_bwd, stream, logits, stats, token, dlogprob, dentropy,
+                                 ignore_index, temperature, None, grad_dtype)
+    pz, ld, code, n, V = _row_logits(logits)
+    ps = _vec(stats, "stats", torch.float32, n * STATS_COLS)
+    if token is None and dlogprob is not None:
+        raise ValueError("dlogprob needs a token")
+    py = None if token is None else _vec(token, "token", torch.int32, n)
+    pl, sl = _per_row(dlogprob, "dlogprob", n)
+    pe, se = _per_row(dentropy, "dentropy", n)
+    pt, st = _per_row(temperature, "temperature", n)
+    dlogits, pg, ldg, gcode = _row_grad("lmhead_logprobs_bwd", logits, dlogits, grad_dtype, in_place)
+    _check("lmhead_logprobs_bwd",
+           lib().lmhead_logprobs_bwd(pz, ld, code, ps, py, int(ignore_index), pt, st, pl, sl, pe, se, pg, ldg,
+                                     gcode, n, V, _stream(stream)))
+    return dlogits
+
+
+def lmhead_distill_workspace_bytes(n_rows, n_cols):
+    """Workspace bytes lmhead_distill_fwd and lmhead_distill_fused need."""
+    need = lib().lmhead_distill_workspace_bytes(int(n_rows), int(n_cols))
+    if need < 0:
+        _check("lmhead_distill_workspace_bytes", -need)
+    return need
+
+
+def _teacher_list(token, value, n):
+    """(token pointer, pitch, value pointer, pitch, dtype code, k) of a teacher's
+    lists [n, k]: rows may be padded, elements of a row are contiguous."""
+    if not isinstance(value, torch.Tensor) or value.dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError("teacher_value: expected a GPU float32 or bfloat16 tensor")
+    pt, ldt = _mat(token, "teacher_token", torch.int32)
+    pv, ldv = _mat(value, "teacher_value", value.dtype)
+    if token.shape != value.shape or token.shape[0] != n:
+        raise ValueError("teacher_token and teacher_value must be [n, k]")
+    return pt, ldt, pv, ldv, _DT[value.dtype], token.shape[1]
+
+
+def lmhead_distill_fwd(logits, teacher_token, teacher_value, tail=False, temperature=None, loss=None,
+                       stats=None, workspace=None, stream=None):
+    """Divergence of softmax(logits / temperature) from a teacher known by its top
+    tokens: (loss [n], stats [n, 8]).
+
+    teacher_token int32 and teacher_value fp32 or bf16, [n, k] with k <= 256;
+    entries of a negative token or of value -inf are absent, rows without any
+    have loss 0.  tail=False: the values are logits, normalised over the list.
+    tail=True: they are log-probabilities (lmhead_logprobs' top_logprob), and
+    what they leave belongs to all other columns as one class.  loss=False skips
+    it; stats is what lmhead_distill_bwd needs."""
+    if stream is not None and (loss is None or stats is None or workspace is None):
+        return _on_stream(lmhead_distill_fwd, stream, workspace, logits, teacher_token, teacher_value, tail,
+                          temperature, loss, stats)
+    pz, ld, code, n, V = _row_logits(logits)
+    teacher = _teacher_list(teacher_token, teacher_value, n)
+    pt, st = _per_row(temperature, "temperature", n)
+    need = lmhead_distill_workspace_bytes(n, V)
+    loss, pl = _row_out(loss, "loss", torch.float32, (n,), logits)
+    stats, ps = _row_out(stats, "stats", torch.float32, (n, DISTILL_STATS_COLS), logits)
+    ws, nbytes = _workspace(need, workspace, logits)
+    _check("lmhead_distill_fwd",
+           lib().lmhead_distill_fwd(pz, ld, code, n, V, *teacher, int(bool(tail)), pt, st, pl, ps,
+                                    ws.data_ptr(), nbytes, _stream(stream)))
+    return loss, stats
+
+
+def lmhead_distill_bwd(logits, stats, teacher_token, teacher_value, dloss, tail=False, temperature=None,
+                       dlogits=None, grad_dtype=None, in_place=False, stream=None):
+    """Gradient of lmhead_distill_fwd's loss with respect to the logits: dlogits
+    [n, V].  stats: the forward's, for the same logits, lists, tail and
+    temperature.  dloss a GPU fp32 tensor of 1 or n elements; rows where it is 0
+    get zeros.  grad_dtype and in_place as in lmhead_logprobs_bwd."""
+    if stream is not None and dlogits is None and not in_place:
+        return _on_launch_stream(lmhead_distill_bwd, stream, logits, stats, teacher_token, teacher_value, dloss,
+                                 tail, temperature, None, grad_dtype)
+    pz, ld, code, n, V = _row_logits(logits)
+    ps = _vec(stats, "stats", torch.float32, n * DISTILL_STATS_COLS)
+    teacher = _teacher_list(teacher_token, teacher_value, n)
+    pt, st = _per_row(temperature, "temperature", n)
+    if dloss is None:
+        raise TypeError("dloss: expected a GPU float32 tensor")
+    pd, sd = _per_row(dloss, "dloss", n)
+    dlogits, pg, ldg, gcode = _row_grad("lmhead_distill_bwd", logits, dlogits, grad_dtype, in_place)
+    _check("lmhead_distill_bwd",
+           lib().lmhead_distill_bwd(pz, ld, code, ps, *teacher, int(bool(tail)), pt, st, pd, sd, pg, ldg, gcode,
+                                    n, V, _stream(stream)))
+    return dlogits
+
+
+def lmhead_distill_fused(logits, teacher_token, teacher_value, dloss, tail=False, temperature=None,
+                         dlogits=None, grad_dtype=None, in_place=False, loss=None, stats=None, workspace=None,
+                         stream=None):
+    """lmhead_distill_fwd and lmhead_distill_bwd in one call, for an upstream
+    gradient known before the forward: (loss [n], stats [n, 8], dlogits)."""
+    if stream is not None and (loss is None or stats is None or workspace is None or
+                               (dlogits is None and not in_place)):
+        return _on_stream(lmhead_distill_fused, stream, workspace, logits, teacher_token, teacher_value, dloss, tail,
+                          temperature, dlogits, grad_dtype, in_place, loss, stats)
+    pz, ld, code, n, V = _row_logits(logits)
+    teacher = _teacher_list(teacher_token, teacher_value, n)
+    pt, st = _per_row(temperature, "temperature", n)
+    if dloss is None:
+        raise TypeError("dloss: expected a GPU float32 tensor")
+    pd, sd = _per_row(dloss, "dloss", n)
+    dlogits, pg, ldg, gcode = _row_grad("lmhead_distill_fused", logits, dlogits, grad_dtype, in_place)
+    need = lmhead_distill_workspace_bytes(n, V)
+    loss, pl = _row_out(loss, "loss", torch.float32, (n,), logits)
+    stats, ps = _row_out(stats, "stats", torch.float32, (n, DISTILL_STATS_COLS), logits)
+    ws, nbytes = _workspace(need, workspace, logits)
+    _check("lmhead_distill_fused",
+           lib().lmhead_distill_fused(pz, ld, code, n, V, *teacher, int(bool(tail)), pt, st, pd, sd, pl, ps, pg,
+                                      ldg, gcode, ws.data_ptr(), nbytes, _stream(stream)))
+    return loss, stats, dlogits
 
 
 MFMA_LOOP_FLOP_PER_WORKGROUP_ITER = 2 * 32 * 32 * 16 * 8 * 4  # 8 chains x 4 waves

@@ -286,6 +286,77 @@ bool beam_sizes_ok(int64_t B, int64_t W, int64_t V, int64_t n_out)
     return B == 0 || lmh::beam_segments(V) <= kMaxLaunchItems / 64 / (B * W);
 }
 
+// Log-probabilities and distillation: rows of at least one column.
+constexpr int64_t kMaxTop = 64;
+
+bool rows_ok(int64_t n, int64_t V)
+{
+    return n >= 0 && n <= kMaxDim && V >= 1 && V <= kMaxDim;
+}
+
+// Number of values behind a pointer of stride 0 (one) or 1 (one per row).
+int64_t strided(const void *p, int64_t stride, int64_t n)
+{
+    return p ? (stride == 0 ? 1 : n) : 0;
+}
+
+// A dlogits operand of [n x V] logits: its own checks, and that it is the logits
+// themselves or apart from them.
+int32_t check_row_grad(const void *logits, int64_t ld, int32_t dt, void *g, int64_t ldg, int32_t gdt, int64_t n,
+                       int64_t V)
+{
+    LMH_TRY(check_matrix(g, n, V, ldg, gdt == LMH_BF16 ? 8 : 4));
+    if (g == logits)
+        return dt == gdt && ld == ldg ? LMH_OK : LMH_ERR_ALIAS;
+    return overlaps(span_of(g, n, V, ldg, gdt == LMH_BF16 ? 2 : 4),
+                    span_of(logits, n, V, ld, dt == LMH_BF16 ? 2 : 4)) ? LMH_ERR_ALIAS : LMH_OK;
+}
+
+struct TeacherArgs {
+    const int32_t *token;
+    int64_t ldt;
+    const void *value;
+    int64_t ldv;
+    int32_t dtype;
+    int64_t k;
+};
+
+bool element_aligned(const void *p, int64_t size)
+{
+    return reinterpret_cast<uintptr_t>(p) % static_cast<uintptr_t>(size) == 0;
+}
+
+// What the distillation calls share: the logits, the lists and the temperature.
+int32_t check_distill(const void *logits, int64_t ld, int32_t dt, int64_t n, int64_t V, const TeacherArgs &t,
+                      const float *temperature, int64_t temperature_stride)
+{
+    LMH_TRY(check_matrix(logits, n, V, ld, dt == LMH_BF16 ? 8 : 4));
+    if (t.k > 0) {
+        if (!t.token || !t.value)
+            return LMH_ERR_NULL;
+        if (t.ldt < t.k || t.ldv < t.k || !span_fits(n, t.k, t.ldt) || !span_fits(n, t.k, t.ldv))
+            return LMH_ERR_SHAPE;
+        if (!aligned4(t.token) || !element_aligned(t.value, t.dtype == LMH_BF16 ? 2 : 4))
+            return LMH_ERR_ALIGN;
+    }
+    if (temperature_stride != 0 && temperature_stride != 1)
+        return LMH_ERR_SHAPE;
+    return aligned4(temperature) ? LMH_OK : LMH_ERR_ALIGN;
+}
+
+lmh::Distill distill_args(const void *logits, int64_t ld, int32_t dt, int64_t n, int64_t V, const TeacherArgs &t,
+                          int32_t tail, const float *temperature, int64_t temperature_stride)
+{
+    lmh::Distill p = {};
+    p.logits = logits, p.ld = ld, p.bf16 = dt == LMH_BF16;
+    p.n = n, p.V = V;
+    p.token = t.token, p.ldt = t.ldt;
+    p.value = t.value, p.ldv = t.ldv, p.value_bf16 = t.dtype == LMH_BF16;
+    p.k = t.k, p.tail = tail != 0;
+    p.temperature = temperature, p.temperature_stride = temperature_stride;
+    return p;
+}
+
 }  // namespace
 
 extern "C" {
@@ -986,6 +1057,227 @@ int32_t lmhead_beam_reorder(const void *src, int64_t src_outer, int64_t src_row,
     return launch_status(lmh::launch_beam_reorder(src, dst, ss, ds, parent, lengths, n_outer, n_requests,
                                                   beams_in, beams_out, n_heads, n_positions,
                                                   position_bytes, static_cast<hipStream_t>(stream)));
+}
+
+int64_t lmhead_logprobs_workspace_bytes(int64_t n_rows, int64_t n_cols, int64_t n_top)
+{
+    if (!rows_ok(n_rows, n_cols) || n_top < 0 || n_top > kMaxTop || n_top > n_cols)
+        return -static_cast<int64_t>(LMH_ERR_SHAPE);
+    return lmh::logprobs_workspace_bytes(n_rows, n_cols, n_top);
+}
+
+int32_t lmhead_logprobs(const void *logits, int64_t ld, int32_t logits_dtype, int64_t n_rows,
+                        int64_t n_cols, const int32_t *token, int32_t ignore_index,
+                        const float *temperature, int64_t temperature_stride, int64_t n_top,
+                        float *logprob, float *entropy, int32_t *rank, float *top_logprob,
+                        int32_t *top_token, float *stats, void *workspace, int64_t workspace_bytes,
+                        void *stream)
+{
+    LMH_TRY(check_dtype_out(logits_dtype));
+    if (!rows_ok(n_rows, n_cols) || n_top < 0 || n_top > kMaxTop || n_top > n_cols || workspace_bytes < 0 ||
+        (temperature_stride != 0 && temperature_stride != 1))
+        return LMH_ERR_SHAPE;
+    if (n_rows == 0)
+        return LMH_OK;
+    const bool bf16 = logits_dtype == LMH_BF16;
+    LMH_TRY(check_matrix(logits, n_rows, n_cols, ld, bf16 ? 8 : 4));
+    if (!stats || !workspace || (n_top > 0 && (!top_logprob || !top_token)) || (!token && (logprob || rank)))
+        return LMH_ERR_NULL;
+    if (n_top == 0)
+        top_logprob = nullptr, top_token = nullptr;
+    if (!aligned4(token) || !aligned4(temperature) || !aligned4(logprob) || !aligned4(entropy) || !aligned4(rank) ||
+        !aligned4(top_logprob) || !aligned4(top_token) || !aligned16(stats) || !aligned16(workspace))
+        return LMH_ERR_ALIGN;
+    const int64_t need = lmh::logprobs_workspace_bytes(n_rows, n_cols, n_top);
+    if (workspace_bytes < need)
+        return LMH_ERR_SHAPE;
+    const Span outs[] = {bytes_span(workspace, need), bytes_span(stats, 16 * n_rows),
+                         bytes_span(logprob, logprob ? 4 * n_rows : 0),
+                         bytes_span(entropy, entropy ? 4 * n_rows : 0), bytes_span(rank, rank ? 4 * n_rows : 0),
+                         bytes_span(top_logprob, 4 * n_rows * n_top), bytes_span(top_token, 4 * n_rows * n_top)};
+    const Span ins[] = {span_of(logits, n_rows, n_cols, ld, bf16 ? 2 : 4),
+                        bytes_span(token, token ? 4 * n_rows : 0),
+                        bytes_span(temperature, 4 * strided(temperature, temperature_stride, n_rows))};
+    if (outputs_clash(outs, 7, ins, 3))
+        return LMH_ERR_ALIAS;
+    lmh::Logprobs p = {};
+    p.logits = logits, p.ld = ld, p.bf16 = bf16;
+    p.n = n_rows, p.V = n_cols;
+    p.token = token, p.ignore_index = ignore_index;
+    p.temperature = temperature, p.temperature_stride = temperature_stride;
+    p.k = n_top;
+    p.logprob = logprob, p.entropy = entropy, p.rank = rank;
+    p.top_logprob = top_logprob, p.top_token = top_token;
+    p.stats = stats;
+    return launch_status(lmh::launch_logprobs(p, workspace, static_cast<hipStream_t>(stream)));
+}
+
+int32_t lmhead_logprobs_bwd(const void *logits, int64_t ld, int32_t logits_dtype,
+                            const float *stats, const int32_t *token, int32_t ignore_index,
+                            const float *temperature, int64_t temperature_stride,
+                            const float *dlogprob, int64_t dlogprob_stride,
+                            const float *dentropy, int64_t dentropy_stride, void *dlogits,
+                            int64_t ldg, int32_t grad_dtype, int64_t n_rows, int64_t n_cols,
+                            void *stream)
+{
+    LMH_TRY(check_dtype_out(logits_dtype));
+    LMH_TRY(check_dtype_out(grad_dtype));
+    if (!rows_ok(n_rows, n_cols))
+        return LMH_ERR_SHAPE;
+    for (const int64_t stride : {temperature_stride, dlogprob_stride, dentropy_stride})
+        if (stride != 0 && stride != 1)
+            return LMH_ERR_SHAPE;
+    if (n_rows == 0)
+        return LMH_OK;
+    LMH_TRY(check_matrix(logits, n_rows, n_cols, ld, logits_dtype == LMH_BF16 ? 8 : 4));
+    LMH_TRY(check_row_grad(logits, ld, logits_dtype, dlogits, ldg, grad_dtype, n_rows, n_cols));
+    if (!stats)
+        return LMH_ERR_NULL;
+    if (!aligned16(stats) || !aligned4(token) || !aligned4(temperature) || !aligned4(dlogprob) ||
+        !aligned4(dentropy))
+        return LMH_ERR_ALIGN;
+    const Span outs[] = {span_of(dlogits, n_rows, n_cols, ldg, grad_dtype == LMH_BF16 ? 2 : 4)};
+    const Span ins[] = {bytes_span(stats, 16 * n_rows), bytes_span(token, token ? 4 * n_rows : 0),
+                        bytes_span(temperature, 4 * strided(temperature, temperature_stride, n_rows)),
+                        bytes_span(dlogprob, 4 * strided(dlogprob, dlogprob_stride, n_rows)),
+                        bytes_span(dentropy, 4 * strided(dentropy, dentropy_stride, n_rows))};
+    if (outputs_clash(outs, 1, ins, 5))
+        return LMH_ERR_ALIAS;
+    lmh::LogprobsBwd p = {};
+    p.logits = logits, p.ld = ld, p.bf16 = logits_dtype == LMH_BF16;
+    p.stats = stats;
+    p.token = token, p.ignore_index = ignore_index;
+    p.temperature = temperature, p.temperature_stride = temperature_stride;
+    p.dlogprob = dlogprob, p.dlogprob_stride = dlogprob_stride;
+    p.dentropy = dentropy, p.dentropy_stride = dentropy_stride;
+    p.dlogits = dlogits, p.ldg = ldg, p.grad_bf16 = grad_dtype == LMH_BF16;
+    p.n = n_rows, p.V = n_cols;
+    return launch_status(lmh::launch_logprobs_bwd(p, static_cast<hipStream_t>(stream)));
+}
+
+int64_t lmhead_distill_workspace_bytes(int64_t n_rows, int64_t n_cols)
+{
+    if (!rows_ok(n_rows, n_cols))
+        return -static_cast<int64_t>(LMH_ERR_SHAPE);
+    return lmh::distill_workspace_bytes(n_rows, n_cols);
+}
+
+int32_t lmhead_distill_fwd(const void *logits, int64_t ld, int32_t logits_dtype, int64_t n_rows,
+                           int64_t n_cols, const int32_t *teacher_token, int64_t ldt,
+                           const void *teacher_value, int64_t ldv, int32_t teacher_dtype,
+                           int64_t n_list, int32_t tail, const float *temperature,
+                           int64_t temperature_stride, float *loss, float *stats, void *workspace,
+                           int64_t workspace_bytes, void *stream)
+{
+    LMH_TRY(check_dtype_out(logits_dtype));
+    LMH_TRY(check_dtype_out(teacher_dtype));
+    if (!rows_ok(n_rows, n_cols) || n_list < 0 || n_list > lmh::kDistillMaxList || workspace_bytes < 0)
+        return LMH_ERR_SHAPE;
+    if (n_rows == 0)
+        return LMH_OK;
+    const TeacherArgs t = {teacher_token, ldt, teacher_value, ldv, teacher_dtype, n_list};
+    LMH_TRY(check_distill(logits, ld, logits_dtype, n_rows, n_cols, t, temperature, temperature_stride));
+    if (!stats || !workspace)
+        return LMH_ERR_NULL;
+    if (!aligned16(stats) || !aligned16(workspace) || !aligned4(loss))
+        return LMH_ERR_ALIGN;
+    const int64_t need = lmh::distill_workspace_bytes(n_rows, n_cols);
+    if (workspace_bytes < need)
+        return LMH_ERR_SHAPE;
+    const Span outs[] = {bytes_span(workspace, need), bytes_span(stats, 32 * n_rows),
+                         bytes_span(loss, loss ? 4 * n_rows : 0)};
+    const Span ins[] = {span_of(logits, n_rows, n_cols, ld, logits_dtype == LMH_BF16 ? 2 : 4),
+                        span_of(teacher_token, n_rows, n_list, ldt, 4),
+                        span_of(teacher_value, n_rows, n_list, ldv, teacher_dtype == LMH_BF16 ? 2 : 4),
+                        bytes_span(temperature, 4 * strided(temperature, temperature_stride, n_rows))};
+    if (outputs_clash(outs, 3, ins, 4))
+        return LMH_ERR_ALIAS;
+    lmh::Distill p = distill_args(logits, ld, logits_dtype, n_rows, n_cols, t, tail, temperature, temperature_stride);
+    p.loss = loss;
+    p.stats = stats;
+    return launch_status(lmh::launch_distill_fwd(p, workspace, static_cast<hipStream_t>(stream)));
+}
+
+int32_t lmhead_distill_bwd(const void *logits, int64_t ld, int32_t logits_dtype,
+                           const float *stats, const int32_t *teacher_token, int64_t ldt,
+                           const void *teacher_value, int64_t ldv, int32_t teacher_dtype,
+                           int64_t n_list, int32_t tail, const float *temperature,
+                           int64_t temperature_stride, const float *dloss, int64_t dloss_stride,
+                           void *dlogits, int64_t ldg, int32_t grad_dtype, int64_t n_rows,
+                           int64_t n_cols, void *stream)
+{
+    LMH_TRY(check_dtype_out(logits_dtype));
+    LMH_TRY(check_dtype_out(teacher_dtype));
+    LMH_TRY(check_dtype_out(grad_dtype));
+    if (!rows_ok(n_rows, n_cols) || n_list < 0 || n_list > lmh::kDistillMaxList ||
+        (dloss_stride != 0 && dloss_stride != 1))
+        return LMH_ERR_SHAPE;
+    if (n_rows == 0)
+        return LMH_OK;
+    const TeacherArgs t = {teacher_token, ldt, teacher_value, ldv, teacher_dtype, n_list};
+    LMH_TRY(check_distill(logits, ld, logits_dtype, n_rows, n_cols, t, temperature, temperature_stride));
+    LMH_TRY(check_row_grad(logits, ld, logits_dtype, dlogits, ldg, grad_dtype, n_rows, n_cols));
+    if (!stats || !dloss)
+        return LMH_ERR_NULL;
+    if (!aligned16(stats) || !aligned4(dloss))
+        return LMH_ERR_ALIGN;
+    const Span outs[] = {span_of(dlogits, n_rows, n_cols, ldg, grad_dtype == LMH_BF16 ? 2 : 4)};
+    const Span ins[] = {bytes_span(stats, 32 * n_rows), span_of(teacher_token, n_rows, n_list, ldt, 4),
+                        span_of(teacher_value, n_rows, n_list, ldv, teacher_dtype == LMH_BF16 ? 2 : 4),
+                        bytes_span(temperature, 4 * strided(temperature, temperature_stride, n_rows)),
+                        bytes_span(dloss, 4 * strided(dloss, dloss_stride, n_rows))};
+    if (outputs_clash(outs, 1, ins, 5))
+        return LMH_ERR_ALIAS;
+    lmh::Distill p = distill_args(logits, ld, logits_dtype, n_rows, n_cols, t, tail, temperature, temperature_stride);
+    p.stats = const_cast<float *>(stats);
+    p.dloss = dloss, p.dloss_stride = dloss_stride;
+    p.dlogits = dlogits, p.ldg = ldg, p.grad_bf16 = grad_dtype == LMH_BF16;
+    return launch_status(lmh::launch_distill_bwd(p, static_cast<hipStream_t>(stream)));
+}
+
+int32_t lmhead_distill_fused(const void *logits, int64_t ld, int32_t logits_dtype, int64_t n_rows,
+                             int64_t n_cols, const int32_t *teacher_token, int64_t ldt,
+                             const void *teacher_value, int64_t ldv, int32_t teacher_dtype,
+                             int64_t n_list, int32_t tail, const float *temperature,
+                             int64_t temperature_stride, const float *dloss, int64_t dloss_stride,
+                             float *loss, float *stats, void *dlogits, int64_t ldg,
+                             int32_t grad_dtype, void *workspace, int64_t workspace_bytes,
+                             void *stream)
+{
+    LMH_TRY(check_dtype_out(logits_dtype));
+    LMH_TRY(check_dtype_out(teacher_dtype));
+    LMH_TRY(check_dtype_out(grad_dtype));
+    if (!rows_ok(n_rows, n_cols) || n_list < 0 || n_list > lmh::kDistillMaxList || workspace_bytes < 0 ||
+        (dloss_stride != 0 && dloss_stride != 1))
+        return LMH_ERR_SHAPE;
+    if (n_rows == 0)
+        return LMH_OK;
+    const TeacherArgs t = {teacher_token, ldt, teacher_value, ldv, teacher_dtype, n_list};
+    LMH_TRY(check_distill(logits, ld, logits_dtype, n_rows, n_cols, t, temperature, temperature_stride));
+    LMH_TRY(check_row_grad(logits, ld, logits_dtype, dlogits, ldg, grad_dtype, n_rows, n_cols));
+    if (!stats || !workspace || !dloss)
+        return LMH_ERR_NULL;
+    if (!aligned16(stats) || !aligned16(workspace) || !aligned4(loss) || !aligned4(dloss))
+        return LMH_ERR_ALIGN;
+    const int64_t need = lmh::distill_workspace_bytes(n_rows, n_cols);
+    if (workspace_bytes < need)
+        return LMH_ERR_SHAPE;
+    const Span z = span_of(logits, n_rows, n_cols, ld, logits_dtype == LMH_BF16 ? 2 : 4);
+    const Span outs[] = {bytes_span(workspace, need), bytes_span(stats, 32 * n_rows),
+                         bytes_span(loss, loss ? 4 * n_rows : 0),
+                         span_of(dlogits, n_rows, n_cols, ldg, grad_dtype == LMH_BF16 ? 2 : 4)};
+    const Span ins[] = {span_of(teacher_token, n_rows, n_list, ldt, 4),
+                        span_of(teacher_value, n_rows, n_list, ldv, teacher_dtype == LMH_BF16 ? 2 : 4),
+                        bytes_span(temperature, 4 * strided(temperature, temperature_stride, n_rows)),
+                        bytes_span(dloss, 4 * strided(dloss, dloss_stride, n_rows))};
+    if (outputs_clash(outs, 4, ins, 4) || overlaps(outs[0], z) || overlaps(outs[1], z) || overlaps(outs[2], z))
+        return LMH_ERR_ALIAS;
+    lmh::Distill p = distill_args(logits, ld, logits_dtype, n_rows, n_cols, t, tail, temperature, temperature_stride);
+    p.loss = loss;
+    p.stats = stats;
+    p.dloss = dloss, p.dloss_stride = dloss_stride;
+    p.dlogits = dlogits, p.ldg = ldg, p.grad_bf16 = grad_dtype == LMH_BF16;
+    return launch_status(lmh::launch_distill_fused(p, workspace, static_cast<hipStream_t>(stream)));
 }
 
 int32_t lmhead_diag_mfma_loop(int64_t iters, int64_t n_workgroups, int32_t operands, float *sink,

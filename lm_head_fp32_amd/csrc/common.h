@@ -169,6 +169,77 @@ hipError_t launch_beam_reorder(const void *src, void *dst, const int64_t (&src_s
                                const int32_t *lengths, int64_t n_outer, int64_t B, int64_t W_in,
                                int64_t W_out, int64_t H, int64_t T, int64_t pos_bytes, hipStream_t s);
 
+// Log-probabilities of given tokens; null outputs (and token, when nothing needs
+// it) are skipped, k = 0 without alternatives.  Strides of the temperature and of
+// the upstream gradients: 0 (one value) or 1 (one per row).
+struct Logprobs {
+    const void *logits;
+    int64_t ld;
+    bool bf16;
+    int64_t n, V;
+    const int32_t *token;
+    int32_t ignore_index;
+    const float *temperature;
+    int64_t temperature_stride;
+    int64_t k;
+    float *logprob, *entropy;
+    int32_t *rank;
+    float *top_logprob;
+    int32_t *top_token;
+    float *stats;
+};
+struct LogprobsBwd {
+    const void *logits;
+    int64_t ld;
+    bool bf16;
+    const float *stats;
+    const int32_t *token;
+    int32_t ignore_index;
+    const float *temperature;
+    int64_t temperature_stride;
+    const float *dlogprob;
+    int64_t dlogprob_stride;
+    const float *dentropy;
+    int64_t dentropy_stride;
+    void *dlogits;
+    int64_t ldg;
+    bool grad_bf16;
+    int64_t n, V;
+};
+int64_t row_segments(int64_t V);
+int64_t logprobs_workspace_bytes(int64_t n_rows, int64_t V, int64_t k);
+hipError_t launch_logprobs(const Logprobs &p, void *workspace, hipStream_t s);
+hipError_t launch_logprobs_bwd(const LogprobsBwd &p, hipStream_t s);
+
+// Cross-entropy against a teacher's listed tokens (k of them per row).
+constexpr int64_t kDistillMaxList = 256;
+struct Distill {
+    const void *logits;
+    int64_t ld;
+    bool bf16;
+    int64_t n, V;
+    const int32_t *token;
+    int64_t ldt;
+    const void *value;
+    int64_t ldv;
+    bool value_bf16;
+    int64_t k;
+    bool tail;
+    const float *temperature;
+    int64_t temperature_stride;
+    float *loss;        // forward; may be null
+    float *stats;       // written by the forward, read by the gradient
+    const float *dloss; // gradient
+    int64_t dloss_stride;
+    void *dlogits;
+    int64_t ldg;
+    bool grad_bf16;
+};
+int64_t distill_workspace_bytes(int64_t n_rows, int64_t V);
+hipError_t launch_distill_fwd(const Distill &p, void *workspace, hipStream_t s);
+hipError_t launch_distill_bwd(const Distill &p, hipStream_t s);
+hipError_t launch_distill_fused(const Distill &p, void *workspace, hipStream_t s);
+
 // exp(z - m) as one hardware base-2 exponential; the same form everywhere the
 // cross-entropy statistics are computed (CE kernels, logits GEMM epilogue).
 constexpr float kLog2e = 1.4426950408889634f;

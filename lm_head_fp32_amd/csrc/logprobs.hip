@@ -1,0 +1,476 @@
+// logprobs.hip -- log-probabilities of given tokens on gfx950, with the rows'
+// entropies, the tokens' ranks and the most likely alternatives, and their
+// gradient.
+//
+// Per row, with the temperature T (1 unless given) and x_j = (z_j - m) / T:
+//   m = max_j z_j,  d = sum_j exp(x_j),  s = sum_j x_j exp(x_j)
+//   log p_j = x_j - log d,  H = -sum_j p_j log p_j = log d - s / d
+// (both terms of H are at least 0, so nothing cancels).  d and s come from one
+// pass, about the maximum of each segment of 2048 columns, and are rescaled where
+// segments meet: exp((m_s - m) / T) d_s, and s_s + (m_s - m) / T d_s for s.
+// The order of the logits is the order of the log-probabilities, so ranks and
+// alternatives are found on the logits themselves and no rounding decides them:
+// equal logits rank by ascending column.
+// Gradient of g log p_y + h H:
+//   dz_j = (1 / T) [ g ([j == y] - p_j) - h p_j (log p_j + H) ].
+#include "common.h"
+#include "rows.h"
+
+#include <math.h>
+
+#include <algorithm>
+#include <type_traits>
+
+namespace lmh {
+
+namespace {
+
+constexpr int64_t kMaxItems = int64_t{1} << 31;  // work-items per launch
+constexpr float kLn2 = 0.6931471805599453f;
+
+// What a wave leaves of a segment of a row: y in place of x in units of log 2.
+struct alignas(16) LogprobRecord {
+    float m;       // maximum; -inf: nothing above -inf
+    float d;       // sum of 2^y, y = (z - m) / T / ln 2; NaN: it holds NaN or +inf
+    float s;       // sum of y 2^y
+    uint32_t before;  // columns that rank before the row's token
+};
+
+// d and s of 32 values about their maximum m (finite); c = log2(e) / T.
+__device__ __forceinline__ void sum_terms(const float (&v)[32], float m, float c, float &d, float &s)
+{
+    float d0 = 0.0f, s0 = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+        const float y = __builtin_elementwise_maximum((v[i] - m) * c, kNoTerm);
+        const float e = __builtin_amdgcn_exp2f(y);
+        d0 += e;
+        s0 = fmaf(e, y, s0);
+    }
+    d = d0;
+    s = s0;
+}
+
+// One wave, a workgroup of its own, per (row, segment of 2048 columns).
+template <bool BF16, bool TOP, bool RANK>
+__global__ __launch_bounds__(64) void logprobs_scan_kernel(
+    const void *__restrict__ logits, int64_t ld, int64_t V, uint32_t nseg,
+    const int32_t *__restrict__ token, const float *__restrict__ temperature, int64_t temperature_stride,
+    int32_t k, LogprobRecord *__restrict__ rec, uint64_t *__restrict__ lists)
+{
+    constexpr int G = Segment<BF16>::G;
+    __shared__ uint64_t mine[TOP ? kCandCap : 1];
+    const int lane = threadIdx.x;
+    const uint32_t id = blockIdx.x, row = id / nseg;  // below 2^25
+    const int64_t j0 = static_cast<int64_t>(id - row * nseg) * kSegCols;
+    const char *zr = static_cast<const char *>(logits) + static_cast<int64_t>(row) * ld * (16 / G);
+    float v[32];
+    {
+        Segment<BF16> sg;
+        sg.load(zr, V, j0, lane);
+        sg.values(v);
+    }
+    const float c = kLog2e * inverse_temperature(temperature, row * temperature_stride);
+    float gm[8], lm = -INFINITY;
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+        gm[u] = __builtin_elementwise_maximum(__builtin_elementwise_maximum(v[4 * u], v[4 * u + 1]),
+                                              __builtin_elementwise_maximum(v[4 * u + 2], v[4 * u + 3]));
+        lm = __builtin_elementwise_maximum(lm, gm[u]);  // NaN stays NaN
+    }
+    const float m = wave_maximum(lm);
+    uint64_t *out = lists + static_cast<int64_t>(id) * k;
+    uint32_t before = 0;
+    if constexpr (RANK) {
+        const int32_t y = token[row];
+        if (y >= 0 && y < V) {
+            const float zy = row_element<BF16>(zr, y);
+            const int32_t rel = y - static_cast<int32_t>(j0) - lane * G;  // columns below it count when equal
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+                const int32_t at = 64 * (i / G) * G + i % G;
+                before += __popcll(__ballot(v[i] > zy || (v[i] == zy && at < rel)));
+            }
+        }
+    }
+    if (!(m < INFINITY) || m == -INFINITY) {
+        // NaN or +inf somewhere (the whole row is then NaN), or only -inf.
+        if (lane == 0)
+            rec[id] = {m, m == -INFINITY ? 0.0f : __int_as_float(0x7fc00000), 0.0f, before};
+        if (TOP && lane < k)
+            out[lane] = 0;
+        return;
+    }
+    float d, s;
+    sum_terms(v, m, c, d, s);
+    d = wave_sum(d);
+    s = wave_sum(s);
+    if (lane == 0)
+        rec[id] = {m, d, s, before};
+    if constexpr (TOP)
+        keep_largest<G>(v, gm, lm, static_cast<uint32_t>(j0), lane, k, mine, out);
+}
+
+// A row's sums, folded by one wave; every lane holds them.
+struct RowSums {
+    float m;
+    double d, s;
+    uint32_t before;
+};
+__device__ __forceinline__ RowSums fold(const LogprobRecord *r, int32_t nseg, int lane, float c)
+{
+    float m = -INFINITY;
+    for (int i = lane; i < nseg; i += 64)
+        m = __builtin_elementwise_maximum(m, r[i].m);
+    m = wave_maximum(m);
+    double d = 0.0, s = 0.0;
+    uint32_t before = 0;
+    for (int i = lane; i < nseg; i += 64) {
+        const LogprobRecord q = r[i];
+        const float dy = __builtin_elementwise_maximum((q.m - m) * c, kNoTerm);
+        const double f = __builtin_amdgcn_exp2f(dy);
+        if (q.d != 0.0f) {  // NaN too
+            d += f * q.d;
+            s += f * (static_cast<double>(q.s) + static_cast<double>(dy) * q.d);
+        }
+        before += q.before;
+    }
+#pragma unroll
+    for (int off = 32; off >= 1; off >>= 1)
+        before += __shfl_xor(before, off, 64);
+    return {m, wave_sum(d), wave_sum(s), before};
+}
+
+// What a row's sums say, written by one lane.
+struct RowOutputs {
+    float *logprob, *entropy;
+    int32_t *rank;
+    float4 *stats;
+};
+__device__ __forceinline__ void write_row(const RowSums &q, double log_d, float inv_t, const char *zr,
+                                          bool bf16, int64_t V, const int32_t *token, int32_t ignore_index,
+                                          int64_t row, const RowOutputs &o)
+{
+    const float nan = __int_as_float(0x7fc00000);
+    const bool bad = !(q.d > 0.0);
+    const float entropy = bad ? nan : static_cast<float>(log_d - q.s * 0.6931471805599453 / q.d);
+    float lp = 0.0f;
+    int32_t rank = -1;
+    if (token) {
+        const int32_t y = token[row];
+        if (y == ignore_index) {
+            lp = 0.0f;
+        } else if (y < 0 || y >= V || bad) {
+            lp = nan;
+        } else {
+            const float zy = bf16 ? row_element<true>(zr, y) : row_element<false>(zr, y);
+            lp = static_cast<float>((static_cast<double>(zy) - q.m) * inv_t - log_d);
+            rank = static_cast<int32_t>(q.before);
+        }
+    }
+    o.stats[row] = make_float4(q.m, static_cast<float>(q.d), entropy, lp);
+    if (o.logprob)
+        o.logprob[row] = lp;
+    if (o.entropy)
+        o.entropy[row] = entropy;
+    if (o.rank)
+        o.rank[row] = rank;
+}
+
+// Rows without alternatives: one wave each.
+__global__ __launch_bounds__(256) void logprobs_merge_kernel(
+    const char *__restrict__ logits, int64_t ld_bytes, int32_t bf16, int64_t n_rows, int64_t V, int32_t nseg,
+    const int32_t *__restrict__ token, int32_t ignore_index, const float *__restrict__ temperature,
+    int64_t temperature_stride, const LogprobRecord *__restrict__ rec, RowOutputs o)
+{
+    const int lane = threadIdx.x & 63;
+    const int64_t row = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
+    if (row >= n_rows)
+        return;
+    const float inv_t = inverse_temperature(temperature, row * temperature_stride);
+    const RowSums q = fold(rec + row * nseg, nseg, lane, kLog2e * inv_t);
+    if (lane == 0)
+        write_row(q, log(q.d), inv_t, logits + row * ld_bytes, bf16 != 0, V, token, ignore_index, row, o);
+}
+
+constexpr int kTopThreads = 256;
+constexpr int kTopCap = 2048;  // candidates of a row in LDS
+
+// Rows with alternatives: one workgroup each.  Of nseg sorted lists of k keys, a
+// lower bound of the k-th largest (from the lists' heads) leaves a few dozen
+// candidates, which are ranked by counting.
+__global__ __launch_bounds__(kTopThreads) void logprobs_top_kernel(
+    const char *__restrict__ logits, int64_t ld_bytes, int32_t bf16, int64_t V, int32_t nseg,
+    const int32_t *__restrict__ token, int32_t ignore_index, const float *__restrict__ temperature,
+    int64_t temperature_stride, int32_t k, const LogprobRecord *__restrict__ rec,
+    const uint64_t *__restrict__ lists, float *__restrict__ top_logprob, int32_t *__restrict__ top_token,
+    RowOutputs o)
+{
+    __shared__ uint64_t cand[kTopCap];
+    __shared__ uint32_t n_cand, bound;
+    __shared__ double sh_log_d;
+    __shared__ float sh_m;
+    __shared__ uint64_t red[kTopThreads / 64];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int64_t row = blockIdx.x;
+    const uint64_t *keys = lists + row * nseg * k;
+    const int64_t n_keys = static_cast<int64_t>(nseg) * k;
+    const float inv_t = inverse_temperature(temperature, row * temperature_stride);
+    if (wave == 0) {
+        const RowSums q = fold(rec + row * nseg, nseg, lane, kLog2e * inv_t);
+        const double log_d = log(q.d);
+        if (lane == 0) {
+            write_row(q, log_d, inv_t, logits + row * ld_bytes, bf16 != 0, V, token, ignore_index, row, o);
+            sh_log_d = q.d > 0.0 ? log_d : static_cast<double>(NAN);
+            sh_m = q.m;
+            n_cand = 0;
+        }
+    } else if (wave == 1) {
+        // 64 distinct entries, the lists' heads first: the k-th largest of them
+        // is a bound that at least k keys reach.
+        uint32_t mine = 0;
+        if (nseg >= 64) {
+            for (int64_t l = lane; l < nseg; l += 64)
+                mine = max(mine, static_cast<uint32_t>(keys[l * k] >> 32));
+        } else if (lane / nseg < k) {
+            mine = static_cast<uint32_t>(keys[static_cast<int64_t>(lane % nseg) * k + lane / nseg] >> 32);
+        }
+        uint32_t t = 0;
+        for (int b = 31; b >= 0; --b) {
+            const uint32_t c = t | (1u << b);
+            if (__popcll(__ballot(mine >= c)) >= k)
+                t = c;
+        }
+        if (lane == 0)
+            bound = t;
+    }
+    __syncthreads();
+    const double log_d = sh_log_d;
+    float *lp = top_logprob + row * k;
+    int32_t *tok = top_token + row * k;
+    if (!(log_d == log_d)) {
+        if (tid < k) {
+            lp[tid] = __int_as_float(0x7fc00000);
+            tok[tid] = -1;
+        }
+        return;
+    }
+    const uint64_t least = max(static_cast<uint64_t>(bound) << 32, uint64_t{1});
+    for (int64_t i = tid; i < n_keys; i += kTopThreads) {
+        const uint64_t key = keys[i];
+        if (key >= least) {
+            const uint32_t at = atomicAdd(&n_cand, 1u);
+            if (at < kTopCap)
+                cand[at] = key;
+        }
+    }
+    __syncthreads();
+    const uint32_t n = n_cand;
+    auto put = [&](int at, uint64_t key) {
+        const float z = key_value(static_cast<uint32_t>(key >> 32));
+        lp[at] = static_cast<float>((static_cast<double>(z) - sh_m) * inv_t - log_d);
+        tok[at] = static_cast<int32_t>(0xffffffffu - static_cast<uint32_t>(key));
+    };
+    if (n <= kTopCap) {
+        for (uint32_t i = tid; i < n; i += kTopThreads) {
+            const uint64_t key = cand[i];
+            int rank = 0;
+            for (uint32_t q = 0; q < n; ++q)
+                rank += cand[q] > key;
+            if (rank < k)
+                put(rank, key);
+        }
+        if (n + tid < static_cast<uint32_t>(k)) {  // fewer than k above -inf
+            lp[n + tid] = -INFINITY;
+            tok[n + tid] = -1;
+        }
+        return;
+    }
+    // More candidates than fit (many equal logits over many segments): k rounds,
+    // each taking the largest key below the last one.
+    uint64_t last = ~0ull;
+    for (int r = 0; r < k; ++r) {
+        uint64_t best = 0;
+        for (int64_t i = tid; i < n_keys; i += kTopThreads) {
+            const uint64_t key = keys[i];
+            if (key < last && key > best)
+                best = key;
+        }
+#pragma unroll
+        for (int off = 32; off >= 1; off >>= 1)
+            best = max(best, shfl_xor_u64(best, off));
+        if (lane == 0)
+            red[wave] = best;
+        __syncthreads();
+        for (int w = 0; w < kTopThreads / 64; ++w)
+            best = max(best, red[w]);
+        __syncthreads();
+        if (tid == 0)
+            put(r, best);  // n > kTopCap >= k: never 0
+        last = best;
+    }
+}
+
+// ------------------------------------------------------------------ gradient
+
+constexpr int kBwdThreads = 256;
+constexpr int kBwdVecs = 4;  // 16-byte loads per thread
+
+// One chunk of kBwdVecs x 256 vectors of 16 bytes of a row per workgroup.  With
+// y = (z - m) / T / ln 2 and e = 2^y, dz = e (a + b y), b = -h ln 2 / (d T) and
+// a = -(g + h (H - log d)) / (d T), and g / T more at the token.
+template <bool ZBF16, bool GBF16, bool ENTROPY>
+__global__ __launch_bounds__(kBwdThreads) void logprobs_bwd_kernel(
+    const void *logits, int64_t ld, const float4 *__restrict__ stats, const int32_t *__restrict__ token,
+    int32_t ignore_index, const float *__restrict__ temperature, int64_t temperature_stride,
+    const float *__restrict__ dlogprob, int64_t dlogprob_stride, const float *__restrict__ dentropy,
+    int64_t dentropy_stride, void *dlogits, int64_t ldg, int64_t V, uint32_t chunks)
+{
+    constexpr int G = ZBF16 ? 8 : 4;
+    const uint32_t id = blockIdx.x, row = id / chunks, chunk = id - row * chunks;
+    const int tid = threadIdx.x;
+    const int64_t nv = V / G;
+    const int32_t y = token ? token[row] : ignore_index;
+    const bool ignored = !token || y == ignore_index;
+    const bool bad = !ignored && (y < 0 || y >= V);
+    const float inv_t = inverse_temperature(temperature, row * temperature_stride);
+    const float g = (ignored || !dlogprob) ? 0.0f : dlogprob[row * dlogprob_stride];
+    const float h = ENTROPY ? dentropy[row * dentropy_stride] : 0.0f;
+    const float4 st = stats[row];
+    const float nan = __int_as_float(0x7fc00000);
+    float a = -(g + (ENTROPY ? h * (st.z - logf(st.y)) : 0.0f)) / st.y * inv_t;
+    const float b = -h * kLn2 / st.y * inv_t, c = kLog2e * inv_t, at_token = g * inv_t;
+    const bool nothing = !bad && g == 0.0f && h == 0.0f;  // the row is not read
+    if (bad)
+        a = nan;
+    const char *zr = static_cast<const char *>(logits) + static_cast<int64_t>(row) * ld * (16 / G);
+    char *gr = static_cast<char *>(dlogits) + static_cast<int64_t>(row) * ldg * (GBF16 ? 2 : 4);
+
+    auto value = [&](float z, bool own) {
+        const float e2 = __builtin_elementwise_maximum((z - st.x) * c, kNoTerm);
+        const float e = __builtin_amdgcn_exp2f(e2);
+        const float w = ENTROPY ? fmaf(b, e2, a) : a;
+        return own ? fmaf(e, w, at_token) : e * w;
+    };
+    const int64_t first = static_cast<int64_t>(chunk) * kBwdThreads * kBwdVecs;
+    uint4 q[kBwdVecs];
+    if (!nothing) {
+#pragma unroll
+        for (int u = 0; u < kBwdVecs; ++u) {
+            const int64_t i = first + u * kBwdThreads + tid;
+            if (i < nv)
+                q[u] = load_row(zr, i);
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < kBwdVecs; ++u) {
+        const int64_t i = first + u * kBwdThreads + tid;
+        if (i >= nv)
+            continue;
+        float o[G];
+        const int64_t rel = static_cast<int64_t>(y) - i * G;
+#pragma unroll
+        for (int e = 0; e < G; ++e)
+            o[e] = nothing ? 0.0f : value(row_value<ZBF16>(q[u], e), !ignored && rel == e);
+        store_row<GBF16>(gr, i, o);
+    }
+    // The last V % G columns, by the row's last chunk.
+    if (chunk == chunks - 1 && tid < G) {
+        const int64_t j = nv * G + tid;
+        if (j < V) {
+            store_element<GBF16>(gr, j, nothing ? 0.0f : value(row_element<ZBF16>(zr, j), !ignored && j == y));
+        }
+    }
+}
+
+}  // namespace
+
+int64_t row_segments(int64_t V)
+{
+    return (V + kSegCols - 1) / kSegCols;
+}
+
+int64_t logprobs_workspace_bytes(int64_t n_rows, int64_t V, int64_t k)
+{
+    return n_rows * row_segments(V) * (static_cast<int64_t>(sizeof(LogprobRecord)) + 8 * k);
+}
+
+hipError_t launch_logprobs(const Logprobs &p, void *workspace, hipStream_t s)
+{
+    const int64_t nseg = row_segments(p.V), esz = p.bf16 ? 2 : 4;
+    LogprobRecord *rec = static_cast<LogprobRecord *>(workspace);
+    uint64_t *lists = reinterpret_cast<uint64_t *>(rec + p.n * nseg);
+    const int32_t k = static_cast<int32_t>(p.k);
+    const int64_t chunk = std::max<int64_t>(1, kMaxItems / 256 / nseg);
+    for (int64_t r0 = 0; r0 < p.n; r0 += chunk) {
+        const int64_t nr = std::min(chunk, p.n - r0);
+        const char *z = static_cast<const char *>(p.logits) + r0 * p.ld * esz;
+        const int32_t *tok = p.token ? p.token + r0 : nullptr;
+        const float *temp = p.temperature ? p.temperature + r0 * p.temperature_stride : nullptr;
+        LogprobRecord *rc = rec + r0 * nseg;
+        uint64_t *ls = lists + r0 * nseg * k;
+        const RowOutputs o = {p.logprob ? p.logprob + r0 : nullptr, p.entropy ? p.entropy + r0 : nullptr,
+                              p.rank ? p.rank + r0 : nullptr, reinterpret_cast<float4 *>(p.stats) + r0};
+        const dim3 grid(static_cast<unsigned>(nr * nseg));
+        auto scan = [&](auto bf16, auto top, auto rank) {
+            hipLaunchKernelGGL((logprobs_scan_kernel<decltype(bf16)::value, decltype(top)::value, decltype(rank)::value>),
+                               grid, dim3(64), 0, s, z, p.ld, p.V, static_cast<uint32_t>(nseg), tok, temp,
+                               p.temperature_stride, k, rc, ls);
+        };
+        const auto yes = std::true_type{};
+        const auto no = std::false_type{};
+        auto with_rank = [&](auto bf16, auto top) { p.rank ? scan(bf16, top, yes) : scan(bf16, top, no); };
+        auto with_top = [&](auto bf16) { k ? with_rank(bf16, yes) : with_rank(bf16, no); };
+        p.bf16 ? with_top(yes) : with_top(no);
+        hipError_t e = hipGetLastError();
+        if (e != hipSuccess)
+            return e;
+        if (k)
+            hipLaunchKernelGGL(logprobs_top_kernel, dim3(static_cast<unsigned>(nr)), dim3(kTopThreads), 0, s, z,
+                               p.ld * esz, p.bf16 ? 1 : 0, p.V, static_cast<int32_t>(nseg), tok, p.ignore_index,
+                               temp, p.temperature_stride, k, rc, ls, p.top_logprob + r0 * k,
+                               p.top_token + r0 * k, o);
+        else
+            hipLaunchKernelGGL(logprobs_merge_kernel, dim3(static_cast<unsigned>((nr + 3) / 4)), dim3(256), 0, s, z,
+                               p.ld * esz, p.bf16 ? 1 : 0, nr, p.V, static_cast<int32_t>(nseg), tok,
+                               p.ignore_index, temp, p.temperature_stride, rc, o);
+        e = hipGetLastError();
+        if (e != hipSuccess)
+            return e;
+    }
+    return hipSuccess;
+}
+
+hipError_t launch_logprobs_bwd(const LogprobsBwd &p, hipStream_t s)
+{
+    const int64_t zsz = p.bf16 ? 2 : 4, gsz = p.grad_bf16 ? 2 : 4, G = 16 / zsz;
+    const int64_t per = kBwdThreads * kBwdVecs;
+    const int64_t chunks = std::max<int64_t>(1, (p.V / G + per - 1) / per);
+    const int64_t rows = std::max<int64_t>(1, kMaxItems / kBwdThreads / chunks);
+    for (int64_t r0 = 0; r0 < p.n; r0 += rows) {
+        const int64_t nr = std::min(rows, p.n - r0);
+        auto go = [&](auto zb, auto gb, auto ent) {
+            hipLaunchKernelGGL((logprobs_bwd_kernel<decltype(zb)::value, decltype(gb)::value, decltype(ent)::value>),
+                               dim3(static_cast<unsigned>(nr * chunks)), dim3(kBwdThreads), 0, s,
+                               static_cast<const char *>(p.logits) + r0 * p.ld * zsz, p.ld,
+                               reinterpret_cast<const float4 *>(p.stats) + r0, p.token ? p.token + r0 : nullptr,
+                               p.ignore_index,
+                               p.temperature ? p.temperature + r0 * p.temperature_stride : nullptr,
+                               p.temperature_stride, p.dlogprob ? p.dlogprob + r0 * p.dlogprob_stride : nullptr,
+                               p.dlogprob_stride, p.dentropy ? p.dentropy + r0 * p.dentropy_stride : nullptr,
+                               p.dentropy_stride, static_cast<char *>(p.dlogits) + r0 * p.ldg * gsz, p.ldg, p.V,
+                               static_cast<uint32_t>(chunks));
+        };
+        const auto yes = std::true_type{};
+        const auto no = std::false_type{};
+        auto with_ent = [&](auto zb, auto gb) { p.dentropy ? go(zb, gb, yes) : go(zb, gb, no); };
+        auto with_grad = [&](auto zb) { p.grad_bf16 ? with_ent(zb, yes) : with_ent(zb, no); };
+        p.bf16 ? with_grad(yes) : with_grad(no);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess)
+            return e;
+    }
+    return hipSuccess;
+}
+
+}  // namespace lmh

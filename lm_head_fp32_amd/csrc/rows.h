@@ -134,6 +134,77 @@ struct Segment {
     }
 };
 
+// The 16 bytes at vector i of a row that is streamed once, as G values (4 FP32 or
+// 8 BF16).
+__device__ __forceinline__ uint4 load_row(const char *row, int64_t i)
+{
+    const u32x4_nt w = __builtin_nontemporal_load(reinterpret_cast<const u32x4_nt *>(row) + i);
+    return make_uint4(w.x, w.y, w.z, w.w);
+}
+template <bool BF16>
+__device__ __forceinline__ float row_value(const uint4 &q, int e)
+{
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+    if constexpr (BF16)
+        return __uint_as_float(e & 1 ? w[e / 2] & 0xffff0000u : w[e / 2] << 16);
+    else
+        return __uint_as_float(w[e & 3]);
+}
+template <bool BF16>
+__device__ __forceinline__ float row_element(const char *row, int64_t j)
+{
+    if constexpr (BF16)
+        return __uint_as_float(static_cast<uint32_t>(reinterpret_cast<const uint16_t *>(row)[j]) << 16);
+    else
+        return reinterpret_cast<const float *>(row)[j];
+}
+
+typedef float f32x2_cvt __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2_cvt __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)  // nearest even
+{
+    const f32x2_cvt v = {lo, hi};
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2_cvt));
+}
+
+// G gradients at vector i of a row, FP32 or rounded once to BF16.
+template <bool BF16, int G>
+__device__ __forceinline__ void store_row(char *row, int64_t i, const float (&o)[G])
+{
+    if constexpr (BF16) {
+        uint16_t *p = reinterpret_cast<uint16_t *>(row) + i * G;
+        if constexpr (G == 8)
+            store16(p, make_uint4(pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3]), pack_bf16(o[4], o[5]),
+                                  pack_bf16(o[6], o[7])), true);
+        else
+            store8(p, make_uint2(pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3])), true);
+    } else {
+        float *p = reinterpret_cast<float *>(row) + i * G;
+#pragma unroll
+        for (int e = 0; e < G; e += 4)
+            store16(p + e, make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]), true);
+    }
+}
+template <bool BF16>
+__device__ __forceinline__ void store_element(char *row, int64_t j, float o)
+{
+    if constexpr (BF16)
+        reinterpret_cast<uint16_t *>(row)[j] = static_cast<uint16_t>(f32_to_bf16_bits(o));
+    else
+        reinterpret_cast<float *>(row)[j] = o;
+}
+
+constexpr float kNoTerm = -200.0f;  // 2^-200 is 0 in FP32: what -inf is cut to
+
+// A temperature that is not positive and finite makes the row NaN.
+__device__ __forceinline__ float inverse_temperature(const float *t, int64_t i)
+{
+    if (!t)
+        return 1.0f;
+    const float v = t[i];
+    return (v > 0.0f && v < INFINITY) ? 1.0f / v : __int_as_float(0x7fc00000);
+}
+
 // The k largest of a segment's values (v, held as Segment loads them, some above
 // -inf, none NaN or +inf; gm the maxima of four at a time, lm the lane's) into
 // out[0 .. k), as keys: order_key above the complement of the column, so that a
