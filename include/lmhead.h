@@ -554,7 +554,8 @@ int32_t lmhead_beam_reorder(const void *src, int64_t src_outer, int64_t src_row,
  *           n_top == 0.
  *  Limits: 1 <= n_cols, n_top <= min(64, n_cols).
  *  workspace as lmhead_logits_lora, of lmhead_logprobs_workspace_bytes(n_rows,
- *  n_cols, n_top) bytes.  Outputs overlap neither inputs nor each other.
+ *  n_cols, n_top) bytes (may be NULL where that is 0).  Outputs overlap neither
+ *  inputs nor each other.
  */
 int64_t lmhead_logprobs_workspace_bytes(int64_t n_rows, int64_t n_cols, int64_t n_top);
 int32_t lmhead_logprobs(const void *logits, int64_t ld, int32_t logits_dtype, int64_t n_rows,

@@ -594,6 +594,14 @@ def _empty_stack(n, rows, cols, like):
     return t if ld == cols else t[:, :, :cols]
 
 
+def _row_workspace(need, workspace, like):
+    """(tensor or None, pointer, bytes) of a workspace that may not be needed."""
+    if workspace is None and need == 0:
+        return None, None, 0
+    ws, nbytes = _workspace(need, workspace, like)
+    return ws, ws.data_ptr(), nbytes
+
+
 def _workspace(need, workspace, like):
     """(tensor, bytes) of a workspace of at least `need` bytes: the caller's, or
     one from torch's caching allocator."""
@@ -1025,10 +1033,10 @@ def lmhead_logprobs(logits, token=None, ignore_index=-100, temperature=None, n_t
     if k and (top_logprob is None or top_token is None):
         raise ValueError("the alternatives are not wanted: n_top = 0")
     stats, ps = _row_out(stats, "stats", torch.float32, (n, STATS_COLS), logits)
-    ws, nbytes = _workspace(need, workspace, logits)
+    ws, pw, nbytes = _row_workspace(need, workspace, logits)
     _check("lmhead_logprobs",
            lib().lmhead_logprobs(pz, ld, code, n, V, py, int(ignore_index), pt, st, k, po, pe, pr, pa, pb, ps,
-                                 ws.data_ptr(), nbytes, _stream(stream)))
+                                 pw, nbytes, _stream(stream)))
     return logprob, entropy, rank, top_logprob, top_token, stats
 
 

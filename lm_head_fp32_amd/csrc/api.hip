@@ -1081,14 +1081,14 @@ int32_t lmhead_logprobs(const void *logits, int64_t ld, int32_t logits_dtype, in
         return LMH_OK;
     const bool bf16 = logits_dtype == LMH_BF16;
     LMH_TRY(check_matrix(logits, n_rows, n_cols, ld, bf16 ? 8 : 4));
-    if (!stats || !workspace || (n_top > 0 && (!top_logprob || !top_token)) || (!token && (logprob || rank)))
+    const int64_t need = lmh::logprobs_workspace_bytes(n_rows, n_cols, n_top);
+    if (!stats || (need > 0 && !workspace) || (n_top > 0 && (!top_logprob || !top_token)) || (!token && (logprob || rank)))
         return LMH_ERR_NULL;
     if (n_top == 0)
         top_logprob = nullptr, top_token = nullptr;
     if (!aligned4(token) || !aligned4(temperature) || !aligned4(logprob) || !aligned4(entropy) || !aligned4(rank) ||
         !aligned4(top_logprob) || !aligned4(top_token) || !aligned16(stats) || !aligned16(workspace))
         return LMH_ERR_ALIGN;
-    const int64_t need = lmh::logprobs_workspace_bytes(n_rows, n_cols, n_top);
     if (workspace_bytes < need)
         return LMH_ERR_SHAPE;
     const Span outs[] = {bytes_span(workspace, need), bytes_span(stats, 16 * n_rows),

@@ -36,79 +36,99 @@ struct alignas(16) LogprobRecord {
     uint32_t before;  // columns that rank before the row's token
 };
 
-// d and s of 32 values about their maximum m (finite); c = log2(e) / T.
-__device__ __forceinline__ void sum_terms(const float (&v)[32], float m, float c, float &d, float &s)
-{
-    float d0 = 0.0f, s0 = 0.0f;
+// Running sums of a lane: d = sum 2^y, s = sum y 2^y about the lane's own maximum m
+// (shift 0 while nothing lies above -inf), rescaled once per 32 values.
+struct LaneSums {
+    float m = -INFINITY, d = 0.0f, s = 0.0f;
+    __device__ __forceinline__ void add(const float (&v)[32], float lm, float c)
+    {
+        const float mn = __builtin_elementwise_maximum(m, lm);
+        const float ms = mn == -INFINITY ? 0.0f : mn;
+        const float dy = __builtin_elementwise_maximum((m - ms) * c, kNoTerm);
+        const float f = __builtin_amdgcn_exp2f(dy);
+        float d0 = d * f, s0 = f * fmaf(dy, d, s);
 #pragma unroll
-    for (int i = 0; i < 32; ++i) {
-        const float y = __builtin_elementwise_maximum((v[i] - m) * c, kNoTerm);
-        const float e = __builtin_amdgcn_exp2f(y);
-        d0 += e;
-        s0 = fmaf(e, y, s0);
+        for (int i = 0; i < 32; ++i) {
+            const float y = __builtin_elementwise_maximum((v[i] - ms) * c, kNoTerm);
+            const float e = __builtin_amdgcn_exp2f(y);
+            d0 += e;
+            s0 = fmaf(e, y, s0);
+        }
+        m = mn;
+        d = d0;
+        s = s0;
     }
-    d = d0;
-    s = s0;
+};
+
+constexpr int kWaveCap = 256;  // candidates a wave keeps in LDS
+constexpr int kListCap = 512;  // candidates of a workgroup that are ranked by counting
+
+// The largest t with at least k of the wave's values >= t, cut to its upper 20
+// bits: a lower bound of the k-th largest, two bits a step.
+__device__ __forceinline__ uint32_t kth_largest(uint32_t mine, int k)
+{
+    uint32_t t = 0;
+#pragma unroll
+    for (int b = 30; b >= 12; b -= 2) {
+        const uint32_t c1 = t | (1u << b), c2 = t | (2u << b), c3 = t | (3u << b);
+        const int n1 = __popcll(__ballot(mine >= c1)), n2 = __popcll(__ballot(mine >= c2)),
+                  n3 = __popcll(__ballot(mine >= c3));
+        t = n3 >= k ? c3 : n2 >= k ? c2 : n1 >= k ? c1 : t;
+    }
+    return t;
 }
 
-// One wave, a workgroup of its own, per (row, segment of 2048 columns).
-template <bool BF16, bool TOP, bool RANK>
-__global__ __launch_bounds__(64) void logprobs_scan_kernel(
-    const void *__restrict__ logits, int64_t ld, int64_t V, uint32_t nseg,
-    const int32_t *__restrict__ token, const float *__restrict__ temperature, int64_t temperature_stride,
-    int32_t k, LogprobRecord *__restrict__ rec, uint64_t *__restrict__ lists)
+// The k largest of n keys (n <= kWaveCap, all different) to the front of the
+// list, by one wave; returns how many that are.
+__device__ __forceinline__ int keep_k(uint64_t *list, int n, int k, int lane)
 {
-    constexpr int G = Segment<BF16>::G;
-    __shared__ uint64_t mine[TOP ? kCandCap : 1];
-    const int lane = threadIdx.x;
-    const uint32_t id = blockIdx.x, row = id / nseg;  // below 2^25
-    const int64_t j0 = static_cast<int64_t>(id - row * nseg) * kSegCols;
-    const char *zr = static_cast<const char *>(logits) + static_cast<int64_t>(row) * ld * (16 / G);
-    float v[32];
-    {
-        Segment<BF16> sg;
-        sg.load(zr, V, j0, lane);
-        sg.values(v);
-    }
-    const float c = kLog2e * inverse_temperature(temperature, row * temperature_stride);
-    float gm[8], lm = -INFINITY;
+    uint64_t key[kWaveCap / 64];
+    int rank[kWaveCap / 64];
 #pragma unroll
-    for (int u = 0; u < 8; ++u) {
-        gm[u] = __builtin_elementwise_maximum(__builtin_elementwise_maximum(v[4 * u], v[4 * u + 1]),
-                                              __builtin_elementwise_maximum(v[4 * u + 2], v[4 * u + 3]));
-        lm = __builtin_elementwise_maximum(lm, gm[u]);  // NaN stays NaN
+    for (int i = 0; i < kWaveCap / 64; ++i) {
+        key[i] = lane + 64 * i < n ? list[lane + 64 * i] : 0;
+        rank[i] = 0;
     }
-    const float m = wave_maximum(lm);
-    uint64_t *out = lists + static_cast<int64_t>(id) * k;
-    uint32_t before = 0;
-    if constexpr (RANK) {
-        const int32_t y = token[row];
-        if (y >= 0 && y < V) {
-            const float zy = row_element<BF16>(zr, y);
-            const int32_t rel = y - static_cast<int32_t>(j0) - lane * G;  // columns below it count when equal
+    for (int q = 0; q < n; ++q) {
+        const uint64_t other = list[q];
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
-                const int32_t at = 64 * (i / G) * G + i % G;
-                before += __popcll(__ballot(v[i] > zy || (v[i] == zy && at < rel)));
-            }
+        for (int i = 0; i < kWaveCap / 64; ++i)
+            rank[i] += other > key[i];
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#pragma unroll
+    for (int i = 0; i < kWaveCap / 64; ++i)
+        if (key[i] != 0 && rank[i] < k)
+            list[rank[i]] = key[i];
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    return min(n, k);
+}
+
+// The keys of a segment that are at least `least` into the wave's list, however
+// many they are (more equal values at the bound than are wanted, or a large k): read
+// again, 64 columns at a time; a full list is cut to its k largest, which then bound
+// what is still to come.
+template <bool BF16>
+__device__ __forceinline__ int collect_all(const char *zr, int64_t V, int64_t j0, uint64_t least,
+                                                     uint64_t *list, int n, int k, int lane)
+{
+    for (int64_t j = j0 + lane; j < j0 + kSegCols; j += 64) {
+        uint64_t key = 0;
+        if (j < V)
+            key = (static_cast<uint64_t>(order_key(row_element<BF16>(zr, j))) << 32) |
+                  (0xffffffffu - static_cast<uint32_t>(j));
+        uint64_t mask = __ballot(key >= least);
+        if (n + __popcll(mask) > kWaveCap) {
+            n = keep_k(list, n, k, lane);
+            least = max(least, list[k - 1]);
+            mask = __ballot(key >= least);
         }
+        if (mask & (1ull << lane))
+            list[n + __popcll(mask & ((1ull << lane) - 1ull))] = key;
+        n += __popcll(mask);
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     }
-    if (!(m < INFINITY) || m == -INFINITY) {
-        // NaN or +inf somewhere (the whole row is then NaN), or only -inf.
-        if (lane == 0)
-            rec[id] = {m, m == -INFINITY ? 0.0f : __int_as_float(0x7fc00000), 0.0f, before};
-        if (TOP && lane < k)
-            out[lane] = 0;
-        return;
-    }
-    float d, s;
-    sum_terms(v, m, c, d, s);
-    d = wave_sum(d);
-    s = wave_sum(s);
-    if (lane == 0)
-        rec[id] = {m, d, s, before};
-    if constexpr (TOP)
-        keep_largest<G>(v, gm, lm, static_cast<uint32_t>(j0), lane, k, mine, out);
+    return n;
 }
 
 // A row's sums, folded by one wave; every lane holds them.
@@ -116,6 +136,15 @@ struct RowSums {
     float m;
     double d, s;
     uint32_t before;
+};
+
+// What a row's sums say, written by one lane.
+struct RowOutputs {
+    float *logprob, *entropy;
+    int32_t *rank;
+    float4 *stats;
+    float *top_logprob;
+    int32_t *top_token;
 };
 __device__ __forceinline__ RowSums fold(const LogprobRecord *r, int32_t nseg, int lane, float c)
 {
@@ -141,19 +170,13 @@ __device__ __forceinline__ RowSums fold(const LogprobRecord *r, int32_t nseg, in
     return {m, wave_sum(d), wave_sum(s), before};
 }
 
-// What a row's sums say, written by one lane.
-struct RowOutputs {
-    float *logprob, *entropy;
-    int32_t *rank;
-    float4 *stats;
-};
-__device__ __forceinline__ void write_row(const RowSums &q, double log_d, float inv_t, const char *zr,
+__device__ __forceinline__ void write_row(const RowSums &q, float log_d, float inv_t, const char *zr,
                                           bool bf16, int64_t V, const int32_t *token, int32_t ignore_index,
                                           int64_t row, const RowOutputs &o)
 {
     const float nan = __int_as_float(0x7fc00000);
     const bool bad = !(q.d > 0.0);
-    const float entropy = bad ? nan : static_cast<float>(log_d - q.s * 0.6931471805599453 / q.d);
+    const float entropy = bad ? nan : log_d - kLn2 * (static_cast<float>(q.s) / static_cast<float>(q.d));
     float lp = 0.0f;
     int32_t rank = -1;
     if (token) {
@@ -165,7 +188,11 @@ __device__ __forceinline__ void write_row(const RowSums &q, double log_d, float 
         } else {
             const float zy = bf16 ? row_element<true>(zr, y) : row_element<false>(zr, y);
             lp = static_cast<float>((static_cast<double>(zy) - q.m) * inv_t - log_d);
-            rank = static_cast<int32_t>(q.before);
+            if (o.rank) {
+                rank = static_cast<int32_t>(q.before);
+                for (int32_t j = y & (bf16 ? ~7 : ~3); j < y; ++j)
+                    rank += (bf16 ? row_element<true>(zr, j) : row_element<false>(zr, j)) == zy;
+            }
         }
     }
     o.stats[row] = make_float4(q.m, static_cast<float>(q.d), entropy, lp);
@@ -175,6 +202,228 @@ __device__ __forceinline__ void write_row(const RowSums &q, double log_d, float 
         o.entropy[row] = entropy;
     if (o.rank)
         o.rank[row] = rank;
+}
+
+// One workgroup of NW waves per (row, part of its segments of 2048 columns); a wave
+// takes every NW-th segment of the part, the next one's loads under way.  With one
+// part per row the workgroup writes the row's results, else a record and its k
+// largest for the merge.
+// Alternatives: slot[l] is the largest value that lane l of any wave has seen, so
+// the k-th largest of the 64 slots is a lower bound of the k-th largest value (k
+// different values reach it), whatever the waves have read so far.  It is taken anew
+// for every round of NW segments, still in registers; the few values that reach it
+// are kept per wave, and at the end those that reach the last bound are ranked by
+// counting.
+template <bool BF16, bool TOP, bool RANK, int NW>
+__global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(4))) void logprobs_row_kernel(
+    const void *__restrict__ logits, int64_t ld, int64_t V, uint32_t parts, int32_t part_segs,
+    const int32_t *__restrict__ token, int32_t ignore_index, const float *__restrict__ temperature,
+    int64_t temperature_stride, int32_t k, LogprobRecord *__restrict__ rec, uint64_t *__restrict__ lists,
+    RowOutputs o)
+{
+    constexpr int G = Segment<BF16>::G;
+    __shared__ uint64_t kept[TOP ? NW * kWaveCap : 1];
+    __shared__ uint64_t cand[TOP ? kListCap : 1];
+    __shared__ uint64_t red[NW];
+    __shared__ uint32_t slot[64];
+    __shared__ LogprobRecord part_rec[NW];
+    __shared__ uint32_t cand_n;
+    __shared__ float sh_log_d;
+    __shared__ float sh_m;
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const uint32_t id = blockIdx.x, row = id / parts;
+    const int32_t seg0 = static_cast<int32_t>(id - row * parts) * part_segs;
+    const int32_t seg1 = min(seg0 + part_segs, static_cast<int32_t>((V + kSegCols - 1) / kSegCols));
+    const char *zr = static_cast<const char *>(logits) + static_cast<int64_t>(row) * ld * (16 / G);
+
+    Segment<BF16> next;
+    int32_t seg = seg0 + wave;
+    next.load(zr, V, static_cast<int64_t>(seg) * kSegCols, lane);
+    const float inv_t = inverse_temperature(temperature, row * temperature_stride);
+    const float c = kLog2e * inv_t;
+    int32_t y = -1;
+    float zy = INFINITY, above = INFINITY;  // above: the next FP32 value
+    if constexpr (RANK) {
+        y = token[row];
+        if (y >= 0 && y < V) {
+            zy = row_element<BF16>(zr, y);
+            above = key_value(order_key(zy) + 1u);
+        }
+    }
+    if constexpr (TOP) {
+        if (tid < 64)
+            slot[tid] = 0;
+        if (tid == 0)
+            cand_n = 0;
+        __syncthreads();
+    }
+    uint64_t *mine = kept + wave * kWaveCap;
+    uint32_t before = 0;
+    LaneSums sums;
+    int n_kept = 0;  // the same in every lane
+    uint64_t least = 0;
+    float bound = -INFINITY;
+    for (int32_t r = seg0; r < seg1; r += NW, seg += NW) {
+        // A segment past the row's end holds -inf only.
+        float v[32], gm[8], lm = -INFINITY;
+        next.values(v);
+        if (r + NW < seg1)
+            next.load(zr, V, static_cast<int64_t>(seg + NW) * kSegCols, lane);
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            gm[u] = __builtin_elementwise_maximum(
+                __builtin_elementwise_maximum(__builtin_elementwise_maximum(v[4 * u], v[4 * u + 1]), v[4 * u + 2]),
+                v[4 * u + 3]);
+            if (u & 1)
+                lm = __builtin_elementwise_maximum(__builtin_elementwise_maximum(lm, gm[u - 1]), gm[u]);  // NaN stays NaN
+        }
+        if constexpr (TOP)
+            atomicMax(&slot[lane], order_key(lm));  // a NaN only raises it: the row is NaN then
+        sums.add(v, lm, c);
+        if constexpr (RANK) {
+            // Vectors before the token's count equal values, those behind it
+            // larger ones only; its own vector's equal ones join in the end.
+            const int32_t rel = y - seg * kSegCols - lane * G;
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                if (!__ballot(gm[u] >= zy))
+                    continue;
+                const float least_ahead = 64 * (4 * u / G) * G + G <= rel ? zy : above;
+#pragma unroll
+                for (int i = 4 * u; i < 4 * u + 4; ++i)
+                    before += __popcll(__ballot(v[i] >= least_ahead));
+            }
+        }
+        if constexpr (TOP) {
+            __syncthreads();
+            if (__ballot(lm >= bound)) {
+                const uint32_t t = max(kth_largest(slot[lane], k), order_key(-INFINITY) + 1u);
+                least = max(least, static_cast<uint64_t>(t) << 32);
+                bound = key_value(static_cast<uint32_t>(least >> 32));
+                const int n_before = n_kept;
+                const uint32_t rest = 0xffffffffu - (static_cast<uint32_t>(seg) * kSegCols + static_cast<uint32_t>(lane * G));
+#pragma unroll
+                for (int u = 0; u < 8; ++u) {
+                    if (!__ballot(gm[u] >= bound))
+                        continue;
+#pragma unroll
+                    for (int i = 4 * u; i < 4 * u + 4; ++i) {
+                        const uint64_t mask = __ballot(v[i] >= bound);
+                        if (!mask)
+                            continue;
+                        // The column's complement is formed here, not for all 32
+                        // values ahead of the branches (64 registers).
+                        uint32_t low = rest;
+                        asm volatile("" : "+v"(low));
+                        low -= static_cast<uint32_t>(64 * (i / G) * G + i % G);
+                        const int at = n_kept + __popcll(mask & ((1ull << lane) - 1ull));
+                        if (v[i] >= bound && at < kWaveCap)
+                            mine[at] = (static_cast<uint64_t>(order_key(v[i])) << 32) | low;
+                        n_kept += __popcll(mask);
+                    }
+                }
+                __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+                if (n_kept > kWaveCap)
+                    n_kept = collect_all<BF16>(zr, V, static_cast<int64_t>(seg) * kSegCols, least, mine, n_before, k, lane);
+            }
+        }
+    }
+    // The wave's sums, then the workgroup's.
+    {
+        const float m = wave_maximum(sums.m);
+        const float ms = m == -INFINITY ? 0.0f : m;
+        const float dy = __builtin_elementwise_maximum((sums.m - ms) * c, kNoTerm);
+        const float f = __builtin_amdgcn_exp2f(dy);
+        const float d = wave_sum(sums.d * f), s = wave_sum(f * fmaf(dy, sums.d, sums.s));
+        if (lane == 0)
+            part_rec[wave] = {m, d, s, before};
+    }
+    __syncthreads();
+    if constexpr (TOP) {
+        // What reaches the last bound (no slot changes any more).
+        least = max(least, static_cast<uint64_t>(kth_largest(slot[lane], k)) << 32);
+        for (int i = lane; i < n_kept; i += 64) {
+            const uint64_t key = mine[i];
+            if (key >= least) {
+                const uint32_t at = atomicAdd(&cand_n, 1u);
+                if (at < kListCap)
+                    cand[at] = key;
+            }
+        }
+    }
+    if (wave == 0) {
+        const RowSums q = fold(part_rec, NW, lane, c);
+        if (parts == 1) {
+            const float log_d = logf(static_cast<float>(q.d));
+            if (lane == 0) {
+                write_row(q, log_d, inv_t, zr, BF16, V, token, ignore_index, row, o);
+                sh_log_d = q.d > 0.0 ? log_d : __int_as_float(0x7fc00000);
+                sh_m = q.m;
+            }
+        } else if (lane == 0) {
+            rec[id] = {q.m, static_cast<float>(q.d), static_cast<float>(q.s), q.before};
+        }
+    }
+    if constexpr (TOP) {
+        __syncthreads();
+        uint64_t *out_keys = lists + static_cast<int64_t>(id) * k;
+        float *lp = o.top_logprob + static_cast<int64_t>(row) * k;
+        int32_t *tok = o.top_token + static_cast<int64_t>(row) * k;
+        const float log_d = sh_log_d;
+        const bool nan_row = parts == 1 && !(log_d == log_d);
+        auto put = [&](int at, uint64_t key) {
+            if (parts != 1) {
+                out_keys[at] = key;
+            } else if (key == 0 || nan_row) {
+                lp[at] = nan_row ? __int_as_float(0x7fc00000) : -INFINITY;
+                tok[at] = -1;
+            } else {
+                const float z = key_value(static_cast<uint32_t>(key >> 32));
+                lp[at] = static_cast<float>((static_cast<double>(z) - sh_m) * inv_t - log_d);
+                tok[at] = static_cast<int32_t>(0xffffffffu - static_cast<uint32_t>(key));
+            }
+        };
+        const int n = static_cast<int>(cand_n);
+        if (nan_row) {
+            if (tid < k)
+                put(tid, 0);
+        } else if (n <= kListCap) {
+            for (int i = tid; i < n; i += NW * 64) {
+                const uint64_t key = cand[i];
+                int rank = 0;
+                for (int q = 0; q < n; ++q)
+                    rank += cand[q] > key;
+                if (rank < k)
+                    put(rank, key);
+            }
+            if (n + tid < k)  // fewer than k above -inf
+                put(n + tid, 0);
+        } else {
+            // More than are ranked at once: k rounds, each taking the largest key
+            // below the last one.
+            uint64_t last = ~0ull;
+            for (int r = 0; r < k; ++r) {
+                uint64_t best = 0;
+                for (int i = lane; i < n_kept; i += 64) {
+                    const uint64_t key = mine[i];
+                    if (key < last && key > best)
+                        best = key;
+                }
+#pragma unroll
+                for (int off = 32; off >= 1; off >>= 1)
+                    best = max(best, shfl_xor_u64(best, off));
+                if (lane == 0)
+                    red[wave] = best;
+                __syncthreads();
+                for (int w = 0; w < NW; ++w)
+                    best = max(best, red[w]);
+                __syncthreads();
+                if (tid == 0)
+                    put(r, best);
+                last = best;
+            }
+        }
+    }
 }
 
 // Rows without alternatives: one wave each.
@@ -190,7 +439,7 @@ __global__ __launch_bounds__(256) void logprobs_merge_kernel(
     const float inv_t = inverse_temperature(temperature, row * temperature_stride);
     const RowSums q = fold(rec + row * nseg, nseg, lane, kLog2e * inv_t);
     if (lane == 0)
-        write_row(q, log(q.d), inv_t, logits + row * ld_bytes, bf16 != 0, V, token, ignore_index, row, o);
+        write_row(q, logf(static_cast<float>(q.d)), inv_t, logits + row * ld_bytes, bf16 != 0, V, token, ignore_index, row, o);
 }
 
 constexpr int kTopThreads = 256;
@@ -203,12 +452,11 @@ __global__ __launch_bounds__(kTopThreads) void logprobs_top_kernel(
     const char *__restrict__ logits, int64_t ld_bytes, int32_t bf16, int64_t V, int32_t nseg,
     const int32_t *__restrict__ token, int32_t ignore_index, const float *__restrict__ temperature,
     int64_t temperature_stride, int32_t k, const LogprobRecord *__restrict__ rec,
-    const uint64_t *__restrict__ lists, float *__restrict__ top_logprob, int32_t *__restrict__ top_token,
-    RowOutputs o)
+    const uint64_t *__restrict__ lists, RowOutputs o)
 {
     __shared__ uint64_t cand[kTopCap];
     __shared__ uint32_t n_cand, bound;
-    __shared__ double sh_log_d;
+    __shared__ float sh_log_d;
     __shared__ float sh_m;
     __shared__ uint64_t red[kTopThreads / 64];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
@@ -218,10 +466,10 @@ __global__ __launch_bounds__(kTopThreads) void logprobs_top_kernel(
     const float inv_t = inverse_temperature(temperature, row * temperature_stride);
     if (wave == 0) {
         const RowSums q = fold(rec + row * nseg, nseg, lane, kLog2e * inv_t);
-        const double log_d = log(q.d);
+        const float log_d = logf(static_cast<float>(q.d));
         if (lane == 0) {
             write_row(q, log_d, inv_t, logits + row * ld_bytes, bf16 != 0, V, token, ignore_index, row, o);
-            sh_log_d = q.d > 0.0 ? log_d : static_cast<double>(NAN);
+            sh_log_d = q.d > 0.0 ? log_d : __int_as_float(0x7fc00000);
             sh_m = q.m;
             n_cand = 0;
         }
@@ -235,19 +483,14 @@ __global__ __launch_bounds__(kTopThreads) void logprobs_top_kernel(
         } else if (lane / nseg < k) {
             mine = static_cast<uint32_t>(keys[static_cast<int64_t>(lane % nseg) * k + lane / nseg] >> 32);
         }
-        uint32_t t = 0;
-        for (int b = 31; b >= 0; --b) {
-            const uint32_t c = t | (1u << b);
-            if (__popcll(__ballot(mine >= c)) >= k)
-                t = c;
-        }
+        const uint32_t t = kth_largest(mine, k);
         if (lane == 0)
             bound = t;
     }
     __syncthreads();
-    const double log_d = sh_log_d;
-    float *lp = top_logprob + row * k;
-    int32_t *tok = top_token + row * k;
+    const float log_d = sh_log_d;
+    float *lp = o.top_logprob + row * k;
+    int32_t *tok = o.top_token + row * k;
     if (!(log_d == log_d)) {
         if (tid < k) {
             lp[tid] = __int_as_float(0x7fc00000);
@@ -390,49 +633,80 @@ int64_t row_segments(int64_t V)
     return (V + kSegCols - 1) / kSegCols;
 }
 
+namespace {
+
+// How the rows are shared out: workgroups of 4 waves, a row each, where there are
+// rows enough for every CU; else of 16 waves, and few rows in parts.
+struct RowPlan {
+    int32_t waves, part_segs;
+    int64_t parts;
+};
+RowPlan row_plan(int64_t n_rows, int64_t V)
+{
+    const int64_t nseg = row_segments(V);
+    if (n_rows >= 512)
+        return {4, static_cast<int32_t>(nseg), 1};
+    const int64_t rounds = (nseg + 15) / 16;  // of a workgroup over the whole row
+    const int64_t want = std::max<int64_t>(1, 512 / std::max<int64_t>(n_rows, 1));
+    const int64_t per = (rounds + want - 1) / want;
+    return {16, static_cast<int32_t>(16 * per), (rounds + per - 1) / per};
+}
+
+}  // namespace
+
 int64_t logprobs_workspace_bytes(int64_t n_rows, int64_t V, int64_t k)
 {
-    return n_rows * row_segments(V) * (static_cast<int64_t>(sizeof(LogprobRecord)) + 8 * k);
+    const int64_t parts = row_plan(n_rows, V).parts;
+    return parts == 1 ? 0 : n_rows * parts * (static_cast<int64_t>(sizeof(LogprobRecord)) + 8 * k);
 }
 
 hipError_t launch_logprobs(const Logprobs &p, void *workspace, hipStream_t s)
 {
-    const int64_t nseg = row_segments(p.V), esz = p.bf16 ? 2 : 4;
+    const RowPlan plan = row_plan(p.n, p.V);
+    const int64_t parts = plan.parts, esz = p.bf16 ? 2 : 4;
     LogprobRecord *rec = static_cast<LogprobRecord *>(workspace);
-    uint64_t *lists = reinterpret_cast<uint64_t *>(rec + p.n * nseg);
+    uint64_t *lists = reinterpret_cast<uint64_t *>(rec + p.n * parts);
     const int32_t k = static_cast<int32_t>(p.k);
-    const int64_t chunk = std::max<int64_t>(1, kMaxItems / 256 / nseg);
+    const int64_t chunk = std::max<int64_t>(1, kMaxItems / 1024 / parts);
     for (int64_t r0 = 0; r0 < p.n; r0 += chunk) {
         const int64_t nr = std::min(chunk, p.n - r0);
         const char *z = static_cast<const char *>(p.logits) + r0 * p.ld * esz;
         const int32_t *tok = p.token ? p.token + r0 : nullptr;
         const float *temp = p.temperature ? p.temperature + r0 * p.temperature_stride : nullptr;
-        LogprobRecord *rc = rec + r0 * nseg;
-        uint64_t *ls = lists + r0 * nseg * k;
+        LogprobRecord *rc = rec + r0 * parts;
+        uint64_t *ls = lists + r0 * parts * k;
         const RowOutputs o = {p.logprob ? p.logprob + r0 : nullptr, p.entropy ? p.entropy + r0 : nullptr,
-                              p.rank ? p.rank + r0 : nullptr, reinterpret_cast<float4 *>(p.stats) + r0};
-        const dim3 grid(static_cast<unsigned>(nr * nseg));
-        auto scan = [&](auto bf16, auto top, auto rank) {
-            hipLaunchKernelGGL((logprobs_scan_kernel<decltype(bf16)::value, decltype(top)::value, decltype(rank)::value>),
-                               grid, dim3(64), 0, s, z, p.ld, p.V, static_cast<uint32_t>(nseg), tok, temp,
-                               p.temperature_stride, k, rc, ls);
+                              p.rank ? p.rank + r0 : nullptr, reinterpret_cast<float4 *>(p.stats) + r0,
+                              k ? p.top_logprob + r0 * k : nullptr, k ? p.top_token + r0 * k : nullptr};
+        auto rows = [&](auto bf16, auto top, auto rank, auto waves) {
+            constexpr int NW = decltype(waves)::value;
+            hipLaunchKernelGGL(
+                (logprobs_row_kernel<decltype(bf16)::value, decltype(top)::value, decltype(rank)::value, NW>),
+                dim3(static_cast<unsigned>(nr * parts)), dim3(NW * 64), 0, s, z, p.ld, p.V,
+                static_cast<uint32_t>(parts), plan.part_segs, tok, p.ignore_index, temp, p.temperature_stride, k,
+                rc, ls, o);
         };
         const auto yes = std::true_type{};
         const auto no = std::false_type{};
-        auto with_rank = [&](auto bf16, auto top) { p.rank ? scan(bf16, top, yes) : scan(bf16, top, no); };
+        auto with_waves = [&](auto bf16, auto top, auto rank) {
+            plan.waves == 4 ? rows(bf16, top, rank, std::integral_constant<int, 4>{})
+                            : rows(bf16, top, rank, std::integral_constant<int, 16>{});
+        };
+        auto with_rank = [&](auto bf16, auto top) { p.rank ? with_waves(bf16, top, yes) : with_waves(bf16, top, no); };
         auto with_top = [&](auto bf16) { k ? with_rank(bf16, yes) : with_rank(bf16, no); };
         p.bf16 ? with_top(yes) : with_top(no);
         hipError_t e = hipGetLastError();
         if (e != hipSuccess)
             return e;
+        if (parts == 1)
+            continue;
         if (k)
             hipLaunchKernelGGL(logprobs_top_kernel, dim3(static_cast<unsigned>(nr)), dim3(kTopThreads), 0, s, z,
-                               p.ld * esz, p.bf16 ? 1 : 0, p.V, static_cast<int32_t>(nseg), tok, p.ignore_index,
-                               temp, p.temperature_stride, k, rc, ls, p.top_logprob + r0 * k,
-                               p.top_token + r0 * k, o);
+                               p.ld * esz, p.bf16 ? 1 : 0, p.V, static_cast<int32_t>(parts), tok, p.ignore_index,
+                               temp, p.temperature_stride, k, rc, ls, o);
         else
             hipLaunchKernelGGL(logprobs_merge_kernel, dim3(static_cast<unsigned>((nr + 3) / 4)), dim3(256), 0, s, z,
-                               p.ld * esz, p.bf16 ? 1 : 0, nr, p.V, static_cast<int32_t>(nseg), tok,
+                               p.ld * esz, p.bf16 ? 1 : 0, nr, p.V, static_cast<int32_t>(parts), tok,
                                p.ignore_index, temp, p.temperature_stride, rc, o);
         e = hipGetLastError();
         if (e != hipSuccess)

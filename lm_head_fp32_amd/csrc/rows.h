@@ -91,29 +91,39 @@ struct Segment {
     uint4 q[NQ];
     __device__ __forceinline__ void load(const void *row, int64_t V, int64_t j0, int lane)
     {
+        const char *base = static_cast<const char *>(row) + j0 * (16 / G);
+        const uint32_t at = static_cast<uint32_t>(lane) * 16;
         if (j0 + kSegCols <= V) {
 #pragma unroll
             for (int u = 0; u < NQ; ++u)
-                q[u] = *reinterpret_cast<const uint4 *>(static_cast<const char *>(row) +
-                                                        (j0 + (64 * u + lane) * G) * (16 / G));
+                q[u] = *reinterpret_cast<const uint4 *>(base + at + 1024 * u);
             return;
         }
+        const uint32_t none = BF16 ? 0xff80ff80u : 0xff800000u;
+        const int32_t cols = static_cast<int32_t>(V - j0), whole = cols / G;
 #pragma unroll
         for (int u = 0; u < NQ; ++u) {
+            q[u] = make_uint4(none, none, none, none);
+            if (64 * u + lane < whole)
+                q[u] = *reinterpret_cast<const uint4 *>(base + at + 1024 * u);
+        }
+        if (whole * G < cols) {  // the one vector that the row's end lies in
             uint32_t w[4];
-            const int64_t j = j0 + (64 * u + lane) * G;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 if constexpr (BF16) {
-                    const uint16_t *p = static_cast<const uint16_t *>(row) + j + 2 * e;
-                    const uint32_t lo = j + 2 * e < V ? p[0] : 0xff80u;
-                    const uint32_t hi = j + 2 * e + 1 < V ? p[1] : 0xff80u;
+                    const uint16_t *p = reinterpret_cast<const uint16_t *>(base) + whole * G + 2 * e;
+                    const uint32_t lo = whole * G + 2 * e < cols ? p[0] : 0xff80u;
+                    const uint32_t hi = whole * G + 2 * e + 1 < cols ? p[1] : 0xff80u;
                     w[e] = lo | (hi << 16);
                 } else {
-                    w[e] = j + e < V ? static_cast<const uint32_t *>(row)[j + e] : 0xff800000u;
+                    w[e] = whole * G + e < cols ? reinterpret_cast<const uint32_t *>(base)[whole * G + e] : none;
                 }
             }
-            q[u] = make_uint4(w[0], w[1], w[2], w[3]);
+#pragma unroll
+            for (int u = 0; u < NQ; ++u)
+                if (64 * u + lane == whole)
+                    q[u] = make_uint4(w[0], w[1], w[2], w[3]);
         }
     }
     __device__ __forceinline__ void values(float (&v)[32]) const

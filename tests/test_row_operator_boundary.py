@@ -45,18 +45,24 @@ def test_logprobs_refusals(L):
 
     assert f(dt=FP16) == DTYPE and f(dt=7) == DTYPE
     for bad in (dict(n=-1), dict(n=MAX), dict(V=0), dict(V=-1), dict(V=MAX), dict(k=-1), dict(k=65), dict(V=5, k=6),
-                dict(ld=96), dict(wsb=-1), dict(wsb=100), dict(ts=2), dict(ts=-1), dict(ld=MAX // 4 * 4)):
+                dict(ld=96), dict(wsb=-1), dict(ts=2), dict(ts=-1), dict(ld=MAX // 4 * 4)):
         assert f(**bad) == SHAPE, bad
-    for bad in (dict(z=None), dict(st=None), dict(ws=None), dict(tl=None), dict(tt=None), dict(y=None),
+    for bad in (dict(z=None), dict(st=None), dict(tl=None), dict(tt=None), dict(y=None),
                 dict(y=None, lp=None), dict(y=None, rk=None)):
         assert f(**bad) == NULL, bad
     for bad in (dict(z=Z + 4), dict(ld=102), dict(dt=BF16, ld=108), dict(y=Y + 2), dict(t=T + 1), dict(lp=LP + 2),
                 dict(h=H + 1), dict(rk=RK + 2), dict(tl=TL + 2), dict(tt=TT + 1), dict(st=ST + 8), dict(ws=WS + 8)):
         assert f(**bad) == ALIGN, bad
-    for bad in (dict(lp=Z), dict(h=LP + 4), dict(rk=Y), dict(tl=T), dict(tt=TL + 8), dict(st=WS), dict(ws=Z + 16),
-                dict(st=Z + 16), dict(rk=T + 36), dict(ws=Y & ~15)):
+    for bad in (dict(lp=Z), dict(h=LP + 4), dict(rk=Y), dict(tl=T), dict(tt=TL + 8), dict(st=LP),
+                dict(st=Z + 16), dict(rk=T + 36)):
         assert f(**bad) == ALIAS, bad
     assert f(n=0, z=None, st=None, ws=None) == OK
+    # the workspace of a few long rows
+    need = L.lmhead_logprobs_workspace_bytes(2, 200000, 6)
+    far = dict(n=2, V=200000, ld=200000)
+    assert need > 0 and L.lmhead_logprobs_workspace_bytes(2, 100, 6) == 0
+    assert f(**far, wsb=need - 1) == SHAPE and f(**far, ws=None) == NULL
+    assert f(**far, ws=Z) == ALIAS and f(**far, ws=TL - 16) == ALIAS
     assert L.lmhead_logprobs_workspace_bytes(4, 0, 0) == -SHAPE
     assert L.lmhead_logprobs_workspace_bytes(-1, 8, 0) == -SHAPE
     assert L.lmhead_logprobs_workspace_bytes(4, 8, 9) == -SHAPE
