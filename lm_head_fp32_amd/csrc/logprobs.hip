@@ -63,19 +63,36 @@ struct LaneSums {
 constexpr int kWaveCap = 256;  // candidates a wave keeps in LDS
 constexpr int kListCap = 512;  // candidates of a workgroup that are ranked by counting
 
-// The largest t with at least k of the wave's values >= t, cut to its upper 20
-// bits: a lower bound of the k-th largest, two bits a step.
-__device__ __forceinline__ uint32_t kth_largest(uint32_t mine, int k)
+// The largest t with at least k of the wave's values (N a lane) >= t, cut to its
+// upper 20 bits: a lower bound of the k-th largest, two bits a step.
+template <int N>
+__device__ __forceinline__ uint32_t kth_largest(const uint32_t (&mine)[N], int k)
 {
     uint32_t t = 0;
+    auto reach = [&](uint32_t c) {
+        int n = 0;
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            n += __popcll(__ballot(mine[i] >= c));
+        return n >= k;
+    };
 #pragma unroll
     for (int b = 30; b >= 12; b -= 2) {
         const uint32_t c1 = t | (1u << b), c2 = t | (2u << b), c3 = t | (3u << b);
-        const int n1 = __popcll(__ballot(mine >= c1)), n2 = __popcll(__ballot(mine >= c2)),
-                  n3 = __popcll(__ballot(mine >= c3));
-        t = n3 >= k ? c3 : n2 >= k ? c2 : n1 >= k ? c1 : t;
+        const bool r1 = reach(c1), r2 = reach(c2), r3 = reach(c3);
+        t = r3 ? c3 : r2 ? c2 : r1 ? c1 : t;
     }
     return t;
+}
+
+// A workgroup's slots: 64, or 128 for more than 32 alternatives (the bound would
+// have a rank of up to 64 ln 64 = 266 otherwise; of 128 slots it is 128 ln 2 = 89).
+constexpr int kFewTop = 32;
+__device__ __forceinline__ uint32_t slots_bound(const uint32_t *slot, int lane, int k)
+{
+    if (k <= kFewTop)
+        return kth_largest<1>({slot[lane]}, k);
+    return kth_largest<2>({slot[lane], slot[lane + 64]}, k);
 }
 
 // The k largest of n keys (n <= kWaveCap, all different) to the front of the
@@ -208,9 +225,10 @@ __device__ __forceinline__ void write_row(const RowSums &q, float log_d, float i
 // takes every NW-th segment of the part, the next one's loads under way.  With one
 // part per row the workgroup writes the row's results, else a record and its k
 // largest for the merge.
-// Alternatives: slot[l] is the largest value that lane l of any wave has seen, so
-// the k-th largest of the 64 slots is a lower bound of the k-th largest value (k
-// different values reach it), whatever the waves have read so far.  It is taken anew
+// Alternatives: slot[l] is the largest value that lane l of any wave has seen (for
+// larger k two slots, for the halves of its values), so the k-th largest of the
+// slots is a lower bound of the k-th largest value (k different values reach it),
+// whatever the waves have read so far.  It is taken anew
 // for every round of NW segments, still in registers; the few values that reach it
 // are kept per wave, and at the end those that reach the last bound are ranked by
 // counting.
@@ -225,7 +243,7 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(4))) vo
     __shared__ uint64_t kept[TOP ? NW * kWaveCap : 1];
     __shared__ uint64_t cand[TOP ? kListCap : 1];
     __shared__ uint64_t red[NW];
-    __shared__ uint32_t slot[64];
+    __shared__ uint32_t slot[128];
     __shared__ LogprobRecord part_rec[NW];
     __shared__ uint32_t cand_n;
     __shared__ float sh_log_d;
@@ -251,7 +269,7 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(4))) vo
         }
     }
     if constexpr (TOP) {
-        if (tid < 64)
+        if (tid < 128)
             slot[tid] = 0;
         if (tid == 0)
             cand_n = 0;
@@ -277,8 +295,22 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(4))) vo
             if (u & 1)
                 lm = __builtin_elementwise_maximum(__builtin_elementwise_maximum(lm, gm[u - 1]), gm[u]);  // NaN stays NaN
         }
-        if constexpr (TOP)
-            atomicMax(&slot[lane], order_key(lm));  // a NaN only raises it: the row is NaN then
+        if constexpr (TOP) {  // a NaN only raises a slot: the row is NaN then
+            if (k <= kFewTop) {
+                atomicMax(&slot[lane], order_key(lm));
+            } else {
+                float half = gm[0];
+#pragma unroll
+                for (int u = 1; u < 8; ++u) {
+                    if (u == 4) {
+                        atomicMax(&slot[lane], order_key(half));
+                        half = gm[4];
+                    }
+                    half = __builtin_elementwise_maximum(half, gm[u]);
+                }
+                atomicMax(&slot[lane + 64], order_key(half));
+            }
+        }
         sums.add(v, lm, c);
         if constexpr (RANK) {
             // Vectors before the token's count equal values, those behind it
@@ -297,7 +329,7 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(4))) vo
         if constexpr (TOP) {
             __syncthreads();
             if (__ballot(lm >= bound)) {
-                const uint32_t t = max(kth_largest(slot[lane], k), order_key(-INFINITY) + 1u);
+                const uint32_t t = max(slots_bound(slot, lane, k), order_key(-INFINITY) + 1u);
                 least = max(least, static_cast<uint64_t>(t) << 32);
                 bound = key_value(static_cast<uint32_t>(least >> 32));
                 const int n_before = n_kept;
@@ -341,7 +373,7 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(4))) vo
     __syncthreads();
     if constexpr (TOP) {
         // What reaches the last bound (no slot changes any more).
-        least = max(least, static_cast<uint64_t>(kth_largest(slot[lane], k)) << 32);
+        least = max(least, static_cast<uint64_t>(slots_bound(slot, lane, k)) << 32);
         for (int i = lane; i < n_kept; i += 64) {
             const uint64_t key = mine[i];
             if (key >= least) {
@@ -483,7 +515,7 @@ __global__ __launch_bounds__(kTopThreads) void logprobs_top_kernel(
         } else if (lane / nseg < k) {
             mine = static_cast<uint32_t>(keys[static_cast<int64_t>(lane % nseg) * k + lane / nseg] >> 32);
         }
-        const uint32_t t = kth_largest(mine, k);
+        const uint32_t t = kth_largest<1>({mine}, k);
         if (lane == 0)
             bound = t;
     }
