@@ -615,7 +615,8 @@ int32_t lmhead_logprobs_bwd(const void *logits, int64_t ld, int32_t logits_dtype
  *  ldt, ldv >= n_list, aligned to their elements.
  *  loss [n_rows] or NULL.  Limits: n_cols >= 1, 0 <= n_list <= 256.
  *  workspace as lmhead_logits_lora, of lmhead_distill_workspace_bytes(n_rows,
- *  n_cols) bytes.  Outputs overlap neither inputs nor each other.
+ *  n_cols) bytes (may be NULL where that is 0).  Outputs overlap neither inputs
+ *  nor each other.
  */
 int64_t lmhead_distill_workspace_bytes(int64_t n_rows, int64_t n_cols);
 int32_t lmhead_distill_fwd(const void *logits, int64_t ld, int32_t logits_dtype, int64_t n_rows,

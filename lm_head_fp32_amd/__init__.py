@@ -936,11 +936,22 @@ def lmhead_beam_reorder(state, parent, out=None, beam_dim=0, len_dim=None, lengt
 
 # ------------------------------------- log-probabilities and distillation
 
+def _rows(t, name, dtype):
+    """(pointer, ld) as _mat's; the ld of a single row, which nothing uses, is
+    given as the library's alignment asks."""
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.dim() == 2 and t.is_cuda
+            and t.get_device() == _current()):
+        (rows, cols), (ld, step) = t.shape, t.stride()
+        if step == 1 or cols <= 1:
+            return t.data_ptr(), ld if rows > 1 else (cols + 7) // 8 * 8
+    return _mat(t, name, dtype)
+
+
 def _row_logits(logits):
     """(pointer, ld, dtype code, n, V) of fp32 or bf16 logits [n, V]."""
     if not isinstance(logits, torch.Tensor) or logits.dtype not in (torch.float32, torch.bfloat16):
         raise TypeError("logits: expected a GPU float32 or bfloat16 tensor")
-    pz, ld = _mat(logits, "logits", logits.dtype)
+    pz, ld = _rows(logits, "logits", logits.dtype)
     return (pz, ld, _DT[logits.dtype], *logits.shape)
 
 
@@ -962,7 +973,7 @@ def _row_out(t, name, dtype, shape, like):
     if t is False:
         return None, None
     if t is None:
-        t = like.new_empty(shape, dtype=dtype)
+        t = torch.empty_strided(shape, (1,) if len(shape) == 1 else (shape[1], 1), dtype=dtype, device=like.device)
         return t, t.data_ptr()
     n = 1
     for s in shape:
@@ -982,7 +993,7 @@ def _row_grad(fn, logits, dlogits, grad_dtype, in_place):
         if code not in (LMH_BF16, LMH_FP32):
             _check(fn, 1)
         dlogits = _empty_rows(*logits.shape, _TORCH_DT[code], logits)
-    pg, ldg = _mat(dlogits, "dlogits", dlogits.dtype)
+    pg, ldg = _rows(dlogits, "dlogits", dlogits.dtype)
     if dlogits.shape != logits.shape:
         raise ValueError("dlogits must be [n, V]")
     return dlogits, pg, ldg, code
@@ -1108,10 +1119,10 @@ def lmhead_distill_fwd(logits, teacher_token, teacher_value, tail=False, tempera
     need = lmhead_distill_workspace_bytes(n, V)
     loss, pl = _row_out(loss, "loss", torch.float32, (n,), logits)
     stats, ps = _row_out(stats, "stats", torch.float32, (n, DISTILL_STATS_COLS), logits)
-    ws, nbytes = _workspace(need, workspace, logits)
+    ws, pw, nbytes = _row_workspace(need, workspace, logits)
     _check("lmhead_distill_fwd",
            lib().lmhead_distill_fwd(pz, ld, code, n, V, *teacher, int(bool(tail)), pt, st, pl, ps,
-                                    ws.data_ptr(), nbytes, _stream(stream)))
+                                    pw, nbytes, _stream(stream)))
     return loss, stats
 
 
@@ -1157,10 +1168,10 @@ def lmhead_distill_fused(logits, teacher_token, teacher_value, dloss, tail=False
     need = lmhead_distill_workspace_bytes(n, V)
     loss, pl = _row_out(loss, "loss", torch.float32, (n,), logits)
     stats, ps = _row_out(stats, "stats", torch.float32, (n, DISTILL_STATS_COLS), logits)
-    ws, nbytes = _workspace(need, workspace, logits)
+    ws, pw, nbytes = _row_workspace(need, workspace, logits)
     _check("lmhead_distill_fused",
            lib().lmhead_distill_fused(pz, ld, code, n, V, *teacher, int(bool(tail)), pt, st, pd, sd, pl, ps, pg,
-                                      ldg, gcode, ws.data_ptr(), nbytes, _stream(stream)))
+                                      ldg, gcode, pw, nbytes, _stream(stream)))
     return loss, stats, dlogits
 
 

@@ -1177,11 +1177,11 @@ int32_t lmhead_distill_fwd(const void *logits, int64_t ld, int32_t logits_dtype,
         return LMH_OK;
     const TeacherArgs t = {teacher_token, ldt, teacher_value, ldv, teacher_dtype, n_list};
     LMH_TRY(check_distill(logits, ld, logits_dtype, n_rows, n_cols, t, temperature, temperature_stride));
-    if (!stats || !workspace)
+    const int64_t need = lmh::distill_workspace_bytes(n_rows, n_cols);
+    if (!stats || (need > 0 && !workspace))
         return LMH_ERR_NULL;
     if (!aligned16(stats) || !aligned16(workspace) || !aligned4(loss))
         return LMH_ERR_ALIGN;
-    const int64_t need = lmh::distill_workspace_bytes(n_rows, n_cols);
     if (workspace_bytes < need)
         return LMH_ERR_SHAPE;
     const Span outs[] = {bytes_span(workspace, need), bytes_span(stats, 32 * n_rows),
@@ -1255,11 +1255,11 @@ int32_t lmhead_distill_fused(const void *logits, int64_t ld, int32_t logits_dtyp
     const TeacherArgs t = {teacher_token, ldt, teacher_value, ldv, teacher_dtype, n_list};
     LMH_TRY(check_distill(logits, ld, logits_dtype, n_rows, n_cols, t, temperature, temperature_stride));
     LMH_TRY(check_row_grad(logits, ld, logits_dtype, dlogits, ldg, grad_dtype, n_rows, n_cols));
-    if (!stats || !workspace || !dloss)
+    const int64_t need = lmh::distill_workspace_bytes(n_rows, n_cols);
+    if (!stats || (need > 0 && !workspace) || !dloss)
         return LMH_ERR_NULL;
     if (!aligned16(stats) || !aligned16(workspace) || !aligned4(loss) || !aligned4(dloss))
         return LMH_ERR_ALIGN;
-    const int64_t need = lmh::distill_workspace_bytes(n_rows, n_cols);
     if (workspace_bytes < need)
         return LMH_ERR_SHAPE;
     const Span z = span_of(logits, n_rows, n_cols, ld, logits_dtype == LMH_BF16 ? 2 : 4);

@@ -206,7 +206,6 @@ struct LogprobsBwd {
     bool grad_bf16;
     int64_t n, V;
 };
-int64_t row_segments(int64_t V);
 int64_t logprobs_workspace_bytes(int64_t n_rows, int64_t V, int64_t k);
 hipError_t launch_logprobs(const Logprobs &p, void *workspace, hipStream_t s);
 hipError_t launch_logprobs_bwd(const LogprobsBwd &p, hipStream_t s);

@@ -69,97 +69,269 @@ struct alignas(16) RowStats {
 };
 static_assert(sizeof(RowStats) == 32, "eight floats");
 
-// One wave, a workgroup of its own, per (row, segment of 2048 columns): {m, d},
-// with TAIL of the columns that are not on the row's list.
-template <bool BF16, bool TAIL>
-__global__ __launch_bounds__(64) void distill_scan_kernel(
-    const void *__restrict__ logits, int64_t ld, int64_t V, uint32_t nseg, ListArgs list,
-    const float *__restrict__ temperature, int64_t temperature_stride, float2 *__restrict__ rec)
+// What the list says of a row, in 64 bits: the teacher's total and entropy term
+// (A = sum q log q), B = sum q z, and the student's sum D over the listed columns,
+// each once, about their maximum m_l (tail mode).
+struct ListSums {
+    double total, A, B, D, sum;
+    float m_l, top;
+    int32_t there;  // entries; 0: the list is empty
+    bool off;       // one lies outside the columns
+    bool twice;     // a token is listed more than once
+};
+
+struct ListShared {
+    int32_t ids[kMaxList];
+    float v_max[kListThreads / 64], z_max[kListThreads / 64];
+    int32_t flags[kListThreads / 64];  // entries, 2^10 those outside, 2^20 those listed before
+    double part[kListThreads / 64][4];
+};
+
+// By a workgroup whose first 256 threads hold an entry each (en, and z, the logit of
+// its column; `again`: another entry may have its token).  Two barriers; q is the
+// thread's own share of the teacher (of nothing: 0).
+template <bool TAIL>
+__device__ __forceinline__ ListSums list_sums(ListShared &sh, const Entry &en, float z, int64_t V, float inv_t,
+                                              int32_t k, bool again, int tid, double &q)
+{
+    const int lane = tid & 63, wave = tid >> 6;
+    constexpr int NW = kListThreads / 64;
+    const bool there = en.token >= 0;
+    if (wave < NW) {
+        const float vm = wave_maximum(there ? en.value : -INFINITY), zm = wave_maximum(z);
+        const int32_t n = __popcll(__ballot(there)), off = __popcll(__ballot(there && en.token >= V)),
+                      more = __popcll(__ballot(again));
+        if (lane == 0) {
+            sh.v_max[wave] = vm;
+            sh.z_max[wave] = zm;
+            sh.flags[wave] = n + (off << 10) + (more << 20);
+        }
+    }
+    __syncthreads();
+    ListSums r;
+    r.top = sh.v_max[0];
+    r.m_l = sh.z_max[0];
+    int32_t flags = sh.flags[0];
+#pragma unroll
+    for (int w = 1; w < NW; ++w) {
+        r.top = __builtin_elementwise_maximum(r.top, sh.v_max[w]);
+        r.m_l = __builtin_elementwise_maximum(r.m_l, sh.z_max[w]);
+        flags += sh.flags[w];
+    }
+    r.there = flags & 0x3ff;
+    r.off = ((flags >> 10) & 0x3ff) != 0;
+    r.twice = (flags >> 20) != 0;
+    if (TAIL)
+        r.top = 0.0f;
+    double x = 0.0, e = 0.0;
+    if (wave < NW) {
+        x = (static_cast<double>(en.value) - r.top) * (TAIL ? 1.0f : inv_t);
+        e = there ? exp(x) : 0.0;
+        double s = wave_sum(e), a = wave_sum(e != 0.0 ? e * x : 0.0), b = wave_sum(e != 0.0 ? e * z : 0.0), dl = 0.0;
+        if constexpr (TAIL) {
+            bool first = there;
+            for (int i = 0; r.twice && i < min(tid, k); ++i)
+                first = first && sh.ids[i] != en.token;
+            dl = wave_sum(first && z != -INFINITY ? exp((static_cast<double>(z) - r.m_l) * inv_t) : 0.0);
+        }
+        if (lane == 0) {
+            sh.part[wave][0] = s;
+            sh.part[wave][1] = a;
+            sh.part[wave][2] = b;
+            sh.part[wave][3] = dl;
+        }
+    }
+    __syncthreads();
+    double s = 0.0, a = 0.0, b = 0.0;
+    r.D = 0.0;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) {
+        s += sh.part[w][0];
+        a += sh.part[w][1];
+        b += sh.part[w][2];
+        r.D += sh.part[w][3];
+    }
+    r.sum = TAIL ? 1.0 : s;
+    const double inv = 1.0 / r.sum;
+    r.total = TAIL ? s : (s == s ? 1.0 : s);
+    r.A = a;
+    r.B = b * inv;
+    q = e * inv;
+    return r;
+}
+
+// The row's numbers from the list's and the scanned columns' (m_o, d_o: all columns,
+// or with TAIL those off the list); by one thread.
+template <bool TAIL>
+__device__ __forceinline__ RowStats finish_row(const ListSums &t, float m_o, double d_o, float inv_t)
+{
+    float m = m_o;
+    double d = d_o, shift = 0.0;
+    if constexpr (TAIL) {
+        m = __builtin_elementwise_maximum(m_o, t.m_l);
+        shift = (static_cast<double>(m_o) - m) * inv_t;
+        d = (t.D != 0.0 ? t.D * exp((static_cast<double>(t.m_l) - m) * inv_t) : 0.0) +
+            (d_o != 0.0 ? d_o * exp(shift) : 0.0);
+    }
+    const double log_d = log(d);
+    // sum q log q: in logits mode of q = exp(x) / sum
+    const double a = TAIL ? t.A : t.A / t.sum - log(t.sum);
+    double l = a - (t.B - m * t.total) * inv_t + log_d * t.total;
+    double weight = t.total, w = t.total / d;
+    if constexpr (TAIL) {
+        w = 0.0;
+        if (d_o != 0.0) {  // there are other columns (or a NaN)
+            const double q_r = fmax(0.0, 1.0 - t.total);
+            weight = t.total + q_r;
+            if (q_r != 0.0)
+                l += q_r * (log(q_r) - (shift + log(d_o) - log_d));
+            w = weight * exp(shift) / d - q_r / d_o;
+        }
+    }
+    if (t.off || !(d > 0.0) || !(t.total < INFINITY))
+        l = w = weight = static_cast<double>(NAN);
+    // No other column above -inf: any finite shift gives them exp(-inf) w = 0.
+    const float other = m_o == -INFINITY ? m : m_o;
+    return {m, static_cast<float>(d), static_cast<float>(l), static_cast<float>(weight),
+            other, static_cast<float>(w), t.top, static_cast<float>(t.sum)};
+}
+
+// One workgroup of NW waves per (row, part of its segments of 2048 columns): {m, d}
+// of the part, with TAIL of the columns that are not on the row's list; with one part
+// per row also the loss and the record.  A row whose list is empty is not read.
+template <bool BF16, bool TAIL, int NW>
+__global__ __launch_bounds__(NW * 64) void distill_row_kernel(
+    const void *__restrict__ logits, int64_t ld, int64_t V, uint32_t parts, int32_t part_segs, ListArgs list,
+    const float *__restrict__ temperature, int64_t temperature_stride, float2 *__restrict__ rec,
+    float *__restrict__ loss, RowStats *__restrict__ stats)
 {
     constexpr int G = Segment<BF16>::G;
-    const int lane = threadIdx.x;
-    const uint32_t id = blockIdx.x, row = id / nseg;  // below 2^25
-    const int64_t j0 = static_cast<int64_t>(id - row * nseg) * kSegCols;
+    extern __shared__ uint32_t listed[];  // TAIL: a bit per column of the part
+    __shared__ ListShared sh;
+    __shared__ float red_m[NW], red_d[NW];
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const uint32_t id = blockIdx.x, row = id / parts;
+    const int32_t seg0 = static_cast<int32_t>(id - row * parts) * part_segs;
+    const int32_t seg1 = min(seg0 + part_segs, static_cast<int32_t>((V + kSegCols - 1) / kSegCols));
     const char *zr = static_cast<const char *>(logits) + static_cast<int64_t>(row) * ld * (16 / G);
-    Segment<BF16> sg;
-    sg.load(zr, V, j0, lane);
-    __shared__ uint32_t listed[TAIL ? kSegCols / 32 : 1];  // a bit per column
-    if constexpr (TAIL) {
-        listed[lane] = 0;
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-        for (int i = lane; i < list.k; i += 64) {
-            const int64_t at = static_cast<int64_t>(entry(list, row, i).token) - j0;
-            if (at >= 0 && at < kSegCols)
-                atomicOr(&listed[at >> 5], 1u << (at & 31));
+
+    Entry en = {-1, 0.0f};
+    if (tid < kMaxList)
+        en = entry(list, row, tid);
+    if (__syncthreads_count(en.token >= 0) == 0) {
+        if (tid == 0 && seg0 == 0) {
+            if (parts == 1) {
+                stats[row] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+                if (loss)
+                    loss[row] = 0.0f;
+            }
         }
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        return;  // the merge of several parts does not read their records either
     }
-    float v[32];
-    sg.values(v);
+    Segment<BF16> next;
+    int32_t seg = seg0 + wave;
+    next.load(zr, V, static_cast<int64_t>(seg) * kSegCols, lane);
+    const float inv_t = inverse_temperature(temperature, row * temperature_stride);
+    const float c = kLog2e * inv_t;
+    float z = -INFINITY;
+    if (parts == 1 && en.token >= 0 && en.token < V)
+        z = row_element<BF16>(zr, en.token);
+    if (tid < kMaxList)
+        sh.ids[tid] = en.token;
+    bool again = false;
     if constexpr (TAIL) {
-#pragma unroll
-        for (int u = 0; u < 32 / G; ++u) {
-            const int col = (64 * u + lane) * G;
-            const uint32_t bits = listed[col >> 5] >> (col & 31);
-#pragma unroll
-            for (int e = 0; e < G; ++e)
-                v[u * G + e] = (bits >> e) & 1u ? -INFINITY : v[u * G + e];
-        }
+        for (int i = tid; i < (seg1 - seg0) * (kSegCols / 32); i += NW * 64)
+            listed[i] = 0;
+        __syncthreads();
+        const int64_t at = en.token - static_cast<int64_t>(seg0) * kSegCols;
+        if (en.token >= 0 && at >= 0 && at < static_cast<int64_t>(seg1 - seg0) * kSegCols)
+            again = (atomicOr(&listed[at >> 5], 1u << (at & 31)) >> (at & 31)) & 1u;
+        __syncthreads();
     }
-    const float c = kLog2e * inverse_temperature(temperature, row * temperature_stride);
-    float lm = -INFINITY;
+    ListSums t;
+    double q;
+    if (parts == 1)
+        t = list_sums<TAIL>(sh, en, z, V, inv_t, list.k, again, tid, q);
+
+    float m = -INFINITY, d = 0.0f;  // the lane's, rescaled once per 32 values
+    for (int32_t r = seg0; r < seg1; r += NW, seg += NW) {
+        float v[32];
+        next.values(v);  // a segment past the row's end holds -inf only
+        if (r + NW < seg1)
+            next.load(zr, V, static_cast<int64_t>(seg + NW) * kSegCols, lane);
+        if constexpr (TAIL) {
+            if (seg < seg1) {
 #pragma unroll
-    for (int i = 0; i < 32; ++i)
-        lm = __builtin_elementwise_maximum(lm, v[i]);  // NaN stays NaN
-    const float m = wave_maximum(lm);
-    float d = 0.0f;
-    if (m != -INFINITY) {  // +inf or NaN make d NaN
+                for (int u = 0; u < 32 / G; ++u) {
+                    const int col = (seg - seg0) * kSegCols + (64 * u + lane) * G;
+                    const uint32_t bits = (listed[col >> 5] >> (col & 31)) & ((1u << G) - 1u);
+                    if (!__ballot(bits != 0))
+                        continue;
+#pragma unroll
+                    for (int e = 0; e < G; ++e)
+                        v[u * G + e] = (bits >> e) & 1u ? -INFINITY : v[u * G + e];
+                }
+            }
+        }
+        float lm = m;
 #pragma unroll
         for (int i = 0; i < 32; ++i)
-            d += __builtin_amdgcn_exp2f((v[i] - m) * c);
-        d = wave_sum(d);
+            lm = __builtin_elementwise_maximum(lm, v[i]);  // NaN stays NaN
+        const float ms = lm == -INFINITY ? 0.0f : lm;
+        d *= __builtin_amdgcn_exp2f((m - ms) * c);
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            d += __builtin_amdgcn_exp2f((v[i] - ms) * c);
+        m = lm;
     }
-    if (lane == 0)
-        rec[id] = make_float2(m, d);
+    {
+        const float mw = wave_maximum(m), ms = mw == -INFINITY ? 0.0f : mw;
+        d = wave_sum(d * __builtin_amdgcn_exp2f((m - ms) * c));
+        if (lane == 0) {
+            red_m[wave] = mw;
+            red_d[wave] = d;
+        }
+    }
+    __syncthreads();
+    if (tid != 0)
+        return;
+    float m_o = -INFINITY;
+    for (int w = 0; w < NW; ++w)
+        m_o = __builtin_elementwise_maximum(m_o, red_m[w]);
+    double d_o = 0.0;
+    for (int w = 0; w < NW; ++w)
+        if (red_d[w] != 0.0f)  // NaN too
+            d_o += static_cast<double>(red_d[w]) * __builtin_amdgcn_exp2f((red_m[w] - m_o) * c);
+    if (parts == 1) {
+        const RowStats st = finish_row<TAIL>(t, m_o, d_o, inv_t);
+        stats[row] = st;
+        if (loss)
+            loss[row] = st.loss;
+    } else {
+        rec[id] = make_float2(m_o, static_cast<float>(d_o));
+    }
 }
 
-__device__ __forceinline__ double block_sum(double v, double *red, int wave, int lane)
-{
-    v = wave_sum(v);
-    __syncthreads();
-    if (lane == 0)
-        red[wave] = v;
-    __syncthreads();
-    v = 0.0;
-    for (int w = 0; w < kListThreads / 64; ++w)
-        v += red[w];
-    return v;
-}
-
-// One workgroup per row, a thread per entry of its list: the row's sums from its
-// segments' records, the loss and what the gradient needs, in 64 bits.
+// Rows in several parts: one workgroup each, a thread per entry of its list.
+template <bool TAIL>
 __global__ __launch_bounds__(kListThreads) void distill_merge_kernel(
-    const char *__restrict__ logits, int64_t ld_bytes, int32_t bf16, int64_t V, int32_t nseg, ListArgs list,
+    const char *__restrict__ logits, int64_t ld_bytes, int32_t bf16, int64_t V, int32_t parts, ListArgs list,
     const float *__restrict__ temperature, int64_t temperature_stride, const float2 *__restrict__ rec,
     float *__restrict__ loss, RowStats *__restrict__ stats)
 {
-    __shared__ int32_t ids[kMaxList];
-    __shared__ double red[kListThreads / 64];
-    __shared__ float red_f[kListThreads / 64];
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    __shared__ ListShared sh;
+    const int tid = threadIdx.x, lane = tid & 63;
     const int64_t row = blockIdx.x;
     const Entry en = entry(list, row, tid);
     const float inv_t = inverse_temperature(temperature, row * temperature_stride);
     const char *zr = logits + row * ld_bytes;
-    const bool there = en.token >= 0;
-    const bool off = there && en.token >= V;
     float z = -INFINITY;
-    if (there && !off)
+    if (en.token >= 0 && en.token < V)
         z = bf16 ? row_element<true>(zr, en.token) : row_element<false>(zr, en.token);
-    ids[tid] = en.token;
-    const int n_there = __syncthreads_count(there);
-    const bool any_off = __syncthreads_or(off);
-    if (n_there == 0) {
+    sh.ids[tid] = en.token;
+    double q;
+    const ListSums t = list_sums<TAIL>(sh, en, z, V, inv_t, list.k, true, tid, q);
+    if (t.there == 0) {
         if (tid == 0) {
             stats[row] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
             if (loss)
@@ -167,81 +339,26 @@ __global__ __launch_bounds__(kListThreads) void distill_merge_kernel(
         }
         return;
     }
-    auto block_max = [&](float v) {
-        v = wave_maximum(v);
-        __syncthreads();
-        if (lane == 0)
-            red_f[wave] = v;
-        __syncthreads();
-        v = red_f[0];
-        for (int w = 1; w < kListThreads / 64; ++w)
-            v = __builtin_elementwise_maximum(v, red_f[w]);
-        return v;
-    };
-    // The student's sums over the scanned columns (all, or those off the list).
-    const float2 *r = rec + row * nseg;
+    if (tid >= 64)
+        return;
+    const float2 *r = rec + row * parts;
     float m_o = -INFINITY;
-    for (int i = tid; i < nseg; i += kListThreads)
+    for (int i = lane; i < parts; i += 64)
         m_o = __builtin_elementwise_maximum(m_o, r[i].x);
-    m_o = block_max(m_o);
+    m_o = wave_maximum(m_o);
     double d_o = 0.0;
-    for (int i = tid; i < nseg; i += kListThreads) {
-        const float2 q = r[i];
-        if (q.y != 0.0f)  // NaN too
-            d_o += static_cast<double>(q.y) * exp((static_cast<double>(q.x) - m_o) * inv_t);
+    for (int i = lane; i < parts; i += 64) {
+        const float2 p = r[i];
+        if (p.y != 0.0f)  // NaN too
+            d_o += static_cast<double>(p.y) * __builtin_amdgcn_exp2f((p.x - m_o) * (kLog2e * inv_t));
     }
-    d_o = block_sum(d_o, red, wave, lane);
-    float m = m_o;
-    double d = d_o;
-    if (list.tail) {
-        // The list's columns join, each once.
-        bool first = there && !off;
-        for (int i = 0; i < tid && first; ++i)
-            first = ids[i] != en.token;
-        m = __builtin_elementwise_maximum(m_o, block_max(z));
-        d = block_sum(first && z != -INFINITY ? exp((static_cast<double>(z) - m) * inv_t) : 0.0, red, wave, lane);
-        if (d_o != 0.0)
-            d += d_o * exp((static_cast<double>(m_o) - m) * inv_t);
-    }
-    // The teacher.
-    float top = 0.0f;
-    double log_q = -INFINITY, sum = 1.0;
-    if (list.tail) {
-        if (there)
-            log_q = en.value;
-    } else {
-        top = block_max(there ? en.value : -INFINITY);
-        const double x = there ? (static_cast<double>(en.value) - top) * inv_t : -static_cast<double>(INFINITY);
-        sum = block_sum(there ? exp(x) : 0.0, red, wave, lane);
-        log_q = x - log(sum);
-    }
-    const double q = there ? exp(log_q) : 0.0;
-    const double log_d = log(d);
-    const double log_p = (static_cast<double>(z) - m) * inv_t - log_d;
-    const double total = block_sum(q, red, wave, lane);
-    double l = block_sum(q != 0.0 ? q * (log_q - log_p) : 0.0, red, wave, lane);
+    d_o = wave_sum(d_o);
     if (tid != 0)
         return;
-    double weight = total, w = total / d;
-    if (list.tail) {
-        w = 0.0;
-        if (d_o != 0.0) {  // there are other columns (or a NaN)
-            const double shift = (static_cast<double>(m_o) - m) * inv_t;
-            const double q_r = total == total ? fmax(0.0, 1.0 - total) : total;
-            weight = total + q_r;
-            if (q_r != 0.0)
-                l += q_r * (log(q_r) - (shift + log(d_o) - log_d));
-            w = weight * exp(shift) / d - q_r / d_o;
-        }
-    }
-    if (any_off || !(d > 0.0) || !(total < INFINITY))
-        l = w = weight = static_cast<double>(NAN);
-    // No other column above -inf: any finite shift gives them exp(-inf) w = 0.
-    const float other = m_o == -INFINITY ? m : m_o;
-    stats[row] = {m, static_cast<float>(d), static_cast<float>(l), static_cast<float>(weight),
-                  other, static_cast<float>(w), top, static_cast<float>(sum)};
+    const RowStats st = finish_row<TAIL>(t, m_o, d_o, inv_t);
+    stats[row] = st;
     if (loss)
-        loss[row] = static_cast<float>(l);
+        loss[row] = st.loss;
 }
 
 // ------------------------------------------------------------------ gradient
@@ -335,11 +452,221 @@ __global__ __launch_bounds__(kBwdThreads) void distill_bwd_kernel(
     }
 }
 
+// ------------------------------------------- loss and gradient in one read
+
+// One workgroup per row, which sits in registers: VALS values per thread, V <= NT VALS.
+// The list's part is worked out while the row's loads are under way.  head[i] names
+// the first entry of the list (plus one) whose column lies in the row's vector i of
+// 16 bytes, next[] the others: so a thread finds the listed columns among its own, in
+// tail mode to leave them out of the sums, in the end to write their gradients in
+// their places.  Entries of the same token hold the same gradient, so that the order
+// in which they are found does not matter.
+template <bool ZBF16, bool GBF16, bool TAIL, int NT, int VALS>
+__global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(4))) void distill_fused_kernel(
+    const void *logits, int64_t ld, int64_t V, ListArgs list, const float *__restrict__ temperature,
+    int64_t temperature_stride, const float *__restrict__ dloss, int64_t dloss_stride, float *__restrict__ loss,
+    RowStats *__restrict__ stats, void *dlogits, int64_t ldg)
+{
+    constexpr int G = ZBF16 ? 8 : 4, PER = VALS / G, NW = NT / 64;
+    __shared__ uint32_t head[NT * PER + 1];
+    __shared__ uint32_t next[kMaxList];
+    __shared__ float grads[kMaxList];
+    __shared__ ListShared sh;
+    __shared__ float2 red[NW];
+    const int64_t row = blockIdx.x;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const char *zr = static_cast<const char *>(logits) + row * ld * (16 / G);
+    char *gr = static_cast<char *>(dlogits) + row * ldg * (GBF16 ? 2 : 4);
+    const int nv = static_cast<int>(V / G);  // whole vectors
+    const int jt = nv * G + tid;             // a column behind them, for tid < G
+    const bool has_tail = tid < G && jt < V;
+
+    Entry en = {-1, 0.0f};
+    if (tid < kMaxList)
+        en = entry(list, row, tid);
+    const float inv_t = inverse_temperature(temperature, row * temperature_stride);
+    const float up = dloss[row * dloss_stride] * inv_t, c = kLog2e * inv_t;
+    auto zero_row = [&]() {
+        const float o[G] = {};
+        for (int i = tid; i < nv; i += NT)
+            store_row<GBF16>(gr, i, o);
+        if (has_tail)
+            store_element<GBF16>(gr, jt, 0.0f);
+    };
+    if (__syncthreads_count(en.token >= 0) == 0) {
+        if (tid == 0) {
+            stats[row] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+            if (loss)
+                loss[row] = 0.0f;
+        }
+        zero_row();
+        return;
+    }
+
+    uint4 raw[PER];
+#pragma unroll
+    for (int p = 0; p < PER; ++p) {
+        const uint32_t none = ZBF16 ? 0xff80ff80u : 0xff800000u;
+        raw[p] = make_uint4(none, none, none, none);
+        if (p * NT + tid < nv)
+            raw[p] = load_row(zr, p * NT + tid);
+    }
+    float tv = has_tail ? row_element<ZBF16>(zr, jt) : -INFINITY;
+    const bool inside = en.token >= 0 && en.token < V;
+    const float z = inside ? row_element<ZBF16>(zr, en.token) : -INFINITY;
+    if (tid < kMaxList)
+        sh.ids[tid] = en.token;
+#pragma unroll
+    for (int p = 0; p < PER; ++p)
+        head[p * NT + tid] = 0;
+    if (tid == 0)
+        head[nv] = 0;  // the columns behind the last whole vector
+    __syncthreads();
+    const int vec = inside ? en.token / G : 0;
+    if (inside)
+        next[tid] = atomicExch(&head[vec], static_cast<uint32_t>(tid) + 1u);
+    __syncthreads();
+    auto listed_in = [&](int i, auto use) {  // use(column within the vector, entry)
+        for (uint32_t e = head[i]; e != 0; e = next[e - 1])
+            use(sh.ids[e - 1] - i * G, static_cast<int>(e) - 1);
+    };
+    bool again = false;
+    if (inside)
+        listed_in(vec, [&](int at, int e) { again = again || (at == en.token - vec * G && e != tid); });
+    double q;
+    const ListSums t = list_sums<TAIL>(sh, en, z, V, inv_t, list.k, again, tid, q);
+
+    float v[VALS];
+#pragma unroll
+    for (int p = 0; p < PER; ++p)
+#pragma unroll
+        for (int e = 0; e < G; ++e)
+            v[p * G + e] = row_value<ZBF16>(raw[p], e);
+    if constexpr (TAIL) {
+#pragma unroll
+        for (int p = 0; p < PER; ++p) {
+            if (p * NT + tid < nv)
+                listed_in(p * NT + tid, [&](int at, int) {
+#pragma unroll
+                    for (int e = 0; e < G; ++e)
+                        v[p * G + e] = at == e ? -INFINITY : v[p * G + e];
+                });
+        }
+        if (has_tail)
+            listed_in(nv, [&](int at, int) { tv = at == tid ? -INFINITY : tv; });
+    }
+    // The thread's own maximum and sum, then the row's; v becomes exp((v - m_t) / T).
+    float m_t = tv;
+#pragma unroll
+    for (int i = 0; i < VALS; ++i)
+        m_t = __builtin_elementwise_maximum(m_t, v[i]);
+    const float ms = m_t == -INFINITY ? 0.0f : m_t;
+    tv = __builtin_amdgcn_exp2f((tv - ms) * c);
+    float d = tv;
+#pragma unroll
+    for (int i = 0; i < VALS; ++i) {
+        v[i] = __builtin_amdgcn_exp2f((v[i] - ms) * c);
+        d += v[i];
+    }
+    float m_o = wave_maximum(m_t);
+    {
+        const float mw = m_o == -INFINITY ? 0.0f : m_o;
+        d = wave_sum(d * __builtin_amdgcn_exp2f((m_t - mw) * c));
+        if (lane == 0)
+            red[wave] = make_float2(m_o, d);
+    }
+    __syncthreads();
+    double d_o;
+    {
+        const float2 r = red[lane & (NW - 1)];
+        m_o = wave_maximum(r.x);
+        const float mw = m_o == -INFINITY ? 0.0f : m_o;
+        d_o = wave_sum(lane < NW ? static_cast<double>(r.y) * __builtin_amdgcn_exp2f((r.x - mw) * c) : 0.0);
+    }
+    // What the gradient needs, in FP32 by every thread: weight / d, and the factor w of
+    // exp((z - m_o) / T) off the list.
+    float m = m_o, wd, w;
+    {
+        const float df = static_cast<float>(d_o);
+        if constexpr (TAIL) {
+            m = __builtin_elementwise_maximum(m_o, t.m_l);
+            const float f = df != 0.0f ? __builtin_amdgcn_exp2f((m_o - m) * c) : 0.0f;
+            const float dl = static_cast<float>(t.D);
+            const float dw = (dl != 0.0f ? dl * __builtin_amdgcn_exp2f((t.m_l - m) * c) : 0.0f) + f * df;
+            const float q_r = df != 0.0f ? static_cast<float>(fmax(0.0, 1.0 - t.total)) : 0.0f;
+            wd = (static_cast<float>(t.total) + q_r) / dw;
+            w = df != 0.0f ? wd * f - q_r / df : 0.0f;
+            if (!(dw > 0.0f))
+                wd = w = __int_as_float(0x7fc00000);
+        } else {
+            wd = w = static_cast<float>(t.total) / df;
+            if (!(df > 0.0f))
+                wd = w = __int_as_float(0x7fc00000);
+        }
+        if (t.off || !(t.total < INFINITY))
+            wd = w = __int_as_float(0x7fc00000);
+    }
+    if (t.twice) {  // the shares of the same token, in the list's order
+        if (tid < kMaxList)
+            grads[tid] = static_cast<float>(q);
+        __syncthreads();
+        float sum = 0.0f;
+        for (int i = 0; inside && i < list.k; ++i)
+            sum += sh.ids[i] == en.token ? grads[i] : 0.0f;
+        q = sum;
+        __syncthreads();
+    }
+    if (tid < kMaxList)
+        grads[tid] = (__builtin_amdgcn_exp2f((z - m) * c) * wd - static_cast<float>(q)) * up;
+    __syncthreads();
+    if (up == 0.0f) {
+        zero_row();
+    } else {
+        const float scale = m_t == -INFINITY && w == w ? 0.0f : __builtin_amdgcn_exp2f((m_t - m_o) * c) * (w * up);
+#pragma unroll
+        for (int p = 0; p < PER; ++p) {
+            const int i = p * NT + tid;
+            if (i >= nv)
+                break;
+            float o[G];
+#pragma unroll
+            for (int e = 0; e < G; ++e)
+                o[e] = v[p * G + e] * scale;
+            listed_in(i, [&](int at, int l) {
+                const float g = grads[l];
+#pragma unroll
+                for (int e = 0; e < G; ++e)
+                    o[e] = at == e ? g : o[e];
+            });
+            store_row<GBF16>(gr, i, o);
+        }
+        if (has_tail) {
+            float o = tv * scale;
+            listed_in(nv, [&](int at, int l) { o = at == tid ? grads[l] : o; });
+            store_element<GBF16>(gr, jt, o);
+        }
+    }
+    if (tid == 0) {
+        const RowStats st = finish_row<TAIL>(t, m_o, d_o, inv_t);
+        stats[row] = st;
+        if (loss)
+            loss[row] = st.loss;
+    }
+}
+
+}  // namespace
+
+namespace {
+
+// A part's listed columns are bits in LDS.
+constexpr int64_t kMaxPartSegs = 128;
+
 }  // namespace
 
 int64_t distill_workspace_bytes(int64_t n_rows, int64_t V)
 {
-    return n_rows * row_segments(V) * static_cast<int64_t>(sizeof(float2));
+    const int64_t parts = row_plan(n_rows, V, kMaxPartSegs).parts;
+    return parts == 1 ? 0 : n_rows * parts * static_cast<int64_t>(sizeof(float2));
 }
 
 namespace {
@@ -354,30 +681,44 @@ ListArgs list_args(const Distill &p, int64_t r0)
 
 hipError_t launch_distill_fwd(const Distill &p, void *workspace, hipStream_t s)
 {
-    const int64_t nseg = row_segments(p.V), esz = p.bf16 ? 2 : 4;
-    const int64_t chunk = std::max<int64_t>(1, kMaxItems / kListThreads / nseg);
+    const RowPlan plan = row_plan(p.n, p.V, kMaxPartSegs);
+    const int64_t parts = plan.parts, esz = p.bf16 ? 2 : 4;
+    const int64_t chunk = std::max<int64_t>(1, kMaxItems / 1024 / parts);
     for (int64_t r0 = 0; r0 < p.n; r0 += chunk) {
         const int64_t nr = std::min(chunk, p.n - r0);
         const char *z = static_cast<const char *>(p.logits) + r0 * p.ld * esz;
         const float *temp = p.temperature ? p.temperature + r0 * p.temperature_stride : nullptr;
-        float2 *rec = static_cast<float2 *>(workspace) + r0 * nseg;
+        float2 *rec = static_cast<float2 *>(workspace) + r0 * parts;
+        float *loss = p.loss ? p.loss + r0 : nullptr;
+        RowStats *stats = reinterpret_cast<RowStats *>(p.stats) + r0;
         const ListArgs list = list_args(p, r0);
-        auto scan = [&](auto bf16, auto tail) {
-            hipLaunchKernelGGL((distill_scan_kernel<decltype(bf16)::value, decltype(tail)::value>),
-                               dim3(static_cast<unsigned>(nr * nseg)), dim3(64), 0, s, z, p.ld, p.V,
-                               static_cast<uint32_t>(nseg), list, temp, p.temperature_stride, rec);
+        const unsigned bits = p.tail ? static_cast<unsigned>(std::min<int64_t>(plan.part_segs, row_segments(p.V))) * (kSegCols / 8) : 0;
+        auto rows = [&](auto bf16, auto tail, auto waves) {
+            constexpr int NW = decltype(waves)::value;
+            hipLaunchKernelGGL((distill_row_kernel<decltype(bf16)::value, decltype(tail)::value, NW>),
+                               dim3(static_cast<unsigned>(nr * parts)), dim3(NW * 64), bits, s, z, p.ld, p.V,
+                               static_cast<uint32_t>(parts), plan.part_segs, list, temp, p.temperature_stride, rec,
+                               loss, stats);
         };
         const auto yes = std::true_type{};
         const auto no = std::false_type{};
-        auto with_tail = [&](auto bf16) { p.tail ? scan(bf16, yes) : scan(bf16, no); };
+        auto with_waves = [&](auto bf16, auto tail) {
+            plan.waves == 4 ? rows(bf16, tail, std::integral_constant<int, 4>{})
+                            : rows(bf16, tail, std::integral_constant<int, 16>{});
+        };
+        auto with_tail = [&](auto bf16) { p.tail ? with_waves(bf16, yes) : with_waves(bf16, no); };
         p.bf16 ? with_tail(yes) : with_tail(no);
         hipError_t e = hipGetLastError();
         if (e != hipSuccess)
             return e;
-        hipLaunchKernelGGL(distill_merge_kernel, dim3(static_cast<unsigned>(nr)), dim3(kListThreads), 0, s, z,
-                           p.ld * esz, p.bf16 ? 1 : 0, p.V, static_cast<int32_t>(nseg), list, temp,
-                           p.temperature_stride, rec, p.loss ? p.loss + r0 : nullptr,
-                           reinterpret_cast<RowStats *>(p.stats) + r0);
+        if (parts == 1)
+            continue;
+        auto merge = [&](auto tail) {
+            hipLaunchKernelGGL((distill_merge_kernel<decltype(tail)::value>), dim3(static_cast<unsigned>(nr)),
+                               dim3(kListThreads), 0, s, z, p.ld * esz, p.bf16 ? 1 : 0, p.V,
+                               static_cast<int32_t>(parts), list, temp, p.temperature_stride, rec, loss, stats);
+        };
+        p.tail ? merge(yes) : merge(no);
         e = hipGetLastError();
         if (e != hipSuccess)
             return e;
@@ -414,10 +755,49 @@ hipError_t launch_distill_bwd(const Distill &p, hipStream_t s)
     return hipSuccess;
 }
 
+// Rows of at most this many columns fit the registers of a workgroup; longer ones
+// are read twice, by the forward and by the gradient.
+constexpr int64_t kFusedMaxCols = 65536;
+
 hipError_t launch_distill_fused(const Distill &p, void *workspace, hipStream_t s)
 {
-    const hipError_t e = launch_distill_fwd(p, workspace, s);
-    return e == hipSuccess ? launch_distill_bwd(p, s) : e;
+    if (p.V > kFusedMaxCols) {
+        const hipError_t e = launch_distill_fwd(p, workspace, s);
+        return e == hipSuccess ? launch_distill_bwd(p, s) : e;
+    }
+    const int64_t zsz = p.bf16 ? 2 : 4, gsz = p.grad_bf16 ? 2 : 4;
+    const int64_t chunk = kMaxItems / 1024;
+    for (int64_t r0 = 0; r0 < p.n; r0 += chunk) {
+        const int64_t nr = std::min(chunk, p.n - r0);
+        auto go = [&](auto zb, auto gb, auto tail, auto threads, auto vals) {
+            constexpr int NT = decltype(threads)::value;
+            hipLaunchKernelGGL((distill_fused_kernel<decltype(zb)::value, decltype(gb)::value, decltype(tail)::value,
+                                                     NT, decltype(vals)::value>),
+                               dim3(static_cast<unsigned>(nr)), dim3(NT), 0, s,
+                               static_cast<const char *>(p.logits) + r0 * p.ld * zsz, p.ld, p.V, list_args(p, r0),
+                               p.temperature ? p.temperature + r0 * p.temperature_stride : nullptr,
+                               p.temperature_stride, p.dloss + r0 * p.dloss_stride, p.dloss_stride,
+                               p.loss ? p.loss + r0 : nullptr, reinterpret_cast<RowStats *>(p.stats) + r0,
+                               static_cast<char *>(p.dlogits) + r0 * p.ldg * gsz, p.ldg);
+        };
+        const auto yes = std::true_type{};
+        const auto no = std::false_type{};
+        auto with_size = [&](auto zb, auto gb, auto tail) {
+            if (p.V <= 512 * 32)
+                go(zb, gb, tail, std::integral_constant<int, 512>{}, std::integral_constant<int, 32>{});
+            else if (p.V <= 512 * 64)
+                go(zb, gb, tail, std::integral_constant<int, 512>{}, std::integral_constant<int, 64>{});
+            else
+                go(zb, gb, tail, std::integral_constant<int, 1024>{}, std::integral_constant<int, 64>{});
+        };
+        auto with_tail = [&](auto zb, auto gb) { p.tail ? with_size(zb, gb, yes) : with_size(zb, gb, no); };
+        auto with_grad = [&](auto zb) { p.grad_bf16 ? with_tail(zb, yes) : with_tail(zb, no); };
+        p.bf16 ? with_grad(yes) : with_grad(no);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess)
+            return e;
+    }
+    return hipSuccess;
 }
 
 }  // namespace lmh

@@ -660,32 +660,6 @@ __global__ __launch_bounds__(kBwdThreads) void logprobs_bwd_kernel(
 
 }  // namespace
 
-int64_t row_segments(int64_t V)
-{
-    return (V + kSegCols - 1) / kSegCols;
-}
-
-namespace {
-
-// How the rows are shared out: workgroups of 4 waves, a row each, where there are
-// rows enough for every CU; else of 16 waves, and few rows in parts.
-struct RowPlan {
-    int32_t waves, part_segs;
-    int64_t parts;
-};
-RowPlan row_plan(int64_t n_rows, int64_t V)
-{
-    const int64_t nseg = row_segments(V);
-    if (n_rows >= 512)
-        return {4, static_cast<int32_t>(nseg), 1};
-    const int64_t rounds = (nseg + 15) / 16;  // of a workgroup over the whole row
-    const int64_t want = std::max<int64_t>(1, 512 / std::max<int64_t>(n_rows, 1));
-    const int64_t per = (rounds + want - 1) / want;
-    return {16, static_cast<int32_t>(16 * per), (rounds + per - 1) / per};
-}
-
-}  // namespace
-
 int64_t logprobs_workspace_bytes(int64_t n_rows, int64_t V, int64_t k)
 {
     const int64_t parts = row_plan(n_rows, V).parts;

@@ -287,6 +287,21 @@ def test_empty_batch():
     assert g.shape == (0, 64)
 
 
+def test_a_row_of_its_own():
+    """One row needs no pitch: any vocabulary size, contiguous."""
+    for V in (1, 5, 50257):
+        for dtype in (F32, BF16):
+            z = torch.randn(1, V, device="cuda").to(dtype)
+            token = torch.tensor([V // 2], dtype=torch.int32, device="cuda")
+            got = lmh.lmhead_logprobs(z, token, n_top=min(V, 3))
+            _check_forward(z, token, None, min(V, 3), got)
+            g = torch.ones(1, device="cuda")
+            want, tol = ref.logprobs_grad(z, token, None, g, None)
+            ref.assert_grad(lmh.lmhead_logprobs_bwd(z, got[5], token, g), want, tol, V)
+            lmh.lmhead_logprobs_bwd(z, got[5], token, g, in_place=True)
+            ref.assert_within(z, want, tol + ref.HALF[dtype] * want.abs() * 1.01, "in place")
+
+
 def test_given_outputs_and_streams():
     z, gen = ref.random_logits(40, 5000, F32, 2)
     token = _tokens(40, 5000, gen)

@@ -121,25 +121,32 @@ def test_distill_refusals(L, name, order, base):
     for bad in only(dict(dt=FP16), dict(vt=FP16), dict(gt=FP16)):
         assert f(**bad) == DTYPE, bad
     for bad in only(dict(n=-1), dict(n=MAX), dict(V=0), dict(V=MAX), dict(k=-1), dict(k=257), dict(ld=96),
-                    dict(ldy=5), dict(ldv=5), dict(ldy=MAX), dict(ts=2), dict(gls=2), dict(ldg=96), dict(wsb=8),
+                    dict(ldy=5), dict(ldv=5), dict(ldy=MAX), dict(ts=2), dict(gls=2), dict(ldg=96),
                     dict(wsb=-1)):
         assert f(**bad) == SHAPE, bad
-    for bad in only(dict(z=None), dict(y=None), dict(v=None), dict(st=None), dict(ws=None), dict(g=None),
+    for bad in only(dict(z=None), dict(y=None), dict(v=None), dict(st=None), dict(g=None),
                     dict(gl=None)):
         assert f(**bad) == NULL, bad
     for bad in only(dict(z=Z + 4), dict(ld=102), dict(y=Y + 2), dict(v=TV + 1), dict(v=TV + 2, vt=FP32),
-                    dict(t=T + 2), dict(st=ST + 8), dict(ws=WS + 4), dict(loss=LP + 1), dict(gl=GL + 2),
+                    dict(t=T + 2), dict(st=ST + 8), dict(loss=LP + 1), dict(gl=GL + 2),
                     dict(g=G + 4), dict(ldg=102), dict(gt=BF16, ldg=108)):
         assert f(**bad) == ALIGN, bad
     out = "g" if "g" in order else "st"
-    for bad in only({out: Y}, {out: TV}, {out: T}, {out: Z + 16}, dict(loss=ST + 4), dict(ws=Z), dict(st=WS),
-                    dict(loss=Y + 4), dict(g=GL), dict(g=Z, gt=BF16), dict(g=Z, ldg=108), dict(st=G), dict(ws=G),
-                    dict(st=TV), dict(ws=Y)):
+    for bad in only({out: Y}, {out: TV}, {out: T}, {out: Z + 16}, dict(loss=ST + 4),
+                    dict(loss=Y + 4), dict(g=GL), dict(g=Z, gt=BF16), dict(g=Z, ldg=108), dict(st=G),
+                    dict(st=TV)):
         if name == "lmhead_distill_bwd" and "st" in bad and bad["st"] != G:
             continue  # an input there
         if G in bad.values() and "g" not in order:
             continue
         assert f(**bad) == ALIAS, bad
+    if "ws" in order:  # the workspace of a few long rows
+        need = L.lmhead_distill_workspace_bytes(2, 200000)
+        far = dict(n=2, V=200000, ld=200000, **({"ldg": 200000} if "ldg" in order else {}))
+        assert need > 0 and L.lmhead_distill_workspace_bytes(10, 100) == 0
+        assert f(**far, wsb=need - 1) == SHAPE and f(**far, ws=None) == NULL and f(**far, ws=WS + 8) == ALIGN
+        for at in [Z, ST, Y, TV - 16] + ([G] if "g" in order else []):
+            assert f(**far, ws=at) == ALIAS, at
     empty = {k: None for k in ("z", "y", "v", "st", "ws", "g", "gl") if k in order}
     assert f(n=0, **empty) == OK
 
