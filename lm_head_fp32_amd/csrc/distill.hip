@@ -228,7 +228,7 @@ __global__ __launch_bounds__(NW * 64) void distill_row_kernel(
         }
         return;  // the merge of several parts does not read their records either
     }
-    Segment<BF16> next;
+    Segment<BF16, true> next;
     int32_t seg = seg0 + wave;
     next.load(zr, V, static_cast<int64_t>(seg) * kSegCols, lane);
     const float inv_t = inverse_temperature(temperature, row * temperature_stride);

@@ -228,10 +228,10 @@ __device__ __forceinline__ void write_row(const RowSums &q, float log_d, float i
 // Alternatives: slot[l] is the largest value that lane l of any wave has seen (for
 // larger k two slots, for the halves of its values), so the k-th largest of the
 // slots is a lower bound of the k-th largest value (k different values reach it),
-// whatever the waves have read so far.  It is taken anew
-// for every round of NW segments, still in registers; the few values that reach it
-// are kept per wave, and at the end those that reach the last bound are ranked by
-// counting.
+// whatever the waves have read so far.  It is taken in the first, second, fourth, ...
+// round of NW segments, still in registers (every round: 39 instead of 36 us for 777
+// rows of 50001); the few values that reach it are kept per wave, and at the end those
+// that reach the last bound are ranked by counting.
 template <bool BF16, bool TOP, bool RANK, int NW>
 __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(4))) void logprobs_row_kernel(
     const void *__restrict__ logits, int64_t ld, int64_t V, uint32_t parts, int32_t part_segs,
@@ -254,7 +254,7 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(4))) vo
     const int32_t seg1 = min(seg0 + part_segs, static_cast<int32_t>((V + kSegCols - 1) / kSegCols));
     const char *zr = static_cast<const char *>(logits) + static_cast<int64_t>(row) * ld * (16 / G);
 
-    Segment<BF16> next;
+    Segment<BF16, true> next;
     int32_t seg = seg0 + wave;
     next.load(zr, V, static_cast<int64_t>(seg) * kSegCols, lane);
     const float inv_t = inverse_temperature(temperature, row * temperature_stride);
@@ -327,11 +327,15 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(4))) vo
             }
         }
         if constexpr (TOP) {
-            __syncthreads();
+            const int32_t round = (r - seg0) / NW;
+            if (round == 0)
+                __syncthreads();  // every wave's slots
             if (__ballot(lm >= bound)) {
-                const uint32_t t = max(slots_bound(slot, lane, k), order_key(-INFINITY) + 1u);
-                least = max(least, static_cast<uint64_t>(t) << 32);
-                bound = key_value(static_cast<uint32_t>(least >> 32));
+                if ((round & (round + 1)) == 0) {
+                    const uint32_t t = max(slots_bound(slot, lane, k), order_key(-INFINITY) + 1u);
+                    least = max(least, static_cast<uint64_t>(t) << 32);
+                    bound = key_value(static_cast<uint32_t>(least >> 32));
+                }
                 const int n_before = n_kept;
                 const uint32_t rest = 0xffffffffu - (static_cast<uint32_t>(seg) * kSegCols + static_cast<uint32_t>(lane * G));
 #pragma unroll

@@ -110,12 +110,25 @@ __device__ __forceinline__ float wave_sum(float d)
     return d + __shfl_xor(d, 32, 64);
 }
 
+// The 16 bytes at vector i of a row that is streamed once, as G values (4 FP32 or
+// 8 BF16).
+__device__ __forceinline__ uint4 load_row(const char *row, int64_t i)
+{
+    const u32x4_nt w = __builtin_nontemporal_load(reinterpret_cast<const u32x4_nt *>(row) + i);
+    return make_uint4(w.x, w.y, w.z, w.w);
+}
+
 // A segment of a row on its way from memory: lane l holds columns
 // j0 + (64 u + l) G + e, G per 16-byte load; columns at or past V read as -inf.
-template <bool BF16>
+// STREAM: the loads are non-temporal (rows that are read once).
+template <bool BF16, bool STREAM = false>
 struct Segment {
     static constexpr int G = BF16 ? 8 : 4, NQ = 32 / G;
     uint4 q[NQ];
+    static __device__ __forceinline__ uint4 load16(const char *p)
+    {
+        return STREAM ? load_row(p, 0) : *reinterpret_cast<const uint4 *>(p);
+    }
     __device__ __forceinline__ void load(const void *row, int64_t V, int64_t j0, int lane)
     {
         const char *base = static_cast<const char *>(row) + j0 * (16 / G);
@@ -123,7 +136,7 @@ struct Segment {
         if (j0 + kSegCols <= V) {
 #pragma unroll
             for (int u = 0; u < NQ; ++u)
-                q[u] = *reinterpret_cast<const uint4 *>(base + at + 1024 * u);
+                q[u] = load16(base + at + 1024 * u);
             return;
         }
         const uint32_t none = BF16 ? 0xff80ff80u : 0xff800000u;
@@ -132,7 +145,7 @@ struct Segment {
         for (int u = 0; u < NQ; ++u) {
             q[u] = make_uint4(none, none, none, none);
             if (64 * u + lane < whole)
-                q[u] = *reinterpret_cast<const uint4 *>(base + at + 1024 * u);
+                q[u] = load16(base + at + 1024 * u);
         }
         if (whole * G < cols) {  // the one vector that the row's end lies in
             uint32_t w[4];
@@ -171,13 +184,6 @@ struct Segment {
     }
 };
 
-// The 16 bytes at vector i of a row that is streamed once, as G values (4 FP32 or
-// 8 BF16).
-__device__ __forceinline__ uint4 load_row(const char *row, int64_t i)
-{
-    const u32x4_nt w = __builtin_nontemporal_load(reinterpret_cast<const u32x4_nt *>(row) + i);
-    return make_uint4(w.x, w.y, w.z, w.w);
-}
 template <bool BF16>
 __device__ __forceinline__ float row_value(const uint4 &q, int e)
 {
