@@ -160,33 +160,47 @@ __device__ __forceinline__ ListSums list_sums(ListShared &sh, const Entry &en, f
     return r;
 }
 
-// The row's numbers from the list's and the scanned columns' (m_o, d_o: all columns,
-// or with TAIL those off the list); by one thread.
-template <bool TAIL>
-__device__ __forceinline__ RowStats finish_row(const ListSums &t, float m_o, double d_o, float inv_t)
+__device__ __forceinline__ double lane_value(double v, int lane)
 {
+    const uint64_t u = __double_as_longlong(v);
+    const uint32_t lo = __builtin_amdgcn_readlane(static_cast<uint32_t>(u), lane);
+    const uint32_t hi = __builtin_amdgcn_readlane(static_cast<uint32_t>(u >> 32), lane);
+    return __longlong_as_double((static_cast<uint64_t>(hi) << 32) | lo);
+}
+
+// The row's numbers from the list's and the scanned columns' (m_o, d_o: all columns,
+// or with TAIL those off the list); by a whole wave, every lane with the same
+// arguments and the same result.  The two exponentials, the three logarithms and the
+// three quotients are taken side by side, a lane each.
+template <bool TAIL>
+__device__ __forceinline__ RowStats finish_row(const ListSums &t, float m_o, double d_o, float inv_t, int lane)
+{
+    const double none = -static_cast<double>(INFINITY);
     float m = m_o;
-    double d = d_o, shift = 0.0;
+    double d = d_o, shift = 0.0, scale = 1.0, q_r = 0.0;
     if constexpr (TAIL) {
         m = __builtin_elementwise_maximum(m_o, t.m_l);
         shift = (static_cast<double>(m_o) - m) * inv_t;
-        d = (t.D != 0.0 ? t.D * exp((static_cast<double>(t.m_l) - m) * inv_t) : 0.0) +
-            (d_o != 0.0 ? d_o * exp(shift) : 0.0);
+        const double x = lane == 0 ? (d_o != 0.0 ? shift : none)
+                                   : (t.D != 0.0 ? (static_cast<double>(t.m_l) - m) * inv_t : none);
+        const double f = exp(x);
+        scale = lane_value(f, 0);
+        d = (d_o != 0.0 ? d_o * scale : 0.0) + (t.D != 0.0 ? t.D * lane_value(f, 1) : 0.0);
+        q_r = d_o != 0.0 ? fmax(0.0, 1.0 - t.total) : 0.0;  // no other column: that class is left out
     }
-    const double log_d = log(d);
+    const double logs = log(lane == 0 ? d : lane == 1 ? (TAIL ? d_o : t.sum) : (q_r != 0.0 ? q_r : 1.0));
+    const double log_d = lane_value(logs, 0), log_2 = lane_value(logs, 1), log_qr = lane_value(logs, 2);
+    const double weight0 = t.total + q_r;
+    const double quot = (lane == 0 ? weight0 : lane == 1 ? q_r : t.A) / (lane == 0 ? d : lane == 1 ? d_o : t.sum);
+    const double per_d = lane_value(quot, 0);
     // sum q log q: in logits mode of q = exp(x) / sum
-    const double a = TAIL ? t.A : t.A / t.sum - log(t.sum);
+    const double a = TAIL ? t.A : lane_value(quot, 2) - log_2;
     double l = a - (t.B - m * t.total) * inv_t + log_d * t.total;
-    double weight = t.total, w = t.total / d;
+    double weight = weight0, w = per_d;
     if constexpr (TAIL) {
-        w = 0.0;
-        if (d_o != 0.0) {  // there are other columns (or a NaN)
-            const double q_r = fmax(0.0, 1.0 - t.total);
-            weight = t.total + q_r;
-            if (q_r != 0.0)
-                l += q_r * (log(q_r) - (shift + log(d_o) - log_d));
-            w = weight * exp(shift) / d - q_r / d_o;
-        }
+        if (q_r != 0.0)
+            l += q_r * (log_qr - (shift + log_2 - log_d));
+        w = d_o != 0.0 ? per_d * scale - (q_r != 0.0 ? lane_value(quot, 1) : 0.0) : 0.0;
     }
     if (t.off || !(d > 0.0) || !(t.total < INFINITY))
         l = w = weight = static_cast<double>(NAN);
@@ -198,7 +212,8 @@ __device__ __forceinline__ RowStats finish_row(const ListSums &t, float m_o, dou
 
 // One workgroup of NW waves per (row, part of its segments of 2048 columns): {m, d}
 // of the part, with TAIL of the columns that are not on the row's list; with one part
-// per row also the loss and the record.  A row whose list is empty is not read.
+// per row also the loss and the record.  Of a row whose list is empty the first round of
+// segments is read at most.
 template <bool BF16, bool TAIL, int NW>
 __global__ __launch_bounds__(NW * 64) void distill_row_kernel(
     const void *__restrict__ logits, int64_t ld, int64_t V, uint32_t parts, int32_t part_segs, ListArgs list,
@@ -218,19 +233,18 @@ __global__ __launch_bounds__(NW * 64) void distill_row_kernel(
     Entry en = {-1, 0.0f};
     if (tid < kMaxList)
         en = entry(list, row, tid);
-    if (__syncthreads_count(en.token >= 0) == 0) {
-        if (tid == 0 && seg0 == 0) {
-            if (parts == 1) {
-                stats[row] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-                if (loss)
-                    loss[row] = 0.0f;
-            }
-        }
-        return;  // the merge of several parts does not read their records either
-    }
+    // The first round's loads do not wait for the list.
     Segment<BF16, true> next;
     int32_t seg = seg0 + wave;
     next.load(zr, V, static_cast<int64_t>(seg) * kSegCols, lane);
+    if (__syncthreads_count(en.token >= 0) == 0) {
+        if (tid == 0 && parts == 1) {
+            stats[row] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+            if (loss)
+                loss[row] = 0.0f;
+        }
+        return;  // the merge of several parts does not read their records either
+    }
     const float inv_t = inverse_temperature(temperature, row * temperature_stride);
     const float c = kLog2e * inv_t;
     float z = -INFINITY;
@@ -293,21 +307,19 @@ __global__ __launch_bounds__(NW * 64) void distill_row_kernel(
         }
     }
     __syncthreads();
-    if (tid != 0)
+    if (wave != 0)
         return;
-    float m_o = -INFINITY;
-    for (int w = 0; w < NW; ++w)
-        m_o = __builtin_elementwise_maximum(m_o, red_m[w]);
-    double d_o = 0.0;
-    for (int w = 0; w < NW; ++w)
-        if (red_d[w] != 0.0f)  // NaN too
-            d_o += static_cast<double>(red_d[w]) * __builtin_amdgcn_exp2f((red_m[w] - m_o) * c);
+    const float rm = lane < NW ? red_m[lane] : -INFINITY, rd = lane < NW ? red_d[lane] : 0.0f;
+    const float m_o = wave_maximum(rm);
+    const double d_o = wave_sum(rd != 0.0f ? static_cast<double>(rd) * __builtin_amdgcn_exp2f((rm - m_o) * c) : 0.0);
     if (parts == 1) {
-        const RowStats st = finish_row<TAIL>(t, m_o, d_o, inv_t);
-        stats[row] = st;
-        if (loss)
-            loss[row] = st.loss;
-    } else {
+        const RowStats st = finish_row<TAIL>(t, m_o, d_o, inv_t, lane);
+        if (lane == 0) {
+            stats[row] = st;
+            if (loss)
+                loss[row] = st.loss;
+        }
+    } else if (lane == 0) {
         rec[id] = make_float2(m_o, static_cast<float>(d_o));
     }
 }
@@ -352,13 +364,12 @@ __global__ __launch_bounds__(kListThreads) void distill_merge_kernel(
         if (p.y != 0.0f)  // NaN too
             d_o += static_cast<double>(p.y) * __builtin_amdgcn_exp2f((p.x - m_o) * (kLog2e * inv_t));
     }
-    d_o = wave_sum(d_o);
-    if (tid != 0)
-        return;
-    const RowStats st = finish_row<TAIL>(t, m_o, d_o, inv_t);
-    stats[row] = st;
-    if (loss)
-        loss[row] = st.loss;
+    const RowStats st = finish_row<TAIL>(t, m_o, wave_sum(d_o), inv_t, lane);
+    if (lane == 0) {
+        stats[row] = st;
+        if (loss)
+            loss[row] = st.loss;
+    }
 }
 
 // ------------------------------------------------------------------ gradient
@@ -646,11 +657,13 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(4))) void di
             store_element<GBF16>(gr, jt, o);
         }
     }
-    if (tid == 0) {
-        const RowStats st = finish_row<TAIL>(t, m_o, d_o, inv_t);
-        stats[row] = st;
-        if (loss)
-            loss[row] = st.loss;
+    if (wave == 0) {
+        const RowStats st = finish_row<TAIL>(t, m_o, d_o, inv_t, lane);
+        if (lane == 0) {
+            stats[row] = st;
+            if (loss)
+                loss[row] = st.loss;
+        }
     }
 }
 
@@ -703,8 +716,12 @@ hipError_t launch_distill_fwd(const Distill &p, void *workspace, hipStream_t s)
         const auto yes = std::true_type{};
         const auto no = std::false_type{};
         auto with_waves = [&](auto bf16, auto tail) {
-            plan.waves == 4 ? rows(bf16, tail, std::integral_constant<int, 4>{})
-                            : rows(bf16, tail, std::integral_constant<int, 16>{});
+            if (plan.waves == 4)
+                rows(bf16, tail, std::integral_constant<int, 4>{});
+            else if (plan.waves == 8)
+                rows(bf16, tail, std::integral_constant<int, 8>{});
+            else
+                rows(bf16, tail, std::integral_constant<int, 16>{});
         };
         auto with_tail = [&](auto bf16) { p.tail ? with_waves(bf16, yes) : with_waves(bf16, no); };
         p.bf16 ? with_tail(yes) : with_tail(no);

@@ -271,6 +271,8 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(4))) vo
     if constexpr (TOP) {
         if (tid < 128)
             slot[tid] = 0;
+        for (int i = tid; i < kListCap; i += NW * 64)
+            cand[i] = 0;
         if (tid == 0)
             cand_n = 0;
         __syncthreads();
@@ -376,8 +378,10 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(4))) vo
     }
     __syncthreads();
     if constexpr (TOP) {
-        // What reaches the last bound (no slot changes any more).
-        least = max(least, static_cast<uint64_t>(slots_bound(slot, lane, k)) << 32);
+        // What reaches the last bound: no slot changes any more, and none has since the
+        // first round if it is the only one.
+        if (seg1 - seg0 > NW)
+            least = max(least, static_cast<uint64_t>(slots_bound(slot, lane, k)) << 32);
         for (int i = lane; i < n_kept; i += 64) {
             const uint64_t key = mine[i];
             if (key >= least) {
@@ -427,8 +431,10 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(4))) vo
             for (int i = tid; i < n; i += NW * 64) {
                 const uint64_t key = cand[i];
                 int rank = 0;
-                for (int q = 0; q < n; ++q)
-                    rank += cand[q] > key;
+                for (int q = 0; q < n; q += 8)  // zeros behind the n-th
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        rank += cand[q + j] > key;
                 if (rank < k)
                     put(rank, key);
             }
@@ -699,8 +705,12 @@ hipError_t launch_logprobs(const Logprobs &p, void *workspace, hipStream_t s)
         const auto yes = std::true_type{};
         const auto no = std::false_type{};
         auto with_waves = [&](auto bf16, auto top, auto rank) {
-            plan.waves == 4 ? rows(bf16, top, rank, std::integral_constant<int, 4>{})
-                            : rows(bf16, top, rank, std::integral_constant<int, 16>{});
+            if (plan.waves == 4)
+                rows(bf16, top, rank, std::integral_constant<int, 4>{});
+            else if (plan.waves == 8)
+                rows(bf16, top, rank, std::integral_constant<int, 8>{});
+            else
+                rows(bf16, top, rank, std::integral_constant<int, 16>{});
         };
         auto with_rank = [&](auto bf16, auto top) { p.rank ? with_waves(bf16, top, yes) : with_waves(bf16, top, no); };
         auto with_top = [&](auto bf16) { k ? with_rank(bf16, yes) : with_rank(bf16, no); };

@@ -17,9 +17,10 @@ inline int64_t row_segments(int64_t V)
     return (V + kSegCols - 1) / kSegCols;
 }
 
-// How the rows of a forward are shared out: workgroups of 4 waves, a row each, where
-// there are rows enough for every CU; else of 16 waves, and few rows in parts.  A
-// part has at most max_segs segments (a multiple of 16).
+// How the rows of a forward are shared out: a workgroup of 4 waves per row where
+// there are rows enough for every CU, of 8 or 16 where there are fewer (no more than
+// the row has segments), and fewer than 256 rows in parts, one round of segments at
+// least each.  A part has at most max_segs segments (a multiple of 16).
 struct RowPlan {
     int32_t waves, part_segs;
     int64_t parts;
@@ -27,14 +28,12 @@ struct RowPlan {
 inline RowPlan row_plan(int64_t n_rows, int64_t V, int64_t max_segs = int64_t{1} << 30)
 {
     const int64_t nseg = row_segments(V);
-    if (n_rows >= 512) {
-        const int64_t per = std::min(nseg, max_segs);
-        return {4, static_cast<int32_t>(per), (nseg + per - 1) / per};
-    }
-    const int64_t rounds = (nseg + 15) / 16;  // of a workgroup over the whole row
-    const int64_t want = std::max<int64_t>(1, 512 / std::max<int64_t>(n_rows, 1));
-    const int64_t per = std::min((rounds + want - 1) / want, max_segs / 16);
-    return {16, static_cast<int32_t>(16 * per), (rounds + per - 1) / per};
+    const int32_t most = nseg <= 4 ? 4 : nseg <= 8 ? 8 : 16;
+    const int32_t waves = std::min<int32_t>(most, n_rows >= 512 ? 4 : n_rows > 256 ? 8 : 16);
+    const int64_t rounds = (nseg + waves - 1) / waves;  // of a workgroup over the whole row
+    const int64_t want = std::max<int64_t>(1, 256 / std::max<int64_t>(n_rows, 1));
+    const int64_t per = std::min((rounds + want - 1) / want, max_segs / waves);
+    return {waves, static_cast<int32_t>(waves * per), (rounds + per - 1) / per};
 }
 
 // FP32 -> uint32 with the same order (-0 and +0 equal); 0 lies below -inf.
