@@ -960,10 +960,14 @@ def _per_row(t, name, n):
     (one per row); (None, 0) of None."""
     if t is None:
         return None, 0
+    if (isinstance(t, torch.Tensor) and t.dtype is torch.float32 and t.is_cuda and t.is_contiguous()
+            and t.get_device() == _current()):
+        if t.numel() == 1:
+            return t.data_ptr(), 0
+        if t.numel() == n:
+            return t.data_ptr(), 1
     if not isinstance(t, torch.Tensor) or t.dtype != torch.float32:
         raise TypeError(f"{name}: expected a GPU float32 tensor of 1 or {n} elements")
-    if t.numel() == 1:
-        return _vec(t, name, torch.float32, 1), 0
     return _vec(t, name, torch.float32, n), 1
 
 
@@ -985,14 +989,18 @@ def _row_out(t, name, dtype, shape, like):
 
 
 def _row_grad(fn, logits, dlogits, grad_dtype, in_place):
-    """(tensor, pointer, ld, dtype code) of the gradient of logits [n, V]."""
+    """(tensor, pointer, ld, dtype code) of the gradient of logits [n, V]; a new
+    one's rows start at multiples of 16 bytes."""
     code = _out_code(fn, logits if in_place else dlogits, grad_dtype, "fp32")
     if in_place:
         dlogits = logits
     elif dlogits is None:
         if code not in (LMH_BF16, LMH_FP32):
             _check(fn, 1)
-        dlogits = _empty_rows(*logits.shape, _TORCH_DT[code], logits)
+        n, V = logits.shape
+        ld = (V + 7) // 8 * 8
+        dlogits = torch.empty_strided((n, V), (ld, 1), dtype=_TORCH_DT[code], device=logits.device)
+        return dlogits, dlogits.data_ptr(), ld, code
     pg, ldg = _rows(dlogits, "dlogits", dlogits.dtype)
     if dlogits.shape != logits.shape:
         raise ValueError("dlogits must be [n, V]")
@@ -1036,14 +1044,30 @@ def lmhead_logprobs(logits, token=None, ignore_index=-100, temperature=None, n_t
         py = _vec(token, "token", torch.int32, n)
     pt, st = _per_row(temperature, "temperature", n)
     need = lmhead_logprobs_workspace_bytes(n, V, k)
-    logprob, po = _row_out(logprob, "logprob", torch.float32, (n,), logits)
-    entropy, pe = _row_out(entropy, "entropy", torch.float32, (n,), logits)
-    rank, pr = _row_out(rank, "rank", torch.int32, (n,), logits)
-    top_logprob, pa = _row_out(top_logprob if k else False, "top_logprob", torch.float32, (n, k), logits)
-    top_token, pb = _row_out(top_token if k else False, "top_token", torch.int32, (n, k), logits)
-    if k and (top_logprob is None or top_token is None):
-        raise ValueError("the alternatives are not wanted: n_top = 0")
-    stats, ps = _row_out(stats, "stats", torch.float32, (n, STATS_COLS), logits)
+    if (logprob is None and entropy is None and rank is None and stats is None and top_logprob is None
+            and top_token is None):
+        # one allocation for all results (17 -> 14 us of host time for a call with alternatives)
+        buf = torch.empty_strided((n * (STATS_COLS + 3 + 2 * k),), (1,), dtype=torch.float32, device=logits.device)
+        stats, logprob, entropy, rank, top_logprob, top_token = buf.split_with_sizes(
+            (STATS_COLS * n, n, n, n, n * k, n * k))
+        stats, rank = stats.view(n, STATS_COLS), rank.view(torch.int32)
+        ps = buf.data_ptr()
+        po = ps + 16 * n
+        pe, pr, pa = po + 4 * n, po + 8 * n, po + 12 * n
+        pb = pa + 4 * n * k
+        if k:
+            top_logprob, top_token = top_logprob.view(n, k), top_token.view(torch.int32).view(n, k)
+        else:
+            top_logprob = top_token = pa = pb = None
+    else:
+        logprob, po = _row_out(logprob, "logprob", torch.float32, (n,), logits)
+        entropy, pe = _row_out(entropy, "entropy", torch.float32, (n,), logits)
+        rank, pr = _row_out(rank, "rank", torch.int32, (n,), logits)
+        top_logprob, pa = _row_out(top_logprob if k else False, "top_logprob", torch.float32, (n, k), logits)
+        top_token, pb = _row_out(top_token if k else False, "top_token", torch.int32, (n, k), logits)
+        if k and (top_logprob is None or top_token is None):
+            raise ValueError("the alternatives are not wanted: n_top = 0")
+        stats, ps = _row_out(stats, "stats", torch.float32, (n, STATS_COLS), logits)
     ws, pw, nbytes = _row_workspace(need, workspace, logits)
     _check("lmhead_logprobs",
            lib().lmhead_logprobs(pz, ld, code, n, V, py, int(ignore_index), pt, st, k, po, pe, pr, pa, pb, ps,
@@ -1092,8 +1116,8 @@ def _teacher_list(token, value, n):
     lists [n, k]: rows may be padded, elements of a row are contiguous."""
     if not isinstance(value, torch.Tensor) or value.dtype not in (torch.float32, torch.bfloat16):
         raise TypeError("teacher_value: expected a GPU float32 or bfloat16 tensor")
-    pt, ldt = _mat(token, "teacher_token", torch.int32)
-    pv, ldv = _mat(value, "teacher_value", value.dtype)
+    pt, ldt = _rows(token, "teacher_token", torch.int32)
+    pv, ldv = _rows(value, "teacher_value", value.dtype)
     if token.shape != value.shape or token.shape[0] != n:
         raise ValueError("teacher_token and teacher_value must be [n, k]")
     return pt, ldt, pv, ldv, _DT[value.dtype], token.shape[1]
