@@ -292,10 +292,11 @@ __global__ __launch_bounds__(NW * 64) void distill_row_kernel(
         for (int i = 0; i < 32; ++i)
             lm = __builtin_elementwise_maximum(lm, v[i]);  // NaN stays NaN
         const float ms = lm == -INFINITY ? 0.0f : lm;
-        d *= __builtin_amdgcn_exp2f((m - ms) * c);
+        float dn[2] = {0.0f, 0.0f};
 #pragma unroll
         for (int i = 0; i < 32; ++i)
-            d += __builtin_amdgcn_exp2f((v[i] - ms) * c);
+            dn[i & 1] += __builtin_amdgcn_exp2f((v[i] - ms) * c);
+        d = fmaf(d, __builtin_amdgcn_exp2f((m - ms) * c), dn[0] + dn[1]);
         m = lm;
     }
     {
@@ -573,12 +574,13 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(4))) void di
         m_t = __builtin_elementwise_maximum(m_t, v[i]);
     const float ms = m_t == -INFINITY ? 0.0f : m_t;
     tv = __builtin_amdgcn_exp2f((tv - ms) * c);
-    float d = tv;
+    float dn[4] = {tv, 0.0f, 0.0f, 0.0f};  // short chains of additions
 #pragma unroll
     for (int i = 0; i < VALS; ++i) {
         v[i] = __builtin_amdgcn_exp2f((v[i] - ms) * c);
-        d += v[i];
+        dn[i & 3] += v[i];
     }
+    float d = (dn[0] + dn[1]) + (dn[2] + dn[3]);
     float m_o = wave_maximum(m_t);
     {
         const float mw = m_o == -INFINITY ? 0.0f : m_o;

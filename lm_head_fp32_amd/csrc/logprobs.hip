@@ -46,17 +46,17 @@ struct LaneSums {
         const float ms = mn == -INFINITY ? 0.0f : mn;
         const float dy = __builtin_elementwise_maximum((m - ms) * c, kNoTerm);
         const float f = __builtin_amdgcn_exp2f(dy);
-        float d0 = d * f, s0 = f * fmaf(dy, d, s);
+        float dn[2] = {0.0f, 0.0f}, sn[2] = {0.0f, 0.0f};  // two chains each
 #pragma unroll
         for (int i = 0; i < 32; ++i) {
             const float y = __builtin_elementwise_maximum((v[i] - ms) * c, kNoTerm);
             const float e = __builtin_amdgcn_exp2f(y);
-            d0 += e;
-            s0 = fmaf(e, y, s0);
+            dn[i & 1] += e;
+            sn[i & 1] = fmaf(e, y, sn[i & 1]);
         }
+        s = fmaf(f, fmaf(dy, d, s), sn[0] + sn[1]);
+        d = fmaf(d, f, dn[0] + dn[1]);
         m = mn;
-        d = d0;
-        s = s0;
     }
 };
 

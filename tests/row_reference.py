@@ -6,9 +6,12 @@ size): the kernels form y = (z - m) c with c = log2(e) (1 / T), so y is off by
 at most 5 u |y| (difference, quotient, constant, two products) and exp2 by 2 u;
 a term's exponential is off by (5 |x| + 2) u of itself, x = y ln 2.  Of the sum
 d, weighted by p, that is 5 u E|x| + 2 u, and E|x| = H - log d' <= ln V (d' >= 1);
-a further exponential where segments meet (2 u), 31 + 6 additions in FP32 (37 u,
-the rest is FP64) and the rounding of d itself.  d is therefore within
-(5 ln V + 42) u of itself, and log d within as much absolutely."""
+a further exponential where waves meet (2 u), at
+most 31 + 6 additions of a lane's segment and of a wave in FP32 (37 u, the rest is
+FP64) and the rounding of d itself.  A lane takes up to V / 8192 segments (four waves
+of 2048 columns); each further one multiplies the sum so far by an exponential and
+adds to it (4 u).  d is therefore within (5 ln V + 42 + 4 V / 8192) u of itself, and
+log d within as much absolutely.  (The one-read kernel adds 15 + 2 + 6 times.)"""
 import math
 
 import torch
@@ -19,7 +22,7 @@ TINY = 2.0 ** -120  # what FP32 may lose below its range
 
 
 def d_bound(V):
-    return (5.0 * math.log(max(V, 2)) + 42.0) * U
+    return (5.0 * math.log(max(V, 2)) + 42.0 + 4.0 * (V // 8192)) * U
 
 
 def temperatures(temperature, n, device):
