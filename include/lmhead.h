@@ -552,7 +552,7 @@ int32_t lmhead_beam_reorder(const void *src, int64_t src_outer, int64_t src_row,
  *  logprob, entropy, rank  [n_rows] or NULL (not wanted).
  *  top_logprob FP32, top_token int32 [n_rows x n_top], contiguous; not used when
  *           n_top == 0.
- *  Limits: 1 <= n_cols, n_top <= min(64, n_cols).
+ *  Limits: 1 <= n_cols <= 2^30, n_top <= min(64, n_cols).
  *  workspace as lmhead_logits_lora, of lmhead_logprobs_workspace_bytes(n_rows,
  *  n_cols, n_top) bytes (may be NULL where that is 0).  Outputs overlap neither
  *  inputs nor each other.
@@ -613,7 +613,7 @@ int32_t lmhead_logprobs_bwd(const void *logits, int64_t ld, int32_t logits_dtype
  *  logits, logits_dtype, temperature as lmhead_logprobs.  teacher_token int32 and
  *  teacher_value FP32 or BF16 (teacher_dtype), [n_rows x n_list], row pitches
  *  ldt, ldv >= n_list, aligned to their elements.
- *  loss [n_rows] or NULL.  Limits: n_cols >= 1, 0 <= n_list <= 256.
+ *  loss [n_rows] or NULL.  Limits: 1 <= n_cols <= 2^30, 0 <= n_list <= 256.
  *  workspace as lmhead_logits_lora, of lmhead_distill_workspace_bytes(n_rows,
  *  n_cols) bytes (may be NULL where that is 0).  Outputs overlap neither inputs
  *  nor each other.

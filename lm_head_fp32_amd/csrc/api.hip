@@ -286,12 +286,14 @@ bool beam_sizes_ok(int64_t B, int64_t W, int64_t V, int64_t n_out)
     return B == 0 || lmh::beam_segments(V) <= kMaxLaunchItems / 64 / (B * W);
 }
 
-// Log-probabilities and distillation: rows of at least one column.
+// Log-probabilities and distillation: rows of at least one column, and of few enough
+// that column numbers past a row's end fit 32 bits.
 constexpr int64_t kMaxTop = 64;
+constexpr int64_t kMaxRowCols = int64_t{1} << 30;
 
 bool rows_ok(int64_t n, int64_t V)
 {
-    return n >= 0 && n <= kMaxDim && V >= 1 && V <= kMaxDim;
+    return n >= 0 && n <= kMaxDim && V >= 1 && V <= kMaxRowCols;
 }
 
 // Number of values behind a pointer of stride 0 (one) or 1 (one per row).

@@ -266,6 +266,8 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(4))) vo
         if (y >= 0 && y < V) {
             zy = row_element<BF16>(zr, y);
             above = key_value(order_key(zy) + 1u);
+        } else {
+            y = -1;
         }
     }
     if constexpr (TOP) {

@@ -220,6 +220,30 @@ def test_pitched_lists_and_given_outputs():
         assert torch.allclose(g, want[2], rtol=1e-5, atol=1e-7)
 
 
+@pytest.mark.parametrize("tail", [False, True])
+def test_rows_in_many_parts(tail):
+    """Few long rows: parts and their merge, over a workspace of any contents."""
+    n, V, k = 2, 1_200_003, 200
+    for dtype in (F32, BF16):
+        z, gen = ref.random_logits(n, V, dtype, 3)
+        ids = torch.randint(0, V, (n, k), device="cuda", generator=gen).int()
+        ids[0, 3] = ids[0, 190] = V - 1
+        vals = torch.log_softmax(torch.randn(n, k, device="cuda", generator=gen), 1) - 0.3
+        up = torch.ones(1, device="cuda")
+        ws = torch.full((lmh.lmhead_distill_workspace_bytes(n, V),), 255, dtype=torch.uint8, device="cuda")
+        assert ws.numel() > 0
+        want = ref.distill(z, ids, vals, tail, None, up)
+        loss, stats, g = lmh.lmhead_distill_fused(z, ids, vals, up, tail=tail, workspace=ws, grad_dtype=F32)
+        ref.assert_within(loss, want["loss"], want["tol_loss"], "loss")
+        ref.assert_grad(g, want["dlogits"], want["tol_dlogits"], "dlogits")
+        ws.fill_(255)
+        again = lmh.lmhead_distill_fwd(z, ids, vals, tail=tail, workspace=ws)
+        assert torch.equal(again[0], loss) and torch.equal(again[1], stats)
+        ids[1] = -1
+        loss, stats = lmh.lmhead_distill_fwd(z, ids, vals, tail=tail, workspace=ws)
+        assert torch.equal(loss[0], again[0][0]) and loss[1] == 0 and (stats[1] == 0).all()
+
+
 def test_offsets_past_32_bits():
     V, n, k = 131072, 16500, 3
     z = torch.zeros(n, V, dtype=BF16, device="cuda")

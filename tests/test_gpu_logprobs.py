@@ -156,6 +156,47 @@ def test_masks_and_bad_rows(V):
     _check_forward(z[rows], token[rows], t[rows], k, tuple(x[rows] for x in got))
 
 
+def test_many_parts_of_equal_logits():
+    """A row in so many parts that their lists pass what is ranked at once, and a
+    workspace whose contents do not matter."""
+    n, V, k = 2, 4_500_003, 64
+    for dtype in (F32, BF16):
+        z = ref.padded(n, V, dtype)
+        z[0] = 2.5
+        z[1] = -math.inf
+        z[1, V - 100:] = -1.0
+        z[1, 7] = -2.0
+        token = torch.tensor([V - 1, 7], dtype=torch.int32, device="cuda")
+        ws = torch.full((lmh.lmhead_logprobs_workspace_bytes(n, V, k),), 255, dtype=torch.uint8, device="cuda")
+        assert ws.numel() > 2048 * 8 * n
+        got = lmh.lmhead_logprobs(z, token, n_top=k, workspace=ws)
+        assert got[4][0].tolist() == list(range(k)) and got[4][1].tolist() == list(range(V - 100, V - 100 + k))
+        assert got[2].tolist() == [V - 1, 100]
+        _check_forward(z, token, None, k, got)
+        ws.fill_(255)
+        assert torch.equal(lmh.lmhead_logprobs(z, token, workspace=ws)[5], got[5])
+
+
+def test_two_streams_at_once():
+    """Calls on two streams, a workspace each."""
+    z, gen = ref.random_logits(3, 200003, F32, 5)
+    token = _tokens(3, 200003, gen)
+    want = lmh.lmhead_logprobs(z, token, n_top=9)
+    g = torch.randn(3, device="cuda", generator=gen)
+    grad = lmh.lmhead_logprobs_bwd(z, want[5], token, g)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = []
+    for _ in range(10):
+        for st in streams:
+            res = lmh.lmhead_logprobs(z, token, n_top=9, stream=st)
+            got.append((*res, lmh.lmhead_logprobs_bwd(z, res[5], token, g, stream=st)))
+    torch.cuda.synchronize()
+    for res in got:
+        for a, b in zip(res, (*want, grad)):
+            assert torch.equal(a, b)
+
+
 def test_long_rows_and_many():
     """Offsets past 2^31 elements and rows past what a short grid holds."""
     V, n = 131072, 16500                           # 2.16e9 elements
