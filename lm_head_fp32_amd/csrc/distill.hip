@@ -375,10 +375,10 @@ __global__ __launch_bounds__(kListThreads) void distill_merge_kernel(
 
 // ------------------------------------------------------------------ gradient
 
-constexpr int kBwdThreads = kListThreads;
+constexpr int kBwdThreads = 128;
 constexpr int kBwdVecs = 4;  // 16-byte loads per thread
 
-// One chunk of kBwdVecs x 256 vectors of 16 bytes of a row per workgroup.  Every
+// One chunk of 4 x 128 vectors of 16 bytes of a row per workgroup.  Every
 // column is first written as if it were off the list; the threads of the chunk's
 // listed columns then write theirs over it.
 template <bool ZBF16, bool GBF16>
@@ -388,10 +388,10 @@ __global__ __launch_bounds__(kBwdThreads) void distill_bwd_kernel(
     int64_t dloss_stride, void *dlogits, int64_t ldg, int64_t V, uint32_t chunks)
 {
     constexpr int G = ZBF16 ? 8 : 4;
-    constexpr int NW = kBwdThreads / 64;
-    __shared__ int32_t ids[kBwdThreads];
-    __shared__ float qs[kBwdThreads];
-    __shared__ int32_t counts[NW];
+    constexpr int NW = kBwdThreads / 64, EPT = kMaxList / kBwdThreads;  // entries per thread
+    __shared__ int32_t ids[kMaxList];
+    __shared__ float qs[kMaxList];
+    __shared__ int32_t counts[kMaxList / 64];
     const uint32_t id = blockIdx.x, row = id / chunks, chunk = id - row * chunks;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int64_t nv = V / G;
@@ -405,8 +405,8 @@ __global__ __launch_bounds__(kBwdThreads) void distill_bwd_kernel(
     const int64_t first = static_cast<int64_t>(chunk) * kBwdThreads * kBwdVecs;
     const bool last = chunk == chunks - 1;
     uint4 q[kBwdVecs];
-    float listed_grad = 0.0f;
-    int64_t listed_at = -1;
+    float listed_grad[EPT];
+    int32_t listed_at[EPT];
     if (!nothing) {
 #pragma unroll
         for (int u = 0; u < kBwdVecs; ++u) {
@@ -414,29 +414,36 @@ __global__ __launch_bounds__(kBwdThreads) void distill_bwd_kernel(
             if (i < nv)
                 q[u] = load_row(zr, i);
         }
-        // The list's entries in this chunk, compacted in each wave's quarter.
-        const Entry en = entry(list, row, tid);
+        // The list's entries in this chunk, compacted by groups of 64.
         const int64_t end = last ? V : (first + kBwdThreads * kBwdVecs) * G;
-        const bool here = en.token >= first * G && en.token < end;
         const float t_inv = list.tail ? 1.0f : inv_t;
-        const uint64_t mask = __ballot(here);
-        if (here) {
-            const int at = wave * 64 + __popcll(mask & ((1ull << lane) - 1ull));
-            ids[at] = en.token;
-            qs[at] = __builtin_amdgcn_exp2f((en.value - st.top) * (kLog2e * t_inv)) / st.sum;
-            const float z = row_element<ZBF16>(zr, en.token);
-            listed_grad = __builtin_amdgcn_exp2f((z - st.m) * c) * (st.weight / st.d);
-            listed_at = en.token;
+#pragma unroll
+        for (int j = 0; j < EPT; ++j) {
+            const Entry en = entry(list, row, j * kBwdThreads + tid);
+            const bool here = en.token >= first * G && en.token < end;
+            const uint64_t mask = __ballot(here);
+            const int group = j * NW + wave;
+            listed_at[j] = here ? en.token : -1;
+            if (here) {
+                const int at = group * 64 + __popcll(mask & ((1ull << lane) - 1ull));
+                ids[at] = en.token;
+                qs[at] = __builtin_amdgcn_exp2f((en.value - st.top) * (kLog2e * t_inv)) / st.sum;
+                const float z = row_element<ZBF16>(zr, en.token);
+                listed_grad[j] = __builtin_amdgcn_exp2f((z - st.m) * c) * (st.weight / st.d);
+            }
+            if (lane == 0)
+                counts[group] = __popcll(mask);
         }
-        if (lane == 0)
-            counts[wave] = __popcll(mask);
         __syncthreads();  // the list's logits are read before the row is written (in place)
-        if (here) {
+#pragma unroll
+        for (int j = 0; j < EPT; ++j) {
+            if (listed_at[j] < 0)
+                continue;
             float sum = 0.0f;
-            for (int v = 0; v < NW; ++v)
+            for (int v = 0; v < kMaxList / 64; ++v)
                 for (int i = 0; i < counts[v]; ++i)
-                    sum += ids[v * 64 + i] == en.token ? qs[v * 64 + i] : 0.0f;
-            listed_grad = (listed_grad - sum) * up;
+                    sum += ids[v * 64 + i] == listed_at[j] ? qs[v * 64 + i] : 0.0f;
+            listed_grad[j] = (listed_grad[j] - sum) * up;
         }
     }
     auto value = [&](float z) { return __builtin_amdgcn_exp2f((z - st.other) * c) * w_up; };
@@ -459,8 +466,10 @@ __global__ __launch_bounds__(kBwdThreads) void distill_bwd_kernel(
     }
     if (!nothing) {
         __syncthreads();  // the chunk is written
-        if (listed_at >= 0)
-            store_element<GBF16>(gr, listed_at, listed_grad);
+#pragma unroll
+        for (int j = 0; j < EPT; ++j)
+            if (listed_at[j] >= 0)
+                store_element<GBF16>(gr, listed_at[j], listed_grad[j]);
     }
 }
 

@@ -600,10 +600,10 @@ __global__ __launch_bounds__(kTopThreads) void logprobs_top_kernel(
 
 // ------------------------------------------------------------------ gradient
 
-constexpr int kBwdThreads = 256;
+constexpr int kBwdThreads = 128;
 constexpr int kBwdVecs = 4;  // 16-byte loads per thread
 
-// One chunk of kBwdVecs x 256 vectors of 16 bytes of a row per workgroup.  With
+// One chunk of 4 x 128 vectors of 16 bytes of a row per workgroup.  With
 // y = (z - m) / T / ln 2 and e = 2^y, dz = e (a + b y), b = -h ln 2 / (d T) and
 // a = -(g + h (H - log d)) / (d T), and g / T more at the token.
 template <bool ZBF16, bool GBF16, bool ENTROPY>
