@@ -87,12 +87,50 @@ struct ListShared {
     double part[kListThreads / 64][4];
 };
 
-// By a workgroup whose first 256 threads hold an entry each (en, and z, the logit of
-// its column; `again`: another entry may have its token).  Two barriers; q is the
-// thread's own share of the teacher (of nothing: 0).
+// The sums of the shared parts; any thread, once list_part is through.
 template <bool TAIL>
-__device__ __forceinline__ ListSums list_sums(ListShared &sh, const Entry &en, float z, int64_t V, float inv_t,
-                                              int32_t k, bool again, int tid, double &q)
+__device__ __forceinline__ ListSums list_sums(const ListShared &sh)
+{
+    constexpr int NW = kListThreads / 64;
+    ListSums r;
+    r.top = sh.v_max[0];
+    r.m_l = sh.z_max[0];
+    int32_t flags = sh.flags[0];
+    double s = sh.part[0][0];
+    r.A = sh.part[0][1];
+    r.B = sh.part[0][2];
+    r.D = sh.part[0][3];
+#pragma unroll
+    for (int w = 1; w < NW; ++w) {
+        r.top = __builtin_elementwise_maximum(r.top, sh.v_max[w]);
+        r.m_l = __builtin_elementwise_maximum(r.m_l, sh.z_max[w]);
+        flags += sh.flags[w];
+        s += sh.part[w][0];
+        r.A += sh.part[w][1];
+        r.B += sh.part[w][2];
+        r.D += sh.part[w][3];
+    }
+    r.there = flags & 0x3ff;
+    r.off = ((flags >> 10) & 0x3ff) != 0;
+    r.twice = (flags >> 20) != 0;
+    r.sum = s;
+    r.total = s;
+    if constexpr (TAIL) {
+        r.top = 0.0f;
+        r.sum = 1.0;
+    } else {
+        r.total = s == s ? 1.0 : s;
+        r.B /= s;
+    }
+    return r;
+}
+
+// By a workgroup whose first 256 threads hold an entry each (en, and z, the logit of
+// its column; `again`: another entry may have its token).  Two barriers.  Returns the
+// thread's own share of the teacher: with TAIL q itself, else q times the sum.
+template <bool TAIL>
+__device__ __forceinline__ double list_part(ListShared &sh, const Entry &en, float z, int64_t V, float inv_t,
+                                            int32_t k, bool again, int tid)
 {
     const int lane = tid & 63, wave = tid >> 6;
     constexpr int NW = kListThreads / 64;
@@ -108,31 +146,25 @@ __device__ __forceinline__ ListSums list_sums(ListShared &sh, const Entry &en, f
         }
     }
     __syncthreads();
-    ListSums r;
-    r.top = sh.v_max[0];
-    r.m_l = sh.z_max[0];
-    int32_t flags = sh.flags[0];
-#pragma unroll
-    for (int w = 1; w < NW; ++w) {
-        r.top = __builtin_elementwise_maximum(r.top, sh.v_max[w]);
-        r.m_l = __builtin_elementwise_maximum(r.m_l, sh.z_max[w]);
-        flags += sh.flags[w];
-    }
-    r.there = flags & 0x3ff;
-    r.off = ((flags >> 10) & 0x3ff) != 0;
-    r.twice = (flags >> 20) != 0;
-    if (TAIL)
-        r.top = 0.0f;
-    double x = 0.0, e = 0.0;
+    double e = 0.0;
     if (wave < NW) {
-        x = (static_cast<double>(en.value) - r.top) * (TAIL ? 1.0f : inv_t);
+        float top = sh.v_max[0], m_l = sh.z_max[0];
+        int32_t flags = sh.flags[0];
+#pragma unroll
+        for (int w = 1; w < NW; ++w) {
+            top = __builtin_elementwise_maximum(top, sh.v_max[w]);
+            m_l = __builtin_elementwise_maximum(m_l, sh.z_max[w]);
+            flags += sh.flags[w];
+        }
+        const double x = TAIL ? static_cast<double>(en.value) : (static_cast<double>(en.value) - top) * inv_t;
         e = there ? exp(x) : 0.0;
-        double s = wave_sum(e), a = wave_sum(e != 0.0 ? e * x : 0.0), b = wave_sum(e != 0.0 ? e * z : 0.0), dl = 0.0;
+        const double s = wave_sum(e), a = wave_sum(e != 0.0 ? e * x : 0.0), b = wave_sum(e != 0.0 ? e * z : 0.0);
+        double dl = 0.0;
         if constexpr (TAIL) {
             bool first = there;
-            for (int i = 0; r.twice && i < min(tid, k); ++i)
+            for (int i = 0; (flags >> 20) && i < min(tid, k); ++i)
                 first = first && sh.ids[i] != en.token;
-            dl = wave_sum(first && z != -INFINITY ? exp((static_cast<double>(z) - r.m_l) * inv_t) : 0.0);
+            dl = wave_sum(first && z != -INFINITY ? exp((static_cast<double>(z) - m_l) * inv_t) : 0.0);
         }
         if (lane == 0) {
             sh.part[wave][0] = s;
@@ -142,22 +174,7 @@ __device__ __forceinline__ ListSums list_sums(ListShared &sh, const Entry &en, f
         }
     }
     __syncthreads();
-    double s = 0.0, a = 0.0, b = 0.0;
-    r.D = 0.0;
-#pragma unroll
-    for (int w = 0; w < NW; ++w) {
-        s += sh.part[w][0];
-        a += sh.part[w][1];
-        b += sh.part[w][2];
-        r.D += sh.part[w][3];
-    }
-    r.sum = TAIL ? 1.0 : s;
-    const double inv = 1.0 / r.sum;
-    r.total = TAIL ? s : (s == s ? 1.0 : s);
-    r.A = a;
-    r.B = b * inv;
-    q = e * inv;
-    return r;
+    return e;
 }
 
 __device__ __forceinline__ double lane_value(double v, int lane)
@@ -262,10 +279,8 @@ __global__ __launch_bounds__(NW * 64) void distill_row_kernel(
             again = (atomicOr(&listed[at >> 5], 1u << (at & 31)) >> (at & 31)) & 1u;
         __syncthreads();
     }
-    ListSums t;
-    double q;
     if (parts == 1)
-        t = list_sums<TAIL>(sh, en, z, V, inv_t, list.k, again, tid, q);
+        list_part<TAIL>(sh, en, z, V, inv_t, list.k, again, tid);
 
     float m = -INFINITY, d = 0.0f;  // the lane's, rescaled once per 32 values
     for (int32_t r = seg0; r < seg1; r += NW, seg += NW) {
@@ -314,7 +329,7 @@ __global__ __launch_bounds__(NW * 64) void distill_row_kernel(
     const float m_o = wave_maximum(rm);
     const double d_o = wave_sum(rd != 0.0f ? static_cast<double>(rd) * __builtin_amdgcn_exp2f((rm - m_o) * c) : 0.0);
     if (parts == 1) {
-        const RowStats st = finish_row<TAIL>(t, m_o, d_o, inv_t, lane);
+        const RowStats st = finish_row<TAIL>(list_sums<TAIL>(sh), m_o, d_o, inv_t, lane);
         if (lane == 0) {
             stats[row] = st;
             if (loss)
@@ -342,8 +357,8 @@ __global__ __launch_bounds__(kListThreads) void distill_merge_kernel(
     if (en.token >= 0 && en.token < V)
         z = bf16 ? row_element<true>(zr, en.token) : row_element<false>(zr, en.token);
     sh.ids[tid] = en.token;
-    double q;
-    const ListSums t = list_sums<TAIL>(sh, en, z, V, inv_t, list.k, true, tid, q);
+    list_part<TAIL>(sh, en, z, V, inv_t, list.k, true, tid);
+    const ListSums t = list_sums<TAIL>(sh);
     if (t.there == 0) {
         if (tid == 0) {
             stats[row] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
@@ -376,9 +391,9 @@ __global__ __launch_bounds__(kListThreads) void distill_merge_kernel(
 // ------------------------------------------------------------------ gradient
 
 constexpr int kBwdThreads = 128;
-constexpr int kBwdVecs = 4;  // 16-byte loads per thread
+constexpr int kBwdVecs = 4;  // vectors per thread
 
-// One chunk of 4 x 128 vectors of 16 bytes of a row per workgroup.  Every
+// One chunk of 4 x 128 vectors of a row per workgroup.  Every
 // column is first written as if it were off the list; the threads of the chunk's
 // listed columns then write theirs over it.
 template <bool ZBF16, bool GBF16>
@@ -387,7 +402,8 @@ __global__ __launch_bounds__(kBwdThreads) void distill_bwd_kernel(
     const float *__restrict__ temperature, int64_t temperature_stride, const float *__restrict__ dloss,
     int64_t dloss_stride, void *dlogits, int64_t ldg, int64_t V, uint32_t chunks)
 {
-    constexpr int G = ZBF16 ? 8 : 4;
+    constexpr int G = kRowVec<ZBF16, GBF16>;
+    using Vec = RowVec<ZBF16, G>;
     constexpr int NW = kBwdThreads / 64, EPT = kMaxList / kBwdThreads;  // entries per thread
     __shared__ int32_t ids[kMaxList];
     __shared__ float qs[kMaxList];
@@ -399,12 +415,12 @@ __global__ __launch_bounds__(kBwdThreads) void distill_bwd_kernel(
     const float inv_t = inverse_temperature(temperature, row * temperature_stride);
     const float c = kLog2e * inv_t, up = dloss[row * dloss_stride] * inv_t, w_up = st.w * up;
     const bool nothing = up == 0.0f || (st.weight == 0.0f && st.w == 0.0f);  // the row is not read
-    const char *zr = static_cast<const char *>(logits) + static_cast<int64_t>(row) * ld * (16 / G);
+    const char *zr = static_cast<const char *>(logits) + static_cast<int64_t>(row) * ld * (ZBF16 ? 2 : 4);
     char *gr = static_cast<char *>(dlogits) + static_cast<int64_t>(row) * ldg * (GBF16 ? 2 : 4);
 
     const int64_t first = static_cast<int64_t>(chunk) * kBwdThreads * kBwdVecs;
     const bool last = chunk == chunks - 1;
-    uint4 q[kBwdVecs];
+    Vec q[kBwdVecs];
     float listed_grad[EPT];
     int32_t listed_at[EPT];
     if (!nothing) {
@@ -412,7 +428,7 @@ __global__ __launch_bounds__(kBwdThreads) void distill_bwd_kernel(
         for (int u = 0; u < kBwdVecs; ++u) {
             const int64_t i = first + u * kBwdThreads + tid;
             if (i < nv)
-                q[u] = load_row(zr, i);
+                q[u].load(zr + i * Vec::kBytes);
         }
         // The list's entries in this chunk, compacted by groups of 64.
         const int64_t end = last ? V : (first + kBwdThreads * kBwdVecs) * G;
@@ -455,7 +471,7 @@ __global__ __launch_bounds__(kBwdThreads) void distill_bwd_kernel(
         float o[G];
 #pragma unroll
         for (int e = 0; e < G; ++e)
-            o[e] = nothing ? 0.0f : value(row_value<ZBF16>(q[u], e));
+            o[e] = nothing ? 0.0f : value(q[u].value(e));
         store_row<GBF16>(gr, i, o);
     }
     // The last V % G columns, by the row's last chunk.
@@ -475,10 +491,14 @@ __global__ __launch_bounds__(kBwdThreads) void distill_bwd_kernel(
 
 // ------------------------------------------- loss and gradient in one read
 
+// A vector of -inf.
+__device__ __attribute__((aligned(16))) uint32_t kNegInfFP32[4] = {0xff800000u, 0xff800000u, 0xff800000u, 0xff800000u};
+__device__ __attribute__((aligned(16))) uint32_t kNegInfBF16[4] = {0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u};
+
 // One workgroup per row, which sits in registers: VALS values per thread, V <= NT VALS.
 // The list's part is worked out while the row's loads are under way.  head[i] names
-// the first entry of the list (plus one) whose column lies in the row's vector i of
-// 16 bytes, next[] the others: so a thread finds the listed columns among its own, in
+// the first entry of the list (plus one) whose column lies in the row's vector i,
+// next[] the others: so a thread finds the listed columns among its own, in
 // tail mode to leave them out of the sums, in the end to write their gradients in
 // their places.  Entries of the same token hold the same gradient, so that the order
 // in which they are found does not matter.
@@ -488,7 +508,8 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(4))) void di
     int64_t temperature_stride, const float *__restrict__ dloss, int64_t dloss_stride, float *__restrict__ loss,
     RowStats *__restrict__ stats, void *dlogits, int64_t ldg)
 {
-    constexpr int G = ZBF16 ? 8 : 4, PER = VALS / G, NW = NT / 64;
+    constexpr int G = kRowVec<ZBF16, GBF16>, PER = VALS / G, NW = NT / 64;
+    using Vec = RowVec<ZBF16, G>;
     __shared__ uint32_t head[NT * PER + 1];
     __shared__ uint32_t next[kMaxList];
     __shared__ float grads[kMaxList];
@@ -496,7 +517,7 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(4))) void di
     __shared__ float2 red[NW];
     const int64_t row = blockIdx.x;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const char *zr = static_cast<const char *>(logits) + row * ld * (16 / G);
+    const char *zr = static_cast<const char *>(logits) + row * ld * (ZBF16 ? 2 : 4);
     char *gr = static_cast<char *>(dlogits) + row * ldg * (GBF16 ? 2 : 4);
     const int nv = static_cast<int>(V / G);  // whole vectors
     const int jt = nv * G + tid;             // a column behind them, for tid < G
@@ -524,17 +545,19 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(4))) void di
         return;
     }
 
-    uint4 raw[PER];
-#pragma unroll
-    for (int p = 0; p < PER; ++p) {
-        const uint32_t none = ZBF16 ? 0xff80ff80u : 0xff800000u;
-        raw[p] = make_uint4(none, none, none, none);
-        if (p * NT + tid < nv)
-            raw[p] = load_row(zr, p * NT + tid);
-    }
-    float tv = has_tail ? row_element<ZBF16>(zr, jt) : -INFINITY;
+    // The list's logits are asked for first: they come back first, and the list's part
+    // is done while the row is on its way.
     const bool inside = en.token >= 0 && en.token < V;
-    const float z = inside ? row_element<ZBF16>(zr, en.token) : -INFINITY;
+    const float z = row_element<ZBF16>(inside ? zr : reinterpret_cast<const char *>(ZBF16 ? kNegInfBF16 : kNegInfFP32),
+                                       inside ? en.token : 0);
+    // Every load is issued, past the row's end from a constant vector of -inf: loads
+    // behind a condition cannot be counted, and the list would have to wait for all.
+    const char *none = reinterpret_cast<const char *>(ZBF16 ? kNegInfBF16 : kNegInfFP32);
+    Vec raw[PER];
+#pragma unroll
+    for (int p = 0; p < PER; ++p)
+        raw[p].load(p * NT + tid < nv ? zr + (p * NT + tid) * Vec::kBytes : none);
+    float tv = row_element<ZBF16>(has_tail ? zr : none, has_tail ? jt : 0);
     if (tid < kMaxList)
         sh.ids[tid] = en.token;
 #pragma unroll
@@ -551,22 +574,29 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(4))) void di
         for (uint32_t e = head[i]; e != 0; e = next[e - 1])
             use(sh.ids[e - 1] - i * G, static_cast<int>(e) - 1);
     };
+    // Which of the thread's vectors hold listed columns (a bit each): read side by side,
+    // where a test at each vector would wait for LDS.
+    uint32_t hits = 0;
+#pragma unroll
+    for (int p = 0; p < PER; ++p)
+        hits |= (p * NT + tid < nv && head[p * NT + tid] != 0) ? 1u << p : 0u;
     bool again = false;
     if (inside)
         listed_in(vec, [&](int at, int e) { again = again || (at == en.token - vec * G && e != tid); });
-    double q;
-    const ListSums t = list_sums<TAIL>(sh, en, z, V, inv_t, list.k, again, tid, q);
+    // What the gradient needs of it is read back from LDS when the row is through (kept
+    // in registers it would be spilled).
+    float q = static_cast<float>(list_part<TAIL>(sh, en, z, V, inv_t, list.k, again, tid));
 
     float v[VALS];
 #pragma unroll
     for (int p = 0; p < PER; ++p)
 #pragma unroll
         for (int e = 0; e < G; ++e)
-            v[p * G + e] = row_value<ZBF16>(raw[p], e);
+            v[p * G + e] = raw[p].value(e);
     if constexpr (TAIL) {
 #pragma unroll
         for (int p = 0; p < PER; ++p) {
-            if (p * NT + tid < nv)
+            if (hits & (1u << p))
                 listed_in(p * NT + tid, [&](int at, int) {
 #pragma unroll
                     for (int e = 0; e < G; ++e)
@@ -607,9 +637,11 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(4))) void di
     }
     // What the gradient needs, in FP32 by every thread: weight / d, and the factor w of
     // exp((z - m_o) / T) off the list.
-    float m = m_o, wd, w;
+    float w;
     {
+        const ListSums t = list_sums<TAIL>(sh);
         const float df = static_cast<float>(d_o);
+        float m = m_o, wd;
         if constexpr (TAIL) {
             m = __builtin_elementwise_maximum(m_o, t.m_l);
             const float f = df != 0.0f ? __builtin_amdgcn_exp2f((m_o - m) * c) : 0.0f;
@@ -622,24 +654,25 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(4))) void di
                 wd = w = __int_as_float(0x7fc00000);
         } else {
             wd = w = static_cast<float>(t.total) / df;
+            q /= static_cast<float>(t.sum);
             if (!(df > 0.0f))
                 wd = w = __int_as_float(0x7fc00000);
         }
         if (t.off || !(t.total < INFINITY))
             wd = w = __int_as_float(0x7fc00000);
-    }
-    if (t.twice) {  // the shares of the same token, in the list's order
+        if (t.twice) {  // the shares of the same token, in the list's order
+            if (tid < kMaxList)
+                grads[tid] = q;
+            __syncthreads();
+            float sum = 0.0f;
+            for (int i = 0; inside && i < list.k; ++i)
+                sum += sh.ids[i] == en.token ? grads[i] : 0.0f;
+            q = sum;
+            __syncthreads();
+        }
         if (tid < kMaxList)
-            grads[tid] = static_cast<float>(q);
-        __syncthreads();
-        float sum = 0.0f;
-        for (int i = 0; inside && i < list.k; ++i)
-            sum += sh.ids[i] == en.token ? grads[i] : 0.0f;
-        q = sum;
-        __syncthreads();
+            grads[tid] = (__builtin_amdgcn_exp2f((z - m) * c) * wd - q) * up;
     }
-    if (tid < kMaxList)
-        grads[tid] = (__builtin_amdgcn_exp2f((z - m) * c) * wd - static_cast<float>(q)) * up;
     __syncthreads();
     if (up == 0.0f) {
         zero_row();
@@ -654,12 +687,13 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(4))) void di
 #pragma unroll
             for (int e = 0; e < G; ++e)
                 o[e] = v[p * G + e] * scale;
-            listed_in(i, [&](int at, int l) {
-                const float g = grads[l];
+            if (hits & (1u << p))
+                listed_in(i, [&](int at, int l) {
+                    const float g = grads[l];
 #pragma unroll
-                for (int e = 0; e < G; ++e)
-                    o[e] = at == e ? g : o[e];
-            });
+                    for (int e = 0; e < G; ++e)
+                        o[e] = at == e ? g : o[e];
+                });
             store_row<GBF16>(gr, i, o);
         }
         if (has_tail) {
@@ -669,7 +703,7 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(4))) void di
         }
     }
     if (wave == 0) {
-        const RowStats st = finish_row<TAIL>(t, m_o, d_o, inv_t, lane);
+        const RowStats st = finish_row<TAIL>(list_sums<TAIL>(sh), m_o, d_o, inv_t, lane);
         if (lane == 0) {
             stats[row] = st;
             if (loss)
@@ -756,7 +790,7 @@ hipError_t launch_distill_fwd(const Distill &p, void *workspace, hipStream_t s)
 
 hipError_t launch_distill_bwd(const Distill &p, hipStream_t s)
 {
-    const int64_t zsz = p.bf16 ? 2 : 4, gsz = p.grad_bf16 ? 2 : 4, G = 16 / zsz;
+    const int64_t zsz = p.bf16 ? 2 : 4, gsz = p.grad_bf16 ? 2 : 4, G = zsz + gsz == 4 ? 8 : 4;
     const int64_t per = kBwdThreads * kBwdVecs;
     const int64_t chunks = std::max<int64_t>(1, (p.V / G + per - 1) / per);
     const int64_t rows = std::max<int64_t>(1, kMaxItems / kBwdThreads / chunks);
@@ -811,7 +845,9 @@ hipError_t launch_distill_fused(const Distill &p, void *workspace, hipStream_t s
         const auto yes = std::true_type{};
         const auto no = std::false_type{};
         auto with_size = [&](auto zb, auto gb, auto tail) {
-            if (p.V <= 512 * 32)
+            if (p.V <= 256 * 32)
+                go(zb, gb, tail, std::integral_constant<int, 256>{}, std::integral_constant<int, 32>{});
+            else if (p.V <= 512 * 32)
                 go(zb, gb, tail, std::integral_constant<int, 512>{}, std::integral_constant<int, 32>{});
             else if (p.V <= 512 * 64)
                 go(zb, gb, tail, std::integral_constant<int, 512>{}, std::integral_constant<int, 64>{});

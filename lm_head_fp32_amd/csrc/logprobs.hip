@@ -601,9 +601,9 @@ __global__ __launch_bounds__(kTopThreads) void logprobs_top_kernel(
 // ------------------------------------------------------------------ gradient
 
 constexpr int kBwdThreads = 128;
-constexpr int kBwdVecs = 4;  // 16-byte loads per thread
+constexpr int kBwdVecs = 4;  // vectors per thread
 
-// One chunk of 4 x 128 vectors of 16 bytes of a row per workgroup.  With
+// One chunk of 4 x 128 vectors of a row per workgroup.  With
 // y = (z - m) / T / ln 2 and e = 2^y, dz = e (a + b y), b = -h ln 2 / (d T) and
 // a = -(g + h (H - log d)) / (d T), and g / T more at the token.
 template <bool ZBF16, bool GBF16, bool ENTROPY>
@@ -613,7 +613,8 @@ __global__ __launch_bounds__(kBwdThreads) void logprobs_bwd_kernel(
     const float *__restrict__ dlogprob, int64_t dlogprob_stride, const float *__restrict__ dentropy,
     int64_t dentropy_stride, void *dlogits, int64_t ldg, int64_t V, uint32_t chunks)
 {
-    constexpr int G = ZBF16 ? 8 : 4;
+    constexpr int G = kRowVec<ZBF16, GBF16>;
+    using Vec = RowVec<ZBF16, G>;
     const uint32_t id = blockIdx.x, row = id / chunks, chunk = id - row * chunks;
     const int tid = threadIdx.x;
     const int64_t nv = V / G;
@@ -630,7 +631,7 @@ __global__ __launch_bounds__(kBwdThreads) void logprobs_bwd_kernel(
     const bool nothing = !bad && g == 0.0f && h == 0.0f;  // the row is not read
     if (bad)
         a = nan;
-    const char *zr = static_cast<const char *>(logits) + static_cast<int64_t>(row) * ld * (16 / G);
+    const char *zr = static_cast<const char *>(logits) + static_cast<int64_t>(row) * ld * (ZBF16 ? 2 : 4);
     char *gr = static_cast<char *>(dlogits) + static_cast<int64_t>(row) * ldg * (GBF16 ? 2 : 4);
 
     auto value = [&](float z, bool own) {
@@ -640,13 +641,13 @@ __global__ __launch_bounds__(kBwdThreads) void logprobs_bwd_kernel(
         return own ? fmaf(e, w, at_token) : e * w;
     };
     const int64_t first = static_cast<int64_t>(chunk) * kBwdThreads * kBwdVecs;
-    uint4 q[kBwdVecs];
+    Vec q[kBwdVecs];
     if (!nothing) {
 #pragma unroll
         for (int u = 0; u < kBwdVecs; ++u) {
             const int64_t i = first + u * kBwdThreads + tid;
             if (i < nv)
-                q[u] = load_row(zr, i);
+                q[u].load(zr + i * Vec::kBytes);
         }
     }
 #pragma unroll
@@ -658,7 +659,7 @@ __global__ __launch_bounds__(kBwdThreads) void logprobs_bwd_kernel(
         const int64_t rel = static_cast<int64_t>(y) - i * G;
 #pragma unroll
         for (int e = 0; e < G; ++e)
-            o[e] = nothing ? 0.0f : value(row_value<ZBF16>(q[u], e), !ignored && rel == e);
+            o[e] = nothing ? 0.0f : value(q[u].value(e), !ignored && rel == e);
         store_row<GBF16>(gr, i, o);
     }
     // The last V % G columns, by the row's last chunk.
@@ -739,7 +740,7 @@ hipError_t launch_logprobs(const Logprobs &p, void *workspace, hipStream_t s)
 
 hipError_t launch_logprobs_bwd(const LogprobsBwd &p, hipStream_t s)
 {
-    const int64_t zsz = p.bf16 ? 2 : 4, gsz = p.grad_bf16 ? 2 : 4, G = 16 / zsz;
+    const int64_t zsz = p.bf16 ? 2 : 4, gsz = p.grad_bf16 ? 2 : 4, G = zsz + gsz == 4 ? 8 : 4;
     const int64_t per = kBwdThreads * kBwdVecs;
     const int64_t chunks = std::max<int64_t>(1, (p.V / G + per - 1) / per);
     const int64_t rows = std::max<int64_t>(1, kMaxItems / kBwdThreads / chunks);

@@ -183,15 +183,35 @@ struct Segment {
     }
 };
 
-template <bool BF16>
-__device__ __forceinline__ float row_value(const uint4 &q, int e)
-{
-    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-    if constexpr (BF16)
-        return __uint_as_float(e & 1 ? w[e / 2] & 0xffff0000u : w[e / 2] << 16);
-    else
-        return __uint_as_float(w[e & 3]);
-}
+// Columns a thread takes at a time of a row that is read and written once: 16 bytes of
+// the wider type (stores of 32 bytes a lane, in two halves, took 1.5 times as long).
+template <bool ZBF16, bool GBF16>
+constexpr int kRowVec = ZBF16 && GBF16 ? 8 : 4;
+
+// G columns of such a row, 8 or 16 bytes.
+template <bool BF16, int G>
+struct RowVec {
+    static constexpr int kBytes = G * (BF16 ? 2 : 4), kWords = kBytes / 4;
+    uint32_t w[kWords];
+    __device__ __forceinline__ void load(const char *p)
+    {
+        if constexpr (kWords == 4) {
+            const u32x4_nt q = __builtin_nontemporal_load(reinterpret_cast<const u32x4_nt *>(p));
+            w[0] = q.x, w[1] = q.y, w[2] = q.z, w[3] = q.w;
+        } else {
+            const u32x2_nt q = __builtin_nontemporal_load(reinterpret_cast<const u32x2_nt *>(p));
+            w[0] = q.x, w[1] = q.y;
+        }
+    }
+    __device__ __forceinline__ float value(int e) const
+    {
+        if constexpr (BF16)
+            return __uint_as_float(e & 1 ? w[e / 2] & 0xffff0000u : w[e / 2] << 16);
+        else
+            return __uint_as_float(w[e]);
+    }
+};
+
 template <bool BF16>
 __device__ __forceinline__ float row_element(const char *row, int64_t j)
 {
