@@ -678,9 +678,11 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(4))) void di
         zero_row();
     } else {
         const float scale = m_t == -INFINITY && w == w ? 0.0f : __builtin_amdgcn_exp2f((m_t - m_o) * c) * (w * up);
+        int t = tid;  // recomputed here: the addresses are not kept over the row's sums
+        asm volatile("" : "+v"(t));
 #pragma unroll
         for (int p = 0; p < PER; ++p) {
-            const int i = p * NT + tid;
+            const int i = p * NT + t;
             if (i >= nv)
                 break;
             float o[G];
