@@ -283,23 +283,21 @@ __global__ __launch_bounds__(NW * 64) void distill_row_kernel(
         list_part<TAIL>(sh, en, z, V, inv_t, list.k, again, tid);
 
     float m = -INFINITY, d = 0.0f;  // the lane's, rescaled once per 32 values
-    for (int32_t r = seg0; r < seg1; r += NW, seg += NW) {
+    for (; seg < seg1; seg += NW) {
         float v[32];
-        next.values(v);  // a segment past the row's end holds -inf only
-        if (r + NW < seg1)
+        next.values(v);
+        if (seg + NW < seg1)
             next.load(zr, V, static_cast<int64_t>(seg + NW) * kSegCols, lane);
         if constexpr (TAIL) {
-            if (seg < seg1) {
 #pragma unroll
-                for (int u = 0; u < 32 / G; ++u) {
-                    const int col = (seg - seg0) * kSegCols + (64 * u + lane) * G;
-                    const uint32_t bits = (listed[col >> 5] >> (col & 31)) & ((1u << G) - 1u);
-                    if (!__ballot(bits != 0))
-                        continue;
+            for (int u = 0; u < 32 / G; ++u) {
+                const int col = (seg - seg0) * kSegCols + (64 * u + lane) * G;
+                const uint32_t bits = (listed[col >> 5] >> (col & 31)) & ((1u << G) - 1u);
+                if (!__ballot(bits != 0))
+                    continue;
 #pragma unroll
-                    for (int e = 0; e < G; ++e)
-                        v[u * G + e] = (bits >> e) & 1u ? -INFINITY : v[u * G + e];
-                }
+                for (int e = 0; e < G; ++e)
+                    v[u * G + e] = (bits >> e) & 1u ? -INFINITY : v[u * G + e];
             }
         }
         float lm = m;

@@ -285,11 +285,12 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(4))) vo
     int n_kept = 0;  // the same in every lane
     uint64_t least = 0;
     float bound = -INFINITY;
-    for (int32_t r = seg0; r < seg1; r += NW, seg += NW) {
-        // A segment past the row's end holds -inf only.
+    // Every wave takes part in the first round (a segment past the row's end holds -inf
+    // only), then each until its segments end.
+    for (int32_t round = 0; round == 0 || seg < seg1; ++round, seg += NW) {
         float v[32], gm[8], lm = -INFINITY;
         next.values(v);
-        if (r + NW < seg1)
+        if (seg + NW < seg1)
             next.load(zr, V, static_cast<int64_t>(seg + NW) * kSegCols, lane);
 #pragma unroll
         for (int u = 0; u < 8; ++u) {
@@ -331,7 +332,6 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(4))) vo
             }
         }
         if constexpr (TOP) {
-            const int32_t round = (r - seg0) / NW;
             if (round == 0)
                 __syncthreads();  // every wave's slots
             if (__ballot(lm >= bound)) {
