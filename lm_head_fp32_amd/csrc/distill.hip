@@ -87,11 +87,17 @@ struct ListShared {
     double part[kListThreads / 64][4];
 };
 
+// Waves that hold entries of a list of k (one at least).
+__device__ __forceinline__ int list_waves(int32_t k)
+{
+    return max((k + 63) / 64, 1);
+}
+
 // The sums of the shared parts; any thread, once list_part is through.
 template <bool TAIL>
-__device__ __forceinline__ ListSums list_sums(const ListShared &sh)
+__device__ __forceinline__ ListSums list_sums(const ListShared &sh, int32_t k)
 {
-    constexpr int NW = kListThreads / 64;
+    const int NW = list_waves(k);
     ListSums r;
     r.top = sh.v_max[0];
     r.m_l = sh.z_max[0];
@@ -100,7 +106,6 @@ __device__ __forceinline__ ListSums list_sums(const ListShared &sh)
     r.A = sh.part[0][1];
     r.B = sh.part[0][2];
     r.D = sh.part[0][3];
-#pragma unroll
     for (int w = 1; w < NW; ++w) {
         r.top = __builtin_elementwise_maximum(r.top, sh.v_max[w]);
         r.m_l = __builtin_elementwise_maximum(r.m_l, sh.z_max[w]);
@@ -133,7 +138,7 @@ __device__ __forceinline__ double list_part(ListShared &sh, const Entry &en, flo
                                             int32_t k, bool again, int tid)
 {
     const int lane = tid & 63, wave = tid >> 6;
-    constexpr int NW = kListThreads / 64;
+    const int NW = list_waves(k);
     const bool there = en.token >= 0;
     if (wave < NW) {
         const float vm = wave_maximum(there ? en.value : -INFINITY), zm = wave_maximum(z);
@@ -150,7 +155,6 @@ __device__ __forceinline__ double list_part(ListShared &sh, const Entry &en, flo
     if (wave < NW) {
         float top = sh.v_max[0], m_l = sh.z_max[0];
         int32_t flags = sh.flags[0];
-#pragma unroll
         for (int w = 1; w < NW; ++w) {
             top = __builtin_elementwise_maximum(top, sh.v_max[w]);
             m_l = __builtin_elementwise_maximum(m_l, sh.z_max[w]);
@@ -327,7 +331,7 @@ __global__ __launch_bounds__(NW * 64) void distill_row_kernel(
     const float m_o = wave_maximum(rm);
     const double d_o = wave_sum(rd != 0.0f ? static_cast<double>(rd) * __builtin_amdgcn_exp2f((rm - m_o) * c) : 0.0);
     if (parts == 1) {
-        const RowStats st = finish_row<TAIL>(list_sums<TAIL>(sh), m_o, d_o, inv_t, lane);
+        const RowStats st = finish_row<TAIL>(list_sums<TAIL>(sh, list.k), m_o, d_o, inv_t, lane);
         if (lane == 0) {
             stats[row] = st;
             if (loss)
@@ -345,7 +349,9 @@ __global__ __launch_bounds__(kListThreads) void distill_merge_kernel(
     const float *__restrict__ temperature, int64_t temperature_stride, const float2 *__restrict__ rec,
     float *__restrict__ loss, RowStats *__restrict__ stats)
 {
+    constexpr int kBuckets = 1024;
     __shared__ ListShared sh;
+    __shared__ uint32_t head[kBuckets], next[kMaxList];
     const int tid = threadIdx.x, lane = tid & 63;
     const int64_t row = blockIdx.x;
     const Entry en = entry(list, row, tid);
@@ -355,8 +361,21 @@ __global__ __launch_bounds__(kListThreads) void distill_merge_kernel(
     if (en.token >= 0 && en.token < V)
         z = bf16 ? row_element<true>(zr, en.token) : row_element<false>(zr, en.token);
     sh.ids[tid] = en.token;
-    list_part<TAIL>(sh, en, z, V, inv_t, list.k, true, tid);
-    const ListSums t = list_sums<TAIL>(sh);
+    bool again = false;
+    if constexpr (TAIL) {  // entries of one token meet in one bucket
+        for (int i = tid; i < kBuckets; i += kListThreads)
+            head[i] = 0;
+        __syncthreads();
+        const uint32_t bucket = (static_cast<uint32_t>(en.token) * 2654435761u) >> 22;
+        if (en.token >= 0)
+            next[tid] = atomicExch(&head[bucket], static_cast<uint32_t>(tid) + 1u);
+        __syncthreads();
+        if (en.token >= 0)
+            for (uint32_t e = head[bucket]; e != 0; e = next[e - 1])
+                again = again || (sh.ids[e - 1] == en.token && static_cast<int>(e) - 1 != tid);
+    }
+    list_part<TAIL>(sh, en, z, V, inv_t, list.k, again, tid);
+    const ListSums t = list_sums<TAIL>(sh, list.k);
     if (t.there == 0) {
         if (tid == 0) {
             stats[row] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
@@ -637,7 +656,7 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(4))) void di
     // exp((z - m_o) / T) off the list.
     float w;
     {
-        const ListSums t = list_sums<TAIL>(sh);
+        const ListSums t = list_sums<TAIL>(sh, list.k);
         const float df = static_cast<float>(d_o);
         float m = m_o, wd;
         if constexpr (TAIL) {
@@ -703,7 +722,7 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(4))) void di
         }
     }
     if (wave == 0) {
-        const RowStats st = finish_row<TAIL>(list_sums<TAIL>(sh), m_o, d_o, inv_t, lane);
+        const RowStats st = finish_row<TAIL>(list_sums<TAIL>(sh, list.k), m_o, d_o, inv_t, lane);
         if (lane == 0) {
             stats[row] = st;
             if (loss)
@@ -723,7 +742,7 @@ constexpr int64_t kMaxPartSegs = 128;
 
 int64_t distill_workspace_bytes(int64_t n_rows, int64_t V)
 {
-    const int64_t parts = row_plan(n_rows, V, kMaxPartSegs).parts;
+    const int64_t parts = row_plan(n_rows, V, 4, kMaxPartSegs).parts;
     return parts == 1 ? 0 : n_rows * parts * static_cast<int64_t>(sizeof(float2));
 }
 
@@ -739,7 +758,7 @@ ListArgs list_args(const Distill &p, int64_t r0)
 
 hipError_t launch_distill_fwd(const Distill &p, void *workspace, hipStream_t s)
 {
-    const RowPlan plan = row_plan(p.n, p.V, kMaxPartSegs);
+    const RowPlan plan = row_plan(p.n, p.V, 4, kMaxPartSegs);
     const int64_t parts = plan.parts, esz = p.bf16 ? 2 : 4;
     const int64_t chunk = std::max<int64_t>(1, kMaxItems / 1024 / parts);
     for (int64_t r0 = 0; r0 < p.n; r0 += chunk) {

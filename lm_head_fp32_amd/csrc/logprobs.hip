@@ -271,8 +271,8 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(4))) vo
         }
     }
     if constexpr (TOP) {
-        if (tid < 128)
-            slot[tid] = 0;
+        for (int i = tid; i < 128; i += NW * 64)
+            slot[i] = 0;
         for (int i = tid; i < kListCap; i += NW * 64)
             cand[i] = 0;
         if (tid == 0)
@@ -304,16 +304,13 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(4))) vo
             if (k <= kFewTop) {
                 atomicMax(&slot[lane], order_key(lm));
             } else {
-                float half = gm[0];
+                // Groups of four in turn, so that both have some where rows are short.
+                float half[2] = {gm[0], gm[1]};
 #pragma unroll
-                for (int u = 1; u < 8; ++u) {
-                    if (u == 4) {
-                        atomicMax(&slot[lane], order_key(half));
-                        half = gm[4];
-                    }
-                    half = __builtin_elementwise_maximum(half, gm[u]);
-                }
-                atomicMax(&slot[lane + 64], order_key(half));
+                for (int u = 2; u < 8; ++u)
+                    half[u & 1] = __builtin_elementwise_maximum(half[u & 1], gm[u]);
+                atomicMax(&slot[lane], order_key(half[0]));
+                atomicMax(&slot[lane + 64], order_key(half[1]));
             }
         }
         sums.add(v, lm, c);
@@ -427,7 +424,7 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(4))) vo
         };
         const int n = static_cast<int>(cand_n);
         if (nan_row) {
-            if (tid < k)
+            if (tid < k)  // k <= 64 threads
                 put(tid, 0);
         } else if (n <= kListCap) {
             for (int i = tid; i < n; i += NW * 64) {
@@ -675,13 +672,13 @@ __global__ __launch_bounds__(kBwdThreads) void logprobs_bwd_kernel(
 
 int64_t logprobs_workspace_bytes(int64_t n_rows, int64_t V, int64_t k)
 {
-    const int64_t parts = row_plan(n_rows, V).parts;
+    const int64_t parts = row_plan(n_rows, V, 1).parts;
     return parts == 1 ? 0 : n_rows * parts * (static_cast<int64_t>(sizeof(LogprobRecord)) + 8 * k);
 }
 
 hipError_t launch_logprobs(const Logprobs &p, void *workspace, hipStream_t s)
 {
-    const RowPlan plan = row_plan(p.n, p.V);
+    const RowPlan plan = row_plan(p.n, p.V, 1);
     const int64_t parts = plan.parts, esz = p.bf16 ? 2 : 4;
     LogprobRecord *rec = static_cast<LogprobRecord *>(workspace);
     uint64_t *lists = reinterpret_cast<uint64_t *>(rec + p.n * parts);
@@ -708,7 +705,9 @@ hipError_t launch_logprobs(const Logprobs &p, void *workspace, hipStream_t s)
         const auto yes = std::true_type{};
         const auto no = std::false_type{};
         auto with_waves = [&](auto bf16, auto top, auto rank) {
-            if (plan.waves == 4)
+            if (plan.waves == 1)
+                rows(bf16, top, rank, std::integral_constant<int, 1>{});
+            else if (plan.waves == 4)
                 rows(bf16, top, rank, std::integral_constant<int, 4>{});
             else if (plan.waves == 8)
                 rows(bf16, top, rank, std::integral_constant<int, 8>{});

@@ -19,16 +19,17 @@ inline int64_t row_segments(int64_t V)
 
 // How the rows of a forward are shared out: a workgroup of 4 waves per row where
 // there are rows enough for every CU, of 8 or 16 where there are fewer (no more than
-// the row has segments), and fewer than 256 rows in parts, one round of segments at
+// the row has segments; of one wave for many rows of one or two: 8192 rows of 1000
+// took 27 us in four waves), and fewer than 256 rows in parts, one round of segments at
 // least each.  A part has at most max_segs segments (a multiple of 16).
 struct RowPlan {
     int32_t waves, part_segs;
     int64_t parts;
 };
-inline RowPlan row_plan(int64_t n_rows, int64_t V, int64_t max_segs = int64_t{1} << 30)
+inline RowPlan row_plan(int64_t n_rows, int64_t V, int32_t min_waves, int64_t max_segs = int64_t{1} << 30)
 {
     const int64_t nseg = row_segments(V);
-    const int32_t most = nseg <= 4 ? 4 : nseg <= 8 ? 8 : 16;
+    const int32_t most = nseg <= 2 && n_rows >= 512 ? min_waves : nseg <= 4 ? 4 : nseg <= 8 ? 8 : 16;
     const int32_t waves = std::min<int32_t>(most, n_rows >= 512 ? 4 : n_rows > 256 ? 8 : 16);
     const int64_t rounds = (nseg + waves - 1) / waves;  // of a workgroup over the whole row
     const int64_t want = std::max<int64_t>(1, 256 / std::max<int64_t>(n_rows, 1));
