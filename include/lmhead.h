@@ -539,9 +539,8 @@ int32_t lmhead_beam_reorder(const void *src, int64_t src_outer, int64_t src_row,
  *                 they leave free holds -inf and -1,
  *    stats[i]   = {m = max z, d = sum exp(x), entropy, logprob}: what
  *                 lmhead_logprobs_bwd needs.
- *  The logits are read once.  The sums are FP32 within 2048 columns and FP64
- *  from there on; ranks and alternatives come from the logits, not from rounded
- *  probabilities.  A row that holds NaN or +inf, one of -inf only, and one whose
+ *  The logits are read once.  A wave's sums are FP32 and joined in FP64; ranks and
+ *  alternatives come from the logits, not from rounded probabilities.  A row that holds NaN or +inf, one of -inf only, and one whose
  *  temperature is not positive and finite, is NaN (tokens -1).
  *
  *  logits   [n_rows x n_cols], leading dimension ld, FP32 or BF16 (logits_dtype),
@@ -648,6 +647,10 @@ int32_t lmhead_distill_bwd(const void *logits, int64_t ld, int32_t logits_dtype,
 /*
  * lmhead_distill_fused -- lmhead_distill_fwd and lmhead_distill_bwd in one call,
  * for an upstream gradient known before the forward
+ *
+ *  Rows of up to 65536 columns are read once, longer ones twice; of a row whose
+ *  list is empty none are read.  Its results agree with the two calls' up to
+ *  rounding.
  */
 int32_t lmhead_distill_fused(const void *logits, int64_t ld, int32_t logits_dtype, int64_t n_rows,
                              int64_t n_cols, const int32_t *teacher_token, int64_t ldt,

