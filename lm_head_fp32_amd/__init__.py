@@ -183,7 +183,7 @@ _current = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 def _stream(stream):
     if stream is None:
         if _raw_stream is not None:  # the handle without a Stream object (2.7 us less)
-            return _vp(_raw_stream(torch.cuda.current_device()))
+            return _raw_stream(_current())
         stream = torch.cuda.current_stream()
     return _vp(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
 
@@ -947,12 +947,20 @@ def _rows(t, name, dtype):
     return _mat(t, name, dtype)
 
 
+_ROW_DT = {torch.float32: LMH_FP32, torch.bfloat16: LMH_BF16}
+
+
 def _row_logits(logits):
     """(pointer, ld, dtype code, n, V) of fp32 or bf16 logits [n, V]."""
-    if not isinstance(logits, torch.Tensor) or logits.dtype not in (torch.float32, torch.bfloat16):
+    code = _ROW_DT.get(logits.dtype) if isinstance(logits, torch.Tensor) else None
+    if code is None:
         raise TypeError("logits: expected a GPU float32 or bfloat16 tensor")
+    if logits.dim() == 2 and logits.is_cuda and logits.get_device() == _current():  # _rows, without a call
+        (n, V), (ld, step) = logits.shape, logits.stride()
+        if step == 1 or V <= 1:
+            return logits.data_ptr(), ld if n > 1 else (V + 7) // 8 * 8, code, n, V
     pz, ld = _rows(logits, "logits", logits.dtype)
-    return (pz, ld, _DT[logits.dtype], *logits.shape)
+    return (pz, ld, code, *logits.shape)
 
 
 def _per_row(t, name, n):
@@ -1114,13 +1122,15 @@ def lmhead_distill_workspace_bytes(n_rows, n_cols):
 def _teacher_list(token, value, n):
     """(token pointer, pitch, value pointer, pitch, dtype code, k) of a teacher's
     lists [n, k]: rows may be padded, elements of a row are contiguous."""
-    if not isinstance(value, torch.Tensor) or value.dtype not in (torch.float32, torch.bfloat16):
+    code = _ROW_DT.get(value.dtype) if isinstance(value, torch.Tensor) else None
+    if code is None:
         raise TypeError("teacher_value: expected a GPU float32 or bfloat16 tensor")
     pt, ldt = _rows(token, "teacher_token", torch.int32)
     pv, ldv = _rows(value, "teacher_value", value.dtype)
-    if token.shape != value.shape or token.shape[0] != n:
+    shape = token.shape
+    if shape != value.shape or shape[0] != n:
         raise ValueError("teacher_token and teacher_value must be [n, k]")
-    return pt, ldt, pv, ldv, _DT[value.dtype], token.shape[1]
+    return pt, ldt, pv, ldv, code, shape[1]
 
 
 def lmhead_distill_fwd(logits, teacher_token, teacher_value, tail=False, temperature=None, loss=None,
