@@ -397,21 +397,25 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(4))) vo
             }
         }
     }
+    RowSums q = {};
+    float own_log_d = 0.0f;
     if (wave == 0) {
-        const RowSums q = fold(part_rec, NW, lane, c);
-        if (parts == 1) {
-            const float log_d = logf(static_cast<float>(q.d));
-            if (lane == 0) {
-                write_row(q, log_d, inv_t, zr, BF16, V, token, ignore_index, row, o);
-                sh_log_d = q.d > 0.0 ? log_d : __int_as_float(0x7fc00000);
-                sh_m = q.m;
-            }
-        } else if (lane == 0) {
-            rec[id] = {q.m, static_cast<float>(q.d), static_cast<float>(q.s), q.before};
+        q = fold(part_rec, NW, lane, c);
+        own_log_d = q.d > 0.0 ? logf(static_cast<float>(q.d)) : __int_as_float(0x7fc00000);
+        if (TOP && lane == 0) {
+            sh_log_d = own_log_d;
+            sh_m = q.m;
         }
     }
-    if constexpr (TOP) {
+    if constexpr (TOP)
         __syncthreads();
+    if (tid == 0) {  // behind the barrier: the token's logit may still be on its way
+        if (parts == 1)
+            write_row(q, own_log_d, inv_t, zr, BF16, V, token, ignore_index, row, o);
+        else
+            rec[id] = {q.m, static_cast<float>(q.d), static_cast<float>(q.s), q.before};
+    }
+    if constexpr (TOP) {
         uint64_t *out_keys = lists + static_cast<int64_t>(id) * k;
         float *lp = o.top_logprob + static_cast<int64_t>(row) * k;
         int32_t *tok = o.top_token + static_cast<int64_t>(row) * k;
@@ -514,12 +518,12 @@ __global__ __launch_bounds__(kTopThreads) void logprobs_top_kernel(
     const uint64_t *keys = lists + row * parts * k;
     const int64_t n_keys = static_cast<int64_t>(parts) * k;
     const float inv_t = inverse_temperature(temperature, row * temperature_stride);
+    const uint64_t first = tid < n_keys ? keys[tid] : 0;  // under way while the sums are folded
+    RowSums q = {};
     if (wave == 0) {
-        const RowSums q = fold(rec + row * parts, parts, lane, kLog2e * inv_t);
-        const float log_d = logf(static_cast<float>(q.d));
+        q = fold(rec + row * parts, parts, lane, kLog2e * inv_t);
         if (lane == 0) {
-            write_row(q, log_d, inv_t, logits + row * ld_bytes, bf16 != 0, V, token, ignore_index, row, o);
-            sh_log_d = q.d > 0.0 ? log_d : __int_as_float(0x7fc00000);
+            sh_log_d = q.d > 0.0 ? logf(static_cast<float>(q.d)) : __int_as_float(0x7fc00000);
             sh_m = q.m;
             n_cand = 0;
         }
@@ -539,6 +543,8 @@ __global__ __launch_bounds__(kTopThreads) void logprobs_top_kernel(
     }
     __syncthreads();
     const float log_d = sh_log_d;
+    if (tid == 0)
+        write_row(q, log_d, inv_t, logits + row * ld_bytes, bf16 != 0, V, token, ignore_index, row, o);
     float *lp = o.top_logprob + row * k;
     int32_t *tok = o.top_token + row * k;
     if (!(log_d == log_d)) {
@@ -550,7 +556,7 @@ __global__ __launch_bounds__(kTopThreads) void logprobs_top_kernel(
     }
     const uint64_t least = max(static_cast<uint64_t>(bound) << 32, uint64_t{1});
     for (int64_t i = tid; i < n_keys; i += kTopThreads) {
-        const uint64_t key = keys[i];
+        const uint64_t key = i == tid ? first : keys[i];
         if (key >= least) {
             const uint32_t at = atomicAdd(&n_cand, 1u);
             if (at < kTopCap)
