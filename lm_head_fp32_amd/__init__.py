@@ -1037,7 +1037,7 @@ def lmhead_logprobs(logits, token=None, ignore_index=-100, temperature=None, n_t
     ascending column; the alternatives come in the same order (at most 64; -1
     and -inf where fewer columns lie above -inf).  False for logprob, entropy or
     rank skips it.  stats = {m, d, entropy, logprob} is what lmhead_logprobs_bwd
-    needs."""
+    needs.  Where all results are made here they share one allocation."""
     if stream is not None and (logprob is None or entropy is None or rank is None or stats is None or
                                workspace is None or (n_top and (top_logprob is None or top_token is None))):
         return _on_stream(lmhead_logprobs, stream, workspace, logits, token, ignore_index, temperature, n_top,
