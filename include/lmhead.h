@@ -570,9 +570,9 @@ int32_t lmhead_logprobs(const void *logits, int64_t ld, int32_t logits_dtype, in
  *    dlogits[i][j] = (1 / T) [ g_i ([j == token[i]] - p_j) - h_i p_j (log p_j + H_i) ],
  *  g = dlogprob, h = dentropy (FP32, stride 0 or 1; NULL: 0), H the entropy.
  *  stats as the forward wrote it for the same logits and temperature.  g counts
- *  as 0 in rows of ignore_index (token NULL: in all rows).  A row whose g and h
- *  are 0 gets zeros, whatever its logits; a row whose token is neither
- *  ignore_index nor a column gets NaN.
+ *  as 0 in rows of ignore_index (token NULL: in all rows).  A row whose token is
+ *  neither ignore_index nor a column gets NaN, whatever its g and h; any other
+ *  whose g and h are 0 gets zeros, whatever its logits and its temperature.
  *  dlogits [n_rows x n_cols], leading dimension ldg, FP32 or BF16 (grad_dtype:
  *  the FP32 value rounded once); it may be the logits themselves when types and
  *  leading dimensions agree, and otherwise overlaps no input.
@@ -634,7 +634,9 @@ int32_t lmhead_distill_fwd(const void *logits, int64_t ld, int32_t logits_dtype,
  *               dlogits[i][j] = (dloss_i / T) p_j (Q - q_r / p_r) off it.
  *  stats as lmhead_distill_fwd wrote it for the same logits, lists, tail and
  *  temperature.  dloss FP32, stride 0 or 1; a row whose dloss is 0 gets zeros,
- *  whatever its logits.  dlogits as lmhead_logprobs_bwd.
+ *  whatever its logits, its list and its temperature (the forward's loss of such
+ *  a row is NaN all the same where one of them is bad).  dlogits as
+ *  lmhead_logprobs_bwd.
  */
 int32_t lmhead_distill_bwd(const void *logits, int64_t ld, int32_t logits_dtype,
                            const float *stats, const int32_t *teacher_token, int64_t ldt,

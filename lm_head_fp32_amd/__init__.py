@@ -1090,9 +1090,9 @@ def lmhead_logprobs_bwd(logits, stats, token, dlogprob, dentropy=None, ignore_in
 
     stats: the forward's, for the same logits and temperature.  dlogprob,
     dentropy: GPU fp32 tensors of 1 element (every row) or n elements, or None
-    (0); rows where both are 0 get zeros.  token may be None when dlogprob is.
-    grad_dtype as in lmhead_xent_bwd; in_place=True writes over `logits` (in
-    their type)."""
+    (0); rows where both are 0 get zeros, at any temperature.  token may be None
+    when dlogprob is.  grad_dtype as in lmhead_xent_bwd; in_place=True writes over
+    `logits` (in their type)."""
     if stream is not None and dlogits is None and not in_place:
         return _on_launch_stream(lmhead_logprobs_bwd, stream, logits, stats, token, dlogprob, dentropy,
                                  ignore_index, temperature, None, grad_dtype)
@@ -1165,7 +1165,8 @@ def lmhead_distill_bwd(logits, stats, teacher_token, teacher_value, dloss, tail=
     """Gradient of lmhead_distill_fwd's loss with respect to the logits: dlogits
     [n, V].  stats: the forward's, for the same logits, lists, tail and
     temperature.  dloss a GPU fp32 tensor of 1 or n elements; rows where it is 0
-    get zeros.  grad_dtype and in_place as in lmhead_logprobs_bwd."""
+    get zeros, at any temperature.  grad_dtype and in_place as in
+    lmhead_logprobs_bwd."""
     if stream is not None and dlogits is None and not in_place:
         return _on_launch_stream(lmhead_distill_bwd, stream, logits, stats, teacher_token, teacher_value, dloss,
                                  tail, temperature, None, grad_dtype)

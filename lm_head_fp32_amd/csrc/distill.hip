@@ -409,6 +409,14 @@ __global__ __launch_bounds__(kListThreads) void distill_merge_kernel(
 
 // ------------------------------------------------------------------ gradient
 
+// The upstream gradient per unit of z / T.  None is none at any temperature: 0 times the
+// NaN of a temperature that is no temperature would make a row that asks for nothing NaN.
+__device__ __forceinline__ float upstream(const float *dloss, int64_t i, float inv_t)
+{
+    const float g = dloss[i];
+    return g == 0.0f ? 0.0f : g * inv_t;
+}
+
 constexpr int kBwdThreads = 128;
 constexpr int kBwdVecs = 4;  // vectors per thread
 
@@ -433,7 +441,7 @@ __global__ __launch_bounds__(kBwdThreads) void distill_bwd_kernel(
     const int64_t nv = V / G;
     const RowStats st = stats[row];
     const float inv_t = inverse_temperature(temperature, row * temperature_stride);
-    const float c = kLog2e * inv_t, up = dloss[row * dloss_stride] * inv_t, w_up = st.w * up;
+    const float c = kLog2e * inv_t, up = upstream(dloss, row * dloss_stride, inv_t), w_up = st.w * up;
     const bool nothing = up == 0.0f || (st.weight == 0.0f && st.w == 0.0f);  // the row is not read
     const char *zr = static_cast<const char *>(logits) + static_cast<int64_t>(row) * ld * (ZBF16 ? 2 : 4);
     char *gr = static_cast<char *>(dlogits) + static_cast<int64_t>(row) * ldg * (GBF16 ? 2 : 4);
@@ -550,7 +558,7 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(4))) void di
     if (tid < kMaxList)
         en = entry(list, row, tid);
     const float inv_t = inverse_temperature(temperature, row * temperature_stride);
-    const float up = dloss[row * dloss_stride] * inv_t, c = kLog2e * inv_t;
+    const float up = upstream(dloss, row * dloss_stride, inv_t), c = kLog2e * inv_t;
     auto zero_row = [&]() {
         const float o[G] = {};
         for (int i = tid; i < nv; i += NT)
