@@ -540,14 +540,17 @@ int32_t lmhead_beam_reorder(const void *src, int64_t src_outer, int64_t src_row,
  *    stats[i]   = {m = max z, d = sum exp(x), entropy, logprob}: what
  *                 lmhead_logprobs_bwd needs.
  *  The logits are read once.  A wave's sums are FP32 and joined in FP64; ranks and
- *  alternatives come from the logits, not from rounded probabilities.  A row that holds NaN or +inf, one of -inf only, and one whose
- *  temperature is not positive and finite, is NaN (tokens -1).
+ *  alternatives come from the logits, not from rounded probabilities.  A row that
+ *  holds NaN or +inf, one of -inf only, and one whose temperature is none, is NaN
+ *  (tokens -1).
  *
  *  logits   [n_rows x n_cols], leading dimension ld, FP32 or BF16 (logits_dtype),
  *           as lmhead_logits writes them.
  *  token    int32 [n_rows], or NULL: then logprob and rank must be NULL too, and
  *           stats holds 0 in logprob's place.
- *  temperature  FP32, stride 0 (one value) or 1 (one per row), or NULL (1).
+ *  temperature  FP32, stride 0 (one value) or 1 (one per row), or NULL (1).  One
+ *           that is not positive and finite is none, and neither is one so small
+ *           (below 4.3e-39) that log2(e) / T is beyond FP32.
  *  logprob, entropy, rank  [n_rows] or NULL (not wanted).
  *  top_logprob FP32, top_token int32 [n_rows x n_top], contiguous; not used when
  *           n_top == 0.
@@ -603,8 +606,8 @@ int32_t lmhead_logprobs_bwd(const void *logits, int64_t ld, int32_t logits_dtype
  *  to scale them as is common).  A token that is listed twice counts twice in q
  *  and once in p.  A row whose list is empty has loss 0 and gradient 0.  A row
  *  with a token >= n_cols, a value of NaN or +inf, a logit of NaN or +inf, no
- *  logit above -inf or a temperature that is not positive and finite is NaN.  A
- *  listed column at -inf with q > 0 makes the loss +inf.
+ *  logit above -inf or a temperature that is none (see lmhead_logprobs) is NaN.
+ *  A listed column at -inf with q > 0 makes the loss +inf.
  *    stats[i] = 8 floats: {max z, sum exp((z - max z) / T), loss, sum of q (with
  *      q_r), o, w, t, u}: off the list the gradient per unit of dloss / T is
  *      exp((z - o) / T) w, and q_l = exp((v_l - t) / T) / u (tail != 0: t = 0,

@@ -1033,7 +1033,8 @@ def lmhead_logprobs(logits, token=None, ignore_index=-100, temperature=None, n_t
 
     logits [n, V] fp32 or bf16; token int32 [n] (ignore_index: logprob 0, rank
     -1) or None (no logprob, no rank); temperature a GPU fp32 tensor of 1 or n
-    elements or None (1).  rank: columns ahead of the token, equal logits by
+    elements or None (1); a row of one that is not positive and finite, or below
+    4.3e-39, is NaN.  rank: columns ahead of the token, equal logits by
     ascending column; the alternatives come in the same order (at most 64; -1
     and -inf where fewer columns lie above -inf).  False for logprob, entropy or
     rank skips it.  stats = {m, d, entropy, logprob} is what lmhead_logprobs_bwd

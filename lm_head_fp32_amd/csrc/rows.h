@@ -259,13 +259,16 @@ __device__ __forceinline__ void store_element(char *row, int64_t j, float o)
 
 constexpr float kNoTerm = -200.0f;  // 2^-200 is 0 in FP32: what -inf is cut to
 
-// A temperature that is not positive and finite makes the row NaN.
+// A temperature that is not positive and finite makes the row NaN, and so does one below
+// 4.3e-39: log2(e) / T, by which the exponents are formed, passes the FP32 range there,
+// and (m - m) log2(e) / T is NaN (but not where every column is listed with a class for
+// the rest, so it is decided here).
 __device__ __forceinline__ float inverse_temperature(const float *t, int64_t i)
 {
     if (!t)
         return 1.0f;
-    const float v = t[i];
-    return (v > 0.0f && v < INFINITY) ? 1.0f / v : __int_as_float(0x7fc00000);
+    const float v = t[i], inv = 1.0f / v;
+    return (v > 0.0f && v < INFINITY && kLog2e * inv < INFINITY) ? inv : __int_as_float(0x7fc00000);
 }
 
 // The k largest of a segment's values (v, held as Segment loads them, some above

@@ -75,3 +75,40 @@ def test_padded_rows_leave_the_weights_gradient_alone():
     want = dz[:11].double().t() @ x[:11].double()
     # M FP32 additions of products of two BF16 values, exact in FP32
     assert ((dW - want).abs() <= M * ref.U * (dz[:11].double().abs().t() @ x[:11].double().abs()) + ref.TINY).all()
+
+
+@pytest.mark.parametrize("tail", [False, True])
+@pytest.mark.parametrize("V", [4, 200, 70000])
+def test_the_smallest_temperatures(V, tail):
+    """From where log2(e) / T passes FP32 (4.24e-39) a row is NaN in every call, with
+    every column listed too; above that it is the largest logits' columns alone."""
+    none = [1e-45, 1e-39, 2.9e-39, 4e-39, 4.2e-39]
+    T = torch.tensor(none + [4.3e-39, 1e-38, 2e-38], device="cuda")
+    n, bad = T.numel(), len(none)
+    assert (T > 0).all()
+    z = ref.padded(n, V, F32)
+    z.fill_(1.5)
+    z[:, 2] = 0.25
+    token = torch.zeros(n, dtype=torch.int32, device="cuda")
+    k = min(V, 256)
+    lp, ent, rank, top_lp, top_tok, stats = lmh.lmhead_logprobs(z, token, temperature=T, n_top=3)
+    one = torch.ones(1, device="cuda")
+    g = lmh.lmhead_logprobs_bwd(z, stats, token, one, dentropy=0.0 * one, temperature=T)
+    assert torch.isnan(lp[:bad]).all() and torch.isnan(ent[:bad]).all() and (rank[:bad] == -1).all()
+    assert torch.isnan(top_lp[:bad]).all() and (top_tok[:bad] == -1).all() and torch.isnan(g[:bad]).all()
+    log_n = math.log(V - 1)
+    for got in (-lp[bad:], ent[bad:], -top_lp[bad:, 0], -top_lp[bad:, 2]):
+        assert ((got.double() - log_n).abs() <= ref.d_bound(V) + 4 * ref.U * log_n).all()
+    assert top_tok[bad:].tolist() == [[0, 1, 3]] * (n - bad) and (rank[bad:] == 0).all()
+    # The teacher gives the lesser column nothing (exp(-1000) is 0 in 64 bits): with any
+    # share its loss would pass FP32.
+    ids = torch.arange(k, dtype=torch.int32, device="cuda").expand(n, k).contiguous()
+    vals = torch.full((n, k), math.log(0.5 / k), device="cuda")
+    vals[:, 2] = -math.inf if not tail else -1000.0
+    loss, stats = lmh.lmhead_distill_fwd(z, ids, vals, tail=tail, temperature=T)
+    dz = lmh.lmhead_distill_bwd(z, stats, ids, vals, one, tail=tail, temperature=T)
+    fused = lmh.lmhead_distill_fused(z, ids, vals, one, tail=tail, temperature=T)
+    for got_loss, got in ((loss, dz), fused[::2]):
+        assert torch.isnan(got_loss[:bad]).all() and torch.isnan(got[:bad]).all()
+        assert torch.isfinite(got_loss[bad:]).all() and torch.isfinite(got[bad:]).all()
+        assert (got[bad:, 2] == 0).all()
