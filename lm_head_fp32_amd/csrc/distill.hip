@@ -70,8 +70,10 @@ struct alignas(16) RowStats {
 static_assert(sizeof(RowStats) == 32, "eight floats");
 
 // What the list says of a row, in 64 bits: the teacher's total and entropy term
-// (A = sum q log q), B = sum q z, and the student's sum D over the listed columns,
-// each once, about their maximum m_l (tail mode).
+// (A = sum q log q), B = sum q (z - m_l) about the listed columns' maximum m_l, and the
+// student's sum D over them, each once, about m_l too (tail mode).  B and (m_l - m) sum q
+// have one sign; sum q z and m sum q would cancel where the logits have a large common
+// part (a row of masks only, at the type's lowest value).
 struct ListSums {
     double total, A, B, D, sum;
     float m_l, top;
@@ -86,6 +88,12 @@ struct ListShared {
     int32_t flags[kListThreads / 64];  // entries, 2^10 those outside, 2^20 those listed before
     double part[kListThreads / 64][4];
 };
+
+// What B is taken about: m_l, or any finite number where no listed column lies above -inf.
+__device__ __forceinline__ float list_shift(float m_l)
+{
+    return m_l == -INFINITY ? 0.0f : m_l;
+}
 
 // Waves that hold entries of a list of k (one at least).
 __device__ __forceinline__ int list_waves(int32_t k)
@@ -162,7 +170,8 @@ __device__ __forceinline__ double list_part(ListShared &sh, const Entry &en, flo
         }
         const double x = TAIL ? static_cast<double>(en.value) : (static_cast<double>(en.value) - top) * inv_t;
         e = there ? exp(x) : 0.0;
-        const double s = wave_sum(e), a = wave_sum(e != 0.0 ? e * x : 0.0), b = wave_sum(e != 0.0 ? e * z : 0.0);
+        const double s = wave_sum(e), a = wave_sum(e != 0.0 ? e * x : 0.0),
+                     b = wave_sum(e != 0.0 ? e * (static_cast<double>(z) - list_shift(m_l)) : 0.0);
         double dl = 0.0;
         if constexpr (TAIL) {
             bool first = there;
@@ -216,7 +225,7 @@ __device__ __forceinline__ RowStats finish_row(const ListSums &t, float m_o, dou
     const double per_d = lane_value(quot, 0);
     // sum q log q: in logits mode of q = exp(x) / sum
     const double a = TAIL ? t.A : lane_value(quot, 2) - log_2;
-    double l = a - (t.B - m * t.total) * inv_t + log_d * t.total;
+    double l = a - (t.B + (static_cast<double>(list_shift(t.m_l)) - m) * t.total) * inv_t + log_d * t.total;
     double weight = weight0, w = per_d;
     if constexpr (TAIL) {
         if (q_r != 0.0)

@@ -112,3 +112,46 @@ def test_the_smallest_temperatures(V, tail):
         assert torch.isnan(got_loss[:bad]).all() and torch.isnan(got[:bad]).all()
         assert torch.isfinite(got_loss[bad:]).all() and torch.isfinite(got[bad:]).all()
         assert (got[bad:, 2] == 0).all()
+
+
+@pytest.mark.parametrize("tail", [False, True])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("n,V", [(6, 50), (6, 5000), (300, 20000), (6, 40000), (6, 70000), (600, 900)])
+def test_logits_with_a_large_common_part(n, V, dtype, tail):
+    """Rows of masks only (all at the type's lowest value), of one large value, of ties
+    at a low temperature: the loss is that of the same row about zero."""
+    z, gen = ref.random_logits(n, V, dtype, V + n)
+    z[0] = torch.finfo(dtype).min
+    z[1] = 1e30
+    z[2] = 0.1
+    z[3] = -3e38
+    z[4] = torch.finfo(dtype).min
+    z[4, 1] = -2.0 ** 127                  # the listed columns' largest: one term alone
+    T = torch.ones(n, device="cuda")
+    T[2] = 1e-15
+    ids = torch.arange(7, device="cuda").expand(n, 7).int().contiguous()
+    vals = torch.log_softmax(torch.randn(n, 7, device="cuda", generator=gen), 1) - 0.3
+    dloss = torch.randn(n, device="cuda", generator=gen)
+    want = ref.distill(z, ids, vals, tail, T, dloss)
+    plain = z.clone()
+    plain[:4] = 0.0
+    T1 = torch.ones(n, device="cuda")
+    if tail:                               # q does not depend on T
+        same = ref.distill(plain[:4], ids[:4], vals[:4], tail, T1[:4], dloss[:4])
+        assert torch.allclose(same["loss"], want["loss"][:4], rtol=1e-12)
+    assert torch.isfinite(want["loss"]).all() and (want["loss"][:4] < 20).all()
+    if tail:
+        # The reference forms the others' shares of p_r from log p - log p_r, whose log(V - 7)
+        # is lost beside 1.7e38: of row 4 they are 1 / (V - 7) each, and p is column 1's.
+        q = torch.exp(vals[4].double())
+        q_r = 1.0 - q.sum()
+        row = torch.full((V,), -float(q_r) / (V - 7), dtype=torch.float64, device="cuda")
+        row[:7] = -q
+        row[1] += 1.0
+        want["dlogits"][4] = row * dloss[4].double()
+    loss, stats = lmh.lmhead_distill_fwd(z, ids, vals, tail=tail, temperature=T)
+    dz = lmh.lmhead_distill_bwd(z, stats, ids, vals, dloss, tail=tail, temperature=T)
+    fused = lmh.lmhead_distill_fused(z, ids, vals, dloss, tail=tail, temperature=T)
+    for got_loss, got in ((loss, dz), fused[::2]):
+        ref.assert_within(got_loss, want["loss"], want["tol_loss"], "loss")
+        ref.assert_grad(got, want["dlogits"], want["tol_dlogits"], "dlogits")
