@@ -616,7 +616,7 @@ constexpr int kBwdThreads = 128;
 constexpr int kBwdVecs = 4;  // vectors per thread
 
 // One chunk of 4 x 128 vectors of a row per workgroup.  With
-// y = (z - m) / T / ln 2 and e = 2^y, dz = e (a + b y), b = -h ln 2 / (d T) and
+// y = (z - m) / T / ln 2 and e = 2^y, dz = e a + (e y) b, b = -h ln 2 / (d T) and
 // a = -(g + h (H - log d)) / (d T), and g / T more at the token.  Bound by the stream
 // read and written: 4096 x 131072 FP32 to BF16 in 505 us, 6.4 TB/s (256 threads: 524;
 // two vectors a thread: 503 - 531, the row's numbers weigh more).
@@ -651,8 +651,10 @@ __global__ __launch_bounds__(kBwdThreads) void logprobs_bwd_kernel(
     auto value = [&](float z, bool own) {
         const float e2 = __builtin_elementwise_maximum((z - st.x) * c, kNoTerm);
         const float e = __builtin_amdgcn_exp2f(e2);
-        const float w = ENTROPY ? fmaf(b, e2, a) : a;
-        return own ? fmaf(e, w, at_token) : e * w;
+        const float ea = own ? fmaf(e, a, at_token) : e * a;
+        // e e2, which lies in (-0.54, 0], before b: b e2 passes FP32 where h / T is large,
+        // and times e = 0 that would be NaN.
+        return ENTROPY ? fmaf(e * e2, b, ea) : ea;
     };
     const int64_t first = static_cast<int64_t>(chunk) * kBwdThreads * kBwdVecs;
     Vec q[kBwdVecs];

@@ -155,3 +155,22 @@ def test_logits_with_a_large_common_part(n, V, dtype, tail):
     for got_loss, got in ((loss, dz), fused[::2]):
         ref.assert_within(got_loss, want["loss"], want["tol_loss"], "loss")
         ref.assert_grad(got, want["dlogits"], want["tol_dlogits"], "dlogits")
+
+
+@pytest.mark.parametrize("grad", [F32, BF16])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("V", [6, 5000])
+def test_entropy_gradient_at_low_temperatures(V, dtype, grad):
+    """Where p is 0 the entropy has no gradient, however large h / T is."""
+    z, gen = ref.random_logits(6, V, dtype, V)
+    token = torch.randint(0, V, (6,), device="cuda", generator=gen).int()
+    T = torch.tensor([1e-37, 1e-38, 4e-37, 1e-36, 1e-3, 1.0], device="cuda")
+    z[2, :2] = 40.0                        # an even pair: entropy log 2
+    g = torch.full((6,), 0.25, device="cuda")
+    h = torch.tensor([1.0, -0.5, 1.0, 50.0, 1e35, 3e37], device="cuda")
+    for dlogprob in (g, None):
+        stats = lmh.lmhead_logprobs(z, token, temperature=T)[5]
+        got = lmh.lmhead_logprobs_bwd(z, stats, token, dlogprob, dentropy=h, temperature=T, grad_dtype=grad)
+        assert torch.isfinite(got).all()
+        want, tol = ref.logprobs_grad(z, token, T, dlogprob, h)
+        ref.assert_grad(got, want, tol, "dlogits")
