@@ -653,9 +653,9 @@ int32_t lmhead_distill_bwd(const void *logits, int64_t ld, int32_t logits_dtype,
  * lmhead_distill_fused -- lmhead_distill_fwd and lmhead_distill_bwd in one call,
  * for an upstream gradient known before the forward
  *
- *  Rows of up to 65536 columns are read once, longer ones twice; of a row whose
- *  list is empty none are read.  Its results agree with the two calls' up to
- *  rounding.
+ *  Rows of up to 65536 columns are read once, longer ones twice; a row whose
+ *  list is empty is not read, or (beyond 65536 columns) as far as its parts' first
+ *  segments by the forward.  Its results agree with the two calls' up to rounding.
  */
 int32_t lmhead_distill_fused(const void *logits, int64_t ld, int32_t logits_dtype, int64_t n_rows,
                              int64_t n_cols, const int32_t *teacher_token, int64_t ldt,

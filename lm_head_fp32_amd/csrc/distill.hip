@@ -244,8 +244,10 @@ __device__ __forceinline__ RowStats finish_row(const ListSums &t, float m_o, dou
 // of the part, with TAIL of the columns that are not on the row's list; with one part
 // per row also the loss and the record.  Of a row whose list is empty the first round of
 // segments is read at most.  Bound by the read where rows are many and long (1024 x
-// 131072 FP32: 83 us, 6.5 TB/s); of short rows by the list's part, 300 FP64 operations
-// of a wave (8192 x 1000: 37 us).
+// 131072 FP32: 83 us, 6.5 TB/s).  Many short rows are far from it (8192 x 1000, 16 listed:
+// 30 us, with a class for the rest 35 - 37; the read is 4.6): the chain of list, barrier,
+// scan, barrier and the row's numbers, in four waves of which one holds the segment and
+// one the list.
 template <bool BF16, bool TAIL, int NW>
 __global__ __launch_bounds__(NW * 64) void distill_row_kernel(
     const void *__restrict__ logits, int64_t ld, int64_t V, uint32_t parts, int32_t part_segs, ListArgs list,
@@ -538,10 +540,13 @@ __device__ __attribute__((aligned(16))) uint32_t kNegInfBF16[4] = {0xff80ff80u, 
 // next[] the others: so a thread finds the listed columns among its own, in
 // tail mode to leave them out of the sums, in the end to write their gradients in
 // their places.  Entries of the same token hold the same gradient, so that the order
-// in which they are found does not matter.  1024 x 32768 FP32 to BF16, two rows to a CU:
-// 39 us, with 64 listed and the rest as a class 41 (forward and gradient in two kernels:
-// 62); a row that fills the CU's registers has nothing to cover its start and end (1024
-// x 50001: 73 - 78 us, 4.0 TB/s, against 94).
+// in which they are found does not matter.  1024 x 32768 FP32 to BF16, two rows to a CU,
+// 64 listed and the rest as a class: 39 - 45 us (forward and gradient in two kernels: 56);
+// a row that fills the CU's registers has nothing to cover its start and end (1024 x 50001:
+// 74 - 86 us, 3.9 TB/s, against 88; two registers are spilled there in tail mode).  Rows of
+// a few thousand columns gain nothing by the one read: the list's chain and the row's are
+// in one workgroup (8192 x 1000, 16 listed and a class: 55 us, against 35 + 15; 8192 x 4096:
+// 61 against 38 + 38).
 template <bool ZBF16, bool GBF16, bool TAIL, int NT, int VALS>
 __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(4))) void distill_fused_kernel(
     const void *logits, int64_t ld, int64_t V, ListArgs list, const float *__restrict__ temperature,

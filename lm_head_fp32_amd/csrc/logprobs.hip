@@ -125,7 +125,9 @@ __device__ __forceinline__ int keep_k(uint64_t *list, int n, int k, int lane)
 // The keys of a segment that are at least `least` into the wave's list, however
 // many they are (more equal values at the bound than are wanted, or a large k): read
 // again, 64 columns at a time; a full list is cut to its k largest, which then bound
-// what is still to come.
+// what is still to come in the segment.  Rows that come here in every segment are slow: of
+// 777 x 50001, ten alternatives, rows of masks at the type's lowest value but for five
+// columns take 278 us, rows in ascending order 730, where others take 35.
 template <bool BF16>
 __device__ __forceinline__ int collect_all(const char *zr, int64_t V, int64_t j0, uint64_t least,
                                            uint64_t *list, int n, int k, int lane)
@@ -228,10 +230,14 @@ __device__ __forceinline__ void write_row(const RowSums &q, float log_d, float i
 // largest for the merge.  Bound by the one read of the logits where rows are many and
 // long: 8192 x 131072 FP32 in 620 us, 6.9 TB/s (plain loads in place of non-temporal
 // ones: 690); 2048 x 50001 with ten alternatives and ranks in 68 us, 6.0 TB/s.  A value
-// costs 5 full-rate operations and an exponential, with alternatives and a rank half as
-// many again, so BF16 rows are bound by these: 8192 x 16000 in 46 us, 5.7 TB/s, with
-// both 77 - 86.  777 rows of 50001 are three to a CU and take 29 us, with both 35: 4.4
-// TB/s.  One row of 32768 is the latency of one workgroup, 5 us, 8 with alternatives.
+// takes 8.0 vector instructions a lane, with alternatives and a rank 12.2 (counted, the
+// row's start and end among them); of BF16 rows of 16000 columns, two rounds a row, 10.8
+// and 17.3, and these bound them: 8192 x 16000 take 46 - 48 us with the vector units
+// busy all the while (the read is 36), with both 77 - 86, busy for 0.78 of it.  777 rows
+// of 50001 are three to a CU and take 28 us, with both 35: 4.4 TB/s.  One row of 32768
+// is the latency of one workgroup, 5 us, 8 with alternatives.  Many short rows are
+// latency as well: 8192 x 1000 in 11 - 12 us, with ten alternatives 18, with 64 27 (the
+// read is 4.6).
 // Alternatives: slot[l] is the largest value that lane l of any wave has seen (for
 // larger k two slots, for the halves of its values), so the k-th largest of the
 // slots is a lower bound of the k-th largest value (k different values reach it),

@@ -20,8 +20,9 @@ inline int64_t row_segments(int64_t V)
 // How the rows of a forward are shared out: a workgroup of 4 waves per row where
 // there are rows enough for every CU, of 8 or 16 where there are fewer (no more than
 // the row has segments; of one wave for many rows of one or two: 8192 rows of 1000
-// took 27 us in four waves), and fewer than 256 rows in parts, one round of segments at
-// least each.  A part has at most max_segs segments (a multiple of 16).
+// took 27 us in four waves), and up to 128 rows in parts, 256 / rows of them and one round
+// of segments at least each (129 rows of 131072, a workgroup each, take as long as 128 in
+// two parts each: 13.5 us).  A part has at most max_segs segments (a multiple of 16).
 struct RowPlan {
     int32_t waves, part_segs;
     int64_t parts;
