@@ -1,5 +1,6 @@
 """Log-probabilities and distillation at the edges of what the calls take: rows
-that ask for nothing, and temperatures at the ends of their range."""
+that ask for no gradient, the smallest temperatures, logits with a large common
+part, and entropy gradients that are large per unit of temperature."""
 import math
 
 import pytest
