@@ -544,9 +544,9 @@ __device__ __attribute__((aligned(16))) uint32_t kNegInfBF16[4] = {0xff80ff80u, 
 // 64 listed and the rest as a class: 39 - 45 us (forward and gradient in two kernels: 56);
 // a row that fills the CU's registers has nothing to cover its start and end (1024 x 50001:
 // 74 - 86 us, 3.9 TB/s, against 88; two registers are spilled there in tail mode).  Rows of
-// a few thousand columns gain nothing by the one read: the list's chain and the row's are
-// in one workgroup (8192 x 1000, 16 listed and a class: 55 us, against 35 + 15; 8192 x 4096:
-// 61 against 38 + 38).
+// a thousand columns lose by the one read, as the list's chain is most of their time and
+// a CU holds four of these workgroups (8192 x 1000, 16 listed and a class: 55 us, against
+// 35 + 15); rows of 4096 gain (61, against 38 + 38).
 template <bool ZBF16, bool GBF16, bool TAIL, int NT, int VALS>
 __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(4))) void distill_fused_kernel(
     const void *logits, int64_t ld, int64_t V, ListArgs list, const float *__restrict__ temperature,
